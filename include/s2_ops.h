@@ -232,6 +232,95 @@ int s2op_attn_decode_noalloc(const float* qkv, int qkv_ld, int B, int m, int H, 
                              void* kv, int kv_bf16, const int32_t* table, int table_ld, float* o,
                              int o_ld, int nsplit, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit KV cache.  The cache's bytes bound decode attention at large batches
+ * and long contexts; these calls keep keys and values in e4m3.
+ *
+ * Pool: n_pages pages of 16 tokens, kv8 [n_pages][2 (K, V)][Hkv][16][hd] e4m3
+ * bytes (16-byte aligned) and kv_scale fp32 [n_pages][2][Hkv]; a cached value
+ * is byte value * scale.  A block (the 16 rows of one page, K or V, head) has
+ * the scale 2^e with the smallest e in [-32, 32] whose 448 * 2^e covers the
+ * block's largest magnitude (NaN does not count and is stored as NaN; values
+ * beyond 448 * 2^32, infinities among them, saturate).  Rounding is to nearest
+ * even, on keys that are normed and rotated to about 2^-44, so the bytes of a
+ * token depend neither on the batch nor on whether a prompt or a single step
+ * appended it.  New rows in a block with older ones take the larger of both
+ * scales; where it grows, the older rows are rescaled (exact, but for values
+ * that become e4m3 subnormals).  Scales must be powers of two as these calls
+ * write them: of a stored scale the exponent field alone is read.
+ *
+ * hd is 64 or 128, H / Hkv 1..8, B 1..1024.  qkv rows as in s2op_attn_decode:
+ * [q (H*hd) | k (Hkv*hd) | v (Hkv*hd)], fp32, qkv_ld >= (H + 2 Hkv) hd;
+ * rope_cos / rope_sin [n_pos][hd/2]; sequence b's page j is table[b *
+ * table_ld + j].  o: rows of H*hd values, pitch o_ld, fp32 (o_bf16 = 0) or
+ * bf16 (1).  Softmax statistics and sums are fp32; the products run on the
+ * tensor cores with q and the probabilities as f16 pairs (hi + lo, 22 bits)
+ * for an fp32 output, e4m3 values being exact in f16.
+ *
+ * A sequence whose new positions do not lie in [0, min(n_pos, 16 table_ld))
+ * (pos[b] = -1, for instance: a padded batch) is left out: nothing is stored
+ * for it and its rows of o are zero.  A table entry outside [0, n_pages) is
+ * not followed: its keys count as masked and its new rows are not stored (a
+ * row without any key is zero).  No two sequences of a call may append to
+ * the same page; reading a page together is fine.  Pages' rows behind the
+ * last appended one keep their bytes.  workspace: zero-initialised, zero
+ * where it has to be again on exit; calls that may overlap in time need one
+ * each. */
+
+/* Decode attention for B sequences with m new rows each, row b*m + i at
+ * position pos[b] + i: q and k normed and rotated, k and v stored, then
+ * attention over all keys up to the row's position.  m * H / Hkv <= 8. */
+size_t s2op_attn_decode_kv8_workspace_bytes(int B, int m, int H, int Hkv, int hd);
+int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int Hkv, int hd,
+                         const float* q_gain, const float* k_gain, float eps, const float* rope_cos,
+                         const float* rope_sin, int n_pos, const int32_t* pos, void* kv8,
+                         float* kv_scale, int n_pages, const int32_t* table, int table_ld, void* o,
+                         int o_bf16, int o_ld, void* workspace, void* stream);
+
+/* Prompt attention of B sequences in one call: sequence b has the rows
+ * row0[b] .. row0[b+1] - 1 (row0: B + 1 non-decreasing entries on the device;
+ * none is fine) at positions pos0[b], pos0[b] + 1, ..., behind pos0[b] cached
+ * tokens.  T bounds row0[B]; rows in no sequence are left as they are. */
+size_t s2op_attn_prefill_kv8_workspace_bytes(int T, int B, int H, int Hkv, int hd);
+int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B, const int32_t* row0,
+                          const int32_t* pos0, int H, int Hkv, int hd, const float* q_gain,
+                          const float* k_gain, float eps, const float* rope_cos,
+                          const float* rope_sin, int n_pos, void* kv8, float* kv_scale, int n_pages,
+                          const int32_t* table, int table_ld, void* o, int o_bf16, int o_ld,
+                          void* workspace, void* stream);
+
+/* Page src[i] of an fp32 (kv_bf16 = 0) or bf16 pool [n_src][2][Hkv][16][hd]
+ * into page dst[i] of an 8-bit pool, i < n (src, dst, fill: device arrays).
+ * fill (NULL: 16 each): rows of the page that are in use; the others become
+ * zero and do not count for the scales.  A pair with an index outside its
+ * pool is left out; no two pairs may have the same dst.  Pools 16-byte
+ * aligned.  Pages of several layers go through one call when the layers'
+ * pools lie one after the other (page p of layer l is page l * n_pages + p). */
+int s2op_kv8_pack_pages(const void* kv, int kv_bf16, int n_src, const int32_t* src,
+                        const int32_t* fill, void* kv8, float* kv_scale, int n_dst,
+                        const int32_t* dst, int n, int Hkv, int hd, void* stream);
+/* The reverse: byte value * scale, exact in fp32 and in bf16. */
+int s2op_kv8_unpack_pages(const void* kv8, const float* kv_scale, int n_src, const int32_t* src,
+                          void* kv, int kv_bf16, int n_dst, const int32_t* dst, int n, int Hkv,
+                          int hd, void* stream);
+
+/* Copy pages within a pool of any cache type (the forking of a sequence's
+ * last, partly filled page; the moving of pages when a pool is compacted):
+ * page src[i] -> dst[i] in each of ``layers`` layers, page p of layer l at
+ * kv + (l * n_pages + p) * page_bytes; with scale != NULL its scale_bytes too.
+ * src and dst are HOST arrays, read during the call (a captured call keeps
+ * these pairs).  A page may be the source of several pairs; S2_EINVAL for an
+ * index outside the pool, a destination named twice or one that is also a
+ * source, page_bytes not a multiple of 16 or kv not 16-byte aligned,
+ * scale_bytes not a multiple of 4. */
+int s2op_kv_copy_pages(void* kv, size_t page_bytes, void* scale, size_t scale_bytes, int n_pages,
+                       int layers, const int32_t* src, const int32_t* dst, int n, void* stream);
+/* Entries of a device page table [rows][cols], pitch table_ld, that equal
+ * src[i] become dst[i] (HOST arrays; S2_EINVAL for a source named twice or one
+ * that is also a destination); all others stay. */
+int s2op_kv_remap_pages(int32_t* table, int rows, int cols, int table_ld, const int32_t* src,
+                        const int32_t* dst, int n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

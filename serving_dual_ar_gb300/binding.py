@@ -90,6 +90,16 @@ def _load():
         "s2op_attn_prefix_set_trace": (i32, [vp, i32]),
         "s2op_attn_prefill": (i32, [vp, i32, i32, i32, i32, i32, i32, vp, vp, f32, vp, vp, vp, i32,
                                     vp, vp, vp, i32, vp]),
+        "s2op_attn_decode_kv8_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "s2op_attn_decode_kv8": (i32, [vp, i32, i32, i32, i32, i32, i32, vp, vp, f32, vp, vp, i32, vp, vp, vp,
+                                       i32, vp, i32, vp, i32, i32, vp, vp]),
+        "s2op_attn_prefill_kv8_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "s2op_attn_prefill_kv8": (i32, [vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, f32, vp, vp, i32, vp,
+                                        vp, i32, vp, i32, vp, i32, i32, vp, vp]),
+        "s2op_kv8_pack_pages": (i32, [vp, i32, i32, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp]),
+        "s2op_kv8_unpack_pages": (i32, [vp, vp, i32, vp, vp, i32, i32, vp, i32, i32, i32, vp]),
+        "s2op_kv_copy_pages": (i32, [vp, sz, vp, sz, i32, i32, vp, vp, i32, vp]),
+        "s2op_kv_remap_pages": (i32, [vp, i32, i32, i32, vp, vp, i32, vp]),
         "s2op_rope_table": (i32, [i32, i32, f32, vp, vp]),
         "s2op_stream_read_scratch_bytes": (sz, [i32]),
         "s2op_stream_read": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp]),
@@ -351,6 +361,72 @@ def s2op_attn_prefill(qkv, qkv_ld, T, pos0, H, Hkv, hd, q_gain, k_gain, eps, rop
                                  eps, ptr(rope_cos), ptr(rope_sin), ptr(kv), int(kv_bf16),
                                  ptr(table), ptr(q_scratch), ptr(o), o_ld, _stream(stream)),
            "s2op_attn_prefill")
+
+
+def s2op_attn_decode_kv8_workspace_bytes(B, m, H, Hkv, hd):
+    return LIB.s2op_attn_decode_kv8_workspace_bytes(B, m, H, Hkv, hd)
+
+
+def s2op_attn_decode_kv8(qkv, qkv_ld, B, m, H, Hkv, hd, q_gain, k_gain, eps, rope_cos, rope_sin, n_pos, pos,
+                         kv8, kv_scale, n_pages, table, table_ld, o, o_bf16, o_ld, workspace, stream=None):
+    """Decode attention over the 8-bit cache: kv8 uint8 (or float8_e4m3fn) [n_pages, 2, Hkv, 16, hd], kv_scale
+    float32 [n_pages, 2, Hkv]; appends the new rows' keys and values."""
+    _check(LIB.s2op_attn_decode_kv8(ptr(qkv), qkv_ld, B, m, H, Hkv, hd, ptr(q_gain), ptr(k_gain), eps,
+                                    ptr(rope_cos), ptr(rope_sin), n_pos, ptr(pos), ptr(kv8), ptr(kv_scale),
+                                    n_pages, ptr(table), table_ld, ptr(o), int(o_bf16), o_ld, ptr(workspace),
+                                    _stream(stream)), "s2op_attn_decode_kv8")
+
+
+def s2op_attn_prefill_kv8_workspace_bytes(T, B, H, Hkv, hd):
+    return LIB.s2op_attn_prefill_kv8_workspace_bytes(T, B, H, Hkv, hd)
+
+
+def s2op_attn_prefill_kv8(qkv, qkv_ld, T, B, row0, pos0, H, Hkv, hd, q_gain, k_gain, eps, rope_cos, rope_sin,
+                          n_pos, kv8, kv_scale, n_pages, table, table_ld, o, o_bf16, o_ld, workspace,
+                          stream=None):
+    """Prompt attention of B ragged sequences (rows row0[b] .. row0[b+1] - 1, at pos0[b] on) over the 8-bit
+    cache, to which their keys and values are appended."""
+    _check(LIB.s2op_attn_prefill_kv8(ptr(qkv), qkv_ld, T, B, ptr(row0), ptr(pos0), H, Hkv, hd, ptr(q_gain),
+                                     ptr(k_gain), eps, ptr(rope_cos), ptr(rope_sin), n_pos, ptr(kv8),
+                                     ptr(kv_scale), n_pages, ptr(table), table_ld, ptr(o), int(o_bf16), o_ld,
+                                     ptr(workspace), _stream(stream)), "s2op_attn_prefill_kv8")
+
+
+def s2op_kv8_pack_pages(kv, kv_bf16, n_src, src, fill, kv8, kv_scale, n_dst, dst, n, Hkv, hd, stream=None):
+    """Pages src[i] of an fp32 / bf16 pool into pages dst[i] of an 8-bit one (device index arrays)."""
+    _check(LIB.s2op_kv8_pack_pages(ptr(kv), int(kv_bf16), n_src, ptr(src), ptr(fill), ptr(kv8), ptr(kv_scale),
+                                   n_dst, ptr(dst), n, Hkv, hd, _stream(stream)), "s2op_kv8_pack_pages")
+
+
+def s2op_kv8_unpack_pages(kv8, kv_scale, n_src, src, kv, kv_bf16, n_dst, dst, n, Hkv, hd, stream=None):
+    """Pages src[i] of an 8-bit pool into pages dst[i] of an fp32 / bf16 one (device index arrays)."""
+    _check(LIB.s2op_kv8_unpack_pages(ptr(kv8), ptr(kv_scale), n_src, ptr(src), ptr(kv), int(kv_bf16), n_dst,
+                                     ptr(dst), n, Hkv, hd, _stream(stream)), "s2op_kv8_unpack_pages")
+
+
+def _host_i32(a):
+    """A host int32 array of the page indices a (numpy, list or host tensor)."""
+    if getattr(a, "is_cuda", False):
+        raise ValueError("page pairs are host arrays")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+def s2op_kv_copy_pages(kv, page_bytes, scale, scale_bytes, n_pages, layers, src, dst, n, stream=None):
+    """Pages src[i] -> dst[i] (host arrays) in each layer of a pool, with their scales if given."""
+    src, dst = _host_i32(src), _host_i32(dst)
+    if src.size < n or dst.size < n:
+        raise ValueError("fewer page pairs than n")
+    _check(LIB.s2op_kv_copy_pages(ptr(kv), page_bytes, ptr(scale), scale_bytes, n_pages, layers, ptr(src),
+                                  ptr(dst), n, _stream(stream)), "s2op_kv_copy_pages")
+
+
+def s2op_kv_remap_pages(table, rows, cols, table_ld, src, dst, n, stream=None):
+    """Entries src[i] of a device page table become dst[i] (host arrays)."""
+    src, dst = _host_i32(src), _host_i32(dst)
+    if src.size < n or dst.size < n:
+        raise ValueError("fewer page pairs than n")
+    _check(LIB.s2op_kv_remap_pages(ptr(table), rows, cols, table_ld, ptr(src), ptr(dst), n, _stream(stream)),
+           "s2op_kv_remap_pages")
 
 
 def s2op_stream_read_scratch_bytes(n_ops):

@@ -226,6 +226,55 @@ cudaError_t launch_attn_prefill_segs(const AttnPrefillArgs& a, cudaStream_t st, 
 cudaError_t launch_attn_prefill_tc(const AttnPrefillArgs& a, cudaStream_t st, bool pdl);
 size_t attn_prefill_part_floats(int T, int H, int hd, int ksplit);
 
+// ------------------------------------------------------------------ 8-bit KV cache
+// Attention of B sequences over pages of e4m3 blocks with a power-of-two scale
+// per (page, K or V, kv head): kv [n_pages][2][Hkv][16][hd] bytes, scale
+// [n_pages][2][Hkv].  Decode (row0 == null): m new rows per sequence, rows
+// b*m + i at positions pos[b] + i.  Prompts: sequence b has rows row0[b] ..
+// row0[b+1] - 1 of the T at positions pos[b], pos[b] + 1, ...
+struct Kv8Args {
+  const float* qkv = nullptr; int qkv_ld = 0;
+  int B = 1, m = 1, T = 0;
+  const int* row0 = nullptr;
+  const int* pos = nullptr;
+  int H = 0, Hkv = 0, hd = 0;
+  const float* q_gain = nullptr; const float* k_gain = nullptr; float eps = 1e-6f;
+  const float* rope_cos = nullptr; const float* rope_sin = nullptr;   // [n_pos][hd/2]
+  int max_pos = 0;          // positions stay below: min(n_pos, 16 table_ld)
+  uint8_t* kv = nullptr; float* scale = nullptr; int n_pages = 0;
+  const int* table = nullptr; int table_ld = 0;
+  float* o = nullptr; __nv_bfloat16* o16 = nullptr; int o_ld = 0;     // one of the two
+  void* ws = nullptr;
+};
+constexpr int kKv8MaxSeqs = 1024;
+constexpr int kKv8MaxRows = 8;      // decode: m * H / Hkv
+cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st);
+cudaError_t launch_kv8_attn_simple(const Kv8Args& a, cudaStream_t st);
+
+// Pages src[i] of one pool into pages dst[i] of another, i < n.
+struct Kv8PackArgs {
+  void* kv = nullptr; int kv_bf16 = 0;      // fp32 / bf16 pages [2][Hkv][16][hd]
+  uint8_t* kv8 = nullptr; float* scale = nullptr;
+  int n_src = 0, n_dst = 0, n = 0;
+  const int* src = nullptr; const int* dst = nullptr;
+  const int* fill = nullptr;                // valid rows of each page (null: 16)
+  int Hkv = 0, hd = 0;
+};
+cudaError_t launch_kv8_pack(const Kv8PackArgs& p, cudaStream_t st);
+cudaError_t launch_kv8_unpack(const Kv8PackArgs& p, cudaStream_t st);
+
+// Page copies within a pool of ``layers`` x n_pages pages, and the rewriting
+// of page tables: pairs are host arrays and travel as kernel arguments.
+constexpr int kPagePairs = 2000;
+struct PagePairs {
+  int src[kPagePairs], dst[kPagePairs];
+};
+cudaError_t launch_kv_copy_pages(uint8_t* kv, long long page_bytes, uint8_t* scale, int scale_bytes, int n_pages,
+                                 int layers, const PagePairs& pairs, int n, cudaStream_t st);
+// pairs sorted by src
+cudaError_t launch_kv_remap(int* table, int rows, int table_ld, int cols, const PagePairs& pairs, int n,
+                            cudaStream_t st);
+
 // ------------------------------------------------------------------ K8 embedding
 struct EmbedArgs {
   const void* tok_emb = nullptr; const void* vq_emb = nullptr; int w_bf16 = 1;
