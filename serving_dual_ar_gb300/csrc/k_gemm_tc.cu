@@ -386,6 +386,19 @@ bool tma_map_bf16_2d(CUtensorMap* m, const void* base, long long rows, int cols,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_kv8(CUtensorMap* m, const void* kv, int n_pages, int Hkv, int hd) {
+  if (!get_encode() || n_pages <= 0 || Hkv <= 0 || (hd != 64 && hd != 128)) return false;
+  const cuuint64_t row = (cuuint64_t)hd, blk = 16 * row, half = blk * Hkv;
+  cuuint64_t dims[5] = {row, 16, (cuuint64_t)Hkv, 2, (cuuint64_t)n_pages};
+  cuuint64_t strides[4] = {row, blk, half, 2 * half};
+  cuuint32_t box[5] = {(cuuint32_t)hd, 16, 1, 2, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(kv), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_gemm_pick_tn(int T, bool two_plane) {
   if (T <= 32) return 32;
   if (T <= 64) return 64;

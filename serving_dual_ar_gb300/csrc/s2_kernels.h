@@ -250,6 +250,8 @@ constexpr int kKv8MaxSeqs = 1024;
 constexpr int kKv8MaxRows = 8;      // decode: m * H / Hkv
 cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st);
 cudaError_t launch_kv8_attn_simple(const Kv8Args& a, cudaStream_t st);
+size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd);
+cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st);
 
 // Pages src[i] of one pool into pages dst[i] of another, i < n.
 struct Kv8PackArgs {

@@ -64,8 +64,8 @@ static bool fill_args(Kv8Args& a, const float* qkv, int qkv_ld, int B, int H, in
 }
 
 extern "C" size_t s2op_attn_decode_kv8_workspace_bytes(int B, int m, int H, int Hkv, int hd) {
-  (void)B, (void)m, (void)H, (void)Hkv, (void)hd;
-  return 16;
+  if (!shape_ok(B, H, Hkv, hd) || m < 1 || (long long)m * (H / Hkv) > kKv8MaxRows) return 0;
+  return kv8_decode_ws_bytes(B, m, H, Hkv, hd);
 }
 
 extern "C" int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int Hkv, int hd,
@@ -80,9 +80,7 @@ extern "C" int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, 
   if (m < 1 || (long long)m * (H / Hkv) > kKv8MaxRows) return S2_EINVAL;
   a.m = m;
   a.T = B * m;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_kv8_append(a, st);
-  return status(e == cudaSuccess ? launch_kv8_attn_simple(a, st) : e);
+  return status(launch_kv8_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" size_t s2op_attn_prefill_kv8_workspace_bytes(int T, int B, int H, int Hkv, int hd) {

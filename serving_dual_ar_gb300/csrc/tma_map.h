@@ -11,4 +11,9 @@ namespace s2 {
 // False when the driver entry point is missing or the encoding is refused.
 bool tma_map_bf16_2d(CUtensorMap* m, const void* base, long long rows, int cols, int ld, int box_rows);
 
+// Pool of 8-bit KV pages [n_pages][2][Hkv][16][hd] as a 5-D byte map whose box
+// is one head's 16 key rows and 16 value rows of a page, swizzled over the
+// row's length (128 or 64 bytes).
+bool tma_map_kv8(CUtensorMap* m, const void* kv, int n_pages, int Hkv, int hd);
+
 }  // namespace s2
