@@ -132,12 +132,14 @@ def strerror(status):
 
 def ptr(a):
     """Raw pointer of a numpy array / torch tensor (None -> NULL)."""
+    try:                     # a tensor, nearly always: this is on the path of every call
+        return a.data_ptr()
+    except AttributeError:
+        pass
     if a is None:
         return None
     if isinstance(a, int):
         return a
-    if hasattr(a, "data_ptr"):
-        return a.data_ptr()
     if isinstance(a, np.ndarray):
         if not a.flags["C_CONTIGUOUS"]:
             raise ValueError("arrays must be C-contiguous")

@@ -19,9 +19,10 @@ constexpr int kDecMinPages = 2;
 
 struct DecLayout {
   int depth;                       // pages in flight per warp
-  int q_off, slot_off, meta_off;   // bytes
+  int slot_off, meta_off;          // bytes
   int slot_floats;                 // one partial: R rows of HD values, then (m, l) of each
   int ctas;
+  int vec;                         // query rows, gains and RoPE rows on 16-byte boundaries
 };
 
 S2_DEV float ex2(float x) {
@@ -59,6 +60,34 @@ template <int HD>
 S2_DEV uint32_t unit_off(int row, int c) {
   return HD == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
+
+template <int N>
+S2_DEV void load_row(const float* p, bool vec, float (&v)[N]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[i + 2] = x.z;
+      v[i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
+  }
+}
+
+// Run ``i`` of the ``runs`` equal ones that U units are cut into starts at
+// unit Cut::start(i); Cut::of(u) is the run that holds unit u.
+struct Cut {
+  unsigned base, more;    // every run has base units, the first ``more`` one more
+  S2_DEV unsigned start(unsigned i) const { return i * base + min(i, more); }
+  S2_DEV unsigned of(unsigned u) const {
+    const unsigned big = more * (base + 1);
+    return u < big ? u / (base + 1) : more + (u - big) / base;
+  }
+};
 
 // What a warp knows of one page of work.
 struct Unit {
@@ -117,23 +146,33 @@ struct Join {
 #pragma unroll
     for (int i = 0; i < HD / 4; ++i) o[i] = 0.f;
   }
-  template <bool kGlobal>
-  S2_DEV void take(const float* slot, int R, int r, int c) {
+  // All of the partials slot(k), first <= k < last, in order: the largest
+  // maximum first, so that the loads of the values wait for nothing.
+  template <bool kGlobal, typename F>
+  S2_DEV void take(F slot, int first, int last, int R, int r, int c) {
     if (r >= R) return;
-    const float* ml = slot + R * HD + 2 * r;
-    const float m2 = kGlobal ? __ldcg(ml) : ml[0], l2 = kGlobal ? __ldcg(ml + 1) : ml[1];
-    if (m2 == -INFINITY && !(l2 != l2)) return;          // no keys
-    const float mn = fmaxf(m, m2), x = ex2(m - mn), y = ex2(m2 - mn);
-    m = mn;
-    l = l * x + l2 * y;
-    const float4* s = reinterpret_cast<const float4*>(slot + r * HD + c * (HD / 4));
+#pragma unroll 4
+    for (int k = first; k < last; ++k) {
+      const float* p = slot(k);
+      if (p) m = fmaxf(m, kGlobal ? __ldcg(p + R * HD + 2 * r) : p[R * HD + 2 * r]);
+    }
+#pragma unroll 2
+    for (int k = first; k < last; ++k) {
+      const float* p = slot(k);
+      if (!p) continue;
+      const float* ml = p + R * HD + 2 * r;
+      const float m2 = kGlobal ? __ldcg(ml) : ml[0], l2 = kGlobal ? __ldcg(ml + 1) : ml[1];
+      const float y = m2 == -INFINITY ? (l2 == l2 ? 0.f : l2) : ex2(m2 - m);   // no keys: nothing; NaN stays
+      l += l2 * y;
+      const float4* s = reinterpret_cast<const float4*>(p + r * HD + c * (HD / 4));
 #pragma unroll
-    for (int i = 0; i < HD / 16; ++i) {
-      const float4 v = kGlobal ? __ldcg(s + i) : s[i];
-      o[4 * i] = o[4 * i] * x + v.x * y;
-      o[4 * i + 1] = o[4 * i + 1] * x + v.y * y;
-      o[4 * i + 2] = o[4 * i + 2] * x + v.z * y;
-      o[4 * i + 3] = o[4 * i + 3] * x + v.w * y;
+      for (int i = 0; i < HD / 16; ++i) {
+        const float4 v = kGlobal ? __ldcg(s + i) : s[i];
+        o[4 * i] += v.x * y;
+        o[4 * i + 1] += v.y * y;
+        o[4 * i + 2] += v.z * y;
+        o[4 * i + 3] += v.w * y;
+      }
     }
   }
   S2_DEV void put(float* slot, int R, int r, int c) const {
@@ -176,7 +215,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   constexpr int NT = HD / 8;              // output tiles of 8 dims
   constexpr int KS = HD / 16;             // k-steps of the scores
   constexpr int UB = 2 * kKv8Page * HD;   // bytes of a unit
-  constexpr int QLD = HD + 8;             // f16 pitch of a staged query row
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ __align__(8) uint64_t bars[kDecWarps][kDecMaxDepth];
@@ -188,7 +226,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   int* first_s = reinterpret_cast<int*>(sm + lay.meta_off);   // pages before sequence b, B + 1 entries
   int* pos_s = first_s + a.B + 1;
   uint8_t* ring = sm + (size_t)warp * D * UB;
-  __half* qst = reinterpret_cast<__half*>(sm + lay.q_off) + (size_t)warp * 2 * R * QLD;
   float* slots = reinterpret_cast<float*>(sm + lay.slot_off) + (size_t)warp * 2 * lay.slot_floats;
   if (tid < kDecWarps * D) mbar_init(&bars[tid / D][tid % D], 1);
   if (tid < 2 * kDecWarps) seg_s[tid] = -1;
@@ -229,27 +266,29 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
         if (a.o) a.o[at] = 0.f;
         else a.o16[at] = __float2bfloat16_rn(0.f);
       }
-  const long long U = (long long)first_s[a.B] * a.Hkv;
+  // units fit 31 bits (the caller refuses more)
+  const unsigned U = (unsigned)first_s[a.B] * a.Hkv;
   if (U == 0) return;
-  const long long W = min((long long)gridDim.x * kDecWarps, (U + kDecMinPages - 1) / kDecMinPages);
-  if ((long long)blockIdx.x * kDecWarps >= W) return;
-  const long long wid = min((long long)blockIdx.x * kDecWarps + warp, W);
-  const long long u0 = U * wid / W, u1 = U * min(wid + 1, W) / W;
-  const int n = (int)(u1 - u0);
+  const unsigned W = min(gridDim.x * kDecWarps, (U + kDecMinPages - 1) / kDecMinPages);
+  if (blockIdx.x * kDecWarps >= W) return;
+  const Cut cut{U / W, U % W};
+  const unsigned wid = min(blockIdx.x * kDecWarps + warp, W);
+  const unsigned u0 = cut.start(wid);
+  const int n = wid < W ? (int)(cut.start(wid + 1) - u0) : 0;
 
   // the unit u0 + t, looked up by lane t % 32
   auto look_up = [&](int t) {
     Unit x{-1, -1, 0, 0};
     if (t >= n) return x;
-    const long long u = u0 + t;
+    const unsigned u = u0 + t;
     int lo = 0, hi = a.B;                       // last b with first unit <= u
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)first_s[mid] * a.Hkv <= u) lo = mid;
+      if ((unsigned)first_s[mid] * a.Hkv <= u) lo = mid;
       else hi = mid;
     }
     const int pages = first_s[lo + 1] - first_s[lo];
-    const int rem = (int)(u - (long long)first_s[lo] * a.Hkv), g = rem / pages;
+    const int rem = (int)(u - (unsigned)first_s[lo] * a.Hkv), g = rem / pages;
     x.j = rem - g * pages;
     x.seg = lo * a.Hkv + g;
     const int p = a.table[(size_t)lo * a.table_ld + x.j];
@@ -291,53 +330,46 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[t][e] = 0.f;
-    constexpr int N = HD / 32;
-    __syncwarp();
-    for (int i = 0; i < R; ++i) {
-      const int p = pos + i / G;
-      const float* x = a.qkv + (size_t)(b * a.m + i / G) * a.qkv_ld + (size_t)(g * G + i % G) * HD;
-      const float* cs = a.rope_cos + (size_t)p * (HD / 2);
-      const float* sn = a.rope_sin + (size_t)p * (HD / 2);
-      float q[N], ss = 0.f;
+    // lane (r, c): dims c HD/4 .. of query row r, whose rotation partners lane
+    // (r, c ^ 2) has; all loads at once
+    float q[HD / 4], gain[HD / 4], co[HD / 4], si[HD / 4];
+    const bool vec = lay.vec;
+    if (r < R) {
+      const int p = pos + r / G, half = (c & 1) * (HD / 4);
+      load_row(a.qkv + (size_t)(b * a.m + r / G) * a.qkv_ld + (size_t)(g * G + r % G) * HD + c * (HD / 4), vec, q);
+      load_row(a.q_gain + c * (HD / 4), vec, gain);
+      load_row(a.rope_cos + (size_t)p * (HD / 2) + half, vec, co);
+      load_row(a.rope_sin + (size_t)p * (HD / 2) + half, vec, si);
+    } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        q[k] = x[lane + 32 * k];
-        ss += q[k] * q[k];
-      }
-      // log2(e) / sqrt(HD): the softmax runs on powers of two
-      const float f = rsqrtf(warp_sum(ss) * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
-#pragma unroll
-      for (int k = 0; k < N; ++k) q[k] *= f * a.q_gain[lane + 32 * k];
-      float mx = 0.f;
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k) {
-        const float u = q[k], w = q[k + N / 2], co = cs[lane + 32 * k], si = sn[lane + 32 * k];
-        q[k] = u * co - w * si;
-        q[k + N / 2] = w * co + u * si;
-        mx = fmaxf(mx, fmaxf(fabsf(q[k]), fabsf(q[k + N / 2])));
-      }
-      // the row's largest magnitude to 2^12 .. 2^13: its pair then is good to
-      // 2^-22 of each value and 2^-37 of the largest
-      const int ex = min(max((int)(__float_as_uint(warp_max(mx)) >> 23) - 127, -100), 100);
-      const float up = pow2f(12 - ex);
-      if (r == i) qf = pow2f(ex - 12);
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float v = q[k] * up;
-        const __half h = __float2half_rn(v);
-        qst[i * QLD + lane + 32 * k] = h;
-        qst[(R + i) * QLD + lane + 32 * k] = __float2half_rn(v - __half2float(h));
-      }
+      for (int i = 0; i < HD / 4; ++i) q[i] = gain[i] = co[i] = si[i] = 0.f;
     }
-    __syncwarp();
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < HD / 4; ++i) ss += q[i] * q[i];
+    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+    // log2(e) / sqrt(HD): the softmax runs on powers of two
+    const float f = rsqrtf(ss * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < HD / 4; ++i) {
+      q[i] *= f * gain[i];
+      const float w = __shfl_xor_sync(0xffffffffu, q[i], 2);
+      q[i] = q[i] * co[i] + (c < 2 ? -w : w) * si[i];
+      mx = fmaxf(mx, fabsf(q[i]));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // the row's largest magnitude to 2^12 .. 2^13: its pair then is good to
+    // 2^-22 of each value and 2^-37 of the largest
+    const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+    const float up = pow2f(12 - ex);
+    qf = pow2f(ex - 12);
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      const uint32_t* h = reinterpret_cast<const uint32_t*>(qst + r * QLD + c * (HD / 4) + 4 * t);
-      const uint32_t* l = reinterpret_cast<const uint32_t*>(qst + (R + r) * QLD + c * (HD / 4) + 4 * t);
-      qa[t][0] = r < R ? h[0] : 0u;
-      qa[t][1] = r < R ? l[0] : 0u;
-      qa[t][2] = r < R ? h[1] : 0u;
-      qa[t][3] = r < R ? l[1] : 0u;
+      split2(q[4 * t] * up, q[4 * t + 1] * up, qa[t][0], qa[t][1]);
+      split2(q[4 * t + 2] * up, q[4 * t + 3] * up, qa[t][2], qa[t][3]);
     }
   };
 
@@ -364,7 +396,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   };
   auto end = [&](int t_end) {    // piece of ``seg`` up to unit t_end of the run
     const int b = seg / a.Hkv, g = seg % a.Hkv, pages = first_s[b + 1] - first_s[b];
-    const long long s0 = (long long)first_s[b] * a.Hkv + (long long)g * pages;
+    const unsigned s0 = (unsigned)first_s[b] * a.Hkv + (unsigned)g * pages;
     Join<HD> x;
     piece(x);
     if (s0 >= u0 && s0 + pages <= u0 + t_end) {
@@ -379,21 +411,24 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     }
   };
 
-  // New rows of this page into its shared-memory copy and to the pool.
+  // One new key (normed, rotated) and value, lane l taking dims l + 32 i.
+  constexpr int N = HD / 32;
+  float k[N], v[N];
+  auto row = [&](int p) {
+    const int b = seg / a.Hkv, g = seg % a.Hkv;
+    const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + g) * HD;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = x[(size_t)a.Hkv * HD + lane + 32 * i];
+    kv8_key_row<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2), a.rope_sin + (size_t)p * (HD / 2), a.eps, lane, k);
+  };
+  // New rows of this page into its shared-memory copy and to the pool; the
+  // page's last new row is in k, v already.
   auto append = [&](uint8_t* blk, int page, int j, int& ke, int& ve) {
-    constexpr int N = HD / 32;
     const int b = seg / a.Hkv, g = seg % a.Hkv;
     const int first = max(pos, j * kKv8Page), last = min(pos + a.m, (j + 1) * kKv8Page);
     const int had = first - j * kKv8Page, rows = last - j * kKv8Page;
-    float k[N], v[N], mk = 0.f, mv = 0.f;
-    auto row = [&](int p) {
-      const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + g) * HD;
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = x[(size_t)a.Hkv * HD + lane + 32 * i];
-      kv8_key_row<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2), a.rope_sin + (size_t)p * (HD / 2), a.eps, lane,
-                      k);
-    };
-    for (int p = first; p < last; ++p) {
+    float mk = abs_max(k, 0.f), mv = abs_max(v, 0.f);
+    for (int p = last - 2; p >= first; --p) {
       row(p);
       mk = abs_max(k, mk);
       mv = abs_max(v, mv);
@@ -421,8 +456,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     for (int i = rows * HD / 16 + lane; i < HD; i += 32)   // rows behind the last one: their weight is 0, not their bytes
       *reinterpret_cast<uint4*>(xv + unit_off<HD>(i / (HD / 16), i % (HD / 16))) = make_uint4(0, 0, 0, 0);
     const float fk = pow2f(-ke), fv = pow2f(-ve);
-    for (int p = last - 1; p >= first; --p) {
-      if (p != last - 1) row(p);
+    for (int p = first; p < last; ++p) {
+      if (p != first) row(p);       // k, v: the first row, the last one computed
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int d = lane + 32 * i;
@@ -475,12 +510,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
       if (seg >= 0) end(t);
       begin(sg);
     }
+    const bool tail = (j + 1) * kKv8Page > pos;
+    if (tail) row(min(pos + a.m, (j + 1) * kKv8Page) - 1);
     bool ok = mbar_wait(&bars[warp][t % D], (uint32_t)(t / D) & 1u, nullptr);
     ok = __all_sync(0xffffffffu, ok) && page >= 0;
     if (ok) {
       uint8_t* blk = ring + (size_t)(t % D) * UB;
       int ke = (ex & 0xff) - 64, ve = (ex >> 8) - 64;
-      const bool tail = (j + 1) * kKv8Page > pos;
       if (tail) append(blk, page, j, ke, ve);
 
       // S = Q K^T for the page's two groups of 8 keys
@@ -575,8 +611,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   __syncthreads();
 
   // partials of this CTA's warps, each cut (sequence, kv head) by the warp of its first one
-  const long long c0 = U * ((long long)blockIdx.x * kDecWarps) / W;
-  const long long c1 = U * min((long long)(blockIdx.x + 1) * kDecWarps, W) / W;
+  const unsigned c0 = cut.start(blockIdx.x * kDecWarps), c1 = cut.start(min((blockIdx.x + 1) * kDecWarps, W));
   unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)a.B * a.Hkv * 4 + 255) / 256 * 256);
   const float* all = reinterpret_cast<const float*>(sm + lay.slot_off);
@@ -588,17 +623,17 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     if (sg < 0 || sg == prev) continue;
     prev = sg;
     Join<HD> x;
-    for (int k = e; k < 2 * kDecWarps; ++k)
-      if (seg_s[k] == sg) x.template take<false>(all + (size_t)k * lay.slot_floats, R, r, c);
+    x.template take<false>(
+        [&](int k) { return seg_s[k] == sg ? all + (size_t)k * lay.slot_floats : nullptr; }, e, 2 * kDecWarps, R, r, c);
     const int b = sg / a.Hkv, g = sg % a.Hkv, pages = first_s[b + 1] - first_s[b];
-    const long long s0 = (long long)first_s[b] * a.Hkv + (long long)g * pages, s1 = s0 + pages;
+    const unsigned s0 = (unsigned)first_s[b] * a.Hkv + (unsigned)g * pages, s1 = s0 + pages;
     if (s0 >= c0 && s1 <= c1) {
       x.finish();
       store_rows<HD>(a, sg, r, c, x.o);
       continue;
     }
     // CTAs that share it: those of its first and of its last page
-    const int f = (int)((((s0 + 1) * W - 1) / U) / kDecWarps), l = (int)(((s1 * W - 1) / U) / kDecWarps);
+    const int f = (int)(cut.of(s0) / kDecWarps), l = (int)(cut.of(s1 - 1) / kDecWarps);
     x.put(parts + ((size_t)blockIdx.x * 2 + (s0 < c0 ? 0 : 1)) * lay.slot_floats, R, r, c);
     __threadfence();
     __syncwarp();
@@ -608,7 +643,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     if (got != (unsigned)(l - f)) continue;
     __threadfence();
     Join<HD> y;
-    for (int k = f; k <= l; ++k) y.template take<true>(parts + ((size_t)k * 2 + (k == f ? 1 : 0)) * lay.slot_floats, R, r, c);
+    y.template take<true>(
+        [&](int k) { return parts + ((size_t)k * 2 + (k == f ? 1 : 0)) * lay.slot_floats; }, f, l + 1, R, r, c);
     y.finish();
     store_rows<HD>(a, sg, r, c, y.o);
     if (lane == 0) tickets[sg] = 0u;
@@ -626,13 +662,11 @@ DecLayout dec_layout(int B, int R, int hd) {
   DecLayout l;
   l.ctas = num_sms();
   l.slot_floats = R * hd + 2 * R + (2 * R) % 4;
-  const int q = kDecWarps * 2 * R * (hd + 8) * 2, slot = kDecWarps * 2 * l.slot_floats * 4;
-  const int meta = (2 * B + 1) * 4, unit = 2 * kKv8Page * hd;
-  const int room = kDecSmem - 1024 - 2048 - q - slot - meta;   // alignment, static
+  const int slot = kDecWarps * 2 * l.slot_floats * 4, meta = (2 * B + 1) * 4, unit = 2 * kKv8Page * hd;
+  const int room = kDecSmem - 1024 - 2048 - slot - meta;   // alignment, static
   l.depth = room / (kDecWarps * unit);
   if (l.depth > kDecMaxDepth) l.depth = kDecMaxDepth;
-  l.q_off = kDecWarps * l.depth * unit;
-  l.slot_off = l.q_off + (q + 15) / 16 * 16;
+  l.slot_off = kDecWarps * l.depth * unit;
   l.meta_off = l.slot_off + (slot + 15) / 16 * 16;
   return l;
 }
@@ -648,7 +682,10 @@ size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd) {
 cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {
   CUtensorMap map;
   if (!tma_map_kv8(&map, a.kv, a.n_pages, a.Hkv, a.hd)) return cudaErrorNotSupported;
-  const DecLayout l = dec_layout(a.B, a.m * (a.H / a.Hkv), a.hd);
+  DecLayout l = dec_layout(a.B, a.m * (a.H / a.Hkv), a.hd);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.qkv) | reinterpret_cast<uintptr_t>(a.q_gain) |
+                       reinterpret_cast<uintptr_t>(a.rope_cos) | reinterpret_cast<uintptr_t>(a.rope_sin);
+  l.vec = (at & 15) == 0 && a.qkv_ld % 4 == 0;
   auto k = a.hd == 128 ? kv8_decode_kernel<128> : kv8_decode_kernel<64>;
   static bool attr[2] = {false, false};
   if (!attr[a.hd == 128]) {
@@ -661,6 +698,12 @@ cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {
   cfg.blockDim = dim3(kDecWarps * 32);
   cfg.dynamicSmemBytes = l.meta_off + (2 * a.B + 1) * 4 + 1024;
   cfg.stream = st;
+  // the kernel reads nothing before its wait on the launch before it
+  cudaLaunchAttribute at1[1];
+  at1[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at1[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at1;
+  cfg.numAttrs = 1;
   return s2_launch(&cfg, k, map, a, l);
 }
 

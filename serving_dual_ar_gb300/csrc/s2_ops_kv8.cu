@@ -78,6 +78,7 @@ extern "C" int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, 
                  n_pages, table, table_ld, o, o_bf16, o_ld, workspace))
     return S2_EINVAL;
   if (m < 1 || (long long)m * (H / Hkv) > kKv8MaxRows) return S2_EINVAL;
+  if ((double)B * Hkv * table_ld >= 2147483648.0) return S2_EINVAL;   // pages to read, counted in 31 bits
   a.m = m;
   a.T = B * m;
   return status(launch_kv8_decode(a, static_cast<cudaStream_t>(stream)));
