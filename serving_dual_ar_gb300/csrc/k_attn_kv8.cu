@@ -10,19 +10,21 @@ namespace s2 {
 
 namespace {
 
-constexpr int kDecWarps = 8;
+constexpr int kDecWarps = 8;       // most warps of a CTA
 constexpr int kDecMaxDepth = 8;
 constexpr int kDecSmem = 227 * 1024;
-
-// Warps in use for U pages of work: at least kDecMinPages each.
-constexpr int kDecMinPages = 2;
+// Pages of a run at least: a cut costs a joining, about as long as four pages.
+constexpr int kDecMinPages = 4;
+// Pieces that one warp joins; more are joined in two levels of about sqrt(n).
+constexpr int kDecFlat = 12;
 
 struct DecLayout {
-  int depth;                       // pages in flight per warp
-  int slot_off, meta_off;          // bytes
-  int slot_floats;                 // one partial: R rows of HD values, then (m, l) of each
+  int groups, heads, slices;   // kv heads in groups of ``heads``; a CTA has heads x slices warps
+  int depth;                   // pages in flight per warp
+  int q_off, meta_off;         // bytes
+  int slot_floats;             // one partial: R rows of HD values, then (m, l) of each
   int ctas;
-  int vec;                         // query rows, gains and RoPE rows on 16-byte boundaries
+  int vec;                     // query rows, gains and RoPE rows on 16-byte boundaries
 };
 
 S2_DEV float ex2(float x) {
@@ -61,21 +63,8 @@ S2_DEV uint32_t unit_off(int row, int c) {
   return HD == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int N>
-S2_DEV void load_row(const float* p, bool vec, float (&v)[N]) {
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + i);
-      v[i] = x.x;
-      v[i + 1] = x.y;
-      v[i + 2] = x.z;
-      v[i + 3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = p[i];
-  }
+S2_DEV float4 load4(const float* p, bool vec) {
+  return vec ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
 }
 
 // Run ``i`` of the ``runs`` equal ones that U units are cut into starts at
@@ -89,9 +78,24 @@ struct Cut {
   }
 };
 
+// The key row as a call: it is rare, long and wanted at three places, and the
+// kernel's other paths share the instruction cache with it.
+template <int HD>
+struct KeyRow {
+  float v[HD / 32];
+};
+template <int HD>
+__device__ __noinline__ KeyRow<HD> key_row_call(const float* x, const float* gain, const float* cs, const float* sn,
+                                                float eps, int lane) {
+  KeyRow<HD> y;
+  kv8_key_row<HD>(x, gain, cs, sn, eps, lane, y.v);
+  return y;
+}
+
 // What a warp knows of one page of work.
 struct Unit {
-  int page, seg, j, exps;   // page id (-1: not to be followed), b * Hkv + g, page of the sequence, K and V exponents
+  int page, seg, j;   // page id (-1: not to be followed), group * B + b, page of the sequence
+  float ks, vs;       // the block scales
 };
 
 template <int HD>
@@ -103,10 +107,9 @@ struct DecState {           // one piece of a (sequence, kv head): all rows, log
 
 // One result row set into o: dims [c * HD/4, (c + 1) * HD/4) of row r.
 template <int HD>
-S2_DEV void store_rows(const Kv8Args& a, int seg, int r, int c, const float (&y)[HD / 4]) {
+S2_DEV void store_rows(const Kv8Args& a, int b, int g, int r, int c, const float (&y)[HD / 4]) {
   const int G = a.H / a.Hkv;
   if (r >= a.m * G) return;
-  const int b = seg / a.Hkv, g = seg % a.Hkv;
   const size_t at = (size_t)(b * a.m + r / G) * a.o_ld + (size_t)(g * G + r % G) * HD + c * (HD / 4);
   if (a.o) {
     float* p = a.o + at;
@@ -146,28 +149,23 @@ struct Join {
 #pragma unroll
     for (int i = 0; i < HD / 4; ++i) o[i] = 0.f;
   }
-  // All of the partials slot(k), first <= k < last, in order: the largest
-  // maximum first, so that the loads of the values wait for nothing.
-  template <bool kGlobal, typename F>
-  S2_DEV void take(F slot, int first, int last, int R, int r, int c) {
+  // The partials slot(0) .. slot(n - 1), in order: the largest maximum first,
+  // so that the loads of the values wait for nothing.
+  template <typename F>
+  S2_DEV void take(F slot, int n, int R, int r, int c) {
     if (r >= R) return;
 #pragma unroll 4
-    for (int k = first; k < last; ++k) {
-      const float* p = slot(k);
-      if (p) m = fmaxf(m, kGlobal ? __ldcg(p + R * HD + 2 * r) : p[R * HD + 2 * r]);
-    }
+    for (int k = 0; k < n; ++k) m = fmaxf(m, __ldcg(slot(k) + R * HD + 2 * r));
 #pragma unroll 2
-    for (int k = first; k < last; ++k) {
+    for (int k = 0; k < n; ++k) {
       const float* p = slot(k);
-      if (!p) continue;
-      const float* ml = p + R * HD + 2 * r;
-      const float m2 = kGlobal ? __ldcg(ml) : ml[0], l2 = kGlobal ? __ldcg(ml + 1) : ml[1];
-      const float y = m2 == -INFINITY ? (l2 == l2 ? 0.f : l2) : ex2(m2 - m);   // no keys: nothing; NaN stays
-      l += l2 * y;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + R * HD + 2 * r));
+      const float y = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2(ml.x - m);   // no keys: nothing; NaN stays
+      l += ml.y * y;
       const float4* s = reinterpret_cast<const float4*>(p + r * HD + c * (HD / 4));
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i) {
-        const float4 v = kGlobal ? __ldcg(s + i) : s[i];
+        const float4 v = __ldcg(s + i);
         o[4 * i] += v.x * y;
         o[4 * i + 1] += v.y * y;
         o[4 * i + 2] += v.z * y;
@@ -192,14 +190,16 @@ struct Join {
   }
 };
 
-// The work is the list of all pages, in the order (sequence, kv head, page),
-// cut into equal runs, one per warp of the grid: ragged lengths, one long
-// sequence and many short ones all load every SM alike.  A warp streams its
-// run through its own ring of shared-memory pages (one TMA copy brings a
-// head's 16 keys and 16 values), with no barrier shared between warps.  A
-// (sequence, kv head) that lies within one run is finished by its warp; one
-// that is cut is joined from partials, first within the CTA, then, if its
-// pages reach into other CTAs, by the last CTA to arrive, in order.
+// The work is the list of all pages in the order (sequence, page), cut into
+// equal runs: ragged lengths, one long sequence and many short ones load every
+// SM alike.  A run is taken by as many warps as there are kv heads, one head
+// each, side by side, so that a page is read whole at about one time (read
+// head by head, with 2 KB here and there, the memory gives half: 26 us instead
+// of 17 for 65 MB).  Each warp streams its head's part of the pages through
+// its own ring in shared memory (one copy brings 16 keys and 16 values) and
+// shares no barrier with another.  A sequence that a run holds whole is
+// finished by it; one that is cut is joined by the last of its runs to arrive,
+// in order, in two levels where there are many.
 //
 // Products: mma.sync m16n8k16 with the up to 8 query rows (new rows x heads
 // of the kv head) as f16 hi parts in rows 0..7 and lo parts in rows 8..15, so
@@ -219,24 +219,25 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ __align__(8) uint64_t bars[kDecWarps][kDecMaxDepth];
   __shared__ int scan_s[kDecWarps + 1];
-  __shared__ int seg_s[2 * kDecWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int r = lane >> 2, c = lane & 3;
   const int D = lay.depth, G = a.H / a.Hkv, R = a.m * G;
+  const int h = warp % lay.heads;                                  // head within its group
+  const unsigned run = blockIdx.x * lay.slices + warp / lay.heads;
   int* first_s = reinterpret_cast<int*>(sm + lay.meta_off);   // pages before sequence b, B + 1 entries
   int* pos_s = first_s + a.B + 1;
   uint8_t* ring = sm + (size_t)warp * D * UB;
-  float* slots = reinterpret_cast<float*>(sm + lay.slot_off) + (size_t)warp * 2 * lay.slot_floats;
-  if (tid < kDecWarps * D) mbar_init(&bars[tid / D][tid % D], 1);
-  if (tid < 2 * kDecWarps) seg_s[tid] = -1;
+  uint4* qst = reinterpret_cast<uint4*>(sm + lay.q_off) + (size_t)warp * R * (HD / 4);
+  for (int i = tid; i < kDecWarps * D; i += threads) mbar_init(&bars[i / D][i % D], 1);
   fence_mbar_init();
   pdl_launch_next();
   pdl_wait();
 
   // pages of each sequence (none for one that is left out), and their sums
   {
-    const int per = (a.B + kDecWarps * 32 - 1) / (kDecWarps * 32), b0 = tid * per;
+    const int per = (a.B + threads - 1) / threads, b0 = tid * per;
     int own = 0;
+#pragma unroll 1
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       const int p = a.pos[b];
       const bool in = p >= 0 && p <= a.max_pos - a.m;
@@ -254,48 +255,57 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     if (tid == 0) scan_s[0] = 0;
     __syncthreads();
     int before = x - own;
+#pragma unroll 1
     for (int w = 0; w <= warp; ++w) before += scan_s[w];
+#pragma unroll 1
     for (int b = b0; b < min(b0 + per, a.B); ++b) first_s[b] += before;
-    if (tid == kDecWarps * 32 - 1) first_s[a.B] = before + own;
+    if (tid == threads - 1) first_s[a.B] = before + own;
     __syncthreads();
   }
+#pragma unroll 1
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
     if (pos_s[b] < 0)
-      for (int i = tid; i < a.m * a.H * HD; i += kDecWarps * 32) {
+#pragma unroll 1
+      for (int i = tid; i < a.m * a.H * HD; i += threads) {
         const size_t at = (size_t)(b * a.m + i / (a.H * HD)) * a.o_ld + i % (a.H * HD);
         if (a.o) a.o[at] = 0.f;
         else a.o16[at] = __float2bfloat16_rn(0.f);
       }
   // units fit 31 bits (the caller refuses more)
-  const unsigned U = (unsigned)first_s[a.B] * a.Hkv;
+  const unsigned P = first_s[a.B], U = P * lay.groups;
   if (U == 0) return;
-  const unsigned W = min(gridDim.x * kDecWarps, (U + kDecMinPages - 1) / kDecMinPages);
-  if (blockIdx.x * kDecWarps >= W) return;
+  const unsigned W = min(gridDim.x * lay.slices, (U + kDecMinPages - 1) / kDecMinPages);
+  if (run >= W) return;
   const Cut cut{U / W, U % W};
-  const unsigned wid = min(blockIdx.x * kDecWarps + warp, W);
-  const unsigned u0 = cut.start(wid);
-  const int n = wid < W ? (int)(cut.start(wid + 1) - u0) : 0;
+  const unsigned u0 = cut.start(run);
+  const int n = (int)(cut.start(run + 1) - u0);
 
-  // the unit u0 + t, looked up by lane t % 32
-  auto look_up = [&](int t) {
-    Unit x{-1, -1, 0, 0};
-    if (t >= n) return x;
-    const unsigned u = u0 + t;
-    int lo = 0, hi = a.B;                       // last b with first unit <= u
-    while (hi - lo > 1) {
+  // (group, sequence) of unit u
+  auto seg_of = [&](unsigned u) {
+    const int group = lay.groups > 1 ? u / P : 0;
+    u -= group * P;
+    int lo = 0;                                 // last b with first page <= u
+#pragma unroll 1
+    for (int hi = a.B; hi - lo > 1;) {
       const int mid = (lo + hi) >> 1;
-      if ((unsigned)first_s[mid] * a.Hkv <= u) lo = mid;
+      if ((unsigned)first_s[mid] <= u) lo = mid;
       else hi = mid;
     }
-    const int pages = first_s[lo + 1] - first_s[lo];
-    const int rem = (int)(u - (unsigned)first_s[lo] * a.Hkv), g = rem / pages;
-    x.j = rem - g * pages;
-    x.seg = lo * a.Hkv + g;
-    const int p = a.table[(size_t)lo * a.table_ld + x.j];
-    if (p >= 0 && p < a.n_pages) {
+    return group * a.B + lo;
+  };
+  auto seg_start = [&](int s) { return (unsigned)(s / a.B) * P + first_s[s % a.B]; };
+  // the unit u0 + t, looked up by lane t % 32
+  auto look_up = [&](int t) {
+    Unit x{-1, -1, 0, 1.f, 1.f};
+    if (t >= n) return x;
+    x.seg = seg_of(u0 + t);
+    x.j = (int)(u0 + t - seg_start(x.seg));
+    const int p = a.table[(size_t)(x.seg % a.B) * a.table_ld + x.j], g = x.seg / a.B * lay.heads + h;
+    if (p >= 0 && p < a.n_pages && g < a.Hkv) {
       x.page = p;
       const float* s = a.scale + (size_t)p * 2 * a.Hkv + g;
-      x.exps = (kv8_scale_exp(s[0]) + 64) | ((kv8_scale_exp(s[a.Hkv]) + 64) << 8);
+      x.ks = s[0];
+      x.vs = s[a.Hkv];
     }
     return x;
   };
@@ -304,24 +314,52 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     if (x.page < 0) mbar_arrive(bar);
     else {
       mbar_arrive_expect_tx(bar, UB);
-      tma_load_page(ring + (size_t)(t % D) * UB, &map, x.seg % a.Hkv, x.page, bar);
+      tma_load_page(ring + (size_t)(t % D) * UB, &map, x.seg / a.B * lay.heads + h, x.page, bar);
     }
   };
-
-  Unit cur = look_up(lane), nxt{-1, -1, 0, 0};
-  if (lane < min(D, n)) issue(cur, lane);
-  if (n > 32) nxt = look_up(32 + lane);
 
   uint32_t qa[KS][4];        // query fragments: {hi, lo} x {dims 4t, 4t+1 | 4t+2, 4t+3}
   float qf = 0.f;            // 2^-(exponent given to row r's query)
   DecState<HD> st;
-  int seg = -1, pos = 0;
+  int seg = -1, pos = 0, b = 0, g = 0;
   bool nan_new = false;      // a new value row after the first holds a NaN
 
+  // HD/4 lanes take a row, four dims each (the rotation's partners are half
+  // a row of lanes apart): whole rows by each load, and the loads of four
+  // rows (or eight half ones) in flight at once.  What lane l holds of row i
+  // is fragment t = l % KS of lane (i, l / KS); a warp's buffer, XORed
+  // against bank conflicts, takes it there.
+  constexpr int LPR = HD / 4, RPS = 32 / LPR, ST = 4;    // rows per load, loads at a time
+  const int l = lane % LPR, d = 4 * l, dh = d % (HD / 2);
+  const bool vec = lay.vec;
+  float4 x[ST] = {}, co[ST] = {}, si[ST] = {};
+  auto load_rows = [&](int s, int k0) {
+    const int b = s % a.B, g = s / a.B * lay.heads + h;
+    if (g >= a.Hkv) return;
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      const int i = k0 + k * RPS + lane / LPR;
+      x[k] = co[k] = si[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < R) {
+        const int p = pos_s[b] + i / G;
+        x[k] = load4(a.qkv + (size_t)(b * a.m + i / G) * a.qkv_ld + (size_t)(g * G + i % G) * HD + d, vec);
+        co[k] = load4(a.rope_cos + (size_t)p * (HD / 2) + dh, vec);
+        si[k] = load4(a.rope_sin + (size_t)p * (HD / 2) + dh, vec);
+      }
+    }
+  };
+  // the first rows' loads go ahead of the stream of pages
+  load_rows(seg_of(u0), 0);
+  Unit cur = look_up(lane);
+  Unit nxt = cur;
+  if (lane < min(D, n)) issue(cur, lane);
+
+  // The query rows of (sequence, kv head) s; ``load_rows(s, 0)`` came before.
   auto begin = [&](int s) {
     seg = s;
     nan_new = false;
-    const int b = s / a.Hkv, g = s % a.Hkv;
+    b = s % a.B;
+    g = s / a.B * lay.heads + h;
     pos = pos_s[b];
     st.m = -INFINITY;
     st.l = 0.f;
@@ -330,47 +368,68 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[t][e] = 0.f;
-    // lane (r, c): dims c HD/4 .. of query row r, whose rotation partners lane
-    // (r, c ^ 2) has; all loads at once
-    float q[HD / 4], gain[HD / 4], co[HD / 4], si[HD / 4];
-    const bool vec = lay.vec;
-    if (r < R) {
-      const int p = pos + r / G, half = (c & 1) * (HD / 4);
-      load_row(a.qkv + (size_t)(b * a.m + r / G) * a.qkv_ld + (size_t)(g * G + r % G) * HD + c * (HD / 4), vec, q);
-      load_row(a.q_gain + c * (HD / 4), vec, gain);
-      load_row(a.rope_cos + (size_t)p * (HD / 2) + half, vec, co);
-      load_row(a.rope_sin + (size_t)p * (HD / 2) + half, vec, si);
-    } else {
+    const float4 gain = load4(a.q_gain + d, vec);
+    const float sg = l < LPR / 2 ? -1.f : 1.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < R; k0 += ST * RPS) {
+      float ss[ST];
+      if (k0 > 0) load_rows(s, k0);
 #pragma unroll
-      for (int i = 0; i < HD / 4; ++i) q[i] = gain[i] = co[i] = si[i] = 0.f;
+      for (int k = 0; k < ST; ++k) ss[k] = x[k].x * x[k].x + x[k].y * x[k].y + x[k].z * x[k].z + x[k].w * x[k].w;
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < ST; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+#pragma unroll
+      for (int k = 0; k < ST; ++k) {
+        // log2(e) / sqrt(HD): the softmax runs on powers of two
+        const float f = rsqrtf(ss[k] * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
+        float4 y = x[k];
+        y.x *= f * gain.x;
+        y.y *= f * gain.y;
+        y.z *= f * gain.z;
+        y.w *= f * gain.w;
+        const float w0 = __shfl_xor_sync(0xffffffffu, y.x, LPR / 2) * sg;
+        const float w1 = __shfl_xor_sync(0xffffffffu, y.y, LPR / 2) * sg;
+        const float w2 = __shfl_xor_sync(0xffffffffu, y.z, LPR / 2) * sg;
+        const float w3 = __shfl_xor_sync(0xffffffffu, y.w, LPR / 2) * sg;
+        y.x = y.x * co[k].x + w0 * si[k].x;
+        y.y = y.y * co[k].y + w1 * si[k].y;
+        y.z = y.z * co[k].z + w2 * si[k].z;
+        y.w = y.w * co[k].w + w3 * si[k].w;
+        x[k] = y;
+        ss[k] = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < ST; ++k) ss[k] = fmaxf(ss[k], __shfl_xor_sync(0xffffffffu, ss[k], o));
+#pragma unroll
+      for (int k = 0; k < ST; ++k) {
+        const int i = k0 + k * RPS + lane / LPR;
+        // the row's largest magnitude to 2^12 .. 2^13: its pair then is good
+        // to 2^-22 of each value and 2^-37 of the largest
+        const int ex = min(max((int)(__float_as_uint(ss[k]) >> 23) - 127, -100), 100);
+        const float up = pow2f(12 - ex);
+        const int ex_r = __shfl_sync(0xffffffffu, ex, (r % RPS) * LPR);
+        if (r / RPS == k0 / RPS + k) qf = pow2f(ex_r - 12);
+        uint4 y;
+        split2(x[k].x * up, x[k].y * up, y.x, y.y);
+        split2(x[k].z * up, x[k].w * up, y.z, y.w);
+        if (i < R) qst[i * LPR + (l ^ ((l / KS) | ((i & 1) << 2)))] = y;
+      }
     }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < HD / 4; ++i) ss += q[i] * q[i];
-    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-    // log2(e) / sqrt(HD): the softmax runs on powers of two
-    const float f = rsqrtf(ss * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < HD / 4; ++i) {
-      q[i] *= f * gain[i];
-      const float w = __shfl_xor_sync(0xffffffffu, q[i], 2);
-      q[i] = q[i] * co[i] + (c < 2 ? -w : w) * si[i];
-      mx = fmaxf(mx, fabsf(q[i]));
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // the row's largest magnitude to 2^12 .. 2^13: its pair then is good to
-    // 2^-22 of each value and 2^-37 of the largest
-    const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-    const float up = pow2f(12 - ex);
-    qf = pow2f(ex - 12);
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      split2(q[4 * t] * up, q[4 * t + 1] * up, qa[t][0], qa[t][1]);
-      split2(q[4 * t + 2] * up, q[4 * t + 3] * up, qa[t][2], qa[t][3]);
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (r < R) y = qst[r * LPR + ((c * KS + t) ^ (c | ((r & 1) << 2)))];
+      qa[t][0] = y.x;
+      qa[t][1] = y.y;
+      qa[t][2] = y.z;
+      qa[t][3] = y.w;
     }
+    __syncwarp();
   };
 
   // The piece's rows relative to 2^m, as a Join: dims 2c NT + t and (2c + 1) NT + t.
@@ -386,48 +445,73 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
       x.o[NT + t] = (st.o[t][1] + st.o[t][3]) * f;
     }
     if (nan_new && r < R) {      // the rows that see it get it back
-      const int b = seg / a.Hkv, g = seg % a.Hkv;
+#pragma unroll 1
       for (int i = 0; i <= r / G; ++i) {
         const float* v = a.qkv + (size_t)(b * a.m + i) * a.qkv_ld + (size_t)(a.H + a.Hkv + g) * HD + c * (HD / 4);
+#pragma unroll
         for (int k = 0; k < HD / 4; ++k)
           if (v[k] != v[k]) x.o[k] = v[k];
       }
     }
   };
-  auto end = [&](int t_end) {    // piece of ``seg`` up to unit t_end of the run
-    const int b = seg / a.Hkv, g = seg % a.Hkv, pages = first_s[b + 1] - first_s[b];
-    const unsigned s0 = (unsigned)first_s[b] * a.Hkv + (unsigned)g * pages;
+  // The end of a piece: stored if it is all of its sequence, else left for,
+  // or joined with, the other runs' pieces.
+  unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);      // [level][run][2][warp of the run]
+  float* parts = reinterpret_cast<float*>(tickets + (size_t)lay.ctas * lay.slices * 4 * lay.heads);
+  auto end = [&] {
+    if (g >= a.Hkv) return;
+    const unsigned s0 = seg_start(seg);
+    const int f = (int)cut.of(s0), n = (int)cut.of(s0 + first_s[b + 1] - first_s[b] - 1) - f + 1;
     Join<HD> x;
     piece(x);
-    if (s0 >= u0 && s0 + pages <= u0 + t_end) {
-      x.finish();
-      store_rows<HD>(a, seg, r, c, x.o);
-    } else {
-      const int k = seg_s[2 * warp] < 0 ? 0 : 1;
-      x.put(slots + k * lay.slot_floats, R, r, c);
+    // piece i of the sequence is run f + i's: its last one if i = 0, else its first
+    auto at = [&](int i) { return ((size_t)(f + i) * 2 + (i == 0)) * lay.heads + h; };
+    int i = (int)run - f, step = 1, per = n;
+    if (n > kDecFlat)
+      for (per = 4; per * per < n;) ++per;
+    while (n > 1) {
+      x.put(parts + at(i) * lay.slot_floats, R, r, c);
+      __threadfence();
       __syncwarp();
-      if (lane == 0) seg_s[2 * warp + k] = seg;
-      __syncwarp();
+      const int i0 = i / per * per, count = (min(n - i0, per) + step - 1) / step;
+      unsigned* ticket = tickets + (step == 1 ? 0 : (size_t)lay.ctas * lay.slices * 2 * lay.heads) + at(i0);
+      unsigned got = 0;
+      if (lane == 0) got = atomicAdd(ticket, 1u);
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (got != (unsigned)(count - 1)) return;
+      __threadfence();
+      if (lane == 0) *ticket = 0u;
+      x = Join<HD>();
+      x.take([&](int k) { return parts + at(i0 + k * step) * lay.slot_floats; }, count, R, r, c);
+      if (per >= n) break;
+      __syncwarp();          // all lanes have read the slot that is written next
+      i = i0;
+      step = per;
+      per = n;
     }
+    x.finish();
+    store_rows<HD>(a, b, g, r, c, x.o);
   };
 
   // One new key (normed, rotated) and value, lane l taking dims l + 32 i.
   constexpr int N = HD / 32;
   float k[N], v[N];
   auto row = [&](int p) {
-    const int b = seg / a.Hkv, g = seg % a.Hkv;
     const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + g) * HD;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = x[(size_t)a.Hkv * HD + lane + 32 * i];
-    kv8_key_row<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2), a.rope_sin + (size_t)p * (HD / 2), a.eps, lane, k);
+    const KeyRow<HD> y = key_row_call<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2),
+                                          a.rope_sin + (size_t)p * (HD / 2), a.eps, lane);
+#pragma unroll
+    for (int i = 0; i < N; ++i) k[i] = y.v[i];
   };
   // New rows of this page into its shared-memory copy and to the pool; the
   // page's last new row is in k, v already.
   auto append = [&](uint8_t* blk, int page, int j, int& ke, int& ve) {
-    const int b = seg / a.Hkv, g = seg % a.Hkv;
     const int first = max(pos, j * kKv8Page), last = min(pos + a.m, (j + 1) * kKv8Page);
     const int had = first - j * kKv8Page, rows = last - j * kKv8Page;
     float mk = abs_max(k, 0.f), mv = abs_max(v, 0.f);
+#pragma unroll 1
     for (int p = last - 2; p >= first; --p) {
       row(p);
       mk = abs_max(k, mk);
@@ -436,26 +520,29 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     const int ko = had ? ke : kKv8EMin, vo = had ? ve : kKv8EMin;
     ke = max(ko, kv8_exponent(warp_max(mk)));
     ve = max(vo, kv8_exponent(warp_max(mv)));
-    const bool grew[2] = {had && ke > ko, had && ve > vo};
-    const float by[2] = {pow2f(ko - ke), pow2f(vo - ve)};
-#pragma unroll
+    const bool grew_k = had && ke > ko, grew_v = had && ve > vo;
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       uint8_t* x = blk + t * (kKv8Page * HD);
-      if (grew[t])
+      const float by = t ? pow2f(vo - ve) : pow2f(ko - ke);
+      if (t ? grew_v : grew_k)
+#pragma unroll 1
         for (int i = lane; i < had * HD / 16; i += 32) {
           uint4* w = reinterpret_cast<uint4*>(x + unit_off<HD>(i / (HD / 16), i % (HD / 16)));
           uint4 y = *w;
-          y.x = e4m3_rescale4(y.x, by[t]);
-          y.y = e4m3_rescale4(y.y, by[t]);
-          y.z = e4m3_rescale4(y.z, by[t]);
-          y.w = e4m3_rescale4(y.w, by[t]);
+          y.x = e4m3_rescale4(y.x, by);
+          y.y = e4m3_rescale4(y.y, by);
+          y.z = e4m3_rescale4(y.z, by);
+          y.w = e4m3_rescale4(y.w, by);
           *w = y;
         }
     }
     uint8_t* xv = blk + kKv8Page * HD;
+#pragma unroll 1
     for (int i = rows * HD / 16 + lane; i < HD; i += 32)   // rows behind the last one: their weight is 0, not their bytes
       *reinterpret_cast<uint4*>(xv + unit_off<HD>(i / (HD / 16), i % (HD / 16))) = make_uint4(0, 0, 0, 0);
     const float fk = pow2f(-ke), fv = pow2f(-ve);
+#pragma unroll 1
     for (int p = first; p < last; ++p) {
       if (p != first) row(p);       // k, v: the first row, the last one computed
 #pragma unroll
@@ -467,11 +554,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
       }
     }
     __syncwarp();
-#pragma unroll
+    fence_proxy_async();     // before the stores below, so as not to wait for them
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       uint8_t* out = a.kv + (((size_t)page * 2 + t) * a.Hkv + g) * (kKv8Page * HD);
       const uint8_t* x = blk + t * (kKv8Page * HD);
-      for (int i = (grew[t] ? 0 : had) * HD / 16 + lane; i < rows * HD / 16; i += 32)
+#pragma unroll 1
+      for (int i = ((t ? grew_v : grew_k) ? 0 : had) * HD / 16 + lane; i < rows * HD / 16; i += 32)
         *reinterpret_cast<uint4*>(out + (size_t)i * 16) =
             *reinterpret_cast<const uint4*>(x + unit_off<HD>(i / (HD / 16), i % (HD / 16)));
     }
@@ -485,6 +574,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     if (a.m > 1) {
       __syncwarp();
       bool any = false;
+#pragma unroll 1
       for (int p = first; p < last; ++p) {
         const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + a.Hkv + g) * HD;
 #pragma unroll
@@ -496,27 +586,36 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
           }
         }
       }
-      nan_new = nan_new || __any_sync(0xffffffffu, any);
+      any = __any_sync(0xffffffffu, any);
+      if (any) fence_proxy_async();
+      nan_new = nan_new || any;
     }
     __syncwarp();
-    fence_proxy_async();
   };
 
-  for (int t = 0; t < n; ++t) {
+#pragma unroll 1
+  for (int t = 0;; ++t) {
     const int src = t & 31;
-    const int page = __shfl_sync(0xffffffffu, cur.page, src), sg = __shfl_sync(0xffffffffu, cur.seg, src);
-    const int j = __shfl_sync(0xffffffffu, cur.j, src), ex = __shfl_sync(0xffffffffu, cur.exps, src);
+    if (src == 0 && t > 0) cur = nxt;
+    if (src == 0 && t + 32 < n) nxt = look_up(t + 32 + lane);
+    const int page = __shfl_sync(0xffffffffu, cur.page, src);
+    const int sg = t < n ? __shfl_sync(0xffffffffu, cur.seg, src) : -1;
+    const int j = __shfl_sync(0xffffffffu, cur.j, src);
     if (sg != seg) {
-      if (seg >= 0) end(t);
+      if (seg >= 0) end();
+      if (sg < 0) break;
+      if (t > 0) load_rows(sg, 0);
       begin(sg);
     }
+    if (sg < 0) break;
     const bool tail = (j + 1) * kKv8Page > pos;
-    if (tail) row(min(pos + a.m, (j + 1) * kKv8Page) - 1);
+    if (tail && page >= 0) row(min(pos + a.m, (j + 1) * kKv8Page) - 1);
     bool ok = mbar_wait(&bars[warp][t % D], (uint32_t)(t / D) & 1u, nullptr);
     ok = __all_sync(0xffffffffu, ok) && page >= 0;
     if (ok) {
       uint8_t* blk = ring + (size_t)(t % D) * UB;
-      int ke = (ex & 0xff) - 64, ve = (ex >> 8) - 64;
+      int ke = kv8_scale_exp(__shfl_sync(0xffffffffu, cur.ks, src));
+      int ve = kv8_scale_exp(__shfl_sync(0xffffffffu, cur.vs, src));
       if (tail) append(blk, page, j, ke, ve);
 
       // S = Q K^T for the page's two groups of 8 keys
@@ -602,52 +701,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     // the slot is free: the unit D further on
     const int ti = t + D;
     if (ti < n && lane == (ti & 31)) issue((ti >> 5) == (t >> 5) ? cur : nxt, ti);
-    if (src == 31) {
-      cur = nxt;
-      nxt = look_up((t & ~31) + 64 + lane);
-    }
-  }
-  if (seg >= 0) end(n);
-  __syncthreads();
-
-  // partials of this CTA's warps, each cut (sequence, kv head) by the warp of its first one
-  const unsigned c0 = cut.start(blockIdx.x * kDecWarps), c1 = cut.start(min((blockIdx.x + 1) * kDecWarps, W));
-  unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);
-  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + ((size_t)a.B * a.Hkv * 4 + 255) / 256 * 256);
-  const float* all = reinterpret_cast<const float*>(sm + lay.slot_off);
-  int prev = -1;
-  for (int e = 0; e < 2 * warp; ++e)
-    if (seg_s[e] >= 0) prev = seg_s[e];
-  for (int e = 2 * warp; e < 2 * warp + 2; ++e) {
-    const int sg = seg_s[e];
-    if (sg < 0 || sg == prev) continue;
-    prev = sg;
-    Join<HD> x;
-    x.template take<false>(
-        [&](int k) { return seg_s[k] == sg ? all + (size_t)k * lay.slot_floats : nullptr; }, e, 2 * kDecWarps, R, r, c);
-    const int b = sg / a.Hkv, g = sg % a.Hkv, pages = first_s[b + 1] - first_s[b];
-    const unsigned s0 = (unsigned)first_s[b] * a.Hkv + (unsigned)g * pages, s1 = s0 + pages;
-    if (s0 >= c0 && s1 <= c1) {
-      x.finish();
-      store_rows<HD>(a, sg, r, c, x.o);
-      continue;
-    }
-    // CTAs that share it: those of its first and of its last page
-    const int f = (int)(cut.of(s0) / kDecWarps), l = (int)(cut.of(s1 - 1) / kDecWarps);
-    x.put(parts + ((size_t)blockIdx.x * 2 + (s0 < c0 ? 0 : 1)) * lay.slot_floats, R, r, c);
-    __threadfence();
-    __syncwarp();
-    unsigned got = 0;
-    if (lane == 0) got = atomicAdd(&tickets[sg], 1u);
-    got = __shfl_sync(0xffffffffu, got, 0);
-    if (got != (unsigned)(l - f)) continue;
-    __threadfence();
-    Join<HD> y;
-    y.template take<true>(
-        [&](int k) { return parts + ((size_t)k * 2 + (k == f ? 1 : 0)) * lay.slot_floats; }, f, l + 1, R, r, c);
-    y.finish();
-    store_rows<HD>(a, sg, r, c, y.o);
-    if (lane == 0) tickets[sg] = 0u;
   }
 }
 
@@ -658,31 +711,34 @@ int num_sms() {
   return n > 0 ? n : 1;
 }
 
-DecLayout dec_layout(int B, int R, int hd) {
+DecLayout dec_layout(int B, int R, int Hkv, int hd) {
   DecLayout l;
   l.ctas = num_sms();
+  l.groups = (Hkv + kDecWarps - 1) / kDecWarps;
+  l.heads = (Hkv + l.groups - 1) / l.groups;
+  l.slices = kDecWarps / l.heads;
   l.slot_floats = R * hd + 2 * R + (2 * R) % 4;
-  const int slot = kDecWarps * 2 * l.slot_floats * 4, meta = (2 * B + 1) * 4, unit = 2 * kKv8Page * hd;
-  const int room = kDecSmem - 1024 - 2048 - slot - meta;   // alignment, static
-  l.depth = room / (kDecWarps * unit);
+  const int warps = l.heads * l.slices, q = warps * R * hd * 4, unit = 2 * kKv8Page * hd;
+  const int room = kDecSmem - 1024 - 2048 - q - (2 * B + 1) * 4;   // alignment, static
+  l.depth = room / (warps * unit);
   if (l.depth > kDecMaxDepth) l.depth = kDecMaxDepth;
-  l.slot_off = kDecWarps * l.depth * unit;
-  l.meta_off = l.slot_off + (slot + 15) / 16 * 16;
+  l.q_off = warps * l.depth * unit;
+  l.meta_off = l.q_off + q;
+  l.vec = 0;
   return l;
 }
 
 }  // namespace
 
 size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd) {
-  const int R = m * (H / Hkv);
-  const DecLayout l = dec_layout(B, R, hd);
-  return ((size_t)B * Hkv * 4 + 255) / 256 * 256 + (size_t)l.ctas * 2 * l.slot_floats * 4;
+  const DecLayout l = dec_layout(B, m * (H / Hkv), Hkv, hd);
+  return (size_t)l.ctas * l.slices * 2 * l.heads * (2 + l.slot_floats) * 4;
 }
 
 cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {
   CUtensorMap map;
   if (!tma_map_kv8(&map, a.kv, a.n_pages, a.Hkv, a.hd)) return cudaErrorNotSupported;
-  DecLayout l = dec_layout(a.B, a.m * (a.H / a.Hkv), a.hd);
+  DecLayout l = dec_layout(a.B, a.m * (a.H / a.Hkv), a.Hkv, a.hd);
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.qkv) | reinterpret_cast<uintptr_t>(a.q_gain) |
                        reinterpret_cast<uintptr_t>(a.rope_cos) | reinterpret_cast<uintptr_t>(a.rope_sin);
   l.vec = (at & 15) == 0 && a.qkv_ld % 4 == 0;
@@ -695,7 +751,7 @@ cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.ctas);
-  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.blockDim = dim3(l.heads * l.slices * 32);
   cfg.dynamicSmemBytes = l.meta_off + (2 * a.B + 1) * 4 + 1024;
   cfg.stream = st;
   // the kernel reads nothing before its wait on the launch before it
