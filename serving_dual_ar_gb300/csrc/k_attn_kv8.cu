@@ -13,18 +13,26 @@ namespace {
 constexpr int kDecWarps = 8;       // most warps of a CTA
 constexpr int kDecMaxDepth = 8;
 constexpr int kDecSmem = 227 * 1024;
-// Pages of a run at least: a cut costs a joining, about as long as four pages.
-constexpr int kDecMinPages = 4;
-// Pieces that one warp joins; more are joined in two levels of about sqrt(n).
-constexpr int kDecFlat = 12;
+constexpr int kDecFlight = 128 * 1024;
+constexpr int kDecPages = 2;       // pages of a unit of work
+// Units of a run at least: a cut costs a joining, about as long as two units.
+constexpr int kDecMinUnits = 2;
+// What starting and ending a sequence costs, in units: the cut counts it.
+constexpr int kDecSeqUnits = 1;
+// Pieces that are joined at once, one per lane; more are joined in two levels
+// of about the square root each.
+constexpr int kDecFlat = 32;
+constexpr int kDecMaxRuns = kDecFlat * kDecFlat;
 
 struct DecLayout {
   int groups, heads, slices;   // kv heads in groups of ``heads``; a CTA has heads x slices warps
-  int depth;                   // pages in flight per warp
-  int q_off, meta_off;         // bytes
+  int depth;                   // units in flight per warp
+  int buf_off, meta_off;       // bytes
+  int buf;                     // a warp's buffer: its rows of HD floats, 4 at least
   int slot_floats;             // one partial: R rows of HD values, then (m, l) of each
   int ctas;
-  int vec;                     // query rows, gains and RoPE rows on 16-byte boundaries
+  int o_vec;                   // rows of o on 16-byte (bf16: 8-byte) boundaries
+  unsigned inv_g;              // i / G = i * inv_g >> 16 for rows i
 };
 
 S2_DEV float ex2(float x) {
@@ -63,8 +71,10 @@ S2_DEV uint32_t unit_off(int row, int c) {
   return HD == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-S2_DEV float4 load4(const float* p, bool vec) {
-  return vec ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+// Four consecutive floats, on a 16-byte boundary if VEC.
+template <bool VEC>
+S2_DEV float4 load4(const float* p) {
+  return VEC ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
 }
 
 // Run ``i`` of the ``runs`` equal ones that U units are cut into starts at
@@ -78,116 +88,27 @@ struct Cut {
   }
 };
 
-// The key row as a call: it is rare, long and wanted at three places, and the
-// kernel's other paths share the instruction cache with it.
-template <int HD>
-struct KeyRow {
-  float v[HD / 32];
-};
-template <int HD>
-__device__ __noinline__ KeyRow<HD> key_row_call(const float* x, const float* gain, const float* cs, const float* sn,
-                                                float eps, int lane) {
-  KeyRow<HD> y;
-  kv8_key_row<HD>(x, gain, cs, sn, eps, lane, y.v);
-  return y;
-}
-
-// What a warp knows of one page of work.
+// What a warp knows of one unit: two pages of a sequence, for one kv head.
 struct Unit {
-  int page, seg, j;   // page id (-1: not to be followed), group * B + b, page of the sequence
-  float ks, vs;       // the block scales
+  int seg, j;              // group * B + b, the sequence's page that comes first
+  int page[kDecPages];     // page ids (-1: none, or not to be followed)
+  float ks[kDecPages], vs[kDecPages];   // the block scales
 };
+// Flags that the pages are there, and the exponents + 64 of their scales.
+struct UnitBits {
+  uint32_t exps;           // K, V of the first page, K, V of the second
+  uint32_t there;
+};
+
+// Weights carry 2^kDecBias, and the running maximum may lag by kDecLag, so that a
+// weight of at most 2^14 fits f16 and the accumulators are rescaled rarely.
+constexpr int kDecBias = 6, kDecLag = 8;
 
 template <int HD>
 struct DecState {           // one piece of a (sequence, kv head): all rows, log2 domain
   float o[HD / 8][4];       // tile t: dims n * HD/8 + t of column n; [0..1] hi part of row r, [2..3] lo part
   float m, l;               // row r = lane / 4 (l: this lane's keys)
-  int E;                    // o counts in units of 2^(E - 14)
-};
-
-// One result row set into o: dims [c * HD/4, (c + 1) * HD/4) of row r.
-template <int HD>
-S2_DEV void store_rows(const Kv8Args& a, int b, int g, int r, int c, const float (&y)[HD / 4]) {
-  const int G = a.H / a.Hkv;
-  if (r >= a.m * G) return;
-  const size_t at = (size_t)(b * a.m + r / G) * a.o_ld + (size_t)(g * G + r % G) * HD + c * (HD / 4);
-  if (a.o) {
-    float* p = a.o + at;
-    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-      for (int i = 0; i < HD / 4; i += 4)
-        *reinterpret_cast<float4*>(p + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) p[i] = y[i];
-    }
-  } else {
-    __nv_bfloat16* p = a.o16 + at;
-    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-      for (int i = 0; i < HD / 4; i += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(y[i + 2 * k], y[i + 2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) p[i] = __float2bfloat16_rn(y[i]);
-    }
-  }
-}
-
-// Joining of partials (rows of HD values relative to 2^m, and (m, l)).
-template <int HD>
-struct Join {
-  float o[HD / 4], m = -INFINITY, l = 0.f;
-  S2_DEV Join() {
-#pragma unroll
-    for (int i = 0; i < HD / 4; ++i) o[i] = 0.f;
-  }
-  // The partials slot(0) .. slot(n - 1), in order: the largest maximum first,
-  // so that the loads of the values wait for nothing.
-  template <typename F>
-  S2_DEV void take(F slot, int n, int R, int r, int c) {
-    if (r >= R) return;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) m = fmaxf(m, __ldcg(slot(k) + R * HD + 2 * r));
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
-      const float* p = slot(k);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + R * HD + 2 * r));
-      const float y = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2(ml.x - m);   // no keys: nothing; NaN stays
-      l += ml.y * y;
-      const float4* s = reinterpret_cast<const float4*>(p + r * HD + c * (HD / 4));
-#pragma unroll
-      for (int i = 0; i < HD / 16; ++i) {
-        const float4 v = __ldcg(s + i);
-        o[4 * i] += v.x * y;
-        o[4 * i + 1] += v.y * y;
-        o[4 * i + 2] += v.z * y;
-        o[4 * i + 3] += v.w * y;
-      }
-    }
-  }
-  S2_DEV void put(float* slot, int R, int r, int c) const {
-    if (r >= R) return;
-    float4* s = reinterpret_cast<float4*>(slot + r * HD + c * (HD / 4));
-#pragma unroll
-    for (int i = 0; i < HD / 16; ++i) s[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    if (c == 0) {
-      slot[R * HD + 2 * r] = m;
-      slot[R * HD + 2 * r + 1] = l;
-    }
-  }
-  S2_DEV void finish() {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < HD / 4; ++i) o[i] *= inv;
-  }
+  int E;                    // o counts in units of 2^(E - kDecBias)
 };
 
 // The work is the list of all pages in the order (sequence, page), cut into
@@ -209,31 +130,35 @@ struct Join {
 // n, and dims n * HD/8 .. of the values of keys 2c, 2c + 1, 2c + 8, 2c + 9.
 // The block scale of K multiplies the scores; the one of V goes into the
 // weights, with the running exponent E handled like the running maximum.
-template <int HD>
+template <int HD, bool VEC>
 __global__ void __launch_bounds__(kDecWarps * 32, 1)
-kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout lay) {
+kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Kv8Args a,
+                  const __grid_constant__ DecLayout lay) {
   constexpr int NT = HD / 8;              // output tiles of 8 dims
   constexpr int KS = HD / 16;             // k-steps of the scores
-  constexpr int UB = 2 * kKv8Page * HD;   // bytes of a unit
+  constexpr int PB = 2 * kKv8Page * HD;   // bytes of a page's part: 16 keys, 16 values
+  constexpr int UB = kDecPages * PB;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ __align__(8) uint64_t bars[kDecWarps][kDecMaxDepth];
   __shared__ int scan_s[kDecWarps + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int r = lane >> 2, c = lane & 3;
-  const int D = lay.depth, G = a.H / a.Hkv, R = a.m * G;
+  const int D = lay.depth, G = a.H / a.Hkv, R = a.m * G, rt = r * lay.inv_g >> 16;   // row r: new row rt
   const int h = warp % lay.heads;                                  // head within its group
   const unsigned run = blockIdx.x * lay.slices + warp / lay.heads;
-  int* first_s = reinterpret_cast<int*>(sm + lay.meta_off);   // pages before sequence b, B + 1 entries
+  int* first_s = reinterpret_cast<int*>(sm + lay.meta_off);   // units before sequence b, B + 1 entries
   int* pos_s = first_s + a.B + 1;
   uint8_t* ring = sm + (size_t)warp * D * UB;
-  uint4* qst = reinterpret_cast<uint4*>(sm + lay.q_off) + (size_t)warp * R * (HD / 4);
+  float* buf = reinterpret_cast<float*>(sm + lay.buf_off + warp * lay.buf);
   for (int i = tid; i < kDecWarps * D; i += threads) mbar_init(&bars[i / D][i % D], 1);
   fence_mbar_init();
   pdl_launch_next();
   pdl_wait();
 
-  // pages of each sequence (none for one that is left out), and their sums
+  // units of each sequence (none for one that is left out; kDecSeqUnits more
+  // than it has, which no page stands for), and their sums
+  auto units_at = [&](int p) { return (p + a.m + kDecPages * kKv8Page - 1) / (kDecPages * kKv8Page); };
   {
     const int per = (a.B + threads - 1) / threads, b0 = tid * per;
     int own = 0;
@@ -243,7 +168,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
       const bool in = p >= 0 && p <= a.max_pos - a.m;
       pos_s[b] = in ? p : -1;
       first_s[b] = own;
-      own += in ? (p + a.m + kKv8Page - 1) / kKv8Page : 0;
+      own += in ? units_at(p) + kDecSeqUnits : 0;
     }
     int x = own;
 #pragma unroll
@@ -266,55 +191,74 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
     if (pos_s[b] < 0)
 #pragma unroll 1
-      for (int i = tid; i < a.m * a.H * HD; i += threads) {
-        const size_t at = (size_t)(b * a.m + i / (a.H * HD)) * a.o_ld + i % (a.H * HD);
-        if (a.o) a.o[at] = 0.f;
-        else a.o16[at] = __float2bfloat16_rn(0.f);
-      }
+      for (int t = 0; t < a.m; ++t)
+#pragma unroll 1
+        for (int i = tid; i < a.H * HD; i += threads) {
+          const size_t at = (size_t)(b * a.m + t) * a.o_ld + i;
+          if (a.o) a.o[at] = 0.f;
+          else a.o16[at] = __float2bfloat16_rn(0.f);
+        }
   // units fit 31 bits (the caller refuses more)
   const unsigned P = first_s[a.B], U = P * lay.groups;
   if (U == 0) return;
-  const unsigned W = min(gridDim.x * lay.slices, (U + kDecMinPages - 1) / kDecMinPages);
+  const unsigned W = min(min(gridDim.x * lay.slices, kDecMaxRuns), (U + kDecMinUnits - 1) / kDecMinUnits);
   if (run >= W) return;
   const Cut cut{U / W, U % W};
   const unsigned u0 = cut.start(run);
   const int n = (int)(cut.start(run + 1) - u0);
 
-  // (group, sequence) of unit u
-  auto seg_of = [&](unsigned u) {
-    const int group = lay.groups > 1 ? u / P : 0;
-    u -= group * P;
-    int lo = 0;                                 // last b with first page <= u
-#pragma unroll 1
-    for (int hi = a.B; hi - lo > 1;) {
-      const int mid = (lo + hi) >> 1;
-      if ((unsigned)first_s[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    return group * a.B + lo;
-  };
-  auto seg_start = [&](int s) { return (unsigned)(s / a.B) * P + first_s[s % a.B]; };
+  // A (group, sequence) is named by group << 16 | b.
+  auto seg_start = [&](int s) { return (unsigned)(s >> 16) * P + first_s[s & 0xffff]; };
+  auto head_of = [&](int s) { return (s >> 16) * lay.heads + h; };
   // the unit u0 + t, looked up by lane t % 32
   auto look_up = [&](int t) {
-    Unit x{-1, -1, 0, 1.f, 1.f};
+    Unit x{-1, 0, {-1, -1}, {1.f, 1.f}, {1.f, 1.f}};
     if (t >= n) return x;
-    x.seg = seg_of(u0 + t);
-    x.j = (int)(u0 + t - seg_start(x.seg));
-    const int p = a.table[(size_t)(x.seg % a.B) * a.table_ld + x.j], g = x.seg / a.B * lay.heads + h;
-    if (p >= 0 && p < a.n_pages && g < a.Hkv) {
-      x.page = p;
-      const float* s = a.scale + (size_t)p * 2 * a.Hkv + g;
-      x.ks = s[0];
-      x.vs = s[a.Hkv];
+    unsigned u = u0 + t;
+    int group = 0, b = 0;                       // last b with first unit <= u
+    for (; u >= P; u -= P) ++group;
+#pragma unroll 1
+    for (int hi = a.B; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if ((unsigned)first_s[mid] <= u) b = mid;
+      else hi = mid;
     }
+    x.j = kDecPages * (int)(u - first_s[b]);
+    if (x.j >= kDecPages * units_at(pos_s[b])) {
+      x.seg = -2;                               // none
+      return x;
+    }
+    x.seg = group << 16 | b;
+    const int g = head_of(x.seg), pages = (pos_s[b] + a.m + kKv8Page - 1) / kKv8Page;
+    const int* row = a.table + (size_t)b * a.table_ld + x.j;
+#pragma unroll
+    for (int i = 0; i < kDecPages; ++i) {
+      const int p = x.j + i < pages ? row[i] : -1;
+      x.page[i] = p >= 0 && p < a.n_pages && g < a.Hkv ? p : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kDecPages; ++i)
+      if (x.page[i] >= 0) {
+        const float* s = a.scale + (size_t)x.page[i] * 2 * a.Hkv + g;
+        x.ks[i] = s[0];
+        x.vs[i] = s[a.Hkv];
+      }
     return x;
   };
-  auto issue = [&](const Unit& x, int t) {      // by the lane that looked it up
-    uint64_t* bar = &bars[warp][t % D];
-    if (x.page < 0) mbar_arrive(bar);
+  auto bits_of = [&](const Unit& x) {           // waits for the scales
+    return UnitBits{(uint32_t)(kv8_scale_exp(x.ks[0]) + 64) | (uint32_t)(kv8_scale_exp(x.vs[0]) + 64) << 8 |
+                        (uint32_t)(kv8_scale_exp(x.ks[1]) + 64) << 16 | (uint32_t)(kv8_scale_exp(x.vs[1]) + 64) << 24,
+                    (x.page[0] >= 0 ? 1u : 0u) | (x.page[1] >= 0 ? 2u : 0u)};
+  };
+  auto issue = [&](const Unit& x, int slot) {   // by the lane that looked it up
+    uint64_t* bar = &bars[warp][slot];
+    const int there = (x.page[0] >= 0) + (x.page[1] >= 0);
+    if (!there) mbar_arrive(bar);
     else {
-      mbar_arrive_expect_tx(bar, UB);
-      tma_load_page(ring + (size_t)(t % D) * UB, &map, x.seg / a.B * lay.heads + h, x.page, bar);
+      mbar_arrive_expect_tx(bar, there * PB);
+#pragma unroll
+      for (int i = 0; i < kDecPages; ++i)
+        if (x.page[i] >= 0) tma_load_page(ring + slot * UB + i * PB, &map, head_of(x.seg), x.page[i], bar);
     }
   };
 
@@ -324,42 +268,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
   int seg = -1, pos = 0, b = 0, g = 0;
   bool nan_new = false;      // a new value row after the first holds a NaN
 
-  // HD/4 lanes take a row, four dims each (the rotation's partners are half
-  // a row of lanes apart): whole rows by each load, and the loads of four
-  // rows (or eight half ones) in flight at once.  What lane l holds of row i
-  // is fragment t = l % KS of lane (i, l / KS); a warp's buffer, XORed
-  // against bank conflicts, takes it there.
-  constexpr int LPR = HD / 4, RPS = 32 / LPR, ST = 4;    // rows per load, loads at a time
-  const int l = lane % LPR, d = 4 * l, dh = d % (HD / 2);
-  const bool vec = lay.vec;
-  float4 x[ST] = {}, co[ST] = {}, si[ST] = {};
-  auto load_rows = [&](int s, int k0) {
-    const int b = s % a.B, g = s / a.B * lay.heads + h;
-    if (g >= a.Hkv) return;
-#pragma unroll
-    for (int k = 0; k < ST; ++k) {
-      const int i = k0 + k * RPS + lane / LPR;
-      x[k] = co[k] = si[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < R) {
-        const int p = pos_s[b] + i / G;
-        x[k] = load4(a.qkv + (size_t)(b * a.m + i / G) * a.qkv_ld + (size_t)(g * G + i % G) * HD + d, vec);
-        co[k] = load4(a.rope_cos + (size_t)p * (HD / 2) + dh, vec);
-        si[k] = load4(a.rope_sin + (size_t)p * (HD / 2) + dh, vec);
-      }
-    }
-  };
-  // the first rows' loads go ahead of the stream of pages
-  load_rows(seg_of(u0), 0);
-  Unit cur = look_up(lane);
-  Unit nxt = cur;
-  if (lane < min(D, n)) issue(cur, lane);
-
-  // The query rows of (sequence, kv head) s; ``load_rows(s, 0)`` came before.
+  // The query rows of (group, sequence) s.  HD/4 lanes take a row, four dims
+  // each (the rotation's partners are half a row of lanes apart): whole rows by
+  // each load, and the loads of four rows (or eight half ones) in flight at
+  // once.  What lane l holds of row i is fragment t = l % KS of lane (i, l / KS);
+  // a warp's buffer, XORed against bank conflicts, takes it there.
   auto begin = [&](int s) {
     seg = s;
     nan_new = false;
-    b = s % a.B;
-    g = s / a.B * lay.heads + h;
+    b = s & 0xffff;
+    g = head_of(s);
     pos = pos_s[b];
     st.m = -INFINITY;
     st.l = 0.f;
@@ -368,12 +286,28 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[t][e] = 0.f;
-    const float4 gain = load4(a.q_gain + d, vec);
+#pragma unroll
+    for (int t = 0; t < KS; ++t) qa[t][0] = qa[t][1] = qa[t][2] = qa[t][3] = 0u;
+    if (g >= a.Hkv) return;
+    constexpr int LPR = HD / 4, RPS = 32 / LPR, ST = 4;    // rows per load, loads at a time
+    const int l = lane % LPR, d = 4 * l;
+    const float4 gain = load4<VEC>(a.q_gain + d);
     const float sg = l < LPR / 2 ? -1.f : 1.f;
+    const float* rows = a.qkv + (size_t)b * a.m * a.qkv_ld + (size_t)g * G * HD + d;
+    const size_t turn = (size_t)pos * (HD / 2) + d % (HD / 2);
+    uint4* qst = reinterpret_cast<uint4*>(buf);
+    __syncwarp();
 #pragma unroll 1
     for (int k0 = 0; k0 < R; k0 += ST * RPS) {
+      float4 x[ST], co[ST], si[ST];
       float ss[ST];
-      if (k0 > 0) load_rows(s, k0);
+#pragma unroll
+      for (int k = 0; k < ST; ++k) {
+        const int i = min(k0 + k * RPS + lane / LPR, R - 1), t = i * lay.inv_g >> 16;
+        x[k] = load4<VEC>(rows + (size_t)t * a.qkv_ld + (i - t * G) * HD);
+        co[k] = load4<VEC>(a.rope_cos + turn + t * (HD / 2));
+        si[k] = load4<VEC>(a.rope_sin + turn + t * (HD / 2));
+      }
 #pragma unroll
       for (int k = 0; k < ST; ++k) ss[k] = x[k].x * x[k].x + x[k].y * x[k].y + x[k].z * x[k].z + x[k].w * x[k].w;
 #pragma unroll
@@ -406,7 +340,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
         for (int k = 0; k < ST; ++k) ss[k] = fmaxf(ss[k], __shfl_xor_sync(0xffffffffu, ss[k], o));
 #pragma unroll
       for (int k = 0; k < ST; ++k) {
-        const int i = k0 + k * RPS + lane / LPR;
+        const int i = k * RPS + lane / LPR;
         // the row's largest magnitude to 2^12 .. 2^13: its pair then is good
         // to 2^-22 of each value and 2^-37 of the largest
         const int ex = min(max((int)(__float_as_uint(ss[k]) >> 23) - 127, -100), 100);
@@ -416,141 +350,272 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
         uint4 y;
         split2(x[k].x * up, x[k].y * up, y.x, y.y);
         split2(x[k].z * up, x[k].w * up, y.z, y.w);
-        if (i < R) qst[i * LPR + (l ^ ((l / KS) | ((i & 1) << 2)))] = y;
+        qst[i * LPR + (l ^ ((l / KS) | ((i & 1) << 2)))] = y;
       }
-    }
-    __syncwarp();
+      __syncwarp();
+      if (r >= k0 && r < min(k0 + ST * RPS, R))
 #pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (r < R) y = qst[r * LPR + ((c * KS + t) ^ (c | ((r & 1) << 2)))];
-      qa[t][0] = y.x;
-      qa[t][1] = y.y;
-      qa[t][2] = y.z;
-      qa[t][3] = y.w;
+        for (int t = 0; t < KS; ++t) {
+          const uint4 y = qst[(r - k0) * LPR + ((c * KS + t) ^ (c | ((r & 1) << 2)))];
+          qa[t][0] = y.x;
+          qa[t][1] = y.y;
+          qa[t][2] = y.z;
+          qa[t][3] = y.w;
+        }
+      __syncwarp();
     }
-    __syncwarp();
   };
 
-  // The piece's rows relative to 2^m, as a Join: dims 2c NT + t and (2c + 1) NT + t.
-  auto piece = [&](Join<HD>& x) {
-    st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
-    st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
-    x.m = st.m;
-    x.l = st.l;
-    const float f = pow2f(st.E - 14);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      x.o[t] = (st.o[t][0] + st.o[t][2]) * f;
-      x.o[NT + t] = (st.o[t][1] + st.o[t][3]) * f;
+  // The end of a piece: into o if it is all of its sequence, else into the
+  // run's slot 1 (a sequence's first piece) or 0 (any other) for the joining.
+  // Nothing waits here: under the stream of pages a round trip to memory takes
+  // microseconds.
+  unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);      // [level][run][slot][warp of the run]
+  float* parts = reinterpret_cast<float*>(tickets + (size_t)lay.ctas * lay.slices * 4 * lay.heads);
+  int open[2] = {-1, -1};
+  // Four values of row i of kv head g of sequence b, at dim d, to o or a slot.
+  auto put = [&](float* slot, int b, int g, int i, int d, float4 y) {
+    if (slot) {
+      *reinterpret_cast<float4*>(slot + i * HD + d) = y;
+      return;
     }
-    if (nan_new && r < R) {      // the rows that see it get it back
-#pragma unroll 1
-      for (int i = 0; i <= r / G; ++i) {
-        const float* v = a.qkv + (size_t)(b * a.m + i) * a.qkv_ld + (size_t)(a.H + a.Hkv + g) * HD + c * (HD / 4);
-#pragma unroll
-        for (int k = 0; k < HD / 4; ++k)
-          if (v[k] != v[k]) x.o[k] = v[k];
+    const int t = i * lay.inv_g >> 16;
+    const size_t at = (size_t)(b * a.m + t) * a.o_ld + (size_t)(g * G + i - t * G) * HD + d;
+    if (a.o) {
+      if (lay.o_vec) {
+        *reinterpret_cast<float4*>(a.o + at) = y;
+      } else {
+        a.o[at] = y.x;
+        a.o[at + 1] = y.y;
+        a.o[at + 2] = y.z;
+        a.o[at + 3] = y.w;
+      }
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+      if (lay.o_vec) {
+        *reinterpret_cast<uint2*>(a.o16 + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        a.o16[at] = lo.x;
+        a.o16[at + 1] = lo.y;
+        a.o16[at + 2] = hi.x;
+        a.o16[at + 3] = hi.y;
       }
     }
   };
-  // The end of a piece: stored if it is all of its sequence, else left for,
-  // or joined with, the other runs' pieces.
-  unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);      // [level][run][2][warp of the run]
-  float* parts = reinterpret_cast<float*>(tickets + (size_t)lay.ctas * lay.slices * 4 * lay.heads);
   auto end = [&] {
     if (g >= a.Hkv) return;
-    const unsigned s0 = seg_start(seg);
-    const int f = (int)cut.of(s0), n = (int)cut.of(s0 + first_s[b + 1] - first_s[b] - 1) - f + 1;
-    Join<HD> x;
-    piece(x);
-    // piece i of the sequence is run f + i's: its last one if i = 0, else its first
-    auto at = [&](int i) { return ((size_t)(f + i) * 2 + (i == 0)) * lay.heads + h; };
-    int i = (int)run - f, step = 1, per = n;
-    if (n > kDecFlat)
-      for (per = 4; per * per < n;) ++per;
-    while (n > 1) {
-      x.put(parts + at(i) * lay.slot_floats, R, r, c);
-      __threadfence();
-      __syncwarp();
-      const int i0 = i / per * per, count = (min(n - i0, per) + step - 1) / step;
-      unsigned* ticket = tickets + (step == 1 ? 0 : (size_t)lay.ctas * lay.slices * 2 * lay.heads) + at(i0);
-      unsigned got = 0;
-      if (lane == 0) got = atomicAdd(ticket, 1u);
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (got != (unsigned)(count - 1)) return;
-      __threadfence();
-      if (lane == 0) *ticket = 0u;
-      x = Join<HD>();
-      x.take([&](int k) { return parts + at(i0 + k * step) * lay.slot_floats; }, count, R, r, c);
-      if (per >= n) break;
-      __syncwarp();          // all lanes have read the slot that is written next
-      i = i0;
-      step = per;
-      per = n;
+    const unsigned s0 = seg_start(seg), s1 = s0 + units_at(pos);
+    const bool whole = s0 >= u0 && s1 <= u0 + n;
+    const int k = s0 >= u0;
+    float* slot = whole ? nullptr : parts + (((size_t)run * 2 + k) * lay.heads + h) * lay.slot_floats;
+    st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
+    st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+    float f = pow2f(st.E - kDecBias);
+    if (whole) f = st.l == 0.f ? 0.f : f * (1.f / st.l);
+    __syncwarp();
+    if (r < R) {
+      float4* y = reinterpret_cast<float4*>(buf + r * HD + c * (HD / 4));
+#pragma unroll
+      for (int t = 0; t < NT; t += 4) {
+        y[t / 4] = make_float4((st.o[t][0] + st.o[t][2]) * f, (st.o[t + 1][0] + st.o[t + 1][2]) * f,
+                               (st.o[t + 2][0] + st.o[t + 2][2]) * f, (st.o[t + 3][0] + st.o[t + 3][2]) * f);
+        y[NT / 4 + t / 4] = make_float4((st.o[t][1] + st.o[t][3]) * f, (st.o[t + 1][1] + st.o[t + 1][3]) * f,
+                                        (st.o[t + 2][1] + st.o[t + 2][3]) * f, (st.o[t + 3][1] + st.o[t + 3][3]) * f);
+      }
+      if (slot && c == 0) *reinterpret_cast<float2*>(slot + R * HD + 2 * r) = make_float2(st.m, st.l);
     }
-    x.finish();
-    store_rows<HD>(a, b, g, r, c, x.o);
+    __syncwarp();
+    if (nan_new) {        // the rows that see a new value's NaN get it back
+#pragma unroll 1
+      for (int i = lane; i < R * HD; i += 32)
+#pragma unroll 1
+        for (int t = 0; t <= (int)(i / HD * lay.inv_g >> 16); ++t) {
+          const float v = a.qkv[(size_t)(b * a.m + t) * a.qkv_ld + (size_t)(a.H + a.Hkv + g) * HD + i % HD];
+          if (v != v) buf[i] = v;
+        }
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int q = 4 * lane; q < R * HD; q += 128)
+      put(slot, b, g, q / HD, q % HD, *reinterpret_cast<const float4*>(buf + q));
+    if (!whole) {
+      if (k) open[1] = seg;
+      else open[0] = seg;
+    }
+  };
+  // After the run: a ticket for each open piece; the last to arrive joins.
+  auto join = [&] {
+    if (open[0] < 0 && open[1] < 0) return;
+    __threadfence();
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int s = k ? open[1] : open[0];
+      if (s < 0) continue;
+      // its pieces are those of the runs f .. f + n - 1
+      const unsigned s0 = seg_start(s), s1 = s0 + units_at(pos_s[s & 0xffff]);
+      const int f = (int)cut.of(s0), n = (int)cut.of(s1 - 1) - f + 1;
+      auto at = [&](int i) { return ((size_t)(f + i) * 2 + (i == 0)) * lay.heads + h; };
+      int per = n, step = 1;
+      if (n > kDecFlat)
+        for (per = 4; per * per < n;) ++per;
+      int i0 = (int)run - f;
+#pragma unroll 1
+      for (;;) {
+        i0 -= i0 % per;
+        const int count = (min(n - i0, per) + step - 1) / step;
+        unsigned* ticket = tickets + (step == 1 ? 0 : (size_t)lay.ctas * lay.slices * 2 * lay.heads) + at(i0);
+        unsigned got = 0;
+        if (lane == 0) got = atomicAdd(ticket, 1u);
+        if (__shfl_sync(0xffffffffu, got, 0) != (unsigned)(count - 1)) break;
+        __threadfence();
+        if (lane == 0) *ticket = 0u;
+        const bool done = per >= n;
+        float* slot = done ? nullptr : parts + at(i0) * lay.slot_floats;
+        // piece q's maxima and sums in lane q, its weight for row i in w[i]
+        float w[kKv8MaxRows], inv[kKv8MaxRows];
+        const float* ml = parts + at(i0 + min(lane, count - 1) * step) * lay.slot_floats + R * HD;
+#pragma unroll
+        for (int i = 0; i < kKv8MaxRows; ++i) {
+          float2 v = make_float2(-INFINITY, 0.f);
+          if (i < R && lane < count) v = __ldcg(reinterpret_cast<const float2*>(ml + 2 * i));
+          w[i] = v.x;
+          inv[i] = v.y;
+        }
+        float m[kKv8MaxRows];
+#pragma unroll
+        for (int i = 0; i < kKv8MaxRows; ++i) m[i] = w[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kKv8MaxRows; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+        for (int i = 0; i < kKv8MaxRows; ++i) {
+          // no keys: nothing; NaN stays
+          w[i] = w[i] == -INFINITY ? (inv[i] == inv[i] ? 0.f : inv[i]) : ex2(w[i] - m[i]);
+          inv[i] *= w[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kKv8MaxRows; ++i) inv[i] += __shfl_xor_sync(0xffffffffu, inv[i], o);
+#pragma unroll
+        for (int i = 0; i < kKv8MaxRows; ++i) {
+          if (slot && lane == 0 && i < R) *reinterpret_cast<float2*>(slot + R * HD + 2 * i) = make_float2(m[i], inv[i]);
+          inv[i] = !done ? 1.f : inv[i] == 0.f ? 0.f : 1.f / inv[i];
+        }
+        // 128 values a step (a row of 128, two of 64), all steps of four pieces
+        // in flight at once: a round trip is half a microsecond
+        constexpr int RPS = 128 / HD, ST = kKv8MaxRows / RPS, Q = 4;
+        float4 o[ST];
+#pragma unroll
+        for (int i = 0; i < ST; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int row = 4 * lane / HD;               // row within a step
+#pragma unroll 1
+        for (int q0 = 0; q0 < count; q0 += Q) {
+          float4 x[Q][ST];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const float* v = parts + at(i0 + min(q0 + q, count - 1) * step) * lay.slot_floats + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < ST; ++i) {
+              x[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (q0 + q < count && i * RPS + row < R) x[q][i] = __ldcg(reinterpret_cast<const float4*>(v + i * 128));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < ST; ++i) {
+              float y = __shfl_sync(0xffffffffu, w[i * RPS], (q0 + q) & 31);
+              if (RPS == 2) {
+                const float y2 = __shfl_sync(0xffffffffu, w[i * RPS + RPS - 1], (q0 + q) & 31);
+                y = row ? y2 : y;
+              }
+              o[i].x += x[q][i].x * y;
+              o[i].y += x[q][i].y * y;
+              o[i].z += x[q][i].z * y;
+              o[i].w += x[q][i].w * y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+          const float y = row ? inv[i * RPS + RPS - 1] : inv[i * RPS];
+          o[i] = make_float4(o[i].x * y, o[i].y * y, o[i].z * y, o[i].w * y);
+        }
+        __syncwarp();        // all lanes have read the slot that is written now
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+          if (i * RPS + row < R) *reinterpret_cast<float4*>(buf + i * 128 + 4 * lane) = o[i];
+        __syncwarp();
+#pragma unroll 1
+        for (int q = 4 * lane; q < R * HD; q += 128)
+          put(slot, s & 0xffff, head_of(s), q / HD, q % HD, *reinterpret_cast<const float4*>(buf + q));
+        if (done) break;
+        __threadfence();
+        __syncwarp();
+        step = per;
+        per = n;
+      }
+    }
   };
 
-  // One new key (normed, rotated) and value, lane l taking dims l + 32 i.
-  constexpr int N = HD / 32;
-  float k[N], v[N];
-  auto row = [&](int p) {
-    const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + g) * HD;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = x[(size_t)a.Hkv * HD + lane + 32 * i];
-    const KeyRow<HD> y = key_row_call<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2),
-                                          a.rope_sin + (size_t)p * (HD / 2), a.eps, lane);
-#pragma unroll
-    for (int i = 0; i < N; ++i) k[i] = y.v[i];
-  };
-  // New rows of this page into its shared-memory copy and to the pool; the
-  // page's last new row is in k, v already.
+  // New rows of this page into its shared-memory copy and to the pool.
   auto append = [&](uint8_t* blk, int page, int j, int& ke, int& ve) {
+    constexpr int N = HD / 32;
     const int first = max(pos, j * kKv8Page), last = min(pos + a.m, (j + 1) * kKv8Page);
-    const int had = first - j * kKv8Page, rows = last - j * kKv8Page;
-    float mk = abs_max(k, 0.f), mv = abs_max(v, 0.f);
-#pragma unroll 1
-    for (int p = last - 2; p >= first; --p) {
-      row(p);
-      mk = abs_max(k, mk);
-      mv = abs_max(v, mv);
-    }
+    const int had = first - j * kKv8Page, rows = last - j * kKv8Page, cnt = last - first;
     const int ko = had ? ke : kKv8EMin, vo = had ? ve : kKv8EMin;
-    ke = max(ko, kv8_exponent(warp_max(mk)));
-    ve = max(vo, kv8_exponent(warp_max(mv)));
-    const bool grew_k = had && ke > ko, grew_v = had && ve > vo;
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      uint8_t* x = blk + t * (kKv8Page * HD);
-      const float by = t ? pow2f(vo - ve) : pow2f(ko - ke);
-      if (t ? grew_v : grew_k)
-#pragma unroll 1
-        for (int i = lane; i < had * HD / 16; i += 32) {
-          uint4* w = reinterpret_cast<uint4*>(x + unit_off<HD>(i / (HD / 16), i % (HD / 16)));
-          uint4 y = *w;
-          y.x = e4m3_rescale4(y.x, by);
-          y.y = e4m3_rescale4(y.y, by);
-          y.z = e4m3_rescale4(y.z, by);
-          y.w = e4m3_rescale4(y.w, by);
-          *w = y;
-        }
-    }
     uint8_t* xv = blk + kKv8Page * HD;
+    float k[N], v[N], mk = 0.f, mv = 0.f;
+    bool grew_k = false, grew_v = false, nan = false;
+    // two passes over the new rows, from the last to the first for their
+    // largest magnitudes, and back to be rounded
 #pragma unroll 1
-    for (int i = rows * HD / 16 + lane; i < HD; i += 32)   // rows behind the last one: their weight is 0, not their bytes
-      *reinterpret_cast<uint4*>(xv + unit_off<HD>(i / (HD / 16), i % (HD / 16))) = make_uint4(0, 0, 0, 0);
-    const float fk = pow2f(-ke), fv = pow2f(-ve);
+    for (int it = 0; it < 2 * cnt; ++it) {
+      const int p = it < cnt ? last - 1 - it : first + it - cnt;
+      if (it != cnt) {
+        const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + g) * HD;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = x[(size_t)a.Hkv * HD + lane + 32 * i];
+        kv8_key_row<HD>(x, a.k_gain, a.rope_cos + (size_t)p * (HD / 2), a.rope_sin + (size_t)p * (HD / 2), a.eps, lane,
+                        k);
+      }
+      if (it < cnt) {
+        mk = abs_max(k, mk);
+        mv = abs_max(v, mv);
+        continue;
+      }
+      if (it == cnt) {
+        ke = max(ko, kv8_exponent(warp_max(mk)));
+        ve = max(vo, kv8_exponent(warp_max(mv)));
+        grew_k = had && ke > ko;
+        grew_v = had && ve > vo;
 #pragma unroll 1
-    for (int p = first; p < last; ++p) {
-      if (p != first) row(p);       // k, v: the first row, the last one computed
+        for (int t = 0; t < 2; ++t)
+          if (t ? grew_v : grew_k) {
+            const float by = t ? pow2f(vo - ve) : pow2f(ko - ke);
+#pragma unroll 1
+            for (int i = lane; i < had * HD / 4; i += 32) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(blk + t * (kKv8Page * HD) +
+                                                        unit_off<HD>(i / (HD / 4), i % (HD / 4) / 4)) + i % 4;
+              *w = e4m3_rescale4(*w, by);
+            }
+          }
+        // rows behind the last one: their weight is 0, not their bytes
+#pragma unroll 1
+        for (int i = rows * HD / 16 + lane; i < HD; i += 32)
+          *reinterpret_cast<uint4*>(xv + unit_off<HD>(i / (HD / 16), i % (HD / 16))) = make_uint4(0, 0, 0, 0);
+      }
+      const float fk = pow2f(-ke), fv = pow2f(-ve);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int d = lane + 32 * i;
-        const uint32_t at = unit_off<HD>(p % kKv8Page, d >> 4) + (d & 15);
-        blk[at] = (uint8_t)e4m3x2(k[i] * fk, 0.f);
-        xv[at] = (uint8_t)e4m3x2(v[i] * fv, 0.f);
+        const uint32_t to = unit_off<HD>(p % kKv8Page, d >> 4) + (d & 15);
+        blk[to] = (uint8_t)e4m3x2(k[i] * fk, 0.f);
+        xv[to] = (uint8_t)e4m3x2(v[i] * fv, 0.f);
+        nan = nan || v[i] != v[i];
       }
     }
     __syncwarp();
@@ -569,139 +634,183 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, Kv8Args a, DecLayout 
       s[0] = pow2f(ke);
       s[a.Hkv] = pow2f(ve);
     }
-    // A NaN among the new values must not reach the rows before it through
-    // 0 * NaN: it leaves the copy, and ``piece`` gives it back to the others.
-    if (a.m > 1) {
-      __syncwarp();
-      bool any = false;
+    // A NaN among several new rows' values must not reach the rows before it
+    // through 0 * NaN: it leaves the copy, and ``end`` gives it back.
+    if (a.m > 1 && __any_sync(0xffffffffu, nan)) {
+      nan_new = true;
 #pragma unroll 1
-      for (int p = first; p < last; ++p) {
-        const float* x = a.qkv + (size_t)(b * a.m + p - pos) * a.qkv_ld + (size_t)(a.H + a.Hkv + g) * HD;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int d = lane + 32 * i;
-          if (x[d] != x[d]) {
-            any = true;
-            xv[unit_off<HD>(p % kKv8Page, d >> 4) + (d & 15)] = 0;
-          }
-        }
+      for (int i = had * HD + lane; i < rows * HD; i += 32) {
+        uint8_t* w = xv + unit_off<HD>(i / HD, i % HD / 16) + i % 16;
+        if ((*w & 0x7f) == 0x7f) *w = 0;
       }
-      any = __any_sync(0xffffffffu, any);
-      if (any) fence_proxy_async();
-      nan_new = nan_new || any;
+      __syncwarp();
+      fence_proxy_async();
     }
     __syncwarp();
   };
 
+  Unit cur = look_up(lane), nxt = cur;
+  if (lane < min(D, n)) issue(cur, lane);
+  UnitBits bits{0u, 0u};
+  int slot = 0;
+  uint32_t phase = 0;
 #pragma unroll 1
   for (int t = 0;; ++t) {
     const int src = t & 31;
-    if (src == 0 && t > 0) cur = nxt;
-    if (src == 0 && t + 32 < n) nxt = look_up(t + 32 + lane);
-    const int page = __shfl_sync(0xffffffffu, cur.page, src);
-    const int sg = t < n ? __shfl_sync(0xffffffffu, cur.seg, src) : -1;
-    const int j = __shfl_sync(0xffffffffu, cur.j, src);
-    if (sg != seg) {
-      if (seg >= 0) end();
-      if (sg < 0) break;
-      if (t > 0) load_rows(sg, 0);
-      begin(sg);
+    if (src == 0) {
+      if (t > 0) cur = nxt;
+      bits = bits_of(cur);
+      if (t + 32 < n) nxt = look_up(t + 32 + lane);
     }
-    if (sg < 0) break;
-    const bool tail = (j + 1) * kKv8Page > pos;
-    if (tail && page >= 0) row(min(pos + a.m, (j + 1) * kKv8Page) - 1);
-    bool ok = mbar_wait(&bars[warp][t % D], (uint32_t)(t / D) & 1u, nullptr);
-    ok = __all_sync(0xffffffffu, ok) && page >= 0;
-    if (ok) {
-      uint8_t* blk = ring + (size_t)(t % D) * UB;
-      int ke = kv8_scale_exp(__shfl_sync(0xffffffffu, cur.ks, src));
-      int ve = kv8_scale_exp(__shfl_sync(0xffffffffu, cur.vs, src));
-      if (tail) append(blk, page, j, ke, ve);
+    const int sg = t < n ? __shfl_sync(0xffffffffu, cur.seg, src) : -1;
+    if (sg != seg && sg != -2) {
+      if (seg >= 0) end();
+      if (sg >= 0) begin(sg);
+    }
+    if (t >= n) break;
+    const int j = __shfl_sync(0xffffffffu, cur.j, src);   // a unit that is none has no pages either
+    const uint32_t exps = __shfl_sync(0xffffffffu, bits.exps, src);
+    const uint32_t there = __shfl_sync(0xffffffffu, bits.there, src);
+    uint8_t* blk = ring + slot * UB;
+    const bool ok = mbar_wait(&bars[warp][slot], phase, nullptr);
+    if (__all_sync(0xffffffffu, ok) && there) {
+      int ke[kDecPages] = {(int)(exps & 0xff) - 64, (int)(exps >> 16 & 0xff) - 64};
+      int ve[kDecPages] = {(int)(exps >> 8 & 0xff) - 64, (int)(exps >> 24) - 64};
+      const bool tail = (j + kDecPages) * kKv8Page > pos || there != 3;
+      if (tail) {
+#pragma unroll 1
+        for (int i = 0; i < kDecPages; ++i) {
+          const int page = __shfl_sync(0xffffffffu, i ? cur.page[1] : cur.page[0], src);
+          if (page < 0) {           // no such page: weights 0, and values that are numbers
+#pragma unroll 1
+            for (int k = lane; k < HD; k += 32)
+              *reinterpret_cast<uint4*>(blk + i * PB + kKv8Page * HD + 16 * k) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+          } else if ((j + i + 1) * kKv8Page > pos) {
+            int k2 = i ? ke[1] : ke[0], v2 = i ? ve[1] : ve[0];
+            append(blk + i * PB, page, j + i, k2, v2);
+            if (i) ke[1] = k2, ve[1] = v2;
+            else ke[0] = k2, ve[0] = v2;
+          }
+        }
+        __syncwarp();
+      }
 
-      // S = Q K^T for the page's two groups of 8 keys
-      float s[2][4];
+      // S = Q K^T: each page's two groups of 8 keys
+      float s[2 * kDecPages][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int q = 0; q < 2 * kDecPages; ++q) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
-        const int key = h * 8 + r;
+        for (int e = 0; e < 4; ++e) s[q][e] = 0.f;
+        const uint8_t* xk = blk + q / 2 * PB;
+        const int key = q % 2 * 8 + r;
         uint32_t w[KS];
         if (HD == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(blk + unit_off<HD>(key, 2 * c));
-          const uint4 y = *reinterpret_cast<const uint4*>(blk + unit_off<HD>(key, 2 * c + 1));
+          const uint4 x = *reinterpret_cast<const uint4*>(xk + unit_off<HD>(key, 2 * c));
+          const uint4 y = *reinterpret_cast<const uint4*>(xk + unit_off<HD>(key, 2 * c + 1));
           w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
           w[KS - 4] = y.x; w[KS - 3] = y.y; w[KS - 2] = y.z; w[KS - 1] = y.w;
         } else {
-          const uint4 x = *reinterpret_cast<const uint4*>(blk + unit_off<HD>(key, c));
+          const uint4 x = *reinterpret_cast<const uint4*>(xk + unit_off<HD>(key, c));
           w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          mma_f16(s[h], qa[k], f16x2_of_e4m3((uint16_t)w[k]), f16x2_of_e4m3((uint16_t)(w[k] >> 16)));
+          mma_f16(s[q], qa[k], f16x2_of_e4m3((uint16_t)w[k]), f16x2_of_e4m3((uint16_t)(w[k] >> 16)));
       }
-      const float f = qf * pow2f(ke);
-      float p[4] = {(s[0][0] + s[0][2]) * f, (s[0][1] + s[0][3]) * f, (s[1][0] + s[1][2]) * f,
-                    (s[1][1] + s[1][3]) * f};
-      if (tail) {
-        const int lim = pos + r / G - j * kKv8Page;
+      float p[4 * kDecPages];          // page i, keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if ((e >> 1) * 8 + 2 * c + (e & 1) > lim) p[e] = -INFINITY;
+      for (int i = 0; i < kDecPages; ++i) {
+        const float f = qf * pow2f(ke[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[4 * i + e] = (s[2 * i + e / 2][e & 1] + s[2 * i + e / 2][2 + (e & 1)]) * f;
       }
-      float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+      if (tail) {
+        const int lim = pos + rt - j * kKv8Page;
+#pragma unroll
+        for (int e = 0; e < 4 * kDecPages; ++e)
+          if (e / 2 * 8 + 2 * c + (e & 1) > lim || !(there >> (e / 4) & 1)) p[e] = -INFINITY;
+      }
+      float mx = p[0];
+#pragma unroll
+      for (int e = 1; e < 4 * kDecPages; ++e) mx = fmaxf(mx, p[e]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(st.m, mx);
-      const int En = max(st.E, ve);
-      if (__any_sync(0xffffffffu, mn > st.m) || En > st.E) {
-        const float x = mn == -INFINITY ? 1.f : ex2(st.m - mn), y = x * pow2f(st.E - En);
+      const int E0 = max(st.E, ve[0]);
+      if (__any_sync(0xffffffffu, mx > st.m + (float)kDecLag) || E0 > st.E) {
+        const float mn = fmaxf(st.m, mx);
+        const float x = mn == -INFINITY ? 1.f : ex2(st.m - mn), y = x * pow2f(st.E - E0);
         st.l *= x;
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) st.o[q][e] *= y;
         st.m = mn;
-        st.E = En;
+        st.E = E0;
       }
-      // weights times 2^14 and the block's scale over 2^E: at most 2^14, a pair
-      // of f16 then is good to 2^-22 of each and 2^-39 of the largest
-      const float sub = (mn == -INFINITY ? 0.f : mn) - (float)(14 + ve - En);
+      // weights times 2^kDecBias and the block's scale over 2^E: at most 2^14,
+      // at least 2^6 for the largest; a pair of f16 then is good to 2^-22 of
+      // each and 2^-31 of the largest
+      const float ref = st.m == -INFINITY ? 0.f : st.m;
+      const int E1 = max(E0, ve[1]);
+      uint32_t pa[kDecPages][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = ex2(p[e] - sub);
-      st.l += ((p[0] + p[1]) + (p[2] + p[3])) * pow2f(En - ve - 14);
-      uint32_t pa[4];
-      split2(p[0], p[1], pa[0], pa[1]);
-      split2(p[2], p[3], pa[2], pa[3]);
+      for (int i = 0; i < kDecPages; ++i) {
+        const int up = kDecBias + ve[i] - (i ? E1 : E0);
+        const float sub = ref - (float)up;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[4 * i + e] = ex2(p[4 * i + e] - sub);
+        st.l += ((p[4 * i] + p[4 * i + 1]) + (p[4 * i + 2] + p[4 * i + 3])) * pow2f(-up);
+        split2(p[4 * i], p[4 * i + 1], pa[i][0], pa[i][1]);
+        split2(p[4 * i + 2], p[4 * i + 3], pa[i][2], pa[i][3]);
+      }
 
       // O += P V
-      const uint8_t* xv = blk + kKv8Page * HD;
-      uint32_t v[4][HD / 32];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = (e >> 1) * 8 + 2 * c + (e & 1);
-        if (HD == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(xv + unit_off<HD>(key, r));
-          v[e][0] = x.x; v[e][1] = x.y; v[e][HD / 32 - 2] = x.z; v[e][HD / 32 - 1] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(xv + unit_off<HD>(key, r >> 1) + (r & 1) * 8);
-          v[e][0] = x.x; v[e][1] = x.y;
+      for (int i = 0; i < kDecPages; ++i) {
+        // page by page: rows that do not see the second one's larger values
+        // keep all bits of theirs
+        if (i && E1 > E0) {
+          const float y = pow2f(E0 - E1);
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[q][e] *= y;
+          st.E = E1;
         }
-      }
+        const uint8_t* xv = blk + i * PB + kKv8Page * HD;
+        uint32_t v[4][HD / 32];
 #pragma unroll
-      for (int k = 0; k < HD / 32; ++k) {
-        const uint32_t a01 = __byte_perm(v[0][k], v[1][k], 0x5140), a23 = __byte_perm(v[0][k], v[1][k], 0x7362);
-        const uint32_t b01 = __byte_perm(v[2][k], v[3][k], 0x5140), b23 = __byte_perm(v[2][k], v[3][k], 0x7362);
-        mma_f16(st.o[4 * k], pa, f16x2_of_e4m3((uint16_t)a01), f16x2_of_e4m3((uint16_t)b01));
-        mma_f16(st.o[4 * k + 1], pa, f16x2_of_e4m3((uint16_t)(a01 >> 16)), f16x2_of_e4m3((uint16_t)(b01 >> 16)));
-        mma_f16(st.o[4 * k + 2], pa, f16x2_of_e4m3((uint16_t)a23), f16x2_of_e4m3((uint16_t)b23));
-        mma_f16(st.o[4 * k + 3], pa, f16x2_of_e4m3((uint16_t)(a23 >> 16)), f16x2_of_e4m3((uint16_t)(b23 >> 16)));
+        for (int e = 0; e < 4; ++e) {
+          const int key = (e >> 1) * 8 + 2 * c + (e & 1);
+          if (HD == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(xv + unit_off<HD>(key, r));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][HD / 32 - 2] = x.z; v[e][HD / 32 - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(xv + unit_off<HD>(key, r >> 1) + (r & 1) * 8);
+            v[e][0] = x.x; v[e][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) {
+          const uint32_t a01 = __byte_perm(v[0][k], v[1][k], 0x5140), a23 = __byte_perm(v[0][k], v[1][k], 0x7362);
+          const uint32_t b01 = __byte_perm(v[2][k], v[3][k], 0x5140), b23 = __byte_perm(v[2][k], v[3][k], 0x7362);
+          mma_f16(st.o[4 * k], pa[i], f16x2_of_e4m3((uint16_t)a01), f16x2_of_e4m3((uint16_t)b01));
+          mma_f16(st.o[4 * k + 1], pa[i], f16x2_of_e4m3((uint16_t)(a01 >> 16)), f16x2_of_e4m3((uint16_t)(b01 >> 16)));
+          mma_f16(st.o[4 * k + 2], pa[i], f16x2_of_e4m3((uint16_t)a23), f16x2_of_e4m3((uint16_t)b23));
+          mma_f16(st.o[4 * k + 3], pa[i], f16x2_of_e4m3((uint16_t)(a23 >> 16)), f16x2_of_e4m3((uint16_t)(b23 >> 16)));
+        }
       }
     }
     __syncwarp();
     // the slot is free: the unit D further on
-    const int ti = t + D;
-    if (ti < n && lane == (ti & 31)) issue((ti >> 5) == (t >> 5) ? cur : nxt, ti);
+    if (t + D < n && lane == ((t + D) & 31)) issue(src + D < 32 ? cur : nxt, slot);
+    if (++slot == D) {
+      slot = 0;
+      phase ^= 1;
+    }
   }
+  join();
 }
 
 int num_sms() {
@@ -711,43 +820,49 @@ int num_sms() {
   return n > 0 ? n : 1;
 }
 
-DecLayout dec_layout(int B, int R, int Hkv, int hd) {
+DecLayout dec_layout(int B, int m, int H, int Hkv, int hd) {
   DecLayout l;
+  const int G = H / Hkv, R = m * G;
   l.ctas = num_sms();
   l.groups = (Hkv + kDecWarps - 1) / kDecWarps;
   l.heads = (Hkv + l.groups - 1) / l.groups;
   l.slices = kDecWarps / l.heads;
   l.slot_floats = R * hd + 2 * R + (2 * R) % 4;
-  const int warps = l.heads * l.slices, q = warps * R * hd * 4, unit = 2 * kKv8Page * hd;
-  const int room = kDecSmem - 1024 - 2048 - q - (2 * B + 1) * 4;   // alignment, static
-  l.depth = room / (warps * unit);
+  l.inv_g = 65536 / G + 1;
+  l.buf = (R > 512 / hd ? R : 512 / hd) * hd * 4;    // four rows of 128 (eight of 64) at a time in ``begin``
+  const int warps = l.heads * l.slices, unit = kDecPages * 2 * kKv8Page * hd;
+  const int room = kDecSmem - 1024 - 2048 - warps * l.buf - (2 * B + 1) * 4;   // alignment, static
+  // 128 KB in flight per SM fill the memory; more only lengthens its queue
+  l.depth = (room < kDecFlight ? room : kDecFlight) / (warps * unit);
   if (l.depth > kDecMaxDepth) l.depth = kDecMaxDepth;
-  l.q_off = warps * l.depth * unit;
-  l.meta_off = l.q_off + q;
-  l.vec = 0;
+  l.buf_off = warps * l.depth * unit;
+  l.meta_off = l.buf_off + warps * l.buf;
   return l;
 }
 
 }  // namespace
 
 size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd) {
-  const DecLayout l = dec_layout(B, m * (H / Hkv), Hkv, hd);
+  const DecLayout l = dec_layout(B, m, H, Hkv, hd);
   return (size_t)l.ctas * l.slices * 2 * l.heads * (2 + l.slot_floats) * 4;
 }
 
 cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {
   CUtensorMap map;
   if (!tma_map_kv8(&map, a.kv, a.n_pages, a.Hkv, a.hd)) return cudaErrorNotSupported;
-  DecLayout l = dec_layout(a.B, a.m * (a.H / a.Hkv), a.Hkv, a.hd);
+  DecLayout l = dec_layout(a.B, a.m, a.H, a.Hkv, a.hd);
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.qkv) | reinterpret_cast<uintptr_t>(a.q_gain) |
                        reinterpret_cast<uintptr_t>(a.rope_cos) | reinterpret_cast<uintptr_t>(a.rope_sin);
-  l.vec = (at & 15) == 0 && a.qkv_ld % 4 == 0;
-  auto k = a.hd == 128 ? kv8_decode_kernel<128> : kv8_decode_kernel<64>;
-  static bool attr[2] = {false, false};
-  if (!attr[a.hd == 128]) {
+  const bool vec = (at & 15) == 0 && a.qkv_ld % 4 == 0;
+  l.o_vec = a.o ? a.o_ld % 4 == 0 && !(reinterpret_cast<uintptr_t>(a.o) & 15)
+                : a.o_ld % 4 == 0 && !(reinterpret_cast<uintptr_t>(a.o16) & 7);
+  auto k = a.hd == 128 ? (vec ? kv8_decode_kernel<128, true> : kv8_decode_kernel<128, false>)
+                       : (vec ? kv8_decode_kernel<64, true> : kv8_decode_kernel<64, false>);
+  static bool attr[4] = {};
+  if (!attr[(a.hd == 128) * 2 + vec]) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem - 2048);
     if (e != cudaSuccess) return e;
-    attr[a.hd == 128] = true;
+    attr[(a.hd == 128) * 2 + vec] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(l.ctas);
