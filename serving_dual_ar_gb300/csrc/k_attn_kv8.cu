@@ -2,6 +2,8 @@
 // new rows, attention of all rows of a (sequence, kv head), one launch.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv8_common.cuh"
 #include "tc_common.cuh"
 #include "tma_map.h"
@@ -15,10 +17,10 @@ constexpr int kDecMaxDepth = 8;
 constexpr int kDecSmem = 227 * 1024;
 constexpr int kDecFlight = 128 * 1024;
 constexpr int kDecPages = 2;       // pages of a unit of work
-// Units of a run at least: a cut costs a joining, about as long as two units.
-constexpr int kDecMinUnits = 2;
+// Units of a run at least: a cut costs a joining, about as long as four units.
+constexpr int kDecMinUnits = 4;
 // What starting and ending a sequence costs, in units: the cut counts it.
-constexpr int kDecSeqUnits = 1;
+constexpr int kDecSeqUnits = 2;
 // Pieces that are joined at once, one per lane; more are joined in two levels
 // of about the square root each.
 constexpr int kDecFlat = 32;
@@ -473,81 +475,87 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
         if (lane == 0) *ticket = 0u;
         const bool done = per >= n;
         float* slot = done ? nullptr : parts + at(i0) * lay.slot_floats;
-        // piece q's maxima and sums in lane q, its weight for row i in w[i]
-        float w[kKv8MaxRows], inv[kKv8MaxRows];
-        const float* ml = parts + at(i0 + min(lane, count - 1) * step) * lay.slot_floats + R * HD;
+        // 128 values a step (a row of 128, two of 64); all steps of four pieces,
+        // and of eight if there are few rows, in flight at once, the first ones
+        // together with the maxima: a round trip is half a microsecond
+        auto gather = [&](auto steps, auto batch) {
+          constexpr int ST = decltype(steps)::value, Q = decltype(batch)::value, RPS = 128 / HD, NR = ST * RPS;
+          const int row = 4 * lane / HD;             // row within a step
+          float4 x[Q][ST], o[ST];
+          auto load = [&](int q0) {
 #pragma unroll
-        for (int i = 0; i < kKv8MaxRows; ++i) {
-          float2 v = make_float2(-INFINITY, 0.f);
-          if (i < R && lane < count) v = __ldcg(reinterpret_cast<const float2*>(ml + 2 * i));
-          w[i] = v.x;
-          inv[i] = v.y;
-        }
-        float m[kKv8MaxRows];
+            for (int q = 0; q < Q; ++q) {
+              const float* v = parts + at(i0 + min(q0 + q, count - 1) * step) * lay.slot_floats + 4 * lane;
 #pragma unroll
-        for (int i = 0; i < kKv8MaxRows; ++i) m[i] = w[i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < kKv8MaxRows; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
-#pragma unroll
-        for (int i = 0; i < kKv8MaxRows; ++i) {
-          // no keys: nothing; NaN stays
-          w[i] = w[i] == -INFINITY ? (inv[i] == inv[i] ? 0.f : inv[i]) : ex2(w[i] - m[i]);
-          inv[i] *= w[i];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < kKv8MaxRows; ++i) inv[i] += __shfl_xor_sync(0xffffffffu, inv[i], o);
-#pragma unroll
-        for (int i = 0; i < kKv8MaxRows; ++i) {
-          if (slot && lane == 0 && i < R) *reinterpret_cast<float2*>(slot + R * HD + 2 * i) = make_float2(m[i], inv[i]);
-          inv[i] = !done ? 1.f : inv[i] == 0.f ? 0.f : 1.f / inv[i];
-        }
-        // 128 values a step (a row of 128, two of 64), all steps of four pieces
-        // in flight at once: a round trip is half a microsecond
-        constexpr int RPS = 128 / HD, ST = kKv8MaxRows / RPS, Q = 4;
-        float4 o[ST];
-#pragma unroll
-        for (int i = 0; i < ST; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int row = 4 * lane / HD;               // row within a step
-#pragma unroll 1
-        for (int q0 = 0; q0 < count; q0 += Q) {
-          float4 x[Q][ST];
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const float* v = parts + at(i0 + min(q0 + q, count - 1) * step) * lay.slot_floats + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < ST; ++i) {
-              x[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (q0 + q < count && i * RPS + row < R) x[q][i] = __ldcg(reinterpret_cast<const float4*>(v + i * 128));
+              for (int i = 0; i < ST; ++i) {
+                x[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q0 + q < count && i * RPS + row < R) x[q][i] = __ldcg(reinterpret_cast<const float4*>(v + i * 128));
+              }
             }
+          };
+          // piece q's maxima and sums in lane q, its weight for row i in w[i]
+          float w[NR], inv[NR], m[NR];
+          const float* ml = parts + at(i0 + min(lane, count - 1) * step) * lay.slot_floats + R * HD;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            float2 v = make_float2(-INFINITY, 0.f);
+            if (i < R && lane < count) v = __ldcg(reinterpret_cast<const float2*>(ml + 2 * i));
+            m[i] = w[i] = v.x;
+            inv[i] = v.y;
+          }
+          load(0);
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1)
+#pragma unroll
+            for (int i = 0; i < NR; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], k));
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            // no keys: nothing; NaN stays
+            w[i] = w[i] == -INFINITY ? (inv[i] == inv[i] ? 0.f : inv[i]) : ex2(w[i] - m[i]);
+            inv[i] *= w[i];
           }
 #pragma unroll
-          for (int q = 0; q < Q; ++q)
+          for (int k = 16; k > 0; k >>= 1)
 #pragma unroll
-            for (int i = 0; i < ST; ++i) {
-              float y = __shfl_sync(0xffffffffu, w[i * RPS], (q0 + q) & 31);
-              if (RPS == 2) {
-                const float y2 = __shfl_sync(0xffffffffu, w[i * RPS + RPS - 1], (q0 + q) & 31);
-                y = row ? y2 : y;
+            for (int i = 0; i < NR; ++i) inv[i] += __shfl_xor_sync(0xffffffffu, inv[i], k);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            if (slot && lane == 0 && i < R) *reinterpret_cast<float2*>(slot + R * HD + 2 * i) = make_float2(m[i], inv[i]);
+            inv[i] = !done ? 1.f : inv[i] == 0.f ? 0.f : 1.f / inv[i];
+          }
+#pragma unroll
+          for (int i = 0; i < ST; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int q0 = 0;;) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+              for (int i = 0; i < ST; ++i) {
+                float y = __shfl_sync(0xffffffffu, w[i * RPS], (q0 + q) & 31);
+                if (RPS == 2) {
+                  const float y2 = __shfl_sync(0xffffffffu, w[i * RPS + RPS - 1], (q0 + q) & 31);
+                  y = row ? y2 : y;
+                }
+                o[i].x += x[q][i].x * y;
+                o[i].y += x[q][i].y * y;
+                o[i].z += x[q][i].z * y;
+                o[i].w += x[q][i].w * y;
               }
-              o[i].x += x[q][i].x * y;
-              o[i].y += x[q][i].y * y;
-              o[i].z += x[q][i].z * y;
-              o[i].w += x[q][i].w * y;
-            }
-        }
+            q0 += Q;
+            if (q0 >= count) break;
+            load(q0);
+          }
+          __syncwarp();      // all lanes have read the slot that is written below
 #pragma unroll
-        for (int i = 0; i < ST; ++i) {
-          const float y = row ? inv[i * RPS + RPS - 1] : inv[i * RPS];
-          o[i] = make_float4(o[i].x * y, o[i].y * y, o[i].z * y, o[i].w * y);
-        }
-        __syncwarp();        // all lanes have read the slot that is written now
-#pragma unroll
-        for (int i = 0; i < ST; ++i)
-          if (i * RPS + row < R) *reinterpret_cast<float4*>(buf + i * 128 + 4 * lane) = o[i];
+          for (int i = 0; i < ST; ++i) {
+            const float y = row ? inv[i * RPS + RPS - 1] : inv[i * RPS];
+            if (i * RPS + row < R)
+              *reinterpret_cast<float4*>(buf + i * 128 + 4 * lane) =
+                  make_float4(o[i].x * y, o[i].y * y, o[i].z * y, o[i].w * y);
+          }
+        };
+        if (R * HD <= 512) gather(std::integral_constant<int, 4>(), std::integral_constant<int, 8>());
+        else gather(std::integral_constant<int, 8 * HD / 128>(), std::integral_constant<int, 4>());
         __syncwarp();
 #pragma unroll 1
         for (int q = 4 * lane; q < R * HD; q += 128)
