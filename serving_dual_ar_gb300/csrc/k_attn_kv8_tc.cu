@@ -1,0 +1,620 @@
+// Prompt attention over the 8-bit KV cache on tcgen05: ragged prompts behind
+// cached pages, grouped queries, causal.
+#include "kv8_common.cuh"
+#include "tc_common.cuh"
+
+namespace s2 {
+
+namespace {
+
+constexpr int kPreRows = 128;                 // rows of a query tile; two tiles a CTA
+constexpr int kPreKeys = 128;                 // keys of a step
+constexpr int kPrePages = kPreKeys / kKv8Page;
+constexpr int kPreThreads = 13 * 32;          // softmax 2 x 4 warps, converters 4, MMA 1
+constexpr int kPreSmem = 227 * 1024;
+constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
+// Weights carry 2^kPreBias; the running maximum may lag by kPreLag.
+constexpr int kPreBias = 6, kPreLag = 8;
+// Binades below its step's largest scale from which on a page's values are added
+// apart: until there 2^-9 of the scale, e4m3's least, is an f16 value.
+constexpr int kPreSmall = 14;
+constexpr int kPreStepBytes = 4;              // what is kept of each step
+
+template <int HD, int PLANES>
+struct PreLayout {
+  static constexpr int kTile = 128 * HD * 2;                  // bytes of 128 rows in f16
+  static constexpr int kStages = PLANES == 1 ? 2 : 1;
+  static constexpr int kQ = 0;                                // [tile][plane]
+  static constexpr int kK = kQ + 2 * PLANES * kTile;          // [stage]
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kMeta = kV + kStages * kTile;
+};
+
+// ---------------------------------------------------------------- tcgen05 pieces
+
+// kind::f16 with f16 A and B, fp32 D; B is K-major, or MN-major if b_mn.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// MN-major operand in the 128-byte swizzled layout: rows (k) of 128 bytes (64
+// values along MN) in 8-row atoms; the next 64 values along MN lie ``block``
+// bytes on.
+S2_DEV uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+S2_DEV void umma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum) : "memory");
+}
+S2_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+S2_DEV float ex2p(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One page's keys into a row's output by fp32 arithmetic: the 16 weights of the
+// row, the page's values x ``by``, the row in tensor memory.  For pages whose
+// values are so small next to others of their step that they would not survive
+// as f16 relative to the step's scale; a row may see those and not the others.
+struct PageWeights {
+  float p[kKv8Page];
+};
+template <int HD>
+__device__ __noinline__ void add_small_page(uint32_t t_row, const PageWeights w, const uint8_t* v, float by) {
+#pragma unroll 1
+  for (int c = 0; c < HD; c += 8) {
+    float o[8];
+    tmem_ld8(t_row + c, o);
+#pragma unroll
+    for (int k = 0; k < kKv8Page; ++k) {
+      const uint2 x = *reinterpret_cast<const uint2*>(v + k * HD + c);
+      const float p = w.p[k] * by;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t h = f16x2_of_e4m3((uint16_t)((e < 2 ? x.x : x.y) >> (e & 1) * 16));
+        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+        o[2 * e] += f.x == f.x ? p * f.x : 0.f;           // NaN: see nan_s
+        o[2 * e + 1] += f.y == f.y ? p * f.y : 0.f;
+      }
+    }
+    tmem_st8(t_row + c, o);
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// One CTA: one kv head, two tiles of 128 / G tokens x the head's G query heads,
+// every key up to its last token in steps of 128.
+//   warps 0..7   prologue: the tiles' queries (norm, RoPE, f16) to shared
+//                memory; then one row per thread: maximum, weights, row sum
+//   warps 8..11  e4m3 keys and values to f16 (exactly; the pages' scales
+//                relative to the step's largest), in the swizzled layout
+//   warp 12      S = Q K^T and O += P V, issued by one thread
+// S and P share tensor memory (P is written over S as f16, and is the A operand
+// from there), O stays in it; V is read as [key][dim], MN-major, so nothing is
+// transposed.  While one tile's softmax runs, the other tile's products do.
+// PLANES = 2 (fp32 output): Q and P as f16 pairs hi + lo, twice the products.
+template <int HD, int PLANES>
+__global__ void __launch_bounds__(kPreThreads, 1)
+kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
+  using L = PreLayout<HD, PLANES>;
+  constexpr int ST = L::kStages, kBlock = 128 * 128;   // a 64-dim block: 128 rows x 128 bytes
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  __shared__ uint32_t tmem_s;
+  __shared__ float qf_s[2 * kPreRows];
+  __shared__ int nan_s[HD];
+  __shared__ int nan_any;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.H / a.Hkv, TT = kPreRows / G;                       // tokens of a tile
+  const int g = blockIdx.y, slot = slots - 1 - (int)blockIdx.x;       // long rows first
+
+  // this CTA's sequence: the last b whose slots start at or before ``slot``
+  // (sequence b's start at row0[b] / (2 TT) + b)
+  __shared__ int seq_s;
+  if (warp == 0) {
+    int n = 0;
+    for (int b = lane; b < a.B; b += 32) n += (a.row0[b] / (2 * TT) + b <= slot) ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n) - 1;
+    if (lane == 0) seq_s = n;
+  }
+  if (tid == 0) {
+    mbar_init(&q_full, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 128);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 128);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    fence_mbar_init();
+    nan_any = 0;
+  }
+  for (int i = tid; i < HD; i += kPreThreads) nan_s[i] = 0x7fffffff;
+  __syncthreads();
+  const int b = seq_s;
+  if (b < 0) return;
+  const int r0 = a.row0[b], rows = min(a.row0[b + 1], a.T) - r0, pos0 = a.pos[b];
+  const int t0 = (slot - (r0 / (2 * TT) + b)) * 2 * TT;               // first token of tile 0
+  if (r0 < 0 || t0 < 0 || t0 >= rows) return;
+  const int nt = t0 + TT < rows ? 2 : 1;                              // tiles with tokens
+  if (pos0 < 0 || pos0 > a.max_pos - rows) {                          // left out: zeros
+    const int cols = G * HD, n = min(rows - t0, 2 * TT);
+    for (int i = tid; i < n * cols; i += kPreThreads) {
+      const size_t at = (size_t)(r0 + t0 + i / cols) * a.o_ld + (size_t)g * cols + i % cols;
+      if (a.o) a.o[at] = 0.f;
+      else a.o16[at] = __float2bfloat16_rn(0.f);
+    }
+    return;
+  }
+  const int keys = pos0 + min(rows, t0 + nt * TT);                    // keys that the last token sees
+  const int steps = (keys + kPreKeys - 1) / kPreKeys;
+  const int* table = a.table + (size_t)b * a.table_ld;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&tmem_s)), "n"(kPreTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // queries (the rows that the append before this kernel reads too)
+  if (warp < 8) {
+    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 4;               // lanes per row, rows per load, loads at a time
+    const int tile = warp / 4, l = lane % LPR, d = 4 * l;
+    const float sg = l < LPR / 2 ? -1.f : 1.f;
+    float gain[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gain[e] = a.q_gain[d + e];
+    uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
+#pragma unroll 1
+    for (int i0 = warp % 4 * 32; i0 < warp % 4 * 32 + 32; i0 += NB * RPS) {
+      float x[NB][4], co[NB][4], si[NB][4], ss[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = i0 + k * RPS + lane / LPR, tt = i / G, t = t0 + tile * TT + tt;
+        const bool on = tt < TT && t < rows;
+        const float* q = a.qkv + (size_t)(r0 + (on ? t : t0)) * a.qkv_ld + (size_t)(g * G + i % G) * HD + d;
+        const size_t turn = (size_t)(pos0 + (on ? t : t0)) * (HD / 2) + d % (HD / 2);
+        ss[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[k][e] = on ? q[e] : 0.f;
+          co[k][e] = a.rope_cos[turn + e];
+          si[k][e] = a.rope_sin[turn + e];
+          ss[k] += x[k][e] * x[k][e];
+        }
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        // log2(e) / sqrt(HD): the softmax runs on powers of two
+        const float f = rsqrtf(ss[k] * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = x[k][e] * (f * gain[e]);
+          const float w = __shfl_xor_sync(0xffffffffu, y, LPR / 2) * sg;
+          x[k][e] = y * co[k][e] + w * si[k][e];
+          mx = fmaxf(mx, fabsf(x[k][e]));
+        }
+        ss[k] = mx;
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < NB; ++k) ss[k] = fmaxf(ss[k], __shfl_xor_sync(0xffffffffu, ss[k], o));
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int i = i0 + k * RPS + lane / LPR;
+        // the row's largest magnitude to 2^6 .. 2^7: products with e4m3 values
+        // stay far inside fp32, and a pair is good to 2^-31 of the largest
+        const int ex = min(max((int)(__float_as_uint(ss[k]) >> 23) - 127, -100), 100);
+        const float up = pow2f(6 - ex);
+        if (l == 0) qf_s[tile * kPreRows + i] = pow2f(ex - 6);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float u = x[k][2 * e] * up, v = x[k][2 * e + 1] * up;
+          const __half2 h = __floats2half2_rn(u, v);
+          const float2 hf = __half22float2(h);
+          const __half2 r = __floats2half2_rn(u - hf.x, v - hf.y);
+          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+          lo[e] = *reinterpret_cast<const uint32_t*>(&r);
+        }
+        const uint32_t to = (d / 64) * kBlock + sw128_offset(i, d % 64 / 8) + (d & 4) * 2;
+        *reinterpret_cast<uint2*>(q_hi + to) = make_uint2(hi[0], hi[1]);
+        if (PLANES == 2) *reinterpret_cast<uint2*>(q_hi + L::kTile + to) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    fence_proxy_async();
+    mbar_arrive(&q_full);
+  }
+  pdl_launch_next();
+  pdl_wait();      // the new rows are in their pages
+
+  // per step: the largest scale exponents of its pages, which pages are there, and
+  // which have small values
+  int8_t* ek_s = reinterpret_cast<int8_t*>(sm + L::kMeta);
+  int8_t* ev_s = ek_s + steps;
+  uint8_t* there_s = reinterpret_cast<uint8_t*>(ev_s + steps);
+  uint8_t* small_s = there_s + steps;
+  {
+    const int pages = (keys + kKv8Page - 1) / kKv8Page;
+    for (int i0 = warp * 32; i0 < steps * kPrePages; i0 += kPreThreads) {
+      const int i = i0 + lane, page = i < pages ? table[i] : -1;
+      const bool in = page >= 0 && page < a.n_pages;
+      int ek = kKv8EMin, ev = kKv8EMin;
+      if (in) {
+        const float* s = a.scale + (size_t)page * 2 * a.Hkv + g;
+        ek = kv8_scale_exp(s[0]);
+        ev = kv8_scale_exp(s[a.Hkv]);
+      }
+      const int own = ev;
+#pragma unroll
+      for (int o = 1; o < kPrePages; o <<= 1) {
+        ek = max(ek, __shfl_xor_sync(0xffffffffu, ek, o));
+        ev = max(ev, __shfl_xor_sync(0xffffffffu, ev, o));
+      }
+      const unsigned there = __ballot_sync(0xffffffffu, in || i >= pages) >> (lane & 24) & 0xff;
+      const unsigned small = __ballot_sync(0xffffffffu, in && ev - own > kPreSmall) >> (lane & 24) & 0xff;
+      if ((lane & 7) == 0 && i < steps * kPrePages) {
+        small_s[i / kPrePages] = (uint8_t)small;
+        ek_s[i / kPrePages] = (int8_t)ek;
+        ev_s[i / kPrePages] = (int8_t)ev;
+        there_s[i / kPrePages] = (uint8_t)there;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  bool ok = true;
+
+  if (warp == 12) {
+    // ------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t i_qk = idesc_f16(kPreRows, kPreKeys, 0), i_pv = idesc_f16(kPreRows, HD, 1);
+      const uint32_t q_at = smem_u32(sm + L::kQ), k_at = smem_u32(sm + L::kK), v_at = smem_u32(sm + L::kV);
+      auto qk = [&](int t, int st) {
+        uint32_t acc = 0;
+#pragma unroll 1
+        for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            const uint32_t off = (ks / 4) * kBlock + (ks % 4) * 32;
+            umma_bf16(tmem + t * 128, smem_desc_sw128(q_at + (t * PLANES + p) * L::kTile + off),
+                      smem_desc_sw128(k_at + st * L::kTile + off), i_qk, acc);
+            acc = 1;
+          }
+        umma_commit(&s_full[t]);
+      };
+      auto pv = [&](int t, int st) {
+#pragma unroll 1
+        for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+          for (int ks = 0; ks < kPreKeys / 16; ++ks) {
+            umma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + p * 64 + ks * 8,
+                        smem_desc_mn(v_at + st * L::kTile + ks * 2048, kBlock), i_pv, 1);
+          }
+      };
+      ok = mbar_wait(&q_full, 0, nullptr) && ok;
+      ok = mbar_wait(&k_full[0], 0, nullptr) && ok;
+      tc_fence_after();
+      for (int t = 0; t < nt; ++t) qk(t, 0);
+      umma_commit(&k_empty[0]);
+#pragma unroll 1
+      for (int j = 0; j < steps; ++j) {
+        const int st = j % ST, sn = (j + 1) % ST;
+        ok = mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr) && ok;
+        for (int t = 0; t < nt; ++t) {
+          ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr) && ok;
+          tc_fence_after();
+          pv(t, st);
+          if (t == nt - 1) umma_commit(&v_empty[st]);
+          if (j + 1 < steps) {
+            if (t == 0) {
+              ok = mbar_wait(&k_full[sn], (uint32_t)((j + 1) / ST) & 1u, nullptr) && ok;
+              tc_fence_after();
+            }
+            qk(t, sn);
+            if (t == nt - 1) umma_commit(&k_empty[sn]);
+          } else {
+            umma_commit(&o_full[t]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------ e4m3 to f16
+    // lane (row = lane / 8 + 4 it, unit = lane % 8) moves 16 bytes of a key's
+    // row: 512 bytes in one piece per load (HD 64: lane / 4, 8 rows a load)
+    constexpr int U = HD / 16, RP = 32 / U, N = 32 / RP;    // units of a row, rows per load, loads of a warp's 32 keys
+    const int w = warp - 8, u = lane % U, rr = lane / U;
+    uint4 x[2][N];                                          // K, V of the step to come
+    auto load = [&](int kind, int j) {
+#pragma unroll
+      for (int it = 0; it < N; ++it) {
+        const int row = w * 32 + it * RP + rr, key = j * kPreKeys + row;
+        x[kind][it] = make_uint4(0, 0, 0, 0);
+        if (key < keys) {
+          const int page = table[key / kKv8Page];
+          if (page >= 0 && page < a.n_pages)
+            x[kind][it] = *reinterpret_cast<const uint4*>(
+                a.kv + ((((size_t)page * 2 + kind) * a.Hkv + g) * kKv8Page + key % kKv8Page) * HD + u * 16);
+        }
+      }
+    };
+    auto store = [&](int kind, int j, uint8_t* to) {
+      // the two pages of this warp's keys: scale over the step's largest one
+      __half2 by[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = j * kPrePages + w * 2 + i;
+        float f = 0.f;
+        if (at * kKv8Page < keys) {
+          const int page = table[at];
+          if (page >= 0 && page < a.n_pages) {
+            const int e = kv8_scale_exp(a.scale[((size_t)page * 2 + kind) * a.Hkv + g]);
+            f = kind && (small_s[j] >> (w * 2 + i) & 1) ? 0.f : pow2f(max(e - (kind ? ev_s[j] : ek_s[j]), -60));
+          }
+        }
+        by[i] = __float2half2_rn(f);
+      }
+#pragma unroll
+      for (int it = 0; it < N; ++it) {
+        const int row = w * 32 + it * RP + rr;
+        uint4 y = x[kind][it];
+        uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+        if (kind == 1) {
+          // a NaN must not reach rows that do not see it through 0 * NaN: it
+          // is left out here, and its first key noted for the epilogue
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((((yw[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u) {
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i)
+                if ((yw[e] >> (8 * i) & 0x7f) == 0x7f) {
+                  atomicMin(&nan_s[u * 16 + e * 4 + i], j * kPreKeys + row);
+                  nan_any = 1;
+                  yw[e] &= ~(0xffu << (8 * i));
+                }
+            }
+        }
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[2 * e] = f16x2_of_e4m3((uint16_t)yw[e]);
+          h[2 * e + 1] = f16x2_of_e4m3((uint16_t)(yw[e] >> 16));
+        }
+        const __half2 f = by[(it * RP + rr) / kKv8Page];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __half2 p = __hmul2(*reinterpret_cast<__half2*>(&h[e]), f);
+          h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        const uint4 first = make_uint4(h[0], h[1], h[2], h[3]), second = make_uint4(h[4], h[5], h[6], h[7]);
+        uint8_t* blk = to + (u / 4) * kBlock;
+        const int c = u % 4 * 2, odd = u / 4 & 1;           // the second block's lanes swap their stores: no bank twice
+        *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + odd)) = odd ? second : first;
+        *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + 1 - odd)) = odd ? first : second;
+      }
+    };
+    load(0, 0);
+    load(1, 0);
+#pragma unroll 1
+    for (int j = 0; j < steps; ++j) {
+      const int st = j % ST;
+      const uint32_t ph = ((uint32_t)(j / ST) & 1u) ^ 1u;
+      ok = mbar_wait(&k_empty[st], ph, nullptr) && ok;
+      store(0, j, sm + L::kK + st * L::kTile);
+      fence_proxy_async();
+      mbar_arrive(&k_full[st]);
+      if (j + 1 < steps) load(0, j + 1);
+      ok = mbar_wait(&v_empty[st], ph, nullptr) && ok;
+      store(1, j, sm + L::kV + st * L::kTile);
+      fence_proxy_async();
+      mbar_arrive(&v_full[st]);
+      if (j + 1 < steps) load(1, j + 1);
+    }
+  } else if (warp / 4 < nt) {
+    // ------------------------------------------------ softmax, a row per thread
+    const int tile = warp / 4, i = tid % kPreRows, tt = i / G, t = t0 + tile * TT + tt;
+    const bool on = tt < TT && t < rows;
+    const int lim = on ? pos0 + t : -1;                    // last key of this row
+    const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
+    const float qf = qf_s[tile * kPreRows + i];
+    float m = -INFINITY, l = 0.f;
+    int E = kKv8EMin;
+    {
+      const float zero[8] = {};
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 8) tmem_st8(to + c, zero);
+    }
+#pragma unroll 1
+    for (int j = 0; j < steps; ++j) {
+      const int k0 = j * kPreKeys, ev = ev_s[j];
+      const uint32_t there = there_s[j], small = small_s[j];
+      const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
+      const float f = qf * pow2f(ek_s[j]);
+      ok = mbar_wait(&s_full[tile], (uint32_t)j & 1u, nullptr) && ok;
+      tc_fence_after();
+      // keys of this row: bit e of word c of 32 keys
+      uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = min(max(lim - (k0 + 32 * c) + 1, 0), 32);
+          see[c] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+          if (!(there >> (2 * c) & 1)) see[c] &= 0xffff0000u;
+          if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float s[32];
+        tmem_ld32(ts + 32 * c, s);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, see[c] >> e & 1 ? s[e] : -INFINITY);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, s[e]);
+        }
+      }
+      mx *= f;
+      const int En = max(E, ev);
+      if (__any_sync(0xffffffffu, mx > m + (float)kPreLag) || En > E) {
+        const float mn = fmaxf(m, mx);
+        const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
+        l *= y;
+        if (j > 0) {         // the products before this step's S are complete
+          const float z = y * pow2f(E - En);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 8) {
+            float v[8];
+            tmem_ld8(to + c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= z;
+            tmem_st8(to + c, v);
+          }
+        }
+        m = mn;
+        E = En;
+      }
+      const int up = kPreBias + ev - E;
+      const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
+      float sum = 0.f;
+      uint32_t lo[2][16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float s[32];
+        tmem_ld32(ts + 32 * c, s);
+        if (PLANES == 2 && c == 2) {          // S of these columns is read: the low parts kept back go there
+          tmem_st16(ts + 64, lo[0]);
+          tmem_st16(ts + 80, lo[1]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e] = see[c] >> e & 1 ? ex2p(fmaf(s[e], f, -sub)) : 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e] = ex2p(fmaf(s[e], f, -sub));
+        }
+        if (small >> (2 * c) & 3) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (small >> (2 * c + q) & 1) {
+              PageWeights w;
+#pragma unroll
+              for (int e = 0; e < kKv8Page; ++e) w.p[e] = s[16 * q + e];
+              const size_t blk = ((size_t)table[j * kPrePages + 2 * c + q] * 2 + 1) * a.Hkv + g;
+              add_small_page<HD>(to, w, a.kv + blk * (kKv8Page * HD), pow2f(kv8_scale_exp(a.scale[blk]) - ev));
+            }
+        }
+        uint32_t hi[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          sum += s[2 * e] + s[2 * e + 1];
+          const __half2 h = __floats2half2_rn(s[2 * e], s[2 * e + 1]);
+          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+          if (PLANES == 2) {
+            const float2 hf = __half22float2(h);
+            const __half2 r = __floats2half2_rn(s[2 * e] - hf.x, s[2 * e + 1] - hf.y);
+            lo[c & 1][e] = *reinterpret_cast<const uint32_t*>(&r);
+          }
+        }
+        tmem_st16(ts + 16 * c, hi);
+        if (PLANES == 2 && c == 3) {
+          tmem_st16(ts + 96, lo[0]);
+          tmem_st16(ts + 112, lo[1]);
+        }
+      }
+      l += sum * pow2f(-up);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[tile]);
+    }
+    ok = mbar_wait(&o_full[tile], 0, nullptr) && ok;
+    tc_fence_after();
+    const float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
+    const size_t at = (size_t)(r0 + (on ? t : t0)) * a.o_ld + (size_t)(g * G + i % G) * HD;
+    const bool nans = nan_any != 0;
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 32) {
+      float y[32];
+      tmem_ld32(to + c, y);
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          y[e] *= inv;
+          if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
+          if (a.o) a.o[at + c + e] = y[e];
+          else a.o16[at + c + e] = __float2bfloat16_rn(y[e]);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kPreTmem) : "memory");
+  }
+}
+
+template <int HD, int PLANES>
+cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
+  auto k = kv8_prefill_kernel<HD, PLANES>;
+  static bool attr = false;
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 4096);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  const int TT = kPreRows / (a.H / a.Hkv), slots = a.T / (2 * TT) + a.B;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(slots, a.Hkv);
+  cfg.blockDim = dim3(kPreThreads);
+  cfg.dynamicSmemBytes = 1024 + PreLayout<HD, PLANES>::kMeta + kPreStepBytes * ((a.max_pos + kPreKeys - 1) / kPreKeys);
+  cfg.stream = st;
+  // runs its queries' part while the append before it ends
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return s2_launch(&cfg, k, a, slots);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_prefill(const Kv8Args& a, cudaStream_t st) {
+  if (a.hd == 128) return a.o ? launch<128, 2>(a, st) : launch<128, 1>(a, st);
+  return a.o ? launch<64, 2>(a, st) : launch<64, 1>(a, st);
+}
+
+}  // namespace s2

@@ -29,8 +29,9 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(Kv8Args a) {
   __shared__ float x[2][kKv8Page][HD];
   __shared__ float amax_s[2][4];
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_next();
+  // the wait first: the attention behind may read qkv as soon as it starts
   pdl_wait();
+  pdl_launch_next();
   const int b = a.row0 ? owner_of_slot(a.row0, a.B, kKv8Page, 2, blockIdx.x, lane) : (int)blockIdx.x / 2;
   if (b < 0) return;
   const int r0 = a.row0 ? a.row0[b] : b * a.m, pos0 = a.pos[b];

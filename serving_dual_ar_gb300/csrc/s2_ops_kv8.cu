@@ -102,9 +102,10 @@ extern "C" int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B,
     return S2_EINVAL;
   a.T = T;
   a.row0 = row0;
+  if (a.max_pos > kKv8MaxPrompt) a.max_pos = kKv8MaxPrompt;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_kv8_append(a, st);
-  return status(e == cudaSuccess ? launch_kv8_attn_simple(a, st) : e);
+  return status(e == cudaSuccess ? launch_kv8_prefill(a, st) : e);
 }
 
 static bool pack_ok(const void* kv, const void* kv8, const void* scale, const int32_t* src, const int32_t* dst,
