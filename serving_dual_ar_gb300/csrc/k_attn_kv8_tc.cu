@@ -30,6 +30,9 @@ struct PreLayout {
   static constexpr int kMeta = kV + kStages * kTile;
 };
 
+template <int PLANES> struct OutOf { using type = float; };
+template <> struct OutOf<1> { using type = __nv_bfloat16; };
+
 // ---------------------------------------------------------------- tcgen05 pieces
 
 // kind::f16 with f16 A and B, fp32 D; B is K-major, or MN-major if b_mn.
@@ -63,6 +66,38 @@ S2_DEV float ex2p(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+template <bool VEC>
+S2_DEV void load4(const float* p, float (&v)[4]) {
+  const float4 x = VEC ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = x.z;
+  v[3] = x.w;
+}
+
+// Two e4m3 bytes (the low ones of w) as f16x2 times f.
+S2_DEV uint32_t widen(uint32_t w, __half2 f) {
+  uint32_t h = f16x2_of_e4m3((uint16_t)w);
+  const __half2 p = __hmul2(*reinterpret_cast<__half2*>(&h), f);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// Nonzero if one of the four bytes is a NaN (0x7f or 0xff).
+S2_DEV uint32_t has_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// The bytes without their NaNs.  A NaN must not reach rows that do not see it
+// through 0 * NaN: it is left out of the products, and the first key that has
+// one in this dim noted for the epilogue.
+__device__ __noinline__ uint4 without_nan(uint4 y, int* first, int* any, int key) {
+  uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if ((w[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) {
+      atomicMin(first + i, key);
+      *any = 1;
+      w[i / 4] &= ~(0xffu << (8 * (i % 4)));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // One page's keys into a row's output by fp32 arithmetic: the 16 weights of the
@@ -107,9 +142,9 @@ __device__ __noinline__ void add_small_page(uint32_t t_row, const PageWeights w,
 // from there), O stays in it; V is read as [key][dim], MN-major, so nothing is
 // transposed.  While one tile's softmax runs, the other tile's products do.
 // PLANES = 2 (fp32 output): Q and P as f16 pairs hi + lo, twice the products.
-template <int HD, int PLANES>
+template <int HD, int PLANES, bool VEC>
 __global__ void __launch_bounds__(kPreThreads, 1)
-kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
+kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   using L = PreLayout<HD, PLANES>;
   constexpr int ST = L::kStages, kBlock = 128 * 128;   // a 64-dim block: 128 rows x 128 bytes
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -174,28 +209,33 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
 
   // queries (the rows that the append before this kernel reads too)
   if (warp < 8) {
-    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 4;               // lanes per row, rows per load, loads at a time
+    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 8 / RPS;         // lanes per row, rows per load, loads at a time
     const int tile = warp / 4, l = lane % LPR, d = 4 * l;
     const float sg = l < LPR / 2 ? -1.f : 1.f;
     float gain[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) gain[e] = a.q_gain[d + e];
+    load4<VEC>(a.q_gain + d, gain);
     uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
 #pragma unroll 1
     for (int i0 = warp % 4 * 32; i0 < warp % 4 * 32 + 32; i0 += NB * RPS) {
       float x[NB][4], co[NB][4], si[NB][4], ss[NB];
+      bool live[NB];
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const int i = i0 + k * RPS + lane / LPR, tt = i / G, t = t0 + tile * TT + tt;
         const bool on = tt < TT && t < rows;
         const float* q = a.qkv + (size_t)(r0 + (on ? t : t0)) * a.qkv_ld + (size_t)(g * G + i % G) * HD + d;
         const size_t turn = (size_t)(pos0 + (on ? t : t0)) * (HD / 2) + d % (HD / 2);
+        load4<VEC>(q, x[k]);
+        load4<VEC>(a.rope_cos + turn, co[k]);
+        load4<VEC>(a.rope_sin + turn, si[k]);
+        live[k] = on;
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
         ss[k] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[k][e] = on ? q[e] : 0.f;
-          co[k][e] = a.rope_cos[turn + e];
-          si[k][e] = a.rope_sin[turn + e];
+          x[k][e] = live[k] ? x[k][e] : 0.f;
           ss[k] += x[k][e] * x[k][e];
         }
       }
@@ -351,90 +391,89 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
     constexpr int U = HD / 16, RP = 32 / U, N = 32 / RP;    // units of a row, rows per load, loads of a warp's 32 keys
     const int w = warp - 8, u = lane % U, rr = lane / U;
     uint4 x[2][N];                                          // K, V of the step to come
-    auto load = [&](int kind, int j) {
-#pragma unroll
-      for (int it = 0; it < N; ++it) {
-        const int row = w * 32 + it * RP + rr, key = j * kPreKeys + row;
-        x[kind][it] = make_uint4(0, 0, 0, 0);
-        if (key < keys) {
-          const int page = table[key / kKv8Page];
-          if (page >= 0 && page < a.n_pages)
-            x[kind][it] = *reinterpret_cast<const uint4*>(
-                a.kv + ((((size_t)page * 2 + kind) * a.Hkv + g) * kKv8Page + key % kKv8Page) * HD + u * 16);
-        }
-      }
-    };
-    auto store = [&](int kind, int j, uint8_t* to) {
-      // the two pages of this warp's keys: scale over the step's largest one
-      __half2 by[2];
+    // this warp's two pages: ids two steps ahead of use, scales one, so that
+    // neither is waited for
+    int page[2], page_next[2];
+    float sc[2][2], sc_next[2][2];                          // [page][K, V]
+    auto load_ids = [&](int j, int (&p)[2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int at = j * kPrePages + w * 2 + i;
-        float f = 0.f;
-        if (at * kKv8Page < keys) {
-          const int page = table[at];
-          if (page >= 0 && page < a.n_pages) {
-            const int e = kv8_scale_exp(a.scale[((size_t)page * 2 + kind) * a.Hkv + g]);
-            f = kind && (small_s[j] >> (w * 2 + i) & 1) ? 0.f : pow2f(max(e - (kind ? ev_s[j] : ek_s[j]), -60));
-          }
-        }
-        by[i] = __float2half2_rn(f);
+        p[i] = at * kKv8Page < keys ? table[at] : -1;
+      }
+    };
+    auto load_scales = [&](int (&p)[2], float (&s)[2][2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (p[i] < 0 || p[i] >= a.n_pages) p[i] = -1;
+        const float* f = a.scale + (size_t)max(p[i], 0) * 2 * a.Hkv + g;
+        s[i][0] = f[0];
+        s[i][1] = f[a.Hkv];
+      }
+    };
+    auto load = [&](int kind, int j, const int (&p)[2]) {
+#pragma unroll
+      for (int it = 0; it < N; ++it) {
+        const int row = it * RP + rr, pg = p[row / kKv8Page];
+        x[kind][it] = make_uint4(0, 0, 0, 0);
+        if (pg >= 0 && j * kPreKeys + w * 32 + row < keys)
+          x[kind][it] = *reinterpret_cast<const uint4*>(
+              a.kv + ((((size_t)pg * 2 + kind) * a.Hkv + g) * kKv8Page + row % kKv8Page) * HD + u * 16);
+      }
+    };
+    auto store = [&](int kind, int j, uint8_t* to) {
+      // the pages' scales over the step's largest one
+      __half2 by[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = kv8_scale_exp(sc[i][kind]) - (kind ? ev_s[j] : ek_s[j]);
+        const bool none = page[i] < 0 || (kind && (small_s[j] >> (w * 2 + i) & 1));
+        by[i] = __float2half2_rn(none ? 0.f : pow2f(max(d, -60)));
       }
 #pragma unroll
       for (int it = 0; it < N; ++it) {
         const int row = w * 32 + it * RP + rr;
         uint4 y = x[kind][it];
-        uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-        if (kind == 1) {
-          // a NaN must not reach rows that do not see it through 0 * NaN: it
-          // is left out here, and its first key noted for the epilogue
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((((yw[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u) {
-#pragma unroll 1
-              for (int i = 0; i < 4; ++i)
-                if ((yw[e] >> (8 * i) & 0x7f) == 0x7f) {
-                  atomicMin(&nan_s[u * 16 + e * 4 + i], j * kPreKeys + row);
-                  nan_any = 1;
-                  yw[e] &= ~(0xffu << (8 * i));
-                }
-            }
-        }
-        uint32_t h[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[2 * e] = f16x2_of_e4m3((uint16_t)yw[e]);
-          h[2 * e + 1] = f16x2_of_e4m3((uint16_t)(yw[e] >> 16));
-        }
-        const __half2 f = by[(it * RP + rr) / kKv8Page];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __half2 p = __hmul2(*reinterpret_cast<__half2*>(&h[e]), f);
-          h[e] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        const uint4 first = make_uint4(h[0], h[1], h[2], h[3]), second = make_uint4(h[4], h[5], h[6], h[7]);
+        if (kind == 1 && (has_nan(y.x) | has_nan(y.y) | has_nan(y.z) | has_nan(y.w)))
+          y = without_nan(y, nan_s + u * 16, &nan_any, j * kPreKeys + row);
+        const __half2 f = by[it * RP / kKv8Page];
+        const uint4 first = make_uint4(widen(y.x, f), widen(y.x >> 16, f), widen(y.y, f), widen(y.y >> 16, f));
+        const uint4 second = make_uint4(widen(y.z, f), widen(y.z >> 16, f), widen(y.w, f), widen(y.w >> 16, f));
         uint8_t* blk = to + (u / 4) * kBlock;
         const int c = u % 4 * 2, odd = u / 4 & 1;           // the second block's lanes swap their stores: no bank twice
         *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + odd)) = odd ? second : first;
         *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + 1 - odd)) = odd ? first : second;
       }
     };
-    load(0, 0);
-    load(1, 0);
+    load_ids(0, page);
+    load_ids(1, page_next);
+    load_scales(page, sc);
+    load(0, 0, page);
+    load(1, 0, page);
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       const int st = j % ST;
       const uint32_t ph = ((uint32_t)(j / ST) & 1u) ^ 1u;
+      int page_2[2];
+      load_ids(j + 2, page_2);
+      load_scales(page_next, sc_next);
       ok = mbar_wait(&k_empty[st], ph, nullptr) && ok;
       store(0, j, sm + L::kK + st * L::kTile);
       fence_proxy_async();
       mbar_arrive(&k_full[st]);
-      if (j + 1 < steps) load(0, j + 1);
+      load(0, j + 1, page_next);
       ok = mbar_wait(&v_empty[st], ph, nullptr) && ok;
       store(1, j, sm + L::kV + st * L::kTile);
       fence_proxy_async();
       mbar_arrive(&v_full[st]);
-      if (j + 1 < steps) load(1, j + 1);
+      load(1, j + 1, page_next);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        page[i] = page_next[i];
+        page_next[i] = page_2[i];
+        sc[i][0] = sc_next[i][0];
+        sc[i][1] = sc_next[i][1];
+      }
     }
   } else if (warp / 4 < nt) {
     // ------------------------------------------------ softmax, a row per thread
@@ -560,22 +599,52 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
     ok = mbar_wait(&o_full[tile], 0, nullptr) && ok;
     tc_fence_after();
     const float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
-    const size_t at = (size_t)(r0 + (on ? t : t0)) * a.o_ld + (size_t)(g * G + i % G) * HD;
     const bool nans = nan_any != 0;
+    // rows by threads to rows by warps, over the tile's queries, which nothing
+    // reads any more: 16-byte units XORed with the row against bank conflicts
+    using T = typename OutOf<PLANES>::type;
+    constexpr int UE = 16 / sizeof(T), UR = HD / UE;        // values of a unit, units of a row
+    uint8_t* rows_s = sm + L::kQ + tile * PLANES * L::kTile + (size_t)(i & ~31) * HD * sizeof(T);
 #pragma unroll 1
     for (int c = 0; c < HD; c += 32) {
       float y[32];
       tmem_ld32(to + c, y);
-      if (on) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          y[e] *= inv;
-          if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
-          if (a.o) a.o[at + c + e] = y[e];
-          else a.o16[at + c + e] = __float2bfloat16_rn(y[e]);
+      for (int e = 0; e < 32; ++e) {
+        y[e] *= inv;
+        if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
+      }
+#pragma unroll
+      for (int q = 0; q < 32 / UE; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (UE == 4) {
+            w[e] = __float_as_uint(y[(4 * q + e) % 32]);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[(8 * q + 2 * e) % 32], y[(8 * q + 2 * e + 1) % 32]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        *reinterpret_cast<uint4*>(rows_s + (size_t)lane * HD * sizeof(T) + (((c / UE + q) ^ lane) % UR) * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+    T* out = reinterpret_cast<T*>(PLANES == 2 ? static_cast<void*>(a.o) : static_cast<void*>(a.o16));
+#pragma unroll 4
+    for (int k = 0; k < UR; ++k) {                          // 32 units a step: 32 / UR rows
+      const int row = (k * 32 + lane) / UR, q = lane % UR, ri = (i & ~31) + row, rt = ri / G;
+      const uint4 y = *reinterpret_cast<const uint4*>(rows_s + (size_t)row * HD * sizeof(T) + ((q ^ row) % UR) * 16);
+      if (rt < TT && t0 + tile * TT + rt < rows) {
+        T* p = out + (size_t)(r0 + t0 + tile * TT + rt) * a.o_ld + (size_t)(g * G + ri - rt * G) * HD + q * UE;
+        if (o_vec) {
+          *reinterpret_cast<uint4*>(p) = y;
+        } else {
+          const T* v = reinterpret_cast<const T*>(&y);
+#pragma unroll
+          for (int e = 0; e < UE; ++e) p[e] = v[e];
         }
       }
-      __syncwarp();
     }
   }
   tc_fence_before();
@@ -586,9 +655,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots) {
   }
 }
 
-template <int HD, int PLANES>
+template <int HD, int PLANES, bool VEC>
 cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
-  auto k = kv8_prefill_kernel<HD, PLANES>;
+  auto k = kv8_prefill_kernel<HD, PLANES, VEC>;
   static bool attr = false;
   if (!attr) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 4096);
@@ -596,10 +665,13 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
     attr = true;
   }
   const int TT = kPreRows / (a.H / a.Hkv), slots = a.T / (2 * TT) + a.B;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.o16);
+  const int o_vec = (o & 15) == 0 && a.o_ld % (PLANES == 2 ? 4 : 8) == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(slots, a.Hkv);
   cfg.blockDim = dim3(kPreThreads);
-  cfg.dynamicSmemBytes = 1024 + PreLayout<HD, PLANES>::kMeta + kPreStepBytes * ((a.max_pos + kPreKeys - 1) / kPreKeys);
+  cfg.dynamicSmemBytes =
+      1024 + PreLayout<HD, PLANES>::kMeta + kPreStepBytes * ((a.max_pos + kPreKeys - 1) / kPreKeys);
   cfg.stream = st;
   // runs its queries' part while the append before it ends
   cudaLaunchAttribute at[1];
@@ -607,7 +679,13 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return s2_launch(&cfg, k, a, slots);
+  return s2_launch(&cfg, k, a, slots, o_vec);
+}
+template <int HD, int PLANES>
+cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.qkv) | reinterpret_cast<uintptr_t>(a.q_gain) |
+                       reinterpret_cast<uintptr_t>(a.rope_cos) | reinterpret_cast<uintptr_t>(a.rope_sin);
+  return (at & 15) == 0 && a.qkv_ld % 4 == 0 ? launch<HD, PLANES, true>(a, st) : launch<HD, PLANES, false>(a, st);
 }
 
 }  // namespace

@@ -32,12 +32,11 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(Kv8Args a) {
   // the wait first: the attention behind may read qkv as soon as it starts
   pdl_wait();
   pdl_launch_next();
-  const int b = a.row0 ? owner_of_slot(a.row0, a.B, kKv8Page, 2, blockIdx.x, lane) : (int)blockIdx.x / 2;
+  const int b = owner_of_slot(a.row0, a.B, kKv8Page, 2, blockIdx.x, lane);
   if (b < 0) return;
-  const int r0 = a.row0 ? a.row0[b] : b * a.m, pos0 = a.pos[b];
-  const int n = a.row0 ? min(a.row0[b + 1], a.T) - r0 : a.m;
+  const int r0 = a.row0[b], n = min(a.row0[b + 1], a.T) - r0, pos0 = a.pos[b];
   if (r0 < 0 || n <= 0 || pos0 < 0 || pos0 > a.max_pos - n) return;
-  const int j = pos0 / kKv8Page + (int)blockIdx.x - ((a.row0 ? r0 / kKv8Page : 0) + 2 * b);
+  const int j = pos0 / kKv8Page + (int)blockIdx.x - (r0 / kKv8Page + 2 * b);
   const int first = max(pos0, j * kKv8Page), end = min(pos0 + n, (j + 1) * kKv8Page);
   if (first >= end) return;
   const int page = a.table[(size_t)b * a.table_ld + j];
@@ -85,81 +84,6 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(Kv8Args a) {
     }
     __syncthreads();   // every thread has read the scale
     if (tid == 0) a.scale[blk] = pow2f(e);
-  }
-}
-
-// ---------------------------------------------------------------- attention, one warp per row and head
-
-template <int HD>
-__global__ void __launch_bounds__(128) kv8_attn_simple_kernel(Kv8Args a) {
-  constexpr int N = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= a.H) return;
-  int b, i;
-  if (a.row0) {
-    b = owner_of_slot(a.row0, a.B, 1, 0, row, lane);
-    if (b < 0 || row >= a.row0[b + 1]) return;
-    i = row - a.row0[b];
-  } else {
-    b = row / a.m;
-    i = row % a.m;
-  }
-  const int n = a.row0 ? min(a.row0[b + 1], a.T) - a.row0[b] : a.m;
-  const int pos0 = a.pos[b], g = h / (a.H / a.Hkv);
-  const bool ok = pos0 >= 0 && pos0 <= a.max_pos - n && (!a.row0 || a.row0[b] >= 0);
-  const int p = pos0 + i;
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int c = 0; c < N; ++c) o[c] = 0.f;
-  if (ok) {
-    const float* x = a.qkv + (size_t)row * a.qkv_ld + (size_t)h * HD;
-    float ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      q[c] = x[lane + 32 * c];
-      ss += q[c] * q[c];
-    }
-    const float r = rsqrtf(warp_sum(ss) * (1.f / HD) + a.eps) * rsqrtf((float)HD);
-#pragma unroll
-    for (int c = 0; c < N; ++c) q[c] *= r * a.q_gain[lane + 32 * c];
-#pragma unroll
-    for (int c = 0; c < N / 2; ++c) {
-      const float cs = a.rope_cos[(size_t)p * (HD / 2) + lane + 32 * c];
-      const float sn = a.rope_sin[(size_t)p * (HD / 2) + lane + 32 * c];
-      const float u = q[c], w = q[c + N / 2];
-      q[c] = u * cs - w * sn;
-      q[c + N / 2] = w * cs + u * sn;
-    }
-    for (int k = 0; k <= p; ++k) {
-      const int page = a.table[(size_t)b * a.table_ld + k / kKv8Page];
-      if (page < 0 || page >= a.n_pages) continue;
-      const size_t kb = ((size_t)page * 2) * a.Hkv + g, vb = kb + a.Hkv;
-      const uint8_t* kr = a.kv + (kb * kKv8Page + k % kKv8Page) * HD;
-      const uint8_t* vr = a.kv + (vb * kKv8Page + k % kKv8Page) * HD;
-      float s = 0.f, v[N];
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        uint32_t w = f16x2_of_e4m3((uint16_t)(kr[lane + 32 * c] | (vr[lane + 32 * c] << 8)));
-        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
-        s += q[c] * f.x;
-        v[c] = f.y;
-      }
-      s = warp_sum(s) * pow2f(kv8_scale_exp(a.scale[kb]));
-      const float vs = pow2f(kv8_scale_exp(a.scale[vb]));
-      const float mn = fmaxf(m, s), al = expf(m - mn), pr = expf(s - mn);
-      l = l * al + pr;
-#pragma unroll
-      for (int c = 0; c < N; ++c) o[c] = o[c] * al + pr * (v[c] * vs);
-      m = mn;
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const size_t at = (size_t)row * a.o_ld + (size_t)h * HD + lane + 32 * c;
-    if (a.o) a.o[at] = o[c] * inv;
-    else a.o16[at] = __float2bfloat16_rn(o[c] * inv);
   }
 }
 
@@ -263,13 +187,8 @@ cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st) {
-  const cudaLaunchConfig_t c = config(dim3((a.row0 ? a.T / kKv8Page : 0) + 2 * a.B, a.Hkv), 128, st);
+  const cudaLaunchConfig_t c = config(dim3(a.T / kKv8Page + 2 * a.B, a.Hkv), 128, st);
   return s2_launch(&c, a.hd == 128 ? kv8_append_kernel<128> : kv8_append_kernel<64>, a);
-}
-
-cudaError_t launch_kv8_attn_simple(const Kv8Args& a, cudaStream_t st) {
-  const cudaLaunchConfig_t c = config(dim3(a.T, (a.H + 3) / 4), 128, st);
-  return s2_launch(&c, a.hd == 128 ? kv8_attn_simple_kernel<128> : kv8_attn_simple_kernel<64>, a);
 }
 
 cudaError_t launch_kv8_pack(const Kv8PackArgs& p, cudaStream_t st) {

@@ -249,7 +249,6 @@ struct Kv8Args {
 constexpr int kKv8MaxSeqs = 1024;
 constexpr int kKv8MaxRows = 8;      // decode: m * H / Hkv
 cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st);
-cudaError_t launch_kv8_attn_simple(const Kv8Args& a, cudaStream_t st);
 // Attention of prompts whose rows launch_kv8_append put into their pages (right
 // before it in the stream).
 cudaError_t launch_kv8_prefill(const Kv8Args& a, cudaStream_t st);
