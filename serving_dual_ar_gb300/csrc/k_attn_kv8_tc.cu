@@ -10,7 +10,11 @@ namespace {
 constexpr int kPreRows = 128;                 // rows of a query tile; two tiles a CTA
 constexpr int kPreKeys = 128;                 // keys of a step
 constexpr int kPrePages = kPreKeys / kKv8Page;
-constexpr int kPreThreads = 13 * 32;          // softmax 2 x 4 warps, converters 4, MMA 1
+constexpr int kPreThreads = 20 * 32;          // softmax 2 x 4 warps, keys 4, values 4, MMA 1 (of 4)
+// Registers: 96 a thread at launch, shared out anew among the five groups of
+// four warps (2 x 152 + 2 x 72 + 32 = 5 x 96).
+constexpr int kPreRegs = 96, kPreRegsSoftmax = 152, kPreRegsWiden = 72, kPreRegsMma = 32;
+static_assert(2 * kPreRegsSoftmax + 2 * kPreRegsWiden + kPreRegsMma == 5 * kPreRegs, "shares of the launch's registers");
 constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
 // Weights carry 2^kPreBias; the running maximum may lag by kPreLag.
@@ -60,8 +64,33 @@ S2_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 32 columns of this thread's lane: the load, and the wait that the values may
+// be used after.
+S2_DEV void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+S2_DEV void tmem_ld32_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
 S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+template <int N>
+S2_DEV void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+S2_DEV void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 S2_DEV float ex2p(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -135,9 +164,9 @@ __device__ __noinline__ void add_small_page(uint32_t t_row, const PageWeights w,
 // every key up to its last token in steps of 128.
 //   warps 0..7   prologue: the tiles' queries (norm, RoPE, f16) to shared
 //                memory; then one row per thread: maximum, weights, row sum
-//   warps 8..11  e4m3 keys and values to f16 (exactly; the pages' scales
-//                relative to the step's largest), in the swizzled layout
-//   warp 12      S = Q K^T and O += P V, issued by one thread
+//   warps 8..11  e4m3 keys to f16 (exactly; the pages' scales relative to the
+//                step's largest), in the swizzled layout; 12..15 the values
+//   warp 16      S = Q K^T and O += P V, issued by one thread
 // S and P share tensor memory (P is written over S as f16, and is the A operand
 // from there), O stays in it; V is read as [key][dim], MN-major, so nothing is
 // transposed.  While one tile's softmax runs, the other tile's products do.
@@ -201,7 +230,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   const int keys = pos0 + min(rows, t0 + nt * TT);                    // keys that the last token sees
   const int steps = (keys + kPreKeys - 1) / kPreKeys;
   const int* table = a.table + (size_t)b * a.table_ld;
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&tmem_s)), "n"(kPreTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -209,7 +238,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
 
   // queries (the rows that the append before this kernel reads too)
   if (warp < 8) {
-    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 8 / RPS;         // lanes per row, rows per load, loads at a time
+    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 4;               // lanes per row, rows per load, loads at a time
     const int tile = warp / 4, l = lane % LPR, d = 4 * l;
     const float sg = l < LPR / 2 ? -1.f : 1.f;
     float gain[4];
@@ -329,9 +358,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   const uint32_t tmem = tmem_s;
   bool ok = true;
 
-  if (warp == 12) {
+  if (warp >= 16) {
     // ------------------------------------------------ products
-    if (lane == 0) {
+    fewer_regs<kPreRegsMma>();
+    if (warp == 16 && lane == 0) {
       constexpr uint32_t i_qk = idesc_f16(kPreRows, kPreKeys, 0), i_pv = idesc_f16(kPreRows, HD, 1);
       const uint32_t q_at = smem_u32(sm + L::kQ), k_at = smem_u32(sm + L::kK), v_at = smem_u32(sm + L::kV);
       auto qk = [&](int t, int st) {
@@ -386,15 +416,25 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------ e4m3 to f16
+    fewer_regs<kPreRegsWiden>();
     // lane (row = lane / 8 + 4 it, unit = lane % 8) moves 16 bytes of a key's
     // row: 512 bytes in one piece per load (HD 64: lane / 4, 8 rows a load)
     constexpr int U = HD / 16, RP = 32 / U, N = 32 / RP;    // units of a row, rows per load, loads of a warp's 32 keys
-    const int w = warp - 8, u = lane % U, rr = lane / U;
-    uint4 x[2][N];                                          // K, V of the step to come
+    const int kind = warp / 4 - 2, w = warp % 4, u = lane % U, rr = lane / U;   // kind 0: keys, 1: values
+    const int8_t* top = kind ? ev_s : ek_s;
+    uint64_t* full = kind ? v_full : k_full;
+    uint64_t* empty = kind ? v_empty : k_empty;
+    uint8_t* to0 = sm + (kind ? L::kV : L::kK) + (u / 4) * kBlock;
+    // the second block's lanes swap their stores: no bank twice
+    const int odd = u / 4 & 1, c0 = u % 4 * 2 + odd, c1 = u % 4 * 2 + 1 - odd;
+    const uint8_t* base = a.kv + ((size_t)kind * a.Hkv + g) * (kKv8Page * HD) + rr * HD + u * 16;
+    const float* scales = a.scale + (size_t)kind * a.Hkv + g;
+    const size_t page_bytes = (size_t)2 * a.Hkv * (kKv8Page * HD);
+    uint4 x[N];                                             // the step to come
     // this warp's two pages: ids two steps ahead of use, scales one, so that
     // neither is waited for
     int page[2], page_next[2];
-    float sc[2][2], sc_next[2][2];                          // [page][K, V]
+    float sc[2], sc_next[2];
     auto load_ids = [&](int j, int (&p)[2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -402,81 +442,78 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         p[i] = at * kKv8Page < keys ? table[at] : -1;
       }
     };
-    auto load_scales = [&](int (&p)[2], float (&s)[2][2]) {
+    auto load_scales = [&](int (&p)[2], float (&f)[2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (p[i] < 0 || p[i] >= a.n_pages) p[i] = -1;
-        const float* f = a.scale + (size_t)max(p[i], 0) * 2 * a.Hkv + g;
-        s[i][0] = f[0];
-        s[i][1] = f[a.Hkv];
+        if (p[i] >= a.n_pages) p[i] = -1;
+        f[i] = scales[(size_t)max(p[i], 0) * 2 * a.Hkv];
       }
     };
-    auto load = [&](int kind, int j, const int (&p)[2]) {
-#pragma unroll
-      for (int it = 0; it < N; ++it) {
-        const int row = it * RP + rr, pg = p[row / kKv8Page];
-        x[kind][it] = make_uint4(0, 0, 0, 0);
-        if (pg >= 0 && j * kPreKeys + w * 32 + row < keys)
-          x[kind][it] = *reinterpret_cast<const uint4*>(
-              a.kv + ((((size_t)pg * 2 + kind) * a.Hkv + g) * kKv8Page + row % kKv8Page) * HD + u * 16);
-      }
-    };
-    auto store = [&](int kind, int j, uint8_t* to) {
-      // the pages' scales over the step's largest one
-      __half2 by[2];
+    auto load = [&](int j, const int (&p)[2]) {
+      const int left = keys - j * kPreKeys - w * 32 - rr;   // rows of this lane that are keys: it * RP < left
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int d = kv8_scale_exp(sc[i][kind]) - (kind ? ev_s[j] : ek_s[j]);
-        const bool none = page[i] < 0 || (kind && (small_s[j] >> (w * 2 + i) & 1));
-        by[i] = __float2half2_rn(none ? 0.f : pow2f(max(d, -60)));
-      }
+        const uint8_t* from = base + max(p[i], 0) * page_bytes;
+        const int n = p[i] < 0 ? 0 : left;
 #pragma unroll
-      for (int it = 0; it < N; ++it) {
-        const int row = w * 32 + it * RP + rr;
-        uint4 y = x[kind][it];
-        if (kind == 1 && (has_nan(y.x) | has_nan(y.y) | has_nan(y.z) | has_nan(y.w)))
-          y = without_nan(y, nan_s + u * 16, &nan_any, j * kPreKeys + row);
-        const __half2 f = by[it * RP / kKv8Page];
-        const uint4 first = make_uint4(widen(y.x, f), widen(y.x >> 16, f), widen(y.y, f), widen(y.y >> 16, f));
-        const uint4 second = make_uint4(widen(y.z, f), widen(y.z >> 16, f), widen(y.w, f), widen(y.w >> 16, f));
-        uint8_t* blk = to + (u / 4) * kBlock;
-        const int c = u % 4 * 2, odd = u / 4 & 1;           // the second block's lanes swap their stores: no bank twice
-        *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + odd)) = odd ? second : first;
-        *reinterpret_cast<uint4*>(blk + sw128_offset(row, c + 1 - odd)) = odd ? first : second;
+        for (int it = i * (N / 2); it < (i + 1) * (N / 2); ++it) {
+          x[it] = make_uint4(0, 0, 0, 0);
+          if (it * RP < n) x[it] = *reinterpret_cast<const uint4*>(from + (it * RP % kKv8Page) * HD);
+        }
       }
     };
     load_ids(0, page);
     load_ids(1, page_next);
     load_scales(page, sc);
-    load(0, 0, page);
-    load(1, 0, page);
+    load(0, page);
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       const int st = j % ST;
-      const uint32_t ph = ((uint32_t)(j / ST) & 1u) ^ 1u;
       int page_2[2];
       load_ids(j + 2, page_2);
       load_scales(page_next, sc_next);
-      ok = mbar_wait(&k_empty[st], ph, nullptr) && ok;
-      store(0, j, sm + L::kK + st * L::kTile);
+      // the two pages' scales over the step's largest one
+      __half2 by[2];
+      const int top_j = top[j], small = kind ? small_s[j] >> (w * 2) : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        by[i] = __float2half2_rn(page[i] < 0 || (small >> i & 1) ? 0.f
+                                                                 : pow2f(max(kv8_scale_exp(sc[i]) - top_j, -60)));
+      ok = mbar_wait(&empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr) && ok;
+      uint8_t* to = to0 + st * L::kTile;
+      if (kind) {
+        uint32_t nan = 0;
+#pragma unroll
+        for (int it = 0; it < N; ++it) nan |= has_nan(x[it].x) | has_nan(x[it].y) | has_nan(x[it].z) | has_nan(x[it].w);
+        if (nan)
+#pragma unroll
+          for (int it = 0; it < N; ++it)
+            x[it] = without_nan(x[it], nan_s + u * 16, &nan_any, j * kPreKeys + w * 32 + it * RP + rr);
+      }
+#pragma unroll
+      for (int it = 0; it < N; ++it) {
+        const int row = w * 32 + it * RP + rr;
+        const __half2 f = by[it * RP / kKv8Page];
+        const uint4 y = x[it];
+        const uint4 first = make_uint4(widen(y.x, f), widen(y.x >> 16, f), widen(y.y, f), widen(y.y >> 16, f));
+        const uint4 second = make_uint4(widen(y.z, f), widen(y.z >> 16, f), widen(y.w, f), widen(y.w >> 16, f));
+        *reinterpret_cast<uint4*>(to + sw128_offset(row, c0)) = odd ? second : first;
+        *reinterpret_cast<uint4*>(to + sw128_offset(row, c1)) = odd ? first : second;
+      }
       fence_proxy_async();
-      mbar_arrive(&k_full[st]);
-      load(0, j + 1, page_next);
-      ok = mbar_wait(&v_empty[st], ph, nullptr) && ok;
-      store(1, j, sm + L::kV + st * L::kTile);
-      fence_proxy_async();
-      mbar_arrive(&v_full[st]);
-      load(1, j + 1, page_next);
+      mbar_arrive(&full[st]);
+      load(j + 1, page_next);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         page[i] = page_next[i];
         page_next[i] = page_2[i];
-        sc[i][0] = sc_next[i][0];
-        sc[i][1] = sc_next[i][1];
+        sc[i] = sc_next[i];
       }
     }
-  } else if (warp / 4 < nt) {
+  } else {
     // ------------------------------------------------ softmax, a row per thread
+    more_regs<kPreRegsSoftmax>();
+    if (warp / 4 < nt) {
     const int tile = warp / 4, i = tid % kPreRows, tt = i / G, t = t0 + tile * TT + tt;
     const bool on = tt < TT && t < rows;
     const int lim = on ? pos0 + t : -1;                    // last key of this row
@@ -510,19 +547,31 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
           if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
         }
       }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float s[32];
-        tmem_ld32(ts + 32 * c, s);
+      uint32_t s0[32], s1[32];               // 32 columns in use, 32 on their way
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto largest = [&](int c, const uint32_t (&s)[32]) {
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, see[c] >> e & 1 ? s[e] : -INFINITY);
+          for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], see[c] >> e & 1 ? __uint_as_float(s[e]) : -INFINITY);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, s[e]);
+          for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(s[e]));
         }
-      }
+      };
+      tmem_ld32_start(ts, s0);
+      tmem_ld32_done(s0);
+      tmem_ld32_start(ts + 32, s1);
+      largest(0, s0);
+      tmem_ld32_done(s1);
+      tmem_ld32_start(ts + 64, s0);
+      largest(1, s1);
+      tmem_ld32_done(s0);
+      tmem_ld32_start(ts + 96, s1);
+      largest(2, s0);
+      tmem_ld32_done(s1);
+      tmem_ld32_start(ts, s0);
+      largest(3, s1);
+      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       mx *= f;
       const int En = max(E, ev);
       if (__any_sync(0xffffffffu, mx > m + (float)kPreLag) || En > E) {
@@ -545,22 +594,18 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       }
       const int up = kPreBias + ev - E;
       const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
-      float sum = 0.f;
+      float sum[4] = {};
       uint32_t lo[2][16];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      // the weights of 32 keys, into tensor memory as f16 (the low parts two
+      // blocks later, when S of their columns is read)
+      auto weights = [&](int c, uint32_t (&r)[32]) {
         float s[32];
-        tmem_ld32(ts + 32 * c, s);
-        if (PLANES == 2 && c == 2) {          // S of these columns is read: the low parts kept back go there
-          tmem_st16(ts + 64, lo[0]);
-          tmem_st16(ts + 80, lo[1]);
-        }
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = see[c] >> e & 1 ? ex2p(fmaf(s[e], f, -sub)) : 0.f;
+          for (int e = 0; e < 32; ++e) s[e] = see[c] >> e & 1 ? ex2p(fmaf(__uint_as_float(r[e]), f, -sub)) : 0.f;
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = ex2p(fmaf(s[e], f, -sub));
+          for (int e = 0; e < 32; ++e) s[e] = ex2p(fmaf(__uint_as_float(r[e]), f, -sub));
         }
         if (small >> (2 * c) & 3) {
 #pragma unroll
@@ -576,22 +621,37 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         uint32_t hi[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          sum += s[2 * e] + s[2 * e + 1];
+          sum[e & 3] += s[2 * e] + s[2 * e + 1];
           const __half2 h = __floats2half2_rn(s[2 * e], s[2 * e + 1]);
           hi[e] = *reinterpret_cast<const uint32_t*>(&h);
           if (PLANES == 2) {
             const float2 hf = __half22float2(h);
-            const __half2 r = __floats2half2_rn(s[2 * e] - hf.x, s[2 * e + 1] - hf.y);
-            lo[c & 1][e] = *reinterpret_cast<const uint32_t*>(&r);
+            const __half2 d = __floats2half2_rn(s[2 * e] - hf.x, s[2 * e + 1] - hf.y);
+            lo[c & 1][e] = *reinterpret_cast<const uint32_t*>(&d);
           }
         }
         tmem_st16(ts + 16 * c, hi);
-        if (PLANES == 2 && c == 3) {
-          tmem_st16(ts + 96, lo[0]);
-          tmem_st16(ts + 112, lo[1]);
-        }
+      };
+      tmem_ld32_done(s0);
+      tmem_ld32_start(ts + 32, s1);
+      weights(0, s0);
+      tmem_ld32_done(s1);
+      tmem_ld32_start(ts + 64, s0);
+      weights(1, s1);
+      tmem_ld32_done(s0);
+      if (PLANES == 2) {
+        tmem_st16(ts + 64, lo[0]);
+        tmem_st16(ts + 80, lo[1]);
       }
-      l += sum * pow2f(-up);
+      tmem_ld32_start(ts + 96, s1);
+      weights(2, s0);
+      tmem_ld32_done(s1);
+      weights(3, s1);
+      if (PLANES == 2) {
+        tmem_st16(ts + 96, lo[0]);
+        tmem_st16(ts + 112, lo[1]);
+      }
+      l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&p_full[tile]);
@@ -646,10 +706,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         }
       }
     }
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kPreTmem) : "memory");
   }
