@@ -12,8 +12,8 @@ constexpr int kPreKeys = 128;                 // keys of a step
 constexpr int kPrePages = kPreKeys / kKv8Page;
 constexpr int kPreThreads = 20 * 32;          // softmax 2 x 4 warps, keys 4, values 4, MMA 1 (of 4)
 // Registers: 96 a thread at launch, shared out anew among the five groups of
-// four warps (2 x 152 + 2 x 72 + 32 = 5 x 96).
-constexpr int kPreRegs = 96, kPreRegsSoftmax = 152, kPreRegsWiden = 72, kPreRegsMma = 32;
+// four warps (2 x 136 + 2 x 72 + 64 = 5 x 96).
+constexpr int kPreRegs = 96, kPreRegsSoftmax = 136, kPreRegsWiden = 72, kPreRegsMma = 64;
 static_assert(2 * kPreRegsSoftmax + 2 * kPreRegsWiden + kPreRegsMma == 5 * kPreRegs, "shares of the launch's registers");
 constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
@@ -43,18 +43,34 @@ template <> struct OutOf<1> { using type = __nv_bfloat16; };
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// MN-major operand in the 128-byte swizzled layout: rows (k) of 128 bytes (64
-// values along MN) in 8-row atoms; the next 64 values along MN lie ``block``
-// bytes on.
-S2_DEV uint64_t smem_desc_mn(uint32_t saddr, uint32_t block) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-S2_DEV void umma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accum) {
+// Shared-memory operands as the two words of their descriptors; the lower one,
+// with the address, is all that differs between products.  128-byte swizzle,
+// 8-row atoms of 128-byte rows one after the other.  K-major: the rows are M or
+// N.  MN-major: the rows are K, 64 values along MN each, the next 64 values
+// ``block`` bytes on.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;   // atom stride, version, swizzle
+S2_DEV uint32_t desc_k(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+S2_DEV uint32_t desc_mn(uint32_t saddr, uint32_t block) { return saddr >> 4 | (block >> 4) << 16; }
+S2_DEV void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accum), "r"(kDescHi) : "memory");
+}
+S2_DEV void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
+      :: "r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHi) : "memory");
+}
+// One lane of a converged warp, chosen such that the compiler knows that it is
+// one: the products' operands then go to uniform registers as they are, where
+// a branch by lane number has each of them moved there in a loop over lanes.
+S2_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 S2_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -197,7 +213,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     if (lane == 0) seq_s = n;
   }
   if (tid == 0) {
-    mbar_init(&q_full, 256);
+    mbar_init(&q_full, kPreThreads);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128);
       mbar_init(&k_empty[i], 1);
@@ -237,15 +253,16 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   }
 
   // queries (the rows that the append before this kernel reads too)
-  if (warp < 8) {
+  {
     constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 4;               // lanes per row, rows per load, loads at a time
-    const int tile = warp / 4, l = lane % LPR, d = 4 * l;
+    const int l = lane % LPR, d = 4 * l;
     const float sg = l < LPR / 2 ? -1.f : 1.f;
     float gain[4];
     load4<VEC>(a.q_gain + d, gain);
-    uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
 #pragma unroll 1
-    for (int i0 = warp % 4 * 32; i0 < warp % 4 * 32 + 32; i0 += NB * RPS) {
+    for (int i1 = warp * NB * RPS; i1 < 2 * kPreRows; i1 += kPreThreads / 32 * NB * RPS) {
+      const int tile = i1 / kPreRows, i0 = i1 % kPreRows;
+      uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
       float x[NB][4], co[NB][4], si[NB][4], ss[NB];
       bool live[NB];
 #pragma unroll
@@ -361,30 +378,29 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   if (warp >= 16) {
     // ------------------------------------------------ products
     fewer_regs<kPreRegsMma>();
-    if (warp == 16 && lane == 0) {
+    if (warp == 16 && elect_one()) {
       constexpr uint32_t i_qk = idesc_f16(kPreRows, kPreKeys, 0), i_pv = idesc_f16(kPreRows, HD, 1);
-      const uint32_t q_at = smem_u32(sm + L::kQ), k_at = smem_u32(sm + L::kK), v_at = smem_u32(sm + L::kV);
+      const uint32_t tm = tmem;
+      const uint32_t q_d = desc_k(smem_u32(sm + L::kQ)), k_d = desc_k(smem_u32(sm + L::kK));
+      const uint32_t v_d = desc_mn(smem_u32(sm + L::kV), kBlock);
       auto qk = [&](int t, int st) {
-        uint32_t acc = 0;
-#pragma unroll 1
+        const uint32_t qt = q_d + (t * PLANES * L::kTile >> 4), kt = k_d + (st * L::kTile >> 4);
+#pragma unroll
         for (int p = 0; p < PLANES; ++p)
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
-            const uint32_t off = (ks / 4) * kBlock + (ks % 4) * 32;
-            umma_bf16(tmem + t * 128, smem_desc_sw128(q_at + (t * PLANES + p) * L::kTile + off),
-                      smem_desc_sw128(k_at + st * L::kTile + off), i_qk, acc);
-            acc = 1;
+            const uint32_t off = ((ks / 4) * kBlock + (ks % 4) * 32) >> 4;
+            umma_ss(tm + t * 128, qt + (p * L::kTile >> 4) + off, kt + off, i_qk, p + ks > 0);
           }
         umma_commit(&s_full[t]);
       };
       auto pv = [&](int t, int st) {
-#pragma unroll 1
+        const uint32_t vt = v_d + (st * L::kTile >> 4);
+#pragma unroll
         for (int p = 0; p < PLANES; ++p)
 #pragma unroll
-          for (int ks = 0; ks < kPreKeys / 16; ++ks) {
-            umma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + p * 64 + ks * 8,
-                        smem_desc_mn(v_at + st * L::kTile + ks * 2048, kBlock), i_pv, 1);
-          }
+          for (int ks = 0; ks < kPreKeys / 16; ++ks)
+            umma_ts(tm + 256 + t * 128, tm + t * 128 + p * 64 + ks * 8, vt + (ks * 2048 >> 4), i_pv);
       };
       ok = mbar_wait(&q_full, 0, nullptr) && ok;
       ok = mbar_wait(&k_full[0], 0, nullptr) && ok;
@@ -395,6 +411,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       for (int j = 0; j < steps; ++j) {
         const int st = j % ST, sn = (j + 1) % ST;
         ok = mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr) && ok;
+#pragma unroll 1
         for (int t = 0; t < nt; ++t) {
           ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr) && ok;
           tc_fence_after();
