@@ -145,32 +145,52 @@ __device__ __noinline__ uint4 without_nan(uint4 y, int* first, int* any, int key
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One page's keys into a row's output by fp32 arithmetic: the 16 weights of the
-// row, the page's values x ``by``, the row in tensor memory.  For pages whose
-// values are so small next to others of their step that they would not survive
-// as f16 relative to the step's scale; a row may see those and not the others.
-struct PageWeights {
-  float p[kKv8Page];
-};
-template <int HD>
-__device__ __noinline__ void add_small_page(uint32_t t_row, const PageWeights w, const uint8_t* v, float by) {
+// The keys of the pages in ``small`` (a bit each) into a row's output by fp32
+// arithmetic: weights from where they were put in tensor memory, times the
+// page's values over 2^ev.  For pages whose values are so small next to others
+// of their step that they would not survive as f16 relative to the step's
+// scale; a row may see those and not the others.
+template <int HD, int PLANES>
+__device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_t small, const Kv8Args& a,
+                                             const int* table, int g, int ev) {
 #pragma unroll 1
-  for (int c = 0; c < HD; c += 8) {
-    float o[8];
-    tmem_ld8(t_row + c, o);
+  for (int q = 0; q < kPrePages; ++q) {
+    if (!(small >> q & 1)) continue;
+    const size_t blk = ((size_t)table[q] * 2 + 1) * a.Hkv + g;
+    const uint8_t* v = a.kv + blk * (kKv8Page * HD);
+    const float by = pow2f(kv8_scale_exp(a.scale[blk]) - ev);
+    float p[kKv8Page];
 #pragma unroll
-    for (int k = 0; k < kKv8Page; ++k) {
-      const uint2 x = *reinterpret_cast<const uint2*>(v + k * HD + c);
-      const float p = w.p[k] * by;
+    for (int i = 0; i < kKv8Page; ++i) p[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t h = f16x2_of_e4m3((uint16_t)((e < 2 ? x.x : x.y) >> (e & 1) * 16));
-        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-        o[2 * e] += f.x == f.x ? p * f.x : 0.f;           // NaN: see nan_s
-        o[2 * e + 1] += f.y == f.y ? p * f.y : 0.f;
+    for (int k = 0; k < PLANES; ++k) {
+      float w[8];
+      tmem_ld8(t_p + 64 * k + 8 * q, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(w[i]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        p[2 * i] += f.x * by;
+        p[2 * i + 1] += f.y * by;
       }
     }
-    tmem_st8(t_row + c, o);
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 8) {
+      float o[8];
+      tmem_ld8(t_o + c, o);
+#pragma unroll
+      for (int k = 0; k < kKv8Page; ++k) {
+        const uint2 x = *reinterpret_cast<const uint2*>(v + k * HD + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t h = f16x2_of_e4m3((uint16_t)((e < 2 ? x.x : x.y) >> (e & 1) * 16));
+          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+          o[2 * e] += f.x == f.x ? p[k] * f.x : 0.f;           // NaN: see nan_s
+          o[2 * e + 1] += f.y == f.y ? p[k] * f.y : 0.f;
+        }
+      }
+      tmem_st8(t_o + c, o);
+    }
   }
 }
 
@@ -624,17 +644,6 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) s[e] = ex2p(fmaf(__uint_as_float(r[e]), f, -sub));
         }
-        if (small >> (2 * c) & 3) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (small >> (2 * c + q) & 1) {
-              PageWeights w;
-#pragma unroll
-              for (int e = 0; e < kKv8Page; ++e) w.p[e] = s[16 * q + e];
-              const size_t blk = ((size_t)table[j * kPrePages + 2 * c + q] * 2 + 1) * a.Hkv + g;
-              add_small_page<HD>(to, w, a.kv + blk * (kKv8Page * HD), pow2f(kv8_scale_exp(a.scale[blk]) - ev));
-            }
-        }
         uint32_t hi[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -670,6 +679,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       }
       l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
       tmem_wait_st();
+      if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + j * kPrePages, g, ev);
       tc_fence_before();
       mbar_arrive(&p_full[tile]);
     }
