@@ -10,11 +10,6 @@ namespace {
 constexpr int kPreRows = 128;                 // rows of a query tile; two tiles a CTA
 constexpr int kPreKeys = 128;                 // keys of a step
 constexpr int kPrePages = kPreKeys / kKv8Page;
-constexpr int kPreThreads = 20 * 32;          // softmax 2 x 4 warps, keys 4, values 4, MMA 1 (of 4)
-// Registers: 96 a thread at launch, shared out anew among the five groups of
-// four warps (2 x 136 + 2 x 72 + 64 = 5 x 96).
-constexpr int kPreRegs = 96, kPreRegsSoftmax = 136, kPreRegsWiden = 72, kPreRegsMma = 64;
-static_assert(2 * kPreRegsSoftmax + 2 * kPreRegsWiden + kPreRegsMma == 5 * kPreRegs, "shares of the launch's registers");
 constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
 // Weights carry 2^kPreBias; the running maximum may lag by kPreLag.
@@ -23,6 +18,20 @@ constexpr int kPreBias = 6, kPreLag = 8;
 // apart: until there 2^-9 of the scale, e4m3's least, is an f16 value.
 constexpr int kPreSmall = 14;
 constexpr int kPreStepBytes = 4;              // what is kept of each step
+
+// Groups of four warps: two of softmax, one for keys and one for values (one
+// for both with an fp32 output, where the products take twice the time), one
+// for the products.  The launch's registers are shared out anew among them:
+// with an fp32 output a softmax thread holds its row's output too.
+template <int PLANES>
+struct PreRoles {
+  static constexpr int kWiden = PLANES == 1 ? 2 : 1, kGroups = 3 + kWiden, kThreads = kGroups * 128;
+  static constexpr int kMma = 8 + 4 * kWiden;                 // first warp of the products' group
+  static constexpr int kRegs = PLANES == 1 ? 96 : 128;        // a thread, at launch
+  static constexpr int kRegsSoftmax = PLANES == 1 ? 136 : 208, kRegsWiden = PLANES == 1 ? 72 : 64,
+                       kRegsMma = PLANES == 1 ? 64 : 32;
+  static_assert(2 * kRegsSoftmax + kWiden * kRegsWiden + kRegsMma == kGroups * kRegs, "the launch's registers");
+};
 
 template <int HD, int PLANES>
 struct PreLayout {
@@ -58,11 +67,11 @@ S2_DEV void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t
       "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
       :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accum), "r"(kDescHi) : "memory");
 }
-S2_DEV void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc) {
+S2_DEV void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 y, {%2, %4};\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
-      :: "r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHi) : "memory");
+      :: "r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accum), "r"(kDescHi) : "memory");
 }
 // One lane of a converged warp, chosen such that the compiler knows that it is
 // one: the products' operands then go to uniform registers as they are, where
@@ -100,6 +109,19 @@ S2_DEV void tmem_ld32_done(uint32_t (&r)[32]) {
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])
                :: "memory");
+}
+S2_DEV void tmem_put8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+S2_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
 }
 S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -200,17 +222,23 @@ __device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_
 // every key up to its last token in steps of 128.
 //   warps 0..7   prologue: the tiles' queries (norm, RoPE, f16) to shared
 //                memory; then one row per thread: maximum, weights, row sum
-//   warps 8..11  e4m3 keys to f16 (exactly; the pages' scales relative to the
-//                step's largest), in the swizzled layout; 12..15 the values
-//   warp 16      S = Q K^T and O += P V, issued by one thread
+//   warps 8..    e4m3 keys and values to f16 (exactly; the pages' scales
+//                relative to the step's largest), in the swizzled layout
+//   last group   S = Q K^T and O += P V, issued by one thread
 // S and P share tensor memory (P is written over S as f16, and is the A operand
 // from there), O stays in it; V is read as [key][dim], MN-major, so nothing is
 // transposed.  While one tile's softmax runs, the other tile's products do.
-// PLANES = 2 (fp32 output): Q and P as f16 pairs hi + lo, twice the products.
+// PLANES = 2 (fp32 output): Q and P as f16 pairs hi + lo, twice the products,
+// the low ones first.  The tensor cores cut what they add to an accumulator
+// off, toward zero; over a thousand steps that grows to 2^-16 of the output.
+// So each step's P V starts from zero, and the row's thread adds it up, rounded
+// to nearest, in registers.
 template <int HD, int PLANES, bool VEC>
-__global__ void __launch_bounds__(kPreThreads, 1)
+__global__ void __launch_bounds__(PreRoles<PLANES>::kThreads, 1)
 kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   using L = PreLayout<HD, PLANES>;
+  using W = PreRoles<PLANES>;
+  constexpr int kThreads = W::kThreads;
   constexpr int ST = L::kStages, kBlock = 128 * 128;   // a 64-dim block: 128 rows x 128 bytes
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
@@ -233,7 +261,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     if (lane == 0) seq_s = n;
   }
   if (tid == 0) {
-    mbar_init(&q_full, kPreThreads);
+    mbar_init(&q_full, kThreads);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128);
       mbar_init(&k_empty[i], 1);
@@ -246,7 +274,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     fence_mbar_init();
     nan_any = 0;
   }
-  for (int i = tid; i < HD; i += kPreThreads) nan_s[i] = 0x7fffffff;
+  for (int i = tid; i < HD; i += kThreads) nan_s[i] = 0x7fffffff;
   __syncthreads();
   const int b = seq_s;
   if (b < 0) return;
@@ -256,7 +284,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   const int nt = t0 + TT < rows ? 2 : 1;                              // tiles with tokens
   if (pos0 < 0 || pos0 > a.max_pos - rows) {                          // left out: zeros
     const int cols = G * HD, n = min(rows - t0, 2 * TT);
-    for (int i = tid; i < n * cols; i += kPreThreads) {
+    for (int i = tid; i < n * cols; i += kThreads) {
       const size_t at = (size_t)(r0 + t0 + i / cols) * a.o_ld + (size_t)g * cols + i % cols;
       if (a.o) a.o[at] = 0.f;
       else a.o16[at] = __float2bfloat16_rn(0.f);
@@ -266,7 +294,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   const int keys = pos0 + min(rows, t0 + nt * TT);                    // keys that the last token sees
   const int steps = (keys + kPreKeys - 1) / kPreKeys;
   const int* table = a.table + (size_t)b * a.table_ld;
-  if (warp == 16) {
+  if (warp == W::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&tmem_s)), "n"(kPreTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -280,7 +308,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     float gain[4];
     load4<VEC>(a.q_gain + d, gain);
 #pragma unroll 1
-    for (int i1 = warp * NB * RPS; i1 < 2 * kPreRows; i1 += kPreThreads / 32 * NB * RPS) {
+    for (int i1 = warp * NB * RPS; i1 < 2 * kPreRows; i1 += kThreads / 32 * NB * RPS) {
       const int tile = i1 / kPreRows, i0 = i1 % kPreRows;
       uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
       float x[NB][4], co[NB][4], si[NB][4], ss[NB];
@@ -364,7 +392,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   uint8_t* small_s = there_s + steps;
   {
     const int pages = (keys + kKv8Page - 1) / kKv8Page;
-    for (int i0 = warp * 32; i0 < steps * kPrePages; i0 += kPreThreads) {
+    for (int i0 = warp * 32; i0 < steps * kPrePages; i0 += kThreads) {
       const int i = i0 + lane, page = i < pages ? table[i] : -1;
       const bool in = page >= 0 && page < a.n_pages;
       int ek = kKv8EMin, ev = kKv8EMin;
@@ -395,10 +423,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   const uint32_t tmem = tmem_s;
   bool ok = true;
 
-  if (warp >= 16) {
+  if (warp >= W::kMma) {
     // ------------------------------------------------ products
-    fewer_regs<kPreRegsMma>();
-    if (warp == 16 && elect_one()) {
+    fewer_regs<W::kRegsMma>();
+    if (warp == W::kMma && elect_one()) {
       constexpr uint32_t i_qk = idesc_f16(kPreRows, kPreKeys, 0), i_pv = idesc_f16(kPreRows, HD, 1);
       const uint32_t tm = tmem;
       const uint32_t q_d = desc_k(smem_u32(sm + L::kQ)), k_d = desc_k(smem_u32(sm + L::kK));
@@ -406,21 +434,22 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       auto qk = [&](int t, int st) {
         const uint32_t qt = q_d + (t * PLANES * L::kTile >> 4), kt = k_d + (st * L::kTile >> 4);
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
+        for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
             const uint32_t off = ((ks / 4) * kBlock + (ks % 4) * 32) >> 4;
-            umma_ss(tm + t * 128, qt + (p * L::kTile >> 4) + off, kt + off, i_qk, p + ks > 0);
+            umma_ss(tm + t * 128, qt + (p * L::kTile >> 4) + off, kt + off, i_qk, p < PLANES - 1 || ks > 0);
           }
         umma_commit(&s_full[t]);
       };
-      auto pv = [&](int t, int st) {
+      auto pv = [&](int t, int st, uint32_t acc) {
         const uint32_t vt = v_d + (st * L::kTile >> 4);
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
+        for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
           for (int ks = 0; ks < kPreKeys / 16; ++ks)
-            umma_ts(tm + 256 + t * 128, tm + t * 128 + p * 64 + ks * 8, vt + (ks * 2048 >> 4), i_pv);
+            umma_ts(tm + 256 + t * 128, tm + t * 128 + p * 64 + ks * 8, vt + (ks * 2048 >> 4), i_pv,
+                    p < PLANES - 1 || ks > 0 ? 1u : acc);
       };
       ok = mbar_wait(&q_full, 0, nullptr) && ok;
       ok = mbar_wait(&k_full[0], 0, nullptr) && ok;
@@ -435,7 +464,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         for (int t = 0; t < nt; ++t) {
           ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr) && ok;
           tc_fence_after();
-          pv(t, st);
+          pv(t, st, PLANES == 1 || small_s[j] ? 1u : 0u);
           if (t == nt - 1) umma_commit(&v_empty[st]);
           if (j + 1 < steps) {
             if (t == 0) {
@@ -453,25 +482,22 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------ e4m3 to f16
-    fewer_regs<kPreRegsWiden>();
+    fewer_regs<W::kRegsWiden>();
     // lane (row = lane / 8 + 4 it, unit = lane % 8) moves 16 bytes of a key's
     // row: 512 bytes in one piece per load (HD 64: lane / 4, 8 rows a load)
     constexpr int U = HD / 16, RP = 32 / U, N = 32 / RP;    // units of a row, rows per load, loads of a warp's 32 keys
-    const int kind = warp / 4 - 2, w = warp % 4, u = lane % U, rr = lane / U;   // kind 0: keys, 1: values
-    const int8_t* top = kind ? ev_s : ek_s;
-    uint64_t* full = kind ? v_full : k_full;
-    uint64_t* empty = kind ? v_empty : k_empty;
-    uint8_t* to0 = sm + (kind ? L::kV : L::kK) + (u / 4) * kBlock;
+    constexpr int KINDS = 3 - W::kWiden;                    // of this warp; kind 0: keys, 1: values
+    const int first = KINDS == 1 ? warp / 4 - 2 : 0, w = warp % 4, u = lane % U, rr = lane / U;
     // the second block's lanes swap their stores: no bank twice
     const int odd = u / 4 & 1, c0 = u % 4 * 2 + odd, c1 = u % 4 * 2 + 1 - odd;
-    const uint8_t* base = a.kv + ((size_t)kind * a.Hkv + g) * (kKv8Page * HD) + rr * HD + u * 16;
-    const float* scales = a.scale + (size_t)kind * a.Hkv + g;
-    const size_t page_bytes = (size_t)2 * a.Hkv * (kKv8Page * HD);
+    const size_t half = (size_t)a.Hkv * (kKv8Page * HD);    // bytes of a page's keys
+    const uint8_t* base = a.kv + first * half + (size_t)g * (kKv8Page * HD) + rr * HD + u * 16;
+    const float* scales = a.scale + (size_t)first * a.Hkv + g;
     uint4 x[N];                                             // the step to come
     // this warp's two pages: ids two steps ahead of use, scales one, so that
     // neither is waited for
     int page[2], page_next[2];
-    float sc[2], sc_next[2];
+    float sc[KINDS][2], sc_next[KINDS][2];
     auto load_ids = [&](int j, int (&p)[2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -479,18 +505,19 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         p[i] = at * kKv8Page < keys ? table[at] : -1;
       }
     };
-    auto load_scales = [&](int (&p)[2], float (&f)[2]) {
+    auto load_scales = [&](int (&p)[2], float (&f)[KINDS][2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (p[i] >= a.n_pages) p[i] = -1;
-        f[i] = scales[(size_t)max(p[i], 0) * 2 * a.Hkv];
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k) f[k][i] = scales[((size_t)max(p[i], 0) * 2 + k) * a.Hkv];
       }
     };
-    auto load = [&](int j, const int (&p)[2]) {
+    auto load = [&](int k, int j, const int (&p)[2]) {
       const int left = keys - j * kPreKeys - w * 32 - rr;   // rows of this lane that are keys: it * RP < left
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* from = base + max(p[i], 0) * page_bytes;
+        const uint8_t* from = base + ((size_t)max(p[i], 0) * 2 + k) * half;
         const int n = p[i] < 0 ? 0 : left;
 #pragma unroll
         for (int it = i * (N / 2); it < (i + 1) * (N / 2); ++it) {
@@ -502,54 +529,61 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     load_ids(0, page);
     load_ids(1, page_next);
     load_scales(page, sc);
-    load(0, page);
+    load(0, 0, page);
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       const int st = j % ST;
       int page_2[2];
       load_ids(j + 2, page_2);
       load_scales(page_next, sc_next);
-      // the two pages' scales over the step's largest one
-      __half2 by[2];
-      const int top_j = top[j], small = kind ? small_s[j] >> (w * 2) : 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        by[i] = __float2half2_rn(page[i] < 0 || (small >> i & 1) ? 0.f
-                                                                 : pow2f(max(kv8_scale_exp(sc[i]) - top_j, -60)));
-      ok = mbar_wait(&empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr) && ok;
-      uint8_t* to = to0 + st * L::kTile;
-      if (kind) {
-        uint32_t nan = 0;
+      for (int k = 0; k < KINDS; ++k) {
+        const int kind = first + k;
+        // the two pages' scales over the step's largest one
+        __half2 by[2];
+        const int top = kind ? ev_s[j] : ek_s[j], small = kind ? small_s[j] >> (w * 2) : 0;
 #pragma unroll
-        for (int it = 0; it < N; ++it) nan |= has_nan(x[it].x) | has_nan(x[it].y) | has_nan(x[it].z) | has_nan(x[it].w);
-        if (nan)
+        for (int i = 0; i < 2; ++i)
+          by[i] = __float2half2_rn(page[i] < 0 || (small >> i & 1) ? 0.f
+                                                                   : pow2f(max(kv8_scale_exp(sc[k][i]) - top, -60)));
+        ok = mbar_wait(kind ? &v_empty[st] : &k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr) && ok;
+        uint8_t* to = sm + (kind ? L::kV : L::kK) + st * L::kTile + (u / 4) * kBlock;
+        if (kind) {
+          uint32_t nan = 0;
 #pragma unroll
           for (int it = 0; it < N; ++it)
-            x[it] = without_nan(x[it], nan_s + u * 16, &nan_any, j * kPreKeys + w * 32 + it * RP + rr);
-      }
+            nan |= has_nan(x[it].x) | has_nan(x[it].y) | has_nan(x[it].z) | has_nan(x[it].w);
+          if (nan)
 #pragma unroll
-      for (int it = 0; it < N; ++it) {
-        const int row = w * 32 + it * RP + rr;
-        const __half2 f = by[it * RP / kKv8Page];
-        const uint4 y = x[it];
-        const uint4 first = make_uint4(widen(y.x, f), widen(y.x >> 16, f), widen(y.y, f), widen(y.y >> 16, f));
-        const uint4 second = make_uint4(widen(y.z, f), widen(y.z >> 16, f), widen(y.w, f), widen(y.w >> 16, f));
-        *reinterpret_cast<uint4*>(to + sw128_offset(row, c0)) = odd ? second : first;
-        *reinterpret_cast<uint4*>(to + sw128_offset(row, c1)) = odd ? first : second;
+            for (int it = 0; it < N; ++it)
+              x[it] = without_nan(x[it], nan_s + u * 16, &nan_any, j * kPreKeys + w * 32 + it * RP + rr);
+        }
+#pragma unroll
+        for (int it = 0; it < N; ++it) {
+          const int row = w * 32 + it * RP + rr;
+          const __half2 f = by[it * RP / kKv8Page];
+          const uint4 y = x[it];
+          const uint4 one = make_uint4(widen(y.x, f), widen(y.x >> 16, f), widen(y.y, f), widen(y.y >> 16, f));
+          const uint4 two = make_uint4(widen(y.z, f), widen(y.z >> 16, f), widen(y.w, f), widen(y.w >> 16, f));
+          *reinterpret_cast<uint4*>(to + sw128_offset(row, c0)) = odd ? two : one;
+          *reinterpret_cast<uint4*>(to + sw128_offset(row, c1)) = odd ? one : two;
+        }
+        fence_proxy_async();
+        mbar_arrive(kind ? &v_full[st] : &k_full[st]);
+        if (k + 1 < KINDS) load(k + 1, j, page);
+        else load(0, j + 1, page_next);
       }
-      fence_proxy_async();
-      mbar_arrive(&full[st]);
-      load(j + 1, page_next);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         page[i] = page_next[i];
         page_next[i] = page_2[i];
-        sc[i] = sc_next[i];
+#pragma unroll
+        for (int k = 0; k < KINDS; ++k) sc[k][i] = sc_next[k][i];
       }
     }
   } else {
     // ------------------------------------------------ softmax, a row per thread
-    more_regs<kPreRegsSoftmax>();
+    more_regs<W::kRegsSoftmax>();
     if (warp / 4 < nt) {
     const int tile = warp / 4, i = tid % kPreRows, tt = i / G, t = t0 + tile * TT + tt;
     const bool on = tt < TT && t < rows;
@@ -560,11 +594,28 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     const float qf = qf_s[tile * kPreRows + i];
     float m = -INFINITY, l = 0.f;
     int E = kKv8EMin;
-    {
+    float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
+    auto clear_o = [&] {
       const float zero[8] = {};
 #pragma unroll 1
       for (int c = 0; c < HD; c += 8) tmem_st8(to + c, zero);
-    }
+    };
+    auto add_step = [&] {                                  // the last step's P V to it
+      if constexpr (PLANES == 2) {
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t y[32];
+          tmem_ld32_start(to + c, y);
+          tmem_ld32_done(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(y[e]);
+        }
+      }
+    };
+    if constexpr (PLANES == 1) clear_o();
+    else
+#pragma unroll
+      for (int c = 0; c < HD; ++c) acc[c] = 0.f;
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       const int k0 = j * kPreKeys, ev = ev_s[j];
@@ -584,7 +635,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
           if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
         }
       }
-      uint32_t s0[32], s1[32];               // 32 columns in use, 32 on their way
+      if (PLANES == 2 && j > 0) add_step();
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto largest = [&](int c, const uint32_t (&s)[32]) {
         if (masked) {
@@ -595,19 +646,29 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
           for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(s[e]));
         }
       };
-      tmem_ld32_start(ts, s0);
-      tmem_ld32_done(s0);
-      tmem_ld32_start(ts + 32, s1);
-      largest(0, s0);
-      tmem_ld32_done(s1);
-      tmem_ld32_start(ts + 64, s0);
-      largest(1, s1);
-      tmem_ld32_done(s0);
-      tmem_ld32_start(ts + 96, s1);
-      largest(2, s0);
-      tmem_ld32_done(s1);
-      tmem_ld32_start(ts, s0);
-      largest(3, s1);
+      uint32_t s0[32], s1[32];               // 32 columns in use, 32 on their way (PLANES 2: no room)
+      if constexpr (PLANES == 1) {
+        tmem_ld32_start(ts, s0);
+        tmem_ld32_done(s0);
+        tmem_ld32_start(ts + 32, s1);
+        largest(0, s0);
+        tmem_ld32_done(s1);
+        tmem_ld32_start(ts + 64, s0);
+        largest(1, s1);
+        tmem_ld32_done(s0);
+        tmem_ld32_start(ts + 96, s1);
+        largest(2, s0);
+        tmem_ld32_done(s1);
+        tmem_ld32_start(ts, s0);
+        largest(3, s1);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32_start(ts + 32 * c, s0);
+          tmem_ld32_done(s0);
+          largest(c, s0);
+        }
+      }
       float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       mx *= f;
       const int En = max(E, ev);
@@ -615,8 +676,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
         const float mn = fmaxf(m, mx);
         const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
         l *= y;
-        if (j > 0) {         // the products before this step's S are complete
-          const float z = y * pow2f(E - En);
+        const float z = y * pow2f(E - En);
+        if constexpr (PLANES == 2) {
+#pragma unroll
+          for (int c = 0; c < HD; ++c) acc[c] *= z;
+        } else if (j > 0) {  // the products before this step's S are complete
 #pragma unroll 1
           for (int c = 0; c < HD; c += 8) {
             float v[8];
@@ -632,59 +696,88 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       const int up = kPreBias + ev - E;
       const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
       float sum[4] = {};
-      uint32_t lo[2][16];
-      // the weights of 32 keys, into tensor memory as f16 (the low parts two
-      // blocks later, when S of their columns is read)
-      auto weights = [&](int c, uint32_t (&r)[32]) {
-        float s[32];
-        if (masked) {
+      // a weight, by its score and whether the row sees the key
+      auto weight = [&](uint32_t r, bool sees) {
+        const float p = ex2p(fmaf(__uint_as_float(r), f, -sub));
+        return !masked || sees ? p : 0.f;
+      };
+      if constexpr (PLANES == 1) {
+        // 32 keys at a time into tensor memory as f16, over their scores
+        auto weights = [&](int c, const uint32_t (&r)[32]) {
+          uint32_t hi[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = see[c] >> e & 1 ? ex2p(fmaf(__uint_as_float(r[e]), f, -sub)) : 0.f;
-        } else {
+          for (int e = 0; e < 16; ++e) {
+            const float x = weight(r[2 * e], see[c] >> (2 * e) & 1), y = weight(r[2 * e + 1], see[c] >> (2 * e + 1) & 1);
+            sum[e & 3] += x + y;
+            const __half2 h = __floats2half2_rn(x, y);
+            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(ts + 16 * c, hi);
+        };
+        tmem_ld32_done(s0);
+        tmem_ld32_start(ts + 32, s1);
+        weights(0, s0);
+        tmem_ld32_done(s1);
+        tmem_ld32_start(ts + 64, s0);
+        weights(1, s1);
+        tmem_ld32_done(s0);
+        tmem_ld32_start(ts + 96, s1);
+        weights(2, s0);
+        tmem_ld32_done(s1);
+        weights(3, s1);
+      } else {
+        // 16 keys at a time; the low parts of the first half are kept back
+        // until the scores in their columns are read
+        uint32_t lo[4][8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = ex2p(fmaf(__uint_as_float(r[e]), f, -sub));
-        }
-        uint32_t hi[16];
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[16], hi[8], rest[8];
+          tmem_ld16(ts + 16 * c, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sum[e & 3] += s[2 * e] + s[2 * e + 1];
-          const __half2 h = __floats2half2_rn(s[2 * e], s[2 * e + 1]);
-          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-          if (PLANES == 2) {
+          for (int e = 0; e < 8; ++e) {
+            const int k = 16 * c + 2 * e;
+            const float x = weight(r[2 * e], see[k / 32] >> (k % 32) & 1);
+            const float y = weight(r[2 * e + 1], see[k / 32] >> (k % 32 + 1) & 1);
+            sum[e & 3] += x + y;
+            const __half2 h = __floats2half2_rn(x, y);
             const float2 hf = __half22float2(h);
-            const __half2 d = __floats2half2_rn(s[2 * e] - hf.x, s[2 * e + 1] - hf.y);
-            lo[c & 1][e] = *reinterpret_cast<const uint32_t*>(&d);
+            const __half2 d = __floats2half2_rn(x - hf.x, y - hf.y);
+            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+            rest[e] = *reinterpret_cast<const uint32_t*>(&d);
+          }
+          tmem_put8(ts + 8 * c, hi);
+          if (c < 4) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lo[c][e] = rest[e];
+          } else {
+            // columns 16 c .. 16 c + 15 are free: two of the eight blocks of low parts
+            if (c < 6) {
+              tmem_put8(ts + 16 * c, lo[2 * (c - 4)]);
+              tmem_put8(ts + 16 * c + 8, lo[2 * (c - 4) + 1]);
+            } else if (c == 6) {
+              tmem_put8(ts + 96, lo[0]);
+              tmem_put8(ts + 104, lo[1]);
+            }
+            if (c == 7) {
+              tmem_put8(ts + 112, lo[2]);
+              tmem_put8(ts + 120, rest);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) lo[c - 4][e] = rest[e];
+            }
           }
         }
-        tmem_st16(ts + 16 * c, hi);
-      };
-      tmem_ld32_done(s0);
-      tmem_ld32_start(ts + 32, s1);
-      weights(0, s0);
-      tmem_ld32_done(s1);
-      tmem_ld32_start(ts + 64, s0);
-      weights(1, s1);
-      tmem_ld32_done(s0);
-      if (PLANES == 2) {
-        tmem_st16(ts + 64, lo[0]);
-        tmem_st16(ts + 80, lo[1]);
-      }
-      tmem_ld32_start(ts + 96, s1);
-      weights(2, s0);
-      tmem_ld32_done(s1);
-      weights(3, s1);
-      if (PLANES == 2) {
-        tmem_st16(ts + 96, lo[0]);
-        tmem_st16(ts + 112, lo[1]);
       }
       l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
       tmem_wait_st();
+      if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
       if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + j * kPrePages, g, ev);
       tc_fence_before();
       mbar_arrive(&p_full[tile]);
     }
     ok = mbar_wait(&o_full[tile], 0, nullptr) && ok;
     tc_fence_after();
+    add_step();
     const float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
     const bool nans = nan_any != 0;
     // rows by threads to rows by warps, over the tile's queries, which nothing
@@ -692,10 +785,15 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     using T = typename OutOf<PLANES>::type;
     constexpr int UE = 16 / sizeof(T), UR = HD / UE;        // values of a unit, units of a row
     uint8_t* rows_s = sm + L::kQ + tile * PLANES * L::kTile + (size_t)(i & ~31) * HD * sizeof(T);
-#pragma unroll 1
+#pragma unroll (PLANES == 2 ? 4 : 1)
     for (int c = 0; c < HD; c += 32) {
       float y[32];
-      tmem_ld32(to + c, y);
+      if constexpr (PLANES == 2) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = acc[c + e];
+      } else {
+        tmem_ld32(to + c, y);
+      }
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         y[e] *= inv;
@@ -737,7 +835,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == W::kMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kPreTmem) : "memory");
   }
@@ -757,7 +855,7 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   const int o_vec = (o & 15) == 0 && a.o_ld % (PLANES == 2 ? 4 : 8) == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(slots, a.Hkv);
-  cfg.blockDim = dim3(kPreThreads);
+  cfg.blockDim = dim3(PreRoles<PLANES>::kThreads);
   cfg.dynamicSmemBytes =
       1024 + PreLayout<HD, PLANES>::kMeta + kPreStepBytes * ((a.max_pos + kPreKeys - 1) / kPreKeys);
   cfg.stream = st;
