@@ -1,5 +1,7 @@
 // Prompt attention over the 8-bit KV cache on tcgen05: ragged prompts behind
 // cached pages, grouped queries, causal.
+#include <type_traits>
+
 #include "kv8_common.cuh"
 #include "tc_common.cuh"
 
@@ -696,10 +698,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
       const int up = kPreBias + ev - E;
       const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
       float sum[4] = {};
+      auto step = [&](auto masks) {
       // a weight, by its score and whether the row sees the key
       auto weight = [&](uint32_t r, bool sees) {
         const float p = ex2p(fmaf(__uint_as_float(r), f, -sub));
-        return !masked || sees ? p : 0.f;
+        return !decltype(masks)::value || sees ? p : 0.f;
       };
       if constexpr (PLANES == 1) {
         // 32 keys at a time into tensor memory as f16, over their scores
@@ -768,6 +771,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
           }
         }
       }
+      };
+      if (masked) step(std::true_type());
+      else step(std::false_type());
       l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
       tmem_wait_st();
       if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
