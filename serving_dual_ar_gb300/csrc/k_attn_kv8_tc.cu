@@ -138,12 +138,15 @@ S2_DEV float ex2p(float x) {
 }
 
 template <bool VEC>
-S2_DEV void load4(const float* p, float (&v)[4]) {
-  const float4 x = VEC ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
-  v[0] = x.x;
-  v[1] = x.y;
-  v[2] = x.z;
-  v[3] = x.w;
+S2_DEV void load8(const float* p, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const float4 x = VEC ? *reinterpret_cast<const float4*>(p + e) : make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]);
+    v[e] = x.x;
+    v[e + 1] = x.y;
+    v[e + 2] = x.z;
+    v[e + 3] = x.w;
+  }
 }
 
 // Two e4m3 bytes (the low ones of w) as f16x2 times f.
@@ -237,7 +240,7 @@ __device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_
 // to nearest, in registers.
 template <int HD, int PLANES, bool VEC>
 __global__ void __launch_bounds__(PreRoles<PLANES>::kThreads, 1)
-kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
+kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsigned inv_g) {
   using L = PreLayout<HD, PLANES>;
   using W = PreRoles<PLANES>;
   constexpr int kThreads = W::kThreads;
@@ -246,7 +249,6 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_s;
-  __shared__ float qf_s[2 * kPreRows];
   __shared__ int nan_s[HD];
   __shared__ int nan_any;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -302,82 +304,69 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // queries (the rows that the append before this kernel reads too)
+  // queries (the rows that the append before this kernel reads too), eight dims
+  // a lane: norm, RoPE, log2(e) / sqrt(HD), and one power of two for the whole
+  // launch: a normed row times the gains has no value above sqrt(HD) times the
+  // largest gain, which goes to 2^9 .. 2^10 (its typical values then to 2^6: a
+  // pair of f16 is good to 2^-22 of a value, and to 2^-34 of the largest)
+  float qf;                                 // the power of two back
   {
-    constexpr int LPR = HD / 4, RPS = 32 / LPR, NB = 4;               // lanes per row, rows per load, loads at a time
-    const int l = lane % LPR, d = 4 * l;
-    const float sg = l < LPR / 2 ? -1.f : 1.f;
-    float gain[4];
-    load4<VEC>(a.q_gain + d, gain);
+    constexpr int LPR = HD / 8, RPS = 32 / LPR, NB = 2;               // lanes per row, rows per load, loads at a time
+    const int l = lane % LPR, d = 8 * l, dh = d % (HD / 2);
+    float gain[8];
+    load8<VEC>(a.q_gain + d, gain);
+    float mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(gain[e]));
+    mx = warp_max(mx) * 1.44269504f;        // log2(e); sqrt(HD) and 1 / sqrt(HD) cancel
+    const int ex = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+    qf = pow2f(ex - 9);
+    const float up = pow2f(9 - ex);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gain[e] *= up * (HD == 128 ? 0.127517431f : 0.180336880f);
+    const bool low = l < LPR / 2;
 #pragma unroll 1
     for (int i1 = warp * NB * RPS; i1 < 2 * kPreRows; i1 += kThreads / 32 * NB * RPS) {
-      const int tile = i1 / kPreRows, i0 = i1 % kPreRows;
-      uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile;
-      float x[NB][4], co[NB][4], si[NB][4], ss[NB];
+      const int tile = i1 / kPreRows;
+      uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile + (d / 64) * kBlock;
+      float x[NB][8], co[NB][8], si[NB][8];
       bool live[NB];
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        const int i = i0 + k * RPS + lane / LPR, tt = i / G, t = t0 + tile * TT + tt;
-        const bool on = tt < TT && t < rows;
-        const float* q = a.qkv + (size_t)(r0 + (on ? t : t0)) * a.qkv_ld + (size_t)(g * G + i % G) * HD + d;
-        const size_t turn = (size_t)(pos0 + (on ? t : t0)) * (HD / 2) + d % (HD / 2);
-        load4<VEC>(q, x[k]);
-        load4<VEC>(a.rope_cos + turn, co[k]);
-        load4<VEC>(a.rope_sin + turn, si[k]);
-        live[k] = on;
+        const int i = i1 % kPreRows + k * RPS + lane / LPR, tt = i * inv_g >> 16, t = t0 + tile * TT + tt;
+        live[k] = tt < TT && t < rows;
+        const int tok = live[k] ? t : t0;
+        load8<VEC>(a.qkv + (size_t)(r0 + tok) * a.qkv_ld + (g * G + i - tt * G) * HD + d, x[k]);
+        load8<VEC>(a.rope_cos + (size_t)(pos0 + tok) * (HD / 2) + dh, co[k]);
+        load8<VEC>(a.rope_sin + (size_t)(pos0 + tok) * (HD / 2) + dh, si[k]);
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        ss[k] = 0.f;
+        const int i = i1 % kPreRows + k * RPS + lane / LPR;
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += x[k][e] * x[k][e];
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float f = live[k] ? rsqrtf(ss * (1.f / HD) + a.eps) : 0.f;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = live[k] ? x[k][e] * (f * gain[e]) : 0.f;
+          const float w = __shfl_xor_sync(0xffffffffu, y, LPR / 2);
+          x[k][e] = y * co[k][e] + (low ? -w : w) * si[k][e];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[k][e] = live[k] ? x[k][e] : 0.f;
-          ss[k] += x[k][e] * x[k][e];
-        }
-      }
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < NB; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        // log2(e) / sqrt(HD): the softmax runs on powers of two
-        const float f = rsqrtf(ss[k] * (1.f / HD) + a.eps) * (HD == 128 ? 0.127517431f : 0.180336880f);
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = x[k][e] * (f * gain[e]);
-          const float w = __shfl_xor_sync(0xffffffffu, y, LPR / 2) * sg;
-          x[k][e] = y * co[k][e] + w * si[k][e];
-          mx = fmaxf(mx, fabsf(x[k][e]));
-        }
-        ss[k] = mx;
-      }
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < NB; ++k) ss[k] = fmaxf(ss[k], __shfl_xor_sync(0xffffffffu, ss[k], o));
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int i = i0 + k * RPS + lane / LPR;
-        // the row's largest magnitude to 2^6 .. 2^7: products with e4m3 values
-        // stay far inside fp32, and a pair is good to 2^-31 of the largest
-        const int ex = min(max((int)(__float_as_uint(ss[k]) >> 23) - 127, -100), 100);
-        const float up = pow2f(6 - ex);
-        if (l == 0) qf_s[tile * kPreRows + i] = pow2f(ex - 6);
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float u = x[k][2 * e] * up, v = x[k][2 * e + 1] * up;
-          const __half2 h = __floats2half2_rn(u, v);
+          const __half2 h = __floats2half2_rn(x[k][2 * e], x[k][2 * e + 1]);
           const float2 hf = __half22float2(h);
-          const __half2 r = __floats2half2_rn(u - hf.x, v - hf.y);
+          const __half2 r = __floats2half2_rn(x[k][2 * e] - hf.x, x[k][2 * e + 1] - hf.y);
           hi[e] = *reinterpret_cast<const uint32_t*>(&h);
           lo[e] = *reinterpret_cast<const uint32_t*>(&r);
         }
-        const uint32_t to = (d / 64) * kBlock + sw128_offset(i, d % 64 / 8) + (d & 4) * 2;
-        *reinterpret_cast<uint2*>(q_hi + to) = make_uint2(hi[0], hi[1]);
-        if (PLANES == 2) *reinterpret_cast<uint2*>(q_hi + L::kTile + to) = make_uint2(lo[0], lo[1]);
+        uint8_t* to = q_hi + sw128_offset(i, l % 8);
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (PLANES == 2) *reinterpret_cast<uint4*>(to + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     fence_proxy_async();
@@ -587,13 +576,12 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     // ------------------------------------------------ softmax, a row per thread
     more_regs<W::kRegsSoftmax>();
     if (warp / 4 < nt) {
-    const int tile = warp / 4, i = tid % kPreRows, tt = i / G, t = t0 + tile * TT + tt;
+    const int tile = warp / 4, i = tid % kPreRows, tt = i * inv_g >> 16, t = t0 + tile * TT + tt;
     const bool on = tt < TT && t < rows;
     const int lim = on ? pos0 + t : -1;                    // last key of this row
     const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
-    const float qf = qf_s[tile * kPreRows + i];
     float m = -INFINITY, l = 0.f;
     int E = kKv8EMin;
     float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
@@ -824,7 +812,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec) {
     T* out = reinterpret_cast<T*>(PLANES == 2 ? static_cast<void*>(a.o) : static_cast<void*>(a.o16));
 #pragma unroll 4
     for (int k = 0; k < UR; ++k) {                          // 32 units a step: 32 / UR rows
-      const int row = (k * 32 + lane) / UR, q = lane % UR, ri = (i & ~31) + row, rt = ri / G;
+      const int row = (k * 32 + lane) / UR, q = lane % UR, ri = (i & ~31) + row, rt = ri * inv_g >> 16;
       const uint4 y = *reinterpret_cast<const uint4*>(rows_s + (size_t)row * HD * sizeof(T) + ((q ^ row) % UR) * 16);
       if (rt < TT && t0 + tile * TT + rt < rows) {
         T* p = out + (size_t)(r0 + t0 + tile * TT + rt) * a.o_ld + (size_t)(g * G + ri - rt * G) * HD + q * UE;
@@ -871,7 +859,7 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return s2_launch(&cfg, k, a, slots, o_vec);
+  return s2_launch(&cfg, k, a, slots, o_vec, 65536u / (a.H / a.Hkv) + 1);   // i / G = i * inv_g >> 16, i < 128
 }
 template <int HD, int PLANES>
 cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
