@@ -269,7 +269,8 @@ int s2op_attn_decode_noalloc(const float* qkv, int qkv_ld, int B, int m, int H, 
 
 /* Decode attention for B sequences with m new rows each, row b*m + i at
  * position pos[b] + i: q and k normed and rotated, k and v stored, then
- * attention over all keys up to the row's position.  m * H / Hkv <= 8. */
+ * attention over all keys up to the row's position.  m * H / Hkv <= 8, B * Hkv *
+ * table_ld < 2^31. */
 size_t s2op_attn_decode_kv8_workspace_bytes(int B, int m, int H, int Hkv, int hd);
 int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int Hkv, int hd,
                          const float* q_gain, const float* k_gain, float eps, const float* rope_cos,
@@ -280,7 +281,8 @@ int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int 
 /* Prompt attention of B sequences in one call: sequence b has the rows
  * row0[b] .. row0[b+1] - 1 (row0: B + 1 non-decreasing entries on the device;
  * none is fine) at positions pos0[b], pos0[b] + 1, ..., behind pos0[b] cached
- * tokens.  T bounds row0[B]; rows in no sequence are left as they are. */
+ * tokens.  T (at most 2^24) bounds row0[B]; rows in no sequence are left as they
+ * are.  Positions at or beyond 2^20 count as outside the table. */
 size_t s2op_attn_prefill_kv8_workspace_bytes(int T, int B, int H, int Hkv, int hd);
 int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B, const int32_t* row0,
                           const int32_t* pos0, int H, int Hkv, int hd, const float* q_gain,

@@ -281,10 +281,16 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   for (int i = tid; i < HD; i += kThreads) nan_s[i] = 0x7fffffff;
   __syncthreads();
   const int b = seq_s;
-  if (b < 0) return;
+  if (b < 0) {
+    pdl_wait();      // as every way out: this grid must not end before the one it follows
+    return;
+  }
   const int r0 = a.row0[b], rows = min(a.row0[b + 1], a.T) - r0, pos0 = a.pos[b];
   const int t0 = (slot - (r0 / (2 * TT) + b)) * 2 * TT;               // first token of tile 0
-  if (r0 < 0 || t0 < 0 || t0 >= rows) return;
+  if (r0 < 0 || t0 < 0 || t0 >= rows) {
+    pdl_wait();
+    return;
+  }
   const int nt = t0 + TT < rows ? 2 : 1;                              // tiles with tokens
   if (pos0 < 0 || pos0 > a.max_pos - rows) {                          // left out: zeros
     const int cols = G * HD, n = min(rows - t0, 2 * TT);
@@ -293,6 +299,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
       if (a.o) a.o[at] = 0.f;
       else a.o16[at] = __float2bfloat16_rn(0.f);
     }
+    pdl_wait();
     return;
   }
   const int keys = pos0 + min(rows, t0 + nt * TT);                    // keys that the last token sees

@@ -89,72 +89,148 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(Kv8Args a) {
 
 // ---------------------------------------------------------------- pack / unpack
 
-// One block (16 rows of one page, K or V, head) per CTA of 128 threads.
+// One block (16 rows of one page, K or V, head) per warp: its 8 KB (fp32) are
+// all in flight at once, the largest magnitude needs no barrier, and the
+// values are rounded from the registers that they were loaded to.  Bound by
+// memory.
+template <typename T> struct Unit16;            // 16 bytes of an unpacked page
+template <> struct Unit16<float> {
+  static constexpr int kValues = 4;
+  static S2_DEV void get(const uint4& u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+  }
+  static S2_DEV uint4 put(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <> struct Unit16<__nv_bfloat16> {
+  static constexpr int kValues = 8;
+  static S2_DEV void get(const uint4& u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16lo(w[i]);
+      v[2 * i + 1] = bf16hi(w[i]);
+    }
+  }
+  static S2_DEV uint4 put(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) kv8_pack_kernel(Kv8PackArgs p) {
-  __shared__ float am_s[4];
-  const int i = blockIdx.x / (2 * p.Hkv), blk = blockIdx.x % (2 * p.Hkv), tid = threadIdx.x;
+  constexpr int V = Unit16<T>::kValues, N = kKv8Page * HD / (32 * V);     // values and units of a lane
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int i = at / (2 * p.Hkv), blk = at % (2 * p.Hkv);
+  if (i >= p.n) return;
   const int src = p.src[i], dst = p.dst[i];
   if (src < 0 || src >= p.n_src || dst < 0 || dst >= p.n_dst) return;
   const int rows = p.fill ? min(max(p.fill[i], 0), kKv8Page) : kKv8Page;
-  const T* x = static_cast<const T*>(p.kv) + ((size_t)src * 2 * p.Hkv + blk) * (kKv8Page * HD);
-  constexpr int W = kKv8Page * HD / 128;   // values of each thread
-  float v[W], m = 0.f;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.kv) +
+                                                  ((size_t)src * 2 * p.Hkv + blk) * (kKv8Page * HD));
+  uint4 u[N];
 #pragma unroll
-  for (int c = 0; c < W; c += 4)
+  for (int c = 0; c < N; ++c) u[c] = (c * 32 + lane) * V < rows * HD ? __ldcs(x + c * 32 + lane) : make_uint4(0, 0, 0, 0);
+  float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int at = (c / 4 * 128 + tid) * 4 + e;
-      v[c + e] = at < rows * HD ? to_f(x[at]) : 0.f;
-      m = fmaxf(m, fabsf(v[c + e]));
-    }
-  m = warp_max(m);
-  if ((tid & 31) == 0) am_s[tid >> 5] = m;
-  __syncthreads();
-  const int e = kv8_exponent(fmaxf(fmaxf(am_s[0], am_s[1]), fmaxf(am_s[2], am_s[3])));
+  for (int c = 0; c < N; ++c) {
+    float v[V];
+    Unit16<T>::get(u[c], v);
+    m = abs_max(v, m);
+  }
+  const int e = kv8_exponent(warp_max(m));
   const float f = pow2f(-e);
   const size_t ob = (size_t)dst * 2 * p.Hkv + blk;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.kv8 + ob * (kKv8Page * HD));
 #pragma unroll
-  for (int c = 0; c < W; c += 4)
-    out[c / 4 * 128 + tid] = e4m3x2(v[c] * f, v[c + 1] * f) | (e4m3x2(v[c + 2] * f, v[c + 3] * f) << 16);
-  if (tid == 0) p.scale[ob] = pow2f(e);
+  for (int c = 0; c < N; ++c) {
+    float v[V];
+    Unit16<T>::get(u[c], v);
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k)
+      w[k] = e4m3x2(v[4 * k] * f, v[4 * k + 1] * f) | (e4m3x2(v[4 * k + 2] * f, v[4 * k + 3] * f) << 16);
+    if constexpr (V == 4) out[c * 32 + lane] = w[0];
+    else reinterpret_cast<uint2*>(out)[c * 32 + lane] = make_uint2(w[0], w[V / 4 - 1]);
+  }
+  if (lane == 0) p.scale[ob] = pow2f(e);
 }
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) kv8_unpack_kernel(Kv8PackArgs p) {
-  const int i = blockIdx.x / (2 * p.Hkv), blk = blockIdx.x % (2 * p.Hkv), tid = threadIdx.x;
+  constexpr int V = Unit16<T>::kValues, N = kKv8Page * HD / (32 * V);
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int i = at / (2 * p.Hkv), blk = at % (2 * p.Hkv);
+  if (i >= p.n) return;
   const int src = p.src[i], dst = p.dst[i];
   if (src < 0 || src >= p.n_src || dst < 0 || dst >= p.n_dst) return;
   const size_t ib = (size_t)src * 2 * p.Hkv + blk;
   const uint32_t* in = reinterpret_cast<const uint32_t*>(p.kv8 + ib * (kKv8Page * HD));
+  uint32_t w[N][V / 4];
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    if constexpr (V == 4) {
+      w[c][0] = in[c * 32 + lane];
+    } else {
+      const uint2 y = reinterpret_cast<const uint2*>(in)[c * 32 + lane];
+      w[c][0] = y.x;
+      w[c][V / 4 - 1] = y.y;
+    }
+  }
   const float f = pow2f(kv8_scale_exp(p.scale[ib]));
-  T* out = static_cast<T*>(p.kv) + ((size_t)dst * 2 * p.Hkv + blk) * (kKv8Page * HD);
-  for (int c = tid; c < kKv8Page * HD / 4; c += 128) {
-    const uint32_t w = in[c];
-    uint32_t a = f16x2_of_e4m3((uint16_t)w), b = f16x2_of_e4m3((uint16_t)(w >> 16));
-    const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a));
-    const float2 y = __half22float2(*reinterpret_cast<__half2*>(&b));
-    out[4 * c] = from_f<T>(x.x * f);
-    out[4 * c + 1] = from_f<T>(x.y * f);
-    out[4 * c + 2] = from_f<T>(y.x * f);
-    out[4 * c + 3] = from_f<T>(y.y * f);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.kv) + ((size_t)dst * 2 * p.Hkv + blk) * (kKv8Page * HD));
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      uint32_t h = f16x2_of_e4m3((uint16_t)(w[c][k / 2] >> (k & 1) * 16));
+      const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h));
+      v[2 * k] = x.x * f;
+      v[2 * k + 1] = x.y * f;
+    }
+    __stcs(out + c * 32 + lane, Unit16<T>::put(v));
   }
 }
 
 // ---------------------------------------------------------------- page copies
 
+// One 16 KB chunk of one page in one layer per CTA, all of it in flight at
+// once; the pairs are a kernel argument, of the smaller size where they fit.
+constexpr int kCopyChunk = 16384;
+template <int N>
+struct Pairs {
+  int src[N], dst[N];
+};
+template <int N>
 __global__ void __launch_bounds__(256)
-kv_copy_pages_kernel(uint8_t* kv, long long page_bytes, uint8_t* scale, int scale_bytes, int n_pages,
-                     const __grid_constant__ PagePairs pairs) {
-  const int i = blockIdx.x;
+kv_copy_pages_kernel(uint8_t* kv, long long page_bytes, uint8_t* scale, int scale_bytes, int n_pages, int chunks,
+                     const __grid_constant__ Pairs<N> pairs) {
+  const int i = blockIdx.x / chunks, chunk = blockIdx.x % chunks, tid = threadIdx.x;
   const size_t base = (size_t)blockIdx.y * n_pages;
   const size_t s = base + pairs.src[i], d = base + pairs.dst[i];
-  const uint4* from = reinterpret_cast<const uint4*>(kv + s * page_bytes);
-  uint4* to = reinterpret_cast<uint4*>(kv + d * page_bytes);
-  for (long long c = threadIdx.x; c < page_bytes / 16; c += 256) to[c] = from[c];
-  if (scale)
-    for (int c = threadIdx.x; c < scale_bytes / 4; c += 256)
+  const uint4* from = reinterpret_cast<const uint4*>(kv + s * page_bytes) + (size_t)chunk * (kCopyChunk / 16);
+  uint4* to = reinterpret_cast<uint4*>(kv + d * page_bytes) + (size_t)chunk * (kCopyChunk / 16);
+  const long long left = page_bytes / 16 - (long long)chunk * (kCopyChunk / 16);
+  uint4 x[kCopyChunk / 4096];
+#pragma unroll
+  for (int c = 0; c < kCopyChunk / 4096; ++c)
+    if (c * 256 + tid < left) x[c] = __ldcs(from + c * 256 + tid);
+#pragma unroll
+  for (int c = 0; c < kCopyChunk / 4096; ++c)
+    if (c * 256 + tid < left) __stcs(to + c * 256 + tid, x[c]);
+  if (scale && chunk == 0)
+    for (int c = tid; c < scale_bytes / 4; c += 256)
       reinterpret_cast<uint32_t*>(scale + d * scale_bytes)[c] =
           reinterpret_cast<const uint32_t*>(scale + s * scale_bytes)[c];
 }
@@ -192,23 +268,36 @@ cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv8_pack(const Kv8PackArgs& p, cudaStream_t st) {
-  const cudaLaunchConfig_t c = config(dim3(p.n * 2 * p.Hkv), 128, st);
+  const cudaLaunchConfig_t c = config(dim3((p.n * 2 * p.Hkv + 3) / 4), 128, st);
   auto k = p.kv_bf16 ? (p.hd == 128 ? kv8_pack_kernel<__nv_bfloat16, 128> : kv8_pack_kernel<__nv_bfloat16, 64>)
                      : (p.hd == 128 ? kv8_pack_kernel<float, 128> : kv8_pack_kernel<float, 64>);
   return s2_launch(&c, k, p);
 }
 
 cudaError_t launch_kv8_unpack(const Kv8PackArgs& p, cudaStream_t st) {
-  const cudaLaunchConfig_t c = config(dim3(p.n * 2 * p.Hkv), 128, st);
+  const cudaLaunchConfig_t c = config(dim3((p.n * 2 * p.Hkv + 3) / 4), 128, st);
   auto k = p.kv_bf16 ? (p.hd == 128 ? kv8_unpack_kernel<__nv_bfloat16, 128> : kv8_unpack_kernel<__nv_bfloat16, 64>)
                      : (p.hd == 128 ? kv8_unpack_kernel<float, 128> : kv8_unpack_kernel<float, 64>);
   return s2_launch(&c, k, p);
 }
 
+template <int N>
+static cudaError_t copy_pages(uint8_t* kv, long long page_bytes, uint8_t* scale, int scale_bytes, int n_pages,
+                              int layers, const PagePairs& pairs, int n, cudaStream_t st) {
+  Pairs<N> few;
+  for (int i = 0; i < n; ++i) {
+    few.src[i] = pairs.src[i];
+    few.dst[i] = pairs.dst[i];
+  }
+  const int chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
+  const cudaLaunchConfig_t c = config(dim3(n * chunks, layers), 256, st);
+  return s2_launch(&c, kv_copy_pages_kernel<N>, kv, page_bytes, scale, scale_bytes, n_pages, chunks, few);
+}
+
 cudaError_t launch_kv_copy_pages(uint8_t* kv, long long page_bytes, uint8_t* scale, int scale_bytes, int n_pages,
                                  int layers, const PagePairs& pairs, int n, cudaStream_t st) {
-  const cudaLaunchConfig_t c = config(dim3(n, layers), 256, st);
-  return s2_launch(&c, kv_copy_pages_kernel, kv, page_bytes, scale, scale_bytes, n_pages, pairs);
+  return (n <= 64 ? copy_pages<64> : copy_pages<kPagePairs>)(kv, page_bytes, scale, scale_bytes, n_pages, layers, pairs,
+                                                             n, st);
 }
 
 cudaError_t launch_kv_remap(int* table, int rows, int table_ld, int cols, const PagePairs& pairs, int n,

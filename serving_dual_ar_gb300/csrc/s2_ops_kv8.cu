@@ -35,8 +35,9 @@ static bool fill_args(Kv8Args& a, const float* qkv, int qkv_ld, int B, int H, in
     return false;
   if (!shape_ok(B, H, Hkv, hd) || n_pos < 1 || n_pages < 1 || table_ld < 1) return false;
   if (qkv_ld < (H + 2 * Hkv) * hd || o_ld < H * hd) return false;
-  if (!aligned(kv8, 16) || !aligned(workspace, 16) || !aligned(qkv, 4) || !aligned(kv_scale, 4) ||
-      !aligned(o, o_bf16 ? 2 : 4))
+  if (!aligned(kv8, 16) || !aligned(workspace, 16) || !aligned(qkv, 4) || !aligned(q_gain, 4) || !aligned(k_gain, 4) ||
+      !aligned(rope_cos, 4) || !aligned(rope_sin, 4) || !aligned(pos, 4) || !aligned(kv_scale, 4) ||
+      !aligned(table, 4) || !aligned(o, o_bf16 ? 2 : 4))
     return false;
   a.qkv = qkv;
   a.qkv_ld = qkv_ld;
@@ -96,7 +97,7 @@ extern "C" int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B,
                                      const int32_t* table, int table_ld, void* o, int o_bf16, int o_ld,
                                      void* workspace, void* stream) {
   Kv8Args a;
-  if (!row0 || T < 1 || T > (1 << 24)) return S2_EINVAL;
+  if (!row0 || !aligned(row0, 4) || T < 1 || T > (1 << 24)) return S2_EINVAL;
   if (!fill_args(a, qkv, qkv_ld, B, H, Hkv, hd, q_gain, k_gain, eps, rope_cos, rope_sin, n_pos, pos0, kv8, kv_scale,
                  n_pages, table, table_ld, o, o_bf16, o_ld, workspace))
     return S2_EINVAL;
@@ -112,13 +113,13 @@ static bool pack_ok(const void* kv, const void* kv8, const void* scale, const in
                     int n_src, int n_dst, int n, int Hkv, int hd) {
   return kv && kv8 && scale && src && dst && n_src >= 1 && n_dst >= 1 && n >= 0 && Hkv >= 1 && Hkv <= 4096 &&
          (long long)n * 2 * Hkv <= 0x7fffffffLL && (hd == 64 || hd == 128) && aligned(kv, 16) && aligned(kv8, 16) &&
-         aligned(scale, 4);
+         aligned(scale, 4) && aligned(src, 4) && aligned(dst, 4);
 }
 
 extern "C" int s2op_kv8_pack_pages(const void* kv, int kv_bf16, int n_src, const int32_t* src, const int32_t* fill,
                                    void* kv8, float* kv_scale, int n_dst, const int32_t* dst, int n, int Hkv, int hd,
                                    void* stream) {
-  if (!pack_ok(kv, kv8, kv_scale, src, dst, n_src, n_dst, n, Hkv, hd)) return S2_EINVAL;
+  if (!pack_ok(kv, kv8, kv_scale, src, dst, n_src, n_dst, n, Hkv, hd) || !aligned(fill, 4)) return S2_EINVAL;
   if (n == 0) return S2_OK;
   Kv8PackArgs p;
   p.kv = const_cast<void*>(kv);

@@ -37,23 +37,25 @@ def prefill_args(**kw):
 BOTH = [dict([(k, None)]) for k in ("qkv", "qg", "kg", "cos", "sin", "pos", "kv", "scale", "table", "o", "ws")] + [
     dict(B=0), dict(B=1025), dict(hd=96), dict(H=9), dict(H=0), dict(Hkv=0), dict(H=18, qkv_ld=10000, o_ld=10000),
     dict(n_pos=0), dict(n_pages=0), dict(table_ld=0), dict(qkv_ld=1535), dict(o_ld=1023), dict(kv=P + 8),
-    dict(scale=P + 2), dict(o=P + 2), dict(o=P + 1, bf16=1), dict(ws=P + 4), dict(qkv=P + 1)]
+    dict(scale=P + 2), dict(o=P + 2), dict(o=P + 1, bf16=1), dict(ws=P + 4), dict(qkv=P + 1), dict(qg=P + 2), dict(kg=P + 1),
+    dict(cos=P + 2), dict(sin=P + 1), dict(pos=P + 2), dict(table=P + 1)]
 
 
 @pytest.mark.parametrize("kw", BOTH + [dict(m=0), dict(m=3), dict(m=-1), dict(H=16, m=2, qkv_ld=4000, o_ld=4000),
-                                       dict(m=2 ** 30)], ids=str)
+                                       dict(m=2 ** 30), dict(B=1024, table_ld=2 ** 20)], ids=str)
 def test_decode_refuses(lib, kw):
     assert lib.LIB.s2op_attn_decode_kv8(*decode_args(**kw)) == lib.S2_EINVAL
 
 
-@pytest.mark.parametrize("kw", BOTH + [dict(T=0), dict(T=-4), dict(T=2 ** 24 + 1), dict(row0=None)], ids=str)
+@pytest.mark.parametrize("kw", BOTH + [dict(T=0), dict(T=-4), dict(T=2 ** 24 + 1), dict(row0=None), dict(row0=P + 2)],
+                         ids=str)
 def test_prefill_refuses(lib, kw):
     assert lib.LIB.s2op_attn_prefill_kv8(*prefill_args(**kw)) == lib.S2_EINVAL
 
 
 @pytest.mark.parametrize("change", [
     {0: None}, {3: None}, {5: None}, {6: None}, {8: None}, {2: 0}, {7: 0}, {9: -1}, {10: 0}, {11: 96}, {0: P + 8},
-    {5: P + 4}, {6: P + 2}, {9: 2 ** 30, 10: 8}], ids=str)
+    {5: P + 4}, {6: P + 2}, {3: P + 1}, {8: P + 2}, {9: 2 ** 30, 10: 8}], ids=str)
 def test_pack_refuses(lib, change):
     # kv, bf16, n_src, src, fill, kv8, scale, n_dst, dst, n, Hkv, hd, stream
     a = [P, 0, 4, P, None, P, P, 4, P, 2, 2, 128, None]
