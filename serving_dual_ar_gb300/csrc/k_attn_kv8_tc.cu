@@ -1,5 +1,6 @@
 // Prompt attention over the 8-bit KV cache on tcgen05: ragged prompts behind
 // cached pages, grouped queries, causal.
+#include <algorithm>
 #include <type_traits>
 
 #include "kv8_common.cuh"
@@ -127,6 +128,8 @@ S2_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A barrier of the n threads that are softmax rows.
+S2_DEV void softmax_sync(int n) { asm volatile("bar.sync 1, %0;" :: "r"(n) : "memory"); }
 template <int N>
 S2_DEV void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 template <int N>
@@ -223,6 +226,15 @@ __device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_
 
 // ---------------------------------------------------------------- the kernel
 
+// Where a few rows stand behind many keys there are too few CTAs: the keys then
+// are cut into up to kPreMaxSplits ranges of whole steps, at least kPreMinSteps
+// each, a CTA for each, and the last one to arrive joins their rows in order.
+constexpr int kPreMaxSplits = 16, kPreMinSteps = 3;
+// A range's rows in the workspace, for each tile: [HD / 4][row] four values,
+// then (maximum, sum) [row].
+template <int HD>
+__device__ constexpr size_t part_floats() { return (size_t)2 * kPreRows * (HD + 2); }
+
 // One CTA: one kv head, two tiles of 128 / G tokens x the head's G query heads,
 // every key up to its last token in steps of 128.
 //   warps 0..7   prologue: the tiles' queries (norm, RoPE, f16) to shared
@@ -241,6 +253,7 @@ __device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_
 template <int HD, int PLANES, bool VEC>
 __global__ void __launch_bounds__(PreRoles<PLANES>::kThreads, 1)
 kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsigned inv_g) {
+  // grid: slots, kv heads, ranges of keys
   using L = PreLayout<HD, PLANES>;
   using W = PreRoles<PLANES>;
   constexpr int kThreads = W::kThreads;
@@ -250,7 +263,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_s;
   __shared__ int nan_s[HD];
-  __shared__ int nan_any;
+  __shared__ int nan_any, last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.H / a.Hkv, TT = kPreRows / G;                       // tokens of a tile
   const int g = blockIdx.y, slot = slots - 1 - (int)blockIdx.x;       // long rows first
@@ -303,7 +316,15 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
     return;
   }
   const int keys = pos0 + min(rows, t0 + nt * TT);                    // keys that the last token sees
-  const int steps = (keys + kPreKeys - 1) / kPreKeys;
+  const int all_steps = (keys + kPreKeys - 1) / kPreKeys;
+  const int ranges = min((int)gridDim.z, max(all_steps / kPreMinSteps, 1));
+  const int per = (all_steps + ranges - 1) / ranges, j0 = (int)blockIdx.z * per;   // this range's first step
+  const int steps = min(all_steps - j0, per);
+  if (steps <= 0) {
+    pdl_wait();
+    return;
+  }
+  const int splits = (all_steps + per - 1) / per;                     // ranges with steps
   const int* table = a.table + (size_t)b * a.table_ld;
   if (warp == W::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -389,9 +410,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   uint8_t* there_s = reinterpret_cast<uint8_t*>(ev_s + steps);
   uint8_t* small_s = there_s + steps;
   {
-    const int pages = (keys + kKv8Page - 1) / kKv8Page;
+    const int pages = (keys + kKv8Page - 1) / kKv8Page - j0 * kPrePages;   // of this range on
     for (int i0 = warp * 32; i0 < steps * kPrePages; i0 += kThreads) {
-      const int i = i0 + lane, page = i < pages ? table[i] : -1;
+      const int i = i0 + lane, page = i < pages ? table[j0 * kPrePages + i] : -1;
       const bool in = page >= 0 && page < a.n_pages;
       int ek = kKv8EMin, ev = kKv8EMin;
       if (in) {
@@ -499,7 +520,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
     auto load_ids = [&](int j, int (&p)[2]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int at = j * kPrePages + w * 2 + i;
+        const int at = (j0 + j) * kPrePages + w * 2 + i;
         p[i] = at * kKv8Page < keys ? table[at] : -1;
       }
     };
@@ -512,7 +533,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
       }
     };
     auto load = [&](int k, int j, const int (&p)[2]) {
-      const int left = keys - j * kPreKeys - w * 32 - rr;   // rows of this lane that are keys: it * RP < left
+      const int left = keys - (j0 + j) * kPreKeys - w * 32 - rr;   // rows of this lane that are keys: it * RP < left
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint8_t* from = base + ((size_t)max(p[i], 0) * 2 + k) * half;
@@ -554,7 +575,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
           if (nan)
 #pragma unroll
             for (int it = 0; it < N; ++it)
-              x[it] = without_nan(x[it], nan_s + u * 16, &nan_any, j * kPreKeys + w * 32 + it * RP + rr);
+              x[it] = without_nan(x[it], nan_s + u * 16, &nan_any, (j0 + j) * kPreKeys + w * 32 + it * RP + rr);
         }
 #pragma unroll
         for (int it = 0; it < N; ++it) {
@@ -615,7 +636,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
       for (int c = 0; c < HD; ++c) acc[c] = 0.f;
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
-      const int k0 = j * kPreKeys, ev = ev_s[j];
+      const int k0 = (j0 + j) * kPreKeys, ev = ev_s[j];
       const uint32_t there = there_s[j], small = small_s[j];
       const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
       const float f = qf * pow2f(ek_s[j]);
@@ -772,15 +793,82 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
       l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
       tmem_wait_st();
       if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
-      if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + j * kPrePages, g, ev);
+      if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + (j0 + j) * kPrePages, g, ev);
       tc_fence_before();
       mbar_arrive(&p_full[tile]);
     }
     ok = mbar_wait(&o_full[tile], 0, nullptr) && ok;
     tc_fence_after();
     add_step();
-    const float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
     const bool nans = nan_any != 0;
+    // 32 dims of the row as it stands, times f
+    auto own = [&](int c, float f, float (&y)[32]) {
+      if constexpr (PLANES == 2) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = acc[(c + e) % HD];
+      } else {
+        tmem_ld32(to + c, y);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        y[e] *= f;
+        if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
+      }
+    };
+    float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
+    float weight[kPreMaxSplits];                            // of each range
+    const float4* parts = nullptr;
+    bool mine = true;
+    if (splits > 1) {
+      const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+      unsigned* ticket = reinterpret_cast<unsigned*>(a.ws) + cta;
+      float* part0 = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
+                                              ((size_t)gridDim.x * gridDim.y * 4 + 255) / 256 * 256) +
+                     cta * gridDim.z * part_floats<HD>();
+      float* part = part0 + blockIdx.z * part_floats<HD>() + tile * (part_floats<HD>() / 2);
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        float y[32];
+        own(c, pow2f(E - kPreBias), y);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          reinterpret_cast<float4*>(part)[(c / 4 + q) * kPreRows + i] =
+              make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+      }
+      reinterpret_cast<float2*>(part + HD * kPreRows)[i] = make_float2(m, l);
+      __threadfence();
+      softmax_sync(nt * kPreRows);
+      if (tid == 0) {
+        const unsigned got = atomicAdd(ticket, 1u);
+        last_s = got == (unsigned)(splits - 1);
+        if (last_s) {
+          __threadfence();
+          *ticket = 0u;
+        }
+      }
+      softmax_sync(nt * kPreRows);
+      mine = last_s;
+      if (mine) {
+        __threadfence();
+        const float* ml = part0 + tile * (part_floats<HD>() / 2) + HD * kPreRows;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int z = 0; z < kPreMaxSplits; ++z)
+          if (z < splits) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i).x);
+#pragma unroll
+        for (int z = 0; z < kPreMaxSplits; ++z) {
+          weight[z] = 0.f;
+          if (z < splits) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i);
+            weight[z] = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2p(v.x - top);   // no keys; NaN stays
+            sum += v.y * weight[z];
+          }
+        }
+        inv = sum == 0.f ? 0.f : 1.f / sum;
+        parts = reinterpret_cast<const float4*>(part0 + tile * (part_floats<HD>() / 2));
+      }
+    }
+    if (mine) {
     // rows by threads to rows by warps, over the tile's queries, which nothing
     // reads any more: 16-byte units XORed with the row against bank conflicts
     using T = typename OutOf<PLANES>::type;
@@ -789,16 +877,24 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
 #pragma unroll (PLANES == 2 ? 4 : 1)
     for (int c = 0; c < HD; c += 32) {
       float y[32];
-      if constexpr (PLANES == 2) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = acc[c + e];
+      if (!parts) {
+        own(c, inv, y);
       } else {
-        tmem_ld32(to + c, y);
-      }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        y[e] *= inv;
-        if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
+        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll
+        for (int z = 0; z < kPreMaxSplits; ++z)
+          if (z < splits)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 v = __ldcg(parts + z * (part_floats<HD>() / 4) + (c / 4 + q) * kPreRows + i);
+              y[4 * q] += v.x * weight[z];
+              y[4 * q + 1] += v.y * weight[z];
+              y[4 * q + 2] += v.z * weight[z];
+              y[4 * q + 3] += v.w * weight[z];
+            }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] *= inv;
       }
 #pragma unroll
       for (int q = 0; q < 32 / UE; ++q) {
@@ -833,6 +929,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
       }
     }
     }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -840,6 +937,20 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kPreTmem) : "memory");
   }
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+int pre_slots(int T, int B, int H, int Hkv) { return T / (2 * (kPreRows / (H / Hkv))) + B; }
+// Ranges of keys: as many as one wave of CTAs holds.
+int pre_splits(int slots, int Hkv) {
+  const long long ctas = (long long)slots * Hkv;
+  const int n = (int)(num_sms() / ctas);
+  return n < 1 ? 1 : n > kPreMaxSplits ? kPreMaxSplits : n;
 }
 
 template <int HD, int PLANES, bool VEC>
@@ -851,11 +962,12 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  const int TT = kPreRows / (a.H / a.Hkv), slots = a.T / (2 * TT) + a.B;
+  const int slots = pre_slots(a.T, a.B, a.H, a.Hkv);
   const uintptr_t o = reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.o16);
   const int o_vec = (o & 15) == 0 && a.o_ld % (PLANES == 2 ? 4 : 8) == 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(slots, a.Hkv);
+  const int most = (a.max_pos + kPreKeys - 1) / kPreKeys / kPreMinSteps;     // ranges that the table has room for
+  cfg.gridDim = dim3(slots, a.Hkv, std::max(1, std::min(pre_splits(slots, a.Hkv), most)));
   cfg.blockDim = dim3(PreRoles<PLANES>::kThreads);
   cfg.dynamicSmemBytes =
       1024 + PreLayout<HD, PLANES>::kMeta + kPreStepBytes * ((a.max_pos + kPreKeys - 1) / kPreKeys);
@@ -876,6 +988,12 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+size_t kv8_prefill_ws_bytes(int T, int B, int H, int Hkv, int hd) {
+  const int slots = pre_slots(T, B, H, Hkv), splits = pre_splits(slots, Hkv);
+  const size_t ctas = (size_t)slots * Hkv;
+  return splits == 1 ? 16 : (ctas * 4 + 255) / 256 * 256 + ctas * splits * 2 * kPreRows * (hd + 2) * 4;
+}
 
 cudaError_t launch_kv8_prefill(const Kv8Args& a, cudaStream_t st) {
   if (a.hd == 128) return a.o ? launch<128, 2>(a, st) : launch<128, 1>(a, st);

@@ -121,10 +121,11 @@ def test_binding_wants_enough_host_pairs(lib):
         lib.s2op_kv_remap_pages(P, 1, 1, 1, [0], [], 1)
 
 
-def test_workspace_sizes_are_positive_and_grow(lib):
+def test_workspace_sizes(lib):
     d, p = lib.s2op_attn_decode_kv8_workspace_bytes, lib.s2op_attn_prefill_kv8_workspace_bytes
     assert 0 < d(1, 1, 32, 8, 128) <= d(128, 1, 32, 8, 128)
-    assert 0 < p(1, 1, 32, 8, 128) <= p(8000, 16, 32, 8, 128)
+    assert p(1, 1, 32, 8, 128) > 0 and p(8000, 16, 32, 8, 128) > 0
+    assert d(1, 3, 32, 8, 128) == 0 and p(0, 1, 32, 8, 128) == 0      # refused sizes
 
 
 # the restatement itself, against torch's own conversion

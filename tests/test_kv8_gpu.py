@@ -220,6 +220,24 @@ def test_nan_in_the_cache_is_seen(b):
     assert np.isnan(want[0, :2, 7]).all() and not np.isnan(want[1]).any()
 
 
+def test_few_rows_behind_a_long_context(b):
+    """The keys are cut into ranges: a NaN, a missing page and a page of large
+    values in different ones, rows that see all of them."""
+    for bf16 in (False, True):
+        s = Setup([3000, 1700, 90], [3, 20, 1], 4, 2, 64, seed=19, spread=3)
+        s.codes[s.table[0, 11], 1, 0, 3, 7] = 0xff
+        s.table[1, 60] = -1
+        s.exps[s.table[1, 3]] += 20
+        s.upload()
+        o, ws = s.run(b, "prefill", bf16)
+        torch.cuda.synchronize()
+        _, want = s.check(o, bf16, planes=1 if bf16 else 2)
+        assert np.isnan(want[:3, :2, 7]).all()
+        o2, _ = s.run(b, "prefill", bf16, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(o.nan_to_num(), o2.nan_to_num())
+
+
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
 def test_bad_pages_are_not_followed(b, kind):
     s = Setup([40, 33, 10, 5], [2, 2, 2, 2], 8, 2, 128, seed=10)
