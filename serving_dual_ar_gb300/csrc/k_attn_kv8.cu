@@ -17,10 +17,13 @@ constexpr int kDecMaxDepth = 8;
 constexpr int kDecSmem = 227 * 1024;
 constexpr int kDecFlight = 128 * 1024;
 constexpr int kDecPages = 2;       // pages of a unit of work
-// Units of a run at least: a cut costs a joining, about as long as four units.
-constexpr int kDecMinUnits = 4;
-// What starting and ending a sequence costs, in units: the cut counts it.
-constexpr int kDecSeqUnits = 2;
+// Units of a run at least: a cut costs a joining, about as long as a few units
+// (one sequence of 1,090 tokens: 15.2 us with 3, 16.9 us with 6).
+constexpr int kDecMinUnits = 3;
+// What starting and ending a sequence costs, in units: the cut counts it (128
+// sequences of up to 1,700 tokens: 57.0 us with 2, 55.3 us with 4; 32 of about
+// 1,000: 27.7 and 25.6 us).
+constexpr int kDecSeqUnits = 4;
 // Pieces that are joined at once, one per lane; more are joined in two levels
 // of about the square root each.
 constexpr int kDecFlat = 32;
@@ -370,11 +373,34 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
 
   // The end of a piece: into o if it is all of its sequence, else into the
   // run's slot 1 (a sequence's first piece) or 0 (any other) for the joining.
-  // Nothing waits here: under the stream of pages a round trip to memory takes
-  // microseconds.
   unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);      // [level][run][slot][warp of the run]
   float* parts = reinterpret_cast<float*>(tickets + (size_t)lay.ctas * lay.slices * 4 * lay.heads);
   int open[2] = {-1, -1};
+  // A sequence's pieces are those of the runs f .. f + n - 1; ``per`` of them are
+  // joined at the first level.
+  struct Pieces {
+    int f, n, per;
+  };
+  auto pieces_of = [&](int s) {
+    const unsigned s0 = seg_start(s), s1 = s0 + units_at(pos_s[s & 0xffff]);
+    Pieces x;
+    x.f = (int)cut.of(s0);
+    x.per = x.n = (int)cut.of(s1 - 1) - x.f + 1;
+    if (x.n > kDecFlat)
+      for (x.per = 4; x.per * x.per < x.n;) ++x.per;
+    return x;
+  };
+  // Slot (and ticket) of piece i: its run's slot 1 if it is the first one.
+  auto at = [&](const Pieces& x, int i) { return ((size_t)(x.f + i) * 2 + (i == 0)) * lay.heads + h; };
+  // The number (lane 0) of those that came to the first level's group before.
+  unsigned came[2] = {0, 0};
+  auto arrive = [&](int s) {
+    __threadfence();
+    __syncwarp();
+    const Pieces x = pieces_of(s);
+    const int i = (int)run - x.f;
+    return lane == 0 ? atomicAdd(tickets + at(x, i - i % x.per), 1u) : 0u;
+  };
   // Four values of row i of kv head g of sequence b, at dim d, to o or a slot.
   auto put = [&](float* slot, int b, int g, int i, int d, float4 y) {
     if (slot) {
@@ -442,60 +468,60 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     for (int q = 4 * lane; q < R * HD; q += 128)
       put(slot, b, g, q / HD, q % HD, *reinterpret_cast<const float4*>(buf + q));
     if (!whole) {
-      if (k) open[1] = seg;
-      else open[0] = seg;
+      // a ticket at once: what is asked of it is looked at after the run, when
+      // the pieces before this one have come, most likely, and join
+      const unsigned c = arrive(seg);
+      if (k) {
+        open[1] = seg;
+        came[1] = c;
+      } else {
+        open[0] = seg;
+        came[0] = c;
+      }
     }
   };
-  // After the run: a ticket for each open piece; the last to arrive joins.
+  // After the run: of each open piece's group the last to arrive joins.
   auto join = [&] {
-    if (open[0] < 0 && open[1] < 0) return;
-    __threadfence();
-    __syncwarp();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int s = k ? open[1] : open[0];
       if (s < 0) continue;
-      // its pieces are those of the runs f .. f + n - 1
-      const unsigned s0 = seg_start(s), s1 = s0 + units_at(pos_s[s & 0xffff]);
-      const int f = (int)cut.of(s0), n = (int)cut.of(s1 - 1) - f + 1;
-      auto at = [&](int i) { return ((size_t)(f + i) * 2 + (i == 0)) * lay.heads + h; };
-      int per = n, step = 1;
-      if (n > kDecFlat)
-        for (per = 4; per * per < n;) ++per;
-      int i0 = (int)run - f;
+      const Pieces x = pieces_of(s);
+      const int n = x.n;
+      int per = x.per, step = 1, i0 = (int)run - x.f;
+      unsigned got = k ? came[1] : came[0];
 #pragma unroll 1
       for (;;) {
         i0 -= i0 % per;
         const int count = (min(n - i0, per) + step - 1) / step;
-        unsigned* ticket = tickets + (step == 1 ? 0 : (size_t)lay.ctas * lay.slices * 2 * lay.heads) + at(i0);
-        unsigned got = 0;
-        if (lane == 0) got = atomicAdd(ticket, 1u);
+        unsigned* ticket = tickets + (step == 1 ? 0 : (size_t)lay.ctas * lay.slices * 2 * lay.heads) + at(x, i0);
+        if (step > 1 && lane == 0) got = atomicAdd(ticket, 1u);
         if (__shfl_sync(0xffffffffu, got, 0) != (unsigned)(count - 1)) break;
         __threadfence();
         if (lane == 0) *ticket = 0u;
         const bool done = per >= n;
-        float* slot = done ? nullptr : parts + at(i0) * lay.slot_floats;
+        float* slot = done ? nullptr : parts + at(x, i0) * lay.slot_floats;
         // 128 values a step (a row of 128, two of 64); all steps of four pieces,
         // and of eight if there are few rows, in flight at once, the first ones
         // together with the maxima: a round trip is half a microsecond
         auto gather = [&](auto steps, auto batch) {
           constexpr int ST = decltype(steps)::value, Q = decltype(batch)::value, RPS = 128 / HD, NR = ST * RPS;
           const int row = 4 * lane / HD;             // row within a step
-          float4 x[Q][ST], o[ST];
+          float4 v4[Q][ST], o[ST];
           auto load = [&](int q0) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-              const float* v = parts + at(i0 + min(q0 + q, count - 1) * step) * lay.slot_floats + 4 * lane;
+              const float* v = parts + at(x, i0 + min(q0 + q, count - 1) * step) * lay.slot_floats + 4 * lane;
 #pragma unroll
               for (int i = 0; i < ST; ++i) {
-                x[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (q0 + q < count && i * RPS + row < R) x[q][i] = __ldcg(reinterpret_cast<const float4*>(v + i * 128));
+                v4[q][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q0 + q < count && i * RPS + row < R) v4[q][i] = __ldcg(reinterpret_cast<const float4*>(v + i * 128));
               }
             }
           };
           // piece q's maxima and sums in lane q, its weight for row i in w[i]
           float w[NR], inv[NR], m[NR];
-          const float* ml = parts + at(i0 + min(lane, count - 1) * step) * lay.slot_floats + R * HD;
+          const float* ml = parts + at(x, i0 + min(lane, count - 1) * step) * lay.slot_floats + R * HD;
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
             float2 v = make_float2(-INFINITY, 0.f);
@@ -536,10 +562,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
                   const float y2 = __shfl_sync(0xffffffffu, w[i * RPS + RPS - 1], (q0 + q) & 31);
                   y = row ? y2 : y;
                 }
-                o[i].x += x[q][i].x * y;
-                o[i].y += x[q][i].y * y;
-                o[i].z += x[q][i].z * y;
-                o[i].w += x[q][i].w * y;
+                o[i].x += v4[q][i].x * y;
+                o[i].y += v4[q][i].y * y;
+                o[i].z += v4[q][i].z * y;
+                o[i].w += v4[q][i].w * y;
               }
             q0 += Q;
             if (q0 >= count) break;
