@@ -602,21 +602,33 @@ def run_reference(args):
 def run_attn_kernel(args, b, torch, cfg):
     """Decode attention (K3+K4) on the S2 heads: ``--rows`` sequences, each
     with ``--ctx`` cached keys plus the new one, fp32 pages (``--kv-bf16``:
-    bf16), one pool per layer of ``--layers``; the split count is the
-    runtime's (s2op_attn_decode_pick_split)."""
+    bf16; ``--kv-8bit``: e4m3 blocks, s2op_attn_decode_kv8), one pool per
+    layer of ``--layers``; the split count is the runtime's
+    (s2op_attn_decode_pick_split)."""
     B, ctx, L = args.rows, args.ctx, args.layers
     H, Hkv, hd = cfg.n_heads, cfg.n_kv, cfg.head_dim
     qd, kvd = H * hd, Hkv * hd
     P = 16
     ppseq = (ctx + 1 + P - 1) // P
     n_pages = B * ppseq
-    kvsz = 2 if args.kv_bf16 else 4
+    kvsz = 1 if args.kv_8bit else 2 if args.kv_bf16 else 4
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     nsplit = b.s2op_attn_decode_pick_split(B, cfg.n_heads, Hkv, cfg.head_dim, args.kv_bf16)
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1234)
     dt = torch.bfloat16 if args.kv_bf16 else torch.float32
     pools = [torch.randn((n_pages, 2, Hkv, P, hd), device="cuda", generator=gen).to(dt) for _ in range(L)]
+    if args.kv_8bit:
+        if args.shared_prefix:
+            raise SystemExit("--kv-8bit has no shared-prefix kernel")
+        ids, packed = torch.arange(n_pages, dtype=torch.int32, device="cuda"), []
+        for x in pools:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+            scale = torch.empty((n_pages, 2, Hkv), device="cuda")
+            b.s2op_kv8_pack_pages(x, args.kv_bf16, n_pages, ids, None, codes, scale, n_pages, ids, n_pages, Hkv, hd)
+            packed.append((codes, scale))
+        torch.cuda.synchronize()
+        pools = packed
     perm = torch.randperm(n_pages, generator=torch.Generator().manual_seed(7)).to(torch.int32)
     table = perm.reshape(B, ppseq).contiguous()
     shared = args.shared_prefix // P * P
@@ -637,8 +649,9 @@ def run_attn_kernel(args, b, torch, cfg):
             b.s2op_attn_prefix_planes(pools[l], int(args.kv_bf16), table, Hkv, hd, shared, ctx + 1, wss[l],
                                       stream=st)
     else:
-        ws = torch.zeros(b.s2op_attn_decode_workspace_bytes(B, 1, H, Hkv, hd, nsplit), dtype=torch.uint8,
-                         device="cuda")
+        size = b.s2op_attn_decode_kv8_workspace_bytes(B, 1, H, Hkv, hd) if args.kv_8bit else \
+            b.s2op_attn_decode_workspace_bytes(B, 1, H, Hkv, hd, nsplit)
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
 
     def one():
@@ -647,6 +660,9 @@ def run_attn_kernel(args, b, torch, cfg):
                 b.s2op_attn_decode_shared_prefix(qkv, qd + 2 * kvd, B, H, Hkv, hd, gain, gain, cfg.eps, cs,
                                                  sn, pos, pools[l], int(args.kv_bf16), table, ppseq, shared,
                                                  ctx + 1, o, qd, nsplit=nsplit, workspace=wss[l], stream=st)
+            elif args.kv_8bit:
+                b.s2op_attn_decode_kv8(qkv, qd + 2 * kvd, B, 1, H, Hkv, hd, gain, gain, cfg.eps, cs, sn, ctx + 1,
+                                       pos, *pools[l], n_pages, table, ppseq, o, False, qd, ws, stream=st)
             else:
                 b.s2op_attn_decode(qkv, qd + 2 * kvd, B, 1, H, Hkv, hd, gain, gain, cfg.eps, cs, sn, pos,
                                    pools[l], int(args.kv_bf16), table, ppseq, o, qd, nsplit=nsplit,
@@ -672,7 +688,7 @@ def run_attn_kernel(args, b, torch, cfg):
     phases = prefix_phase_trace(b, torch, one, B, Hkv) if (shared and args.trace) else None
     print(json.dumps({"kernel": "attn", "rows": B, "ctx": ctx, "shared_prefix": shared, "layers": L,
                       "prefix_phases_us": phases, "nsplit": nsplit,
-                      "kv": "bf16" if args.kv_bf16 else "fp32", "launches": launches,
+                      "kv": "e4m3" if args.kv_8bit else "bf16" if args.kv_bf16 else "fp32", "launches": launches,
                       "us_per_launch": 1000 * ms / launches, "bytes_per_launch": per,
                       "gbs": gbs, "frac_hbm": gbs / pk["hbm_gbs"], "peak_kind": kind}), flush=True)
 
@@ -1089,6 +1105,7 @@ def main():
                     help="skip the DAC vocoder record the default (workload 1) run adds")
     ap.add_argument("--int8", action="store_true",
                     help="per-channel INT8 weights (reported separately; not the bf16 headline)")
+    ap.add_argument("--kv-8bit", action="store_true", help="--kernel attn: 8-bit KV cache (e4m3, a scale per page and head)")
     ap.add_argument("--kv-bf16", action="store_true",
                     help="bf16 Slow AR KV cache (default fp32)")
     ap.add_argument("--persist", action="store_true",
