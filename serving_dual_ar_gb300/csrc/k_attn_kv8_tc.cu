@@ -128,6 +128,7 @@ S2_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+S2_DEV void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" :: "l"(p)); }
 // A barrier of the n threads that are softmax rows.
 S2_DEV void softmax_sync(int n) { asm volatile("bar.sync 1, %0;" :: "r"(n) : "memory"); }
 template <int N>
@@ -273,7 +274,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   __shared__ int seq_s;
   if (warp == 0) {
     int n = 0;
-    for (int b = lane; b < a.B; b += 32) n += (a.row0[b] / (2 * TT) + b <= slot) ? 1 : 0;
+    for (int b = lane; b < a.B; b += 32) {
+      prefetch_l1(a.pos + b);                // wanted next
+      n += (a.row0[b] / (2 * TT) + b <= slot) ? 1 : 0;
+    }
     n = __reduce_add_sync(0xffffffffu, n) - 1;
     if (lane == 0) seq_s = n;
   }
@@ -339,8 +343,8 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   // pair of f16 is good to 2^-22 of a value, and to 2^-34 of the largest)
   float qf;                                 // the power of two back
   {
-    constexpr int LPR = HD / 8, RPS = 32 / LPR, NB = 2;               // lanes per row, rows per load, loads at a time
-    const int l = lane % LPR, d = 8 * l, dh = d % (HD / 2);
+    constexpr int LPR = HD / 8, TPW = 32 / LPR;                       // lanes of a row, tokens of a warp
+    const int l = lane % LPR, d = 8 * l;
     float gain[8];
     load8<VEC>(a.q_gain + d, gain);
     float mx = 0.f;
@@ -352,50 +356,62 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
     const float up = pow2f(9 - ex);
 #pragma unroll
     for (int e = 0; e < 8; ++e) gain[e] *= up * (HD == 128 ? 0.127517431f : 0.180336880f);
-    const bool low = l < LPR / 2;
+    // a token's heads one after the other, two in flight: its RoPE rows once
 #pragma unroll 1
-    for (int i1 = warp * NB * RPS; i1 < 2 * kPreRows; i1 += kThreads / 32 * NB * RPS) {
-      const int tile = i1 / kPreRows;
+    for (int q0 = warp * TPW; q0 < 2 * TT; q0 += kThreads / 32 * TPW) {
+      const int q = q0 + lane / LPR, tile = q >= TT ? 1 : 0, i0 = (q - tile * TT) * G;
+      const bool live = q < 2 * TT && t0 + q < rows;
+      const int tok = live ? t0 + q : t0;
+      const float* x0 = a.qkv + (size_t)(r0 + tok) * a.qkv_ld + g * G * HD + d;
       uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile + (d / 64) * kBlock;
-      float x[NB][8], co[NB][8], si[NB][8];
-      bool live[NB];
+      float co[8], si[8];
+      load8<VEC>(a.rope_cos + (size_t)(pos0 + tok) * (HD / 2) + d % (HD / 2), co);
+      load8<VEC>(a.rope_sin + (size_t)(pos0 + tok) * (HD / 2) + d % (HD / 2), si);
+      const float turn = l < LPR / 2 ? -1.f : 1.f;
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int i = i1 % kPreRows + k * RPS + lane / LPR, tt = i * inv_g >> 16, t = t0 + tile * TT + tt;
-        live[k] = tt < TT && t < rows;
-        const int tok = live[k] ? t : t0;
-        load8<VEC>(a.qkv + (size_t)(r0 + tok) * a.qkv_ld + (g * G + i - tt * G) * HD + d, x[k]);
-        load8<VEC>(a.rope_cos + (size_t)(pos0 + tok) * (HD / 2) + dh, co[k]);
-        load8<VEC>(a.rope_sin + (size_t)(pos0 + tok) * (HD / 2) + dh, si[k]);
-      }
+      for (int e = 0; e < 8; ++e) si[e] *= turn;
+#pragma unroll 1
+      for (int h = 0; h < G; h += 2) {
+        float x[2][8];
+        load8<VEC>(x0 + h * HD, x[0]);
+        load8<VEC>(x0 + min(h + 1, G - 1) * HD, x[1]);
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int i = i1 % kPreRows + k * RPS + lane / LPR;
-        float ss = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[k][e] * x[k][e];
+          for (int e = 0; e < 8; ++e) ss += x[k][e] * x[k][e];
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float f = live[k] ? rsqrtf(ss * (1.f / HD) + a.eps) : 0.f;
-        uint32_t hi[4], lo[4];
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float f = live ? rsqrtf(ss * (1.f / HD) + a.eps) : 0.f;
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = live[k] ? x[k][e] * (f * gain[e]) : 0.f;
-          const float w = __shfl_xor_sync(0xffffffffu, y, LPR / 2);
-          x[k][e] = y * co[k][e] + (low ? -w : w) * si[k][e];
+          for (int e = 0; e < 8; ++e) x[k][e] = live ? x[k][e] * (f * gain[e]) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float w0 = __shfl_xor_sync(0xffffffffu, x[k][2 * e], LPR / 2);
+            const float w1 = __shfl_xor_sync(0xffffffffu, x[k][2 * e + 1], LPR / 2);
+            const float u = x[k][2 * e] * co[2 * e] + w0 * si[2 * e];
+            const float v = x[k][2 * e + 1] * co[2 * e + 1] + w1 * si[2 * e + 1];
+            const __half2 y = __floats2half2_rn(u, v);
+            const float2 yf = __half22float2(y);
+            const __half2 r = __floats2half2_rn(u - yf.x, v - yf.y);
+            hi[e] = *reinterpret_cast<const uint32_t*>(&y);
+            lo[e] = *reinterpret_cast<const uint32_t*>(&r);
+          }
+          if (q < 2 * TT && h + k < G) {
+            uint8_t* to = q_hi + sw128_offset(i0 + h + k, l % 8);
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (PLANES == 2) *reinterpret_cast<uint4*>(to + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 h = __floats2half2_rn(x[k][2 * e], x[k][2 * e + 1]);
-          const float2 hf = __half22float2(h);
-          const __half2 r = __floats2half2_rn(x[k][2 * e] - hf.x, x[k][2 * e + 1] - hf.y);
-          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-          lo[e] = *reinterpret_cast<const uint32_t*>(&r);
-        }
-        uint8_t* to = q_hi + sw128_offset(i, l % 8);
-        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (PLANES == 2) *reinterpret_cast<uint4*>(to + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+    }
+    // rows of no token are zeros: the rows beside them must not depend on what
+    // the memory held, not even by when their maximum is taken over
+    for (int i = tid; i < (kPreRows - TT * G) * 2 * PLANES * (HD / 8); i += kThreads) {
+      const int c = i % (HD / 8), row = TT * G + i / (HD / 8) / (2 * PLANES), at = i / (HD / 8) % (2 * PLANES);
+      *reinterpret_cast<uint4*>(sm + L::kQ + at * L::kTile + c / 8 * kBlock + sw128_offset(row, c % 8)) =
+          make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async();
     mbar_arrive(&q_full);
