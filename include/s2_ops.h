@@ -246,16 +246,17 @@ int s2op_attn_decode_noalloc(const float* qkv, int qkv_ld, int B, int m, int H, 
  * token depend neither on the batch nor on whether a prompt or a single step
  * appended it.  New rows in a block with older ones take the larger of both
  * scales; where it grows, the older rows are rescaled (exact, but for values
- * that become e4m3 subnormals).  Scales must be powers of two as these calls
- * write them: of a stored scale the exponent field alone is read.
+ * that become e4m3 subnormals).  Scales are powers of two as these calls write
+ * them: in place of another value the power of two next to it is taken.
  *
  * hd is 64 or 128, H / Hkv 1..8, B 1..1024.  qkv rows as in s2op_attn_decode:
  * [q (H*hd) | k (Hkv*hd) | v (Hkv*hd)], fp32, qkv_ld >= (H + 2 Hkv) hd;
  * rope_cos / rope_sin [n_pos][hd/2]; sequence b's page j is table[b *
  * table_ld + j].  o: rows of H*hd values, pitch o_ld, fp32 (o_bf16 = 0) or
  * bf16 (1).  Softmax statistics and sums are fp32; the products run on the
- * tensor cores with q and the probabilities as f16 pairs (hi + lo, 22 bits)
- * for an fp32 output, e4m3 values being exact in f16.
+ * tensor cores, e4m3 values being exact in f16, with q and the probabilities
+ * as f16 pairs (hi + lo, 22 bits) -- in prompt attention with a bf16 output as
+ * single f16 (11 bits), since its own rounding is coarser by 8 times.
  *
  * A sequence whose new positions do not lie in [0, min(n_pos, 16 table_ld))
  * (pos[b] = -1, for instance: a padded batch) is left out: nothing is stored

@@ -21,10 +21,11 @@ constexpr int kKv8EMin = -32, kKv8EMax = 32;
 // ---------------------------------------------------------------- scales
 
 S2_DEV float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| <= 126
-// Exponent of a stored scale (its exponent field alone is read, clamped to
-// the range that the kernels write).
+// Exponent of a stored scale: of the power of two next to it (one that a library
+// function computed may lie a bit beside it), within the range that the
+// kernels write.
 S2_DEV int kv8_scale_exp(float s) {
-  const int e = (int)((__float_as_uint(s) >> 23) & 0xff) - 127;
+  const int e = (int)(((__float_as_uint(s) & 0x7fffffffu) + 0x400000u) >> 23) - 127;
   return min(max(e, kKv8EMin), kKv8EMax);
 }
 // The smallest e in [-32, 32] with amax <= 448 * 2^e (448 = 1.75 * 2^8);

@@ -171,6 +171,22 @@ def test_block_scales_far_apart(b, kind):
 
 
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_scales_a_bit_beside_a_power_of_two(b, kind):
+    s = Setup([150, 61], [1, 1], 8, 2, 128, seed=17)
+    d = s.upload()
+    d["scale"].mul_(torch.tensor([1 - 2.0 ** -23, 1 + 2.0 ** -22], device="cuda").repeat(s.n_pages)[:s.n_pages, None, None])
+    touched = {int(s.table[0, 9]), int(s.table[1, 3])}
+    o, _ = s.run(b, kind, False)
+    torch.cuda.synchronize()
+    got = d["scale"].clone()
+    exact = torch.from_numpy((2.0 ** s.exps).astype(np.float32)).cuda()
+    rest = [p for p in range(s.n_pages) if p not in touched]
+    assert ((got[rest] / exact[rest] - 1).abs() < 1e-6).all()      # left as they were
+    d["scale"][rest] = exact[rest]
+    s.check(o, False)
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
 def test_scale_grows_and_old_rows_move(b, kind):
     s = Setup([5, 12, 30], [2, 2, 2], 8, 2, 128, seed=6)
     s.qkv[:, (s.H + s.Hkv) * s.hd:] *= np.float32(300)
