@@ -262,16 +262,18 @@ int s2op_attn_decode_noalloc(const float* qkv, int qkv_ld, int B, int m, int H, 
  * (pos[b] = -1, for instance: a padded batch) is left out: nothing is stored
  * for it and its rows of o are zero.  A table entry outside [0, n_pages) is
  * not followed: its keys count as masked and its new rows are not stored (a
- * row without any key is zero).  No two sequences of a call may append to
- * the same page; reading a page together is fine.  Pages' rows behind the
- * last appended one keep their bytes.  workspace: zero-initialised, zero
- * where it has to be again on exit; calls that may overlap in time need one
- * each. */
+ * row without any key is zero).  Sequences of a call may read a page together,
+ * but one that a sequence appends to must not be among another's pages.
+ * Pages' rows behind the last appended one keep their bytes.  workspace
+ * (16-byte aligned): zero-initialised, zero where it has to be again on exit.
+ * One of the largest size serves calls of both kinds and of any sizes one after
+ * the other; calls that may overlap in time need one each. */
 
 /* Decode attention for B sequences with m new rows each, row b*m + i at
  * position pos[b] + i: q and k normed and rotated, k and v stored, then
  * attention over all keys up to the row's position.  m * H / Hkv <= 8, B * Hkv *
- * table_ld < 2^31. */
+ * table_ld < 2^31.  The workspace's size depends on m, H, Hkv and hd and grows
+ * with m. */
 size_t s2op_attn_decode_kv8_workspace_bytes(int B, int m, int H, int Hkv, int hd);
 int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int Hkv, int hd,
                          const float* q_gain, const float* k_gain, float eps, const float* rope_cos,
@@ -283,7 +285,8 @@ int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, int H, int 
  * row0[b] .. row0[b+1] - 1 (row0: B + 1 non-decreasing entries on the device;
  * none is fine) at positions pos0[b], pos0[b] + 1, ..., behind pos0[b] cached
  * tokens.  T (at most 2^24) bounds row0[B]; rows in no sequence are left as they
- * are.  Positions at or beyond 2^20 count as outside the table. */
+ * are.  Positions at or beyond 2^20 count as outside the table.  The workspace's size
+ * depends on hd alone. */
 size_t s2op_attn_prefill_kv8_workspace_bytes(int T, int B, int H, int Hkv, int hd);
 int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B, const int32_t* row0,
                           const int32_t* pos0, int H, int Hkv, int hd, const float* q_gain,

@@ -36,6 +36,7 @@ struct DecLayout {
   int buf;                     // a warp's buffer: its rows of HD floats, 4 at least
   int slot_floats;             // one partial: R rows of HD values, then (m, l) of each
   int ctas;
+  int parts_off;               // of the partials in the workspace, bytes
   int o_vec;                   // rows of o on 16-byte (bf16: 8-byte) boundaries
   unsigned inv_g;              // i / G = i * inv_g >> 16 for rows i
 };
@@ -374,7 +375,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   // The end of a piece: into o if it is all of its sequence, else into the
   // run's slot 1 (a sequence's first piece) or 0 (any other) for the joining.
   unsigned* tickets = reinterpret_cast<unsigned*>(a.ws);      // [level][run][slot][warp of the run]
-  float* parts = reinterpret_cast<float*>(tickets + (size_t)lay.ctas * lay.slices * 4 * lay.heads);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.parts_off);
   int open[2] = {-1, -1};
   // A sequence's pieces are those of the runs f .. f + n - 1; ``per`` of them are
   // joined at the first level.
@@ -847,17 +848,11 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   join();
 }
 
-int num_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 DecLayout dec_layout(int B, int m, int H, int Hkv, int hd) {
   DecLayout l;
   const int G = H / Hkv, R = m * G;
-  l.ctas = num_sms();
+  l.ctas = kv8_sms();
+  l.parts_off = (int)kv8_ticket_bytes(l.ctas);
   l.groups = (Hkv + kDecWarps - 1) / kDecWarps;
   l.heads = (Hkv + l.groups - 1) / l.groups;
   l.slices = kDecWarps / l.heads;
@@ -878,7 +873,7 @@ DecLayout dec_layout(int B, int m, int H, int Hkv, int hd) {
 
 size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd) {
   const DecLayout l = dec_layout(B, m, H, Hkv, hd);
-  return (size_t)l.ctas * l.slices * 2 * l.heads * (2 + l.slot_floats) * 4;
+  return kv8_ticket_bytes(l.ctas) + (size_t)l.ctas * l.slices * 2 * l.heads * l.slot_floats * 4;
 }
 
 cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st) {

@@ -253,7 +253,7 @@ __device__ constexpr size_t part_floats() { return (size_t)2 * kPreRows * (HD + 
 // to nearest, in registers.
 template <int HD, int PLANES, bool VEC>
 __global__ void __launch_bounds__(PreRoles<PLANES>::kThreads, 1)
-kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsigned inv_g) {
+kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, int o_vec, unsigned inv_g) {
   // grid: slots, kv heads, ranges of keys
   using L = PreLayout<HD, PLANES>;
   using W = PreRoles<PLANES>;
@@ -838,9 +838,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
     if (splits > 1) {
       const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
       unsigned* ticket = reinterpret_cast<unsigned*>(a.ws) + cta;
-      float* part0 = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
-                                              ((size_t)gridDim.x * gridDim.y * 4 + 255) / 256 * 256) +
-                     cta * gridDim.z * part_floats<HD>();
+      float* part0 = reinterpret_cast<float*>(static_cast<char*>(a.ws) + parts_off) + cta * gridDim.z * part_floats<HD>();
       float* part = part0 + blockIdx.z * part_floats<HD>() + tile * (part_floats<HD>() / 2);
 #pragma unroll
       for (int c = 0; c < HD; c += 32) {
@@ -955,17 +953,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int o_vec, unsi
   }
 }
 
-int num_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
 int pre_slots(int T, int B, int H, int Hkv) { return T / (2 * (kPreRows / (H / Hkv))) + B; }
 // Ranges of keys: as many as one wave of CTAs holds.
 int pre_splits(int slots, int Hkv) {
   const long long ctas = (long long)slots * Hkv;
-  const int n = (int)(num_sms() / ctas);
+  const int n = (int)(kv8_sms() / ctas);
   return n < 1 ? 1 : n > kPreMaxSplits ? kPreMaxSplits : n;
 }
 
@@ -994,7 +986,7 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return s2_launch(&cfg, k, a, slots, o_vec, 65536u / (a.H / a.Hkv) + 1);   // i / G = i * inv_g >> 16, i < 128
+  return s2_launch(&cfg, k, a, slots, (int)kv8_ticket_bytes(kv8_sms()), o_vec, 65536u / (a.H / a.Hkv) + 1);   // i / G = i * inv_g >> 16, i < 128
 }
 template <int HD, int PLANES>
 cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
@@ -1005,10 +997,9 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv8_prefill_ws_bytes(int T, int B, int H, int Hkv, int hd) {
-  const int slots = pre_slots(T, B, H, Hkv), splits = pre_splits(slots, Hkv);
-  const size_t ctas = (size_t)slots * Hkv;
-  return splits == 1 ? 16 : (ctas * 4 + 255) / 256 * 256 + ctas * splits * 2 * kPreRows * (hd + 2) * 4;
+size_t kv8_prefill_ws_bytes(int hd) {   // the ranges of all slots and heads are one wave, an SM each
+  const int sms = kv8_sms();
+  return kv8_ticket_bytes(sms) + (size_t)sms * 2 * kPreRows * (hd + 2) * 4;
 }
 
 cudaError_t launch_kv8_prefill(const Kv8Args& a, cudaStream_t st) {

@@ -18,6 +18,20 @@ namespace s2 {
 constexpr int kKv8Page = 16;
 constexpr int kKv8EMin = -32, kKv8EMax = 32;
 
+// ---------------------------------------------------------------- workspace
+
+inline int kv8_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+// Tickets come first in a workspace, partial sums behind them from the same
+// place on in every call: what one call leaves there another of other sizes, or
+// of the other kind, never takes for a ticket.  Tickets: two levels of two slots
+// for up to eight warps an SM (decode), one an SM (prompts).
+inline size_t kv8_ticket_bytes(int sms) { return (size_t)sms * 2 * 2 * 8 * 4; }
+
 // ---------------------------------------------------------------- scales
 
 S2_DEV float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| <= 126

@@ -252,7 +252,7 @@ cudaError_t launch_kv8_append(const Kv8Args& a, cudaStream_t st);
 // Attention of prompts whose rows launch_kv8_append put into their pages (right
 // before it in the stream).
 cudaError_t launch_kv8_prefill(const Kv8Args& a, cudaStream_t st);
-size_t kv8_prefill_ws_bytes(int T, int B, int H, int Hkv, int hd);
+size_t kv8_prefill_ws_bytes(int hd);
 constexpr int kKv8MaxPrompt = 1 << 20;   // positions of a prompt
 size_t kv8_decode_ws_bytes(int B, int m, int H, int Hkv, int hd);
 cudaError_t launch_kv8_decode(const Kv8Args& a, cudaStream_t st);

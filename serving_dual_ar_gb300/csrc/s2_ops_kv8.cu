@@ -87,7 +87,7 @@ extern "C" int s2op_attn_decode_kv8(const float* qkv, int qkv_ld, int B, int m, 
 
 extern "C" size_t s2op_attn_prefill_kv8_workspace_bytes(int T, int B, int H, int Hkv, int hd) {
   if (!shape_ok(B, H, Hkv, hd) || T < 1 || T > (1 << 24)) return 0;
-  return kv8_prefill_ws_bytes(T, B, H, Hkv, hd);
+  return kv8_prefill_ws_bytes(hd);
 }
 
 extern "C" int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B, const int32_t* row0,

@@ -125,6 +125,8 @@ def test_workspace_sizes(lib):
     d, p = lib.s2op_attn_decode_kv8_workspace_bytes, lib.s2op_attn_prefill_kv8_workspace_bytes
     assert 0 < d(1, 1, 32, 8, 128) <= d(128, 1, 32, 8, 128)
     assert p(1, 1, 32, 8, 128) > 0 and p(8000, 16, 32, 8, 128) > 0
+    assert p(1, 1, 32, 8, 128) == p(8000, 16, 32, 8, 128) == p(8000, 1, 7, 7, 128)   # fewer rows never need more
+    assert d(1, 1, 32, 8, 128) == d(128, 1, 32, 8, 128) < d(1, 2, 32, 8, 128)
     assert d(1, 3, 32, 8, 128) == 0 and p(0, 1, 32, 8, 128) == 0      # refused sizes
 
 

@@ -450,6 +450,31 @@ def test_two_streams_with_a_workspace_each(b):
         s.check(o, False)
 
 
+def test_one_workspace_for_calls_of_all_sizes(b):
+    """Prompts of other sizes and kv heads, single tokens and prompts in turn
+    over one workspace: what a call leaves in it is no ticket to the next."""
+    sizes = [b.s2op_attn_decode_kv8_workspace_bytes(4, m, H, Hkv, hd) for m, H, Hkv, hd in
+             ((1, 32, 8, 128), (2, 9, 3, 128), (1, 20, 20, 64))]
+    sizes += [b.s2op_attn_prefill_kv8_workspace_bytes(T, B, 8, 2, hd) for T, B in ((8000, 1), (3, 2)) for hd in (64, 128)]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    calls = [
+        ("prefill", [2500], [3], 32, 8, 128),
+        ("prefill", [1500, 900], [150, 3], 22, 11, 64),     # 66 CTAs a range
+        ("decode", [1090, 900, 1003], [1] * 3, 32, 8, 128),
+        ("prefill", [1100] * 8, [2] * 8, 18, 9, 128),       # 72 CTAs a range
+        ("decode", [2000, 77], [2] * 2, 9, 3, 128),
+        ("decode", [2000, 1000], [1] * 2, 20, 20, 64),      # three groups of kv heads
+        ("prefill", [2500], [3], 32, 8, 128),
+        ("decode", [41], [1], 32, 8, 128),
+    ]
+    for i, (kind, pos, new, H, Hkv, hd) in enumerate(calls):
+        s = Setup(pos, new, H, Hkv, hd, seed=40 + i)
+        s.upload()
+        o, _ = s.run(b, kind, False, ws=ws)
+        torch.cuda.synchronize()
+        s.check(o, False)
+
+
 # --------------------------------------------------------------------- packing
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
