@@ -961,12 +961,16 @@ int pre_splits(int slots, int Hkv) {
   return n < 1 ? 1 : n > kPreMaxSplits ? kPreMaxSplits : n;
 }
 
+static_assert(1024 + PreLayout<128, 2>::kMeta + kPreStepBytes * (kKv8MaxPrompt / kPreKeys) <= kPreSmem - 2048 &&
+                  1024 + PreLayout<128, 1>::kMeta + kPreStepBytes * (kKv8MaxPrompt / kPreKeys) <= kPreSmem - 2048,
+              "the longest prompt's steps");
+
 template <int HD, int PLANES, bool VEC>
 cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   auto k = kv8_prefill_kernel<HD, PLANES, VEC>;
   static bool attr = false;
   if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 4096);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 2048);   // the rest: static
     if (e != cudaSuccess) return e;
     attr = true;
   }

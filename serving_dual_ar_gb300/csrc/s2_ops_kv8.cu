@@ -112,7 +112,7 @@ extern "C" int s2op_attn_prefill_kv8(const float* qkv, int qkv_ld, int T, int B,
 static bool pack_ok(const void* kv, const void* kv8, const void* scale, const int32_t* src, const int32_t* dst,
                     int n_src, int n_dst, int n, int Hkv, int hd) {
   return kv && kv8 && scale && src && dst && n_src >= 1 && n_dst >= 1 && n >= 0 && Hkv >= 1 && Hkv <= 4096 &&
-         (long long)n * 2 * Hkv <= 0x7fffffffLL && (hd == 64 || hd == 128) && aligned(kv, 16) && aligned(kv8, 16) &&
+         (long long)n * 2 * Hkv <= 0x7ffffffcLL && (hd == 64 || hd == 128) && aligned(kv, 16) && aligned(kv8, 16) &&
          aligned(scale, 4) && aligned(src, 4) && aligned(dst, 4);
 }
 

@@ -55,7 +55,7 @@ def test_prefill_refuses(lib, kw):
 
 @pytest.mark.parametrize("change", [
     {0: None}, {3: None}, {5: None}, {6: None}, {8: None}, {2: 0}, {7: 0}, {9: -1}, {10: 0}, {11: 96}, {0: P + 8},
-    {5: P + 4}, {6: P + 2}, {3: P + 1}, {8: P + 2}, {9: 2 ** 30, 10: 8}], ids=str)
+    {5: P + 4}, {6: P + 2}, {3: P + 1}, {8: P + 2}, {9: 2 ** 30, 10: 8}, {9: 2 ** 30 - 1, 10: 1}], ids=str)
 def test_pack_refuses(lib, change):
     # kv, bf16, n_src, src, fill, kv8, scale, n_dst, dst, n, Hkv, hd, stream
     a = [P, 0, 4, P, None, P, P, 4, P, 2, 2, 128, None]

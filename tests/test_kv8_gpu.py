@@ -475,6 +475,48 @@ def test_one_workspace_for_calls_of_all_sizes(b):
         s.check(o, False)
 
 
+@pytest.mark.parametrize("hd,bf16", [(128, False), (128, True), (64, False)])
+def test_prompt_whose_table_has_the_longest_row(b, hd, bf16):
+    """A table and RoPE rows for 2^20 positions: the call takes the sizes that its
+    documentation gives."""
+    s = Setup([50, 0], [3, 20], 4, 2, hd, seed=23)
+    d = s.upload()
+    wide = torch.full((2, 65536), -1, dtype=torch.int32, device="cuda")
+    wide[:, :s.cols] = d["table"]
+    for k in ("cos", "sin"):
+        x = torch.zeros((2 ** 20, hd // 2), device="cuda")
+        x[:s.n_pos] = d[k]
+        d[k] = x
+    d["table"] = wide
+    cols, n_pos = s.cols, s.n_pos
+    s.cols, s.n_pos = 65536, 2 ** 20
+    o, _ = s.run(b, "prefill", bf16)
+    torch.cuda.synchronize()
+    s.cols, s.n_pos = cols, n_pos
+    s.check(o, bf16, planes=1 if bf16 else 2)
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_pool_of_more_than_four_gigabytes(b, kind):
+    """Pages whose bytes lie beyond 2^32."""
+    s = Setup([70, 33], [2, 2], 16, 8, 128, seed=24)
+    small = s.upload()
+    n = 2 ** 32 // (2 * 8 * 16 * 128) + s.n_pages
+    off = n - s.n_pages
+    codes = torch.zeros((n, 2, 8, 16, 128), dtype=torch.uint8, device="cuda")
+    scale = torch.ones((n, 2, 8), device="cuda")
+    codes[off:] = small["codes"]
+    scale[off:] = small["scale"]
+    s.d = dict(small, codes=codes, scale=scale, table=small["table"] + off)
+    few, s.n_pages = s.n_pages, n
+    o, _ = s.run(b, kind, False)
+    torch.cuda.synchronize()
+    s.n_pages = few
+    s.d["codes"], s.d["scale"] = codes[off:], scale[off:]
+    assert not codes[:off].any()
+    s.check(o, False)
+
+
 # --------------------------------------------------------------------- packing
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
