@@ -269,6 +269,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   };
 
   uint32_t qa[KS][4];        // query fragments: {hi, lo} x {dims 4t, 4t+1 | 4t+2, 4t+3}
+  uint32_t polls = 2000000;  // of a wait; 1 after one that gave up
   float qf = 0.f;            // 2^-(exponent given to row r's query)
   DecState<HD> st;
   int seg = -1, pos = 0, b = 0, g = 0;
@@ -286,7 +287,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     g = head_of(s);
     pos = pos_s[b];
     st.m = -INFINITY;
-    st.l = 0.f;
+    st.l = polls > 1 ? 0.f : __int_as_float(0x7fffffff);
     st.E = kKv8EMin;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -689,6 +690,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   UnitBits bits{0u, 0u};
   int slot = 0;
   uint32_t phase = 0;
+  int issued = n;            // units that were copied, or will be
 #pragma unroll 1
   for (int t = 0;; ++t) {
     const int src = t & 31;
@@ -707,8 +709,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     const uint32_t exps = __shfl_sync(0xffffffffu, bits.exps, src);
     const uint32_t there = __shfl_sync(0xffffffffu, bits.there, src);
     uint8_t* blk = ring + slot * UB;
-    const bool ok = mbar_wait(&bars[warp][slot], phase, nullptr);
-    if (__all_sync(0xffffffffu, ok) && there) {
+    const bool came = __all_sync(0xffffffffu, mbar_wait(&bars[warp][slot], phase, nullptr, polls));
+    if (!came) {              // gave up: no more copies, outputs from here on are NaN
+      polls = 1;
+      st.l = __int_as_float(0x7fffffff);
+      issued = min(issued, t + D);
+    }
+    if (came && there) {
       int ke[kDecPages] = {(int)(exps & 0xff) - 64, (int)(exps >> 16 & 0xff) - 64};
       int ve[kDecPages] = {(int)(exps >> 8 & 0xff) - 64, (int)(exps >> 24) - 64};
       const bool tail = (j + kDecPages) * kKv8Page > pos || there != 3;
@@ -839,12 +846,15 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     }
     __syncwarp();
     // the slot is free: the unit D further on
-    if (t + D < n && lane == ((t + D) & 31)) issue(src + D < 32 ? cur : nxt, slot);
+    if (t + D < issued && lane == ((t + D) & 31)) issue(src + D < 32 ? cur : nxt, slot);
     if (++slot == D) {
       slot = 0;
       phase ^= 1;
     }
   }
+  if (polls == 1)            // copies that were not seen to end are waited for once more
+#pragma unroll 1
+    for (int k = 0; k < min(D, n); ++k) mbar_wait(&bars[warp][k], (issued - 1 - k) / D & 1, nullptr);
   join();
 }
 

@@ -456,7 +456,6 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
-  bool ok = true;
 
   if (warp >= W::kMma) {
     // ------------------------------------------------ products
@@ -486,24 +485,24 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             umma_ts(tm + 256 + t * 128, tm + t * 128 + p * 64 + ks * 8, vt + (ks * 2048 >> 4), i_pv,
                     p < PLANES - 1 || ks > 0 ? 1u : acc);
       };
-      ok = mbar_wait(&q_full, 0, nullptr) && ok;
-      ok = mbar_wait(&k_full[0], 0, nullptr) && ok;
+      mbar_wait(&q_full, 0, nullptr);
+      mbar_wait(&k_full[0], 0, nullptr);
       tc_fence_after();
       for (int t = 0; t < nt; ++t) qk(t, 0);
       umma_commit(&k_empty[0]);
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int st = j % ST, sn = (j + 1) % ST;
-        ok = mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr) && ok;
+        mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr);
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
-          ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr) && ok;
+          mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr);
           tc_fence_after();
           pv(t, st, PLANES == 1 || small_s[j] ? 1u : 0u);
           if (t == nt - 1) umma_commit(&v_empty[st]);
           if (j + 1 < steps) {
             if (t == 0) {
-              ok = mbar_wait(&k_full[sn], (uint32_t)((j + 1) / ST) & 1u, nullptr) && ok;
+              mbar_wait(&k_full[sn], (uint32_t)((j + 1) / ST) & 1u, nullptr);
               tc_fence_after();
             }
             qk(t, sn);
@@ -581,7 +580,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         for (int i = 0; i < 2; ++i)
           by[i] = __float2half2_rn(page[i] < 0 || (small >> i & 1) ? 0.f
                                                                    : pow2f(max(kv8_scale_exp(sc[k][i]) - top, -60)));
-        ok = mbar_wait(kind ? &v_empty[st] : &k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr) && ok;
+        mbar_wait(kind ? &v_empty[st] : &k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr);
         uint8_t* to = sm + (kind ? L::kV : L::kK) + st * L::kTile + (u / 4) * kBlock;
         if (kind) {
           uint32_t nan = 0;
@@ -620,329 +619,337 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
     // ------------------------------------------------ softmax, a row per thread
     more_regs<W::kRegsSoftmax>();
     if (warp / 4 < nt) {
-    const int tile = warp / 4, i = tid % kPreRows, tt = i * inv_g >> 16, t = t0 + tile * TT + tt;
-    const bool on = tt < TT && t < rows;
-    const int lim = on ? pos0 + t : -1;                    // last key of this row
-    const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
-    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-    const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
-    float m = -INFINITY, l = 0.f;
-    int E = kKv8EMin;
-    float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
-    auto clear_o = [&] {
-      const float zero[8] = {};
+      const int tile = warp / 4, i = tid % kPreRows, tt = i * inv_g >> 16, t = t0 + tile * TT + tt;
+      const bool on = tt < TT && t < rows;
+      const int lim = on ? pos0 + t : -1;                    // last key of this row
+      const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
+      const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+      const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
+      float m = -INFINITY, l = 0.f;
+      int E = kKv8EMin;
+      float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
+      auto clear_o = [&] {
+        const float zero[8] = {};
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 8) tmem_st8(to + c, zero);
-    };
-    auto add_step = [&] {                                  // the last step's P V to it
-      if constexpr (PLANES == 2) {
-#pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          uint32_t y[32];
-          tmem_ld32_start(to + c, y);
-          tmem_ld32_done(y);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(y[e]);
-        }
-      }
-    };
-    if constexpr (PLANES == 1) clear_o();
-    else
-#pragma unroll
-      for (int c = 0; c < HD; ++c) acc[c] = 0.f;
-#pragma unroll 1
-    for (int j = 0; j < steps; ++j) {
-      const int k0 = (j0 + j) * kPreKeys, ev = ev_s[j];
-      const uint32_t there = there_s[j], small = small_s[j];
-      const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
-      const float f = qf * pow2f(ek_s[j]);
-      ok = mbar_wait(&s_full[tile], (uint32_t)j & 1u, nullptr) && ok;
-      tc_fence_after();
-      // keys of this row: bit e of word c of 32 keys
-      uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = min(max(lim - (k0 + 32 * c) + 1, 0), 32);
-          see[c] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
-          if (!(there >> (2 * c) & 1)) see[c] &= 0xffff0000u;
-          if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
-        }
-      }
-      if (PLANES == 2 && j > 0) add_step();
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto largest = [&](int c, const uint32_t (&s)[32]) {
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], see[c] >> e & 1 ? __uint_as_float(s[e]) : -INFINITY);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(s[e]));
-        }
+        for (int c = 0; c < HD; c += 8) tmem_st8(to + c, zero);
       };
-      uint32_t s0[32], s1[32];               // 32 columns in use, 32 on their way (PLANES 2: no room)
-      if constexpr (PLANES == 1) {
-        tmem_ld32_start(ts, s0);
-        tmem_ld32_done(s0);
-        tmem_ld32_start(ts + 32, s1);
-        largest(0, s0);
-        tmem_ld32_done(s1);
-        tmem_ld32_start(ts + 64, s0);
-        largest(1, s1);
-        tmem_ld32_done(s0);
-        tmem_ld32_start(ts + 96, s1);
-        largest(2, s0);
-        tmem_ld32_done(s1);
-        tmem_ld32_start(ts, s0);
-        largest(3, s1);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32_start(ts + 32 * c, s0);
-          tmem_ld32_done(s0);
-          largest(c, s0);
-        }
-      }
-      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      mx *= f;
-      const int En = max(E, ev);
-      if (__any_sync(0xffffffffu, mx > m + (float)kPreLag) || En > E) {
-        const float mn = fmaxf(m, mx);
-        const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
-        l *= y;
-        const float z = y * pow2f(E - En);
+      auto add_step = [&] {                                  // the last step's P V to it
         if constexpr (PLANES == 2) {
 #pragma unroll
-          for (int c = 0; c < HD; ++c) acc[c] *= z;
-        } else if (j > 0) {  // the products before this step's S are complete
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t y[32];
+            tmem_ld32_start(to + c, y);
+            tmem_ld32_done(y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(y[e]);
+          }
+        }
+      };
+      if constexpr (PLANES == 1) clear_o();
+      else
+#pragma unroll
+        for (int c = 0; c < HD; ++c) acc[c] = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 8) {
-            float v[8];
-            tmem_ld8(to + c, v);
+      for (int j = 0; j < steps; ++j) {
+        const int k0 = (j0 + j) * kPreKeys, ev = ev_s[j];
+        const uint32_t there = there_s[j], small = small_s[j];
+        const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
+        const float f = qf * pow2f(ek_s[j]);
+        mbar_wait(&s_full[tile], (uint32_t)j & 1u, nullptr);
+        tc_fence_after();
+        // keys of this row: bit e of word c of 32 keys
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= z;
-            tmem_st8(to + c, v);
+          for (int c = 0; c < 4; ++c) {
+            const int n = min(max(lim - (k0 + 32 * c) + 1, 0), 32);
+            see[c] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            if (!(there >> (2 * c) & 1)) see[c] &= 0xffff0000u;
+            if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
           }
         }
-        m = mn;
-        E = En;
-      }
-      const int up = kPreBias + ev - E;
-      const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
-      float sum[4] = {};
-      auto step = [&](auto masks) {
-      // a weight, by its score and whether the row sees the key
-      auto weight = [&](uint32_t r, bool sees) {
-        const float p = ex2p(fmaf(__uint_as_float(r), f, -sub));
-        return !decltype(masks)::value || sees ? p : 0.f;
-      };
-      if constexpr (PLANES == 1) {
-        // 32 keys at a time into tensor memory as f16, over their scores
-        auto weights = [&](int c, const uint32_t (&r)[32]) {
-          uint32_t hi[16];
+        if (PLANES == 2 && j > 0) add_step();
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&](int c, const uint32_t (&s)[32]) {
+          if (masked) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float x = weight(r[2 * e], see[c] >> (2 * e) & 1), y = weight(r[2 * e + 1], see[c] >> (2 * e + 1) & 1);
-            sum[e & 3] += x + y;
-            const __half2 h = __floats2half2_rn(x, y);
-            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int e = 0; e < 32; ++e)
+              mx4[e & 3] = fmaxf(mx4[e & 3], see[c] >> e & 1 ? __uint_as_float(s[e]) : -INFINITY);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(s[e]));
           }
-          tmem_st16(ts + 16 * c, hi);
         };
-        tmem_ld32_done(s0);
-        tmem_ld32_start(ts + 32, s1);
-        weights(0, s0);
-        tmem_ld32_done(s1);
-        tmem_ld32_start(ts + 64, s0);
-        weights(1, s1);
-        tmem_ld32_done(s0);
-        tmem_ld32_start(ts + 96, s1);
-        weights(2, s0);
-        tmem_ld32_done(s1);
-        weights(3, s1);
-      } else {
-        // 16 keys at a time; the low parts of the first half are kept back
-        // until the scores in their columns are read
-        uint32_t lo[4][8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t r[16], hi[8], rest[8];
-          tmem_ld16(ts + 16 * c, r);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 16 * c + 2 * e;
-            const float x = weight(r[2 * e], see[k / 32] >> (k % 32) & 1);
-            const float y = weight(r[2 * e + 1], see[k / 32] >> (k % 32 + 1) & 1);
-            sum[e & 3] += x + y;
-            const __half2 h = __floats2half2_rn(x, y);
-            const float2 hf = __half22float2(h);
-            const __half2 d = __floats2half2_rn(x - hf.x, y - hf.y);
-            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-            rest[e] = *reinterpret_cast<const uint32_t*>(&d);
-          }
-          tmem_put8(ts + 8 * c, hi);
-          if (c < 4) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lo[c][e] = rest[e];
-          } else {
-            // columns 16 c .. 16 c + 15 are free: two of the eight blocks of low parts
-            if (c < 6) {
-              tmem_put8(ts + 16 * c, lo[2 * (c - 4)]);
-              tmem_put8(ts + 16 * c + 8, lo[2 * (c - 4) + 1]);
-            } else if (c == 6) {
-              tmem_put8(ts + 96, lo[0]);
-              tmem_put8(ts + 104, lo[1]);
-            }
-            if (c == 7) {
-              tmem_put8(ts + 112, lo[2]);
-              tmem_put8(ts + 120, rest);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) lo[c - 4][e] = rest[e];
-            }
-          }
-        }
-      }
-      };
-      if (masked) step(std::true_type());
-      else step(std::false_type());
-      l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
-      tmem_wait_st();
-      if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
-      if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + (j0 + j) * kPrePages, g, ev);
-      tc_fence_before();
-      mbar_arrive(&p_full[tile]);
-    }
-    ok = mbar_wait(&o_full[tile], 0, nullptr) && ok;
-    tc_fence_after();
-    add_step();
-    const bool nans = nan_any != 0;
-    // 32 dims of the row as it stands, times f
-    auto own = [&](int c, float f, float (&y)[32]) {
-      if constexpr (PLANES == 2) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = acc[(c + e) % HD];
-      } else {
-        tmem_ld32(to + c, y);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        y[e] *= f;
-        if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
-      }
-    };
-    float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
-    float weight[kPreMaxSplits];                            // of each range
-    const float4* parts = nullptr;
-    bool mine = true;
-    if (splits > 1) {
-      const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-      unsigned* ticket = reinterpret_cast<unsigned*>(a.ws) + cta;
-      float* part0 = reinterpret_cast<float*>(static_cast<char*>(a.ws) + parts_off) + cta * gridDim.z * part_floats<HD>();
-      float* part = part0 + blockIdx.z * part_floats<HD>() + tile * (part_floats<HD>() / 2);
-#pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        float y[32];
-        own(c, pow2f(E - kPreBias), y);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          reinterpret_cast<float4*>(part)[(c / 4 + q) * kPreRows + i] =
-              make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-      }
-      reinterpret_cast<float2*>(part + HD * kPreRows)[i] = make_float2(m, l);
-      __threadfence();
-      softmax_sync(nt * kPreRows);
-      if (tid == 0) {
-        const unsigned got = atomicAdd(ticket, 1u);
-        last_s = got == (unsigned)(splits - 1);
-        if (last_s) {
-          __threadfence();
-          *ticket = 0u;
-        }
-      }
-      softmax_sync(nt * kPreRows);
-      mine = last_s;
-      if (mine) {
-        __threadfence();
-        const float* ml = part0 + tile * (part_floats<HD>() / 2) + HD * kPreRows;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int z = 0; z < kPreMaxSplits; ++z)
-          if (z < splits) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i).x);
-#pragma unroll
-        for (int z = 0; z < kPreMaxSplits; ++z) {
-          weight[z] = 0.f;
-          if (z < splits) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i);
-            weight[z] = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2p(v.x - top);   // no keys; NaN stays
-            sum += v.y * weight[z];
-          }
-        }
-        inv = sum == 0.f ? 0.f : 1.f / sum;
-        parts = reinterpret_cast<const float4*>(part0 + tile * (part_floats<HD>() / 2));
-      }
-    }
-    if (mine) {
-    // rows by threads to rows by warps, over the tile's queries, which nothing
-    // reads any more: 16-byte units XORed with the row against bank conflicts
-    using T = typename OutOf<PLANES>::type;
-    constexpr int UE = 16 / sizeof(T), UR = HD / UE;        // values of a unit, units of a row
-    uint8_t* rows_s = sm + L::kQ + tile * PLANES * L::kTile + (size_t)(i & ~31) * HD * sizeof(T);
-#pragma unroll (PLANES == 2 ? 4 : 1)
-    for (int c = 0; c < HD; c += 32) {
-      float y[32];
-      if (!parts) {
-        own(c, inv, y);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = 0.f;
-#pragma unroll
-        for (int z = 0; z < kPreMaxSplits; ++z)
-          if (z < splits)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 v = __ldcg(parts + z * (part_floats<HD>() / 4) + (c / 4 + q) * kPreRows + i);
-              y[4 * q] += v.x * weight[z];
-              y[4 * q + 1] += v.y * weight[z];
-              y[4 * q + 2] += v.z * weight[z];
-              y[4 * q + 3] += v.w * weight[z];
-            }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] *= inv;
-      }
-#pragma unroll
-      for (int q = 0; q < 32 / UE; ++q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (UE == 4) {
-            w[e] = __float_as_uint(y[(4 * q + e) % 32]);
-          } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y[(8 * q + 2 * e) % 32], y[(8 * q + 2 * e + 1) % 32]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        *reinterpret_cast<uint4*>(rows_s + (size_t)lane * HD * sizeof(T) + (((c / UE + q) ^ lane) % UR) * 16) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    __syncwarp();
-    T* out = reinterpret_cast<T*>(PLANES == 2 ? static_cast<void*>(a.o) : static_cast<void*>(a.o16));
-#pragma unroll 4
-    for (int k = 0; k < UR; ++k) {                          // 32 units a step: 32 / UR rows
-      const int row = (k * 32 + lane) / UR, q = lane % UR, ri = (i & ~31) + row, rt = ri * inv_g >> 16;
-      const uint4 y = *reinterpret_cast<const uint4*>(rows_s + (size_t)row * HD * sizeof(T) + ((q ^ row) % UR) * 16);
-      if (rt < TT && t0 + tile * TT + rt < rows) {
-        T* p = out + (size_t)(r0 + t0 + tile * TT + rt) * a.o_ld + (size_t)(g * G + ri - rt * G) * HD + q * UE;
-        if (o_vec) {
-          *reinterpret_cast<uint4*>(p) = y;
+        uint32_t s0[32], s1[32];               // 32 columns in use, 32 on their way (PLANES 2: no room)
+        if constexpr (PLANES == 1) {
+          tmem_ld32_start(ts, s0);
+          tmem_ld32_done(s0);
+          tmem_ld32_start(ts + 32, s1);
+          largest(0, s0);
+          tmem_ld32_done(s1);
+          tmem_ld32_start(ts + 64, s0);
+          largest(1, s1);
+          tmem_ld32_done(s0);
+          tmem_ld32_start(ts + 96, s1);
+          largest(2, s0);
+          tmem_ld32_done(s1);
+          tmem_ld32_start(ts, s0);
+          largest(3, s1);
         } else {
-          const T* v = reinterpret_cast<const T*>(&y);
 #pragma unroll
-          for (int e = 0; e < UE; ++e) p[e] = v[e];
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32_start(ts + 32 * c, s0);
+            tmem_ld32_done(s0);
+            largest(c, s0);
+          }
+        }
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        mx *= f;
+        const int En = max(E, ev);
+        if (__any_sync(0xffffffffu, mx > m + (float)kPreLag) || En > E) {
+          const float mn = fmaxf(m, mx);
+          const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
+          l *= y;
+          const float z = y * pow2f(E - En);
+          if constexpr (PLANES == 2) {
+#pragma unroll
+            for (int c = 0; c < HD; ++c) acc[c] *= z;
+          } else if (j > 0) {  // the products before this step's S are complete
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 8) {
+              float v[8];
+              tmem_ld8(to + c, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= z;
+              tmem_st8(to + c, v);
+            }
+          }
+          m = mn;
+          E = En;
+        }
+        const int up = kPreBias + ev - E;
+        const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
+        float sum[4] = {};
+        auto step = [&](auto masks) {
+          // a weight, by its score and whether the row sees the key
+          auto weight = [&](uint32_t r, bool sees) {
+            const float p = ex2p(fmaf(__uint_as_float(r), f, -sub));
+            return !decltype(masks)::value || sees ? p : 0.f;
+          };
+          if constexpr (PLANES == 1) {
+            // 32 keys at a time into tensor memory as f16, over their scores
+            auto weights = [&](int c, const uint32_t (&r)[32]) {
+              uint32_t hi[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float x = weight(r[2 * e], see[c] >> (2 * e) & 1);
+                const float y = weight(r[2 * e + 1], see[c] >> (2 * e + 1) & 1);
+                sum[e & 3] += x + y;
+                const __half2 h = __floats2half2_rn(x, y);
+                hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              tmem_st16(ts + 16 * c, hi);
+            };
+            tmem_ld32_done(s0);
+            tmem_ld32_start(ts + 32, s1);
+            weights(0, s0);
+            tmem_ld32_done(s1);
+            tmem_ld32_start(ts + 64, s0);
+            weights(1, s1);
+            tmem_ld32_done(s0);
+            tmem_ld32_start(ts + 96, s1);
+            weights(2, s0);
+            tmem_ld32_done(s1);
+            weights(3, s1);
+          } else {
+            // 16 keys at a time; the low parts of the first half are kept back
+            // until the scores in their columns are read
+            uint32_t lo[4][8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t r[16], hi[8], rest[8];
+              tmem_ld16(ts + 16 * c, r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int k = 16 * c + 2 * e;
+                const float x = weight(r[2 * e], see[k / 32] >> (k % 32) & 1);
+                const float y = weight(r[2 * e + 1], see[k / 32] >> (k % 32 + 1) & 1);
+                sum[e & 3] += x + y;
+                const __half2 h = __floats2half2_rn(x, y);
+                const float2 hf = __half22float2(h);
+                const __half2 d = __floats2half2_rn(x - hf.x, y - hf.y);
+                hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+                rest[e] = *reinterpret_cast<const uint32_t*>(&d);
+              }
+              tmem_put8(ts + 8 * c, hi);
+              if (c < 4) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) lo[c][e] = rest[e];
+              } else {
+                // columns 16 c .. 16 c + 15 are free: two of the eight blocks of low parts
+                if (c < 6) {
+                  tmem_put8(ts + 16 * c, lo[2 * (c - 4)]);
+                  tmem_put8(ts + 16 * c + 8, lo[2 * (c - 4) + 1]);
+                } else if (c == 6) {
+                  tmem_put8(ts + 96, lo[0]);
+                  tmem_put8(ts + 104, lo[1]);
+                }
+                if (c == 7) {
+                  tmem_put8(ts + 112, lo[2]);
+                  tmem_put8(ts + 120, rest);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) lo[c - 4][e] = rest[e];
+                }
+              }
+            }
+          }
+        };
+        if (masked) step(std::true_type());
+        else step(std::false_type());
+        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
+        tmem_wait_st();
+        if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
+        if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + (j0 + j) * kPrePages, g, ev);
+        tc_fence_before();
+        mbar_arrive(&p_full[tile]);
+      }
+      // All other waits hang on the products too; where these did not end, the
+      // output is NaN (and tensor memory is not freed under them before one more wait).
+      if (!mbar_wait(&o_full[tile], 0, nullptr)) {
+        mbar_wait(&o_full[tile], 0, nullptr);
+        l = __int_as_float(0x7fffffff);
+      }
+      tc_fence_after();
+      add_step();
+      const bool nans = nan_any != 0;
+      // 32 dims of the row as it stands, times f
+      auto own = [&](int c, float f, float (&y)[32]) {
+        if constexpr (PLANES == 2) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = acc[(c + e) % HD];
+        } else {
+          tmem_ld32(to + c, y);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          y[e] *= f;
+          if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
+        }
+      };
+      float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
+      float weight[kPreMaxSplits];                            // of each range
+      const float4* parts = nullptr;
+      bool mine = true;
+      if (splits > 1) {
+        const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+        unsigned* ticket = reinterpret_cast<unsigned*>(a.ws) + cta;
+        float* part0 =
+            reinterpret_cast<float*>(static_cast<char*>(a.ws) + parts_off) + cta * gridDim.z * part_floats<HD>();
+        float* part = part0 + blockIdx.z * part_floats<HD>() + tile * (part_floats<HD>() / 2);
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          float y[32];
+          own(c, pow2f(E - kPreBias), y);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            reinterpret_cast<float4*>(part)[(c / 4 + q) * kPreRows + i] =
+                make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+        }
+        reinterpret_cast<float2*>(part + HD * kPreRows)[i] = make_float2(m, l);
+        __threadfence();
+        softmax_sync(nt * kPreRows);
+        if (tid == 0) {
+          const unsigned got = atomicAdd(ticket, 1u);
+          last_s = got == (unsigned)(splits - 1);
+          if (last_s) {
+            __threadfence();
+            *ticket = 0u;
+          }
+        }
+        softmax_sync(nt * kPreRows);
+        mine = last_s;
+        if (mine) {
+          __threadfence();
+          const float* ml = part0 + tile * (part_floats<HD>() / 2) + HD * kPreRows;
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int z = 0; z < kPreMaxSplits; ++z)
+            if (z < splits) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i).x);
+#pragma unroll
+          for (int z = 0; z < kPreMaxSplits; ++z) {
+            weight[z] = 0.f;
+            if (z < splits) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + z * part_floats<HD>()) + i);
+              weight[z] = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2p(v.x - top);   // no keys; NaN stays
+              sum += v.y * weight[z];
+            }
+          }
+          inv = sum == 0.f ? 0.f : 1.f / sum;
+          parts = reinterpret_cast<const float4*>(part0 + tile * (part_floats<HD>() / 2));
         }
       }
-    }
-    }
+      if (mine) {
+        // rows by threads to rows by warps, over the tile's queries, which nothing
+        // reads any more: 16-byte units XORed with the row against bank conflicts
+        using T = typename OutOf<PLANES>::type;
+        constexpr int UE = 16 / sizeof(T), UR = HD / UE;        // values of a unit, units of a row
+        uint8_t* rows_s = sm + L::kQ + tile * PLANES * L::kTile + (size_t)(i & ~31) * HD * sizeof(T);
+#pragma unroll (PLANES == 2 ? 4 : 1)
+        for (int c = 0; c < HD; c += 32) {
+          float y[32];
+          if (!parts) {
+            own(c, inv, y);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = 0.f;
+#pragma unroll
+            for (int z = 0; z < kPreMaxSplits; ++z)
+              if (z < splits)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  const float4 v = __ldcg(parts + z * (part_floats<HD>() / 4) + (c / 4 + q) * kPreRows + i);
+                  y[4 * q] += v.x * weight[z];
+                  y[4 * q + 1] += v.y * weight[z];
+                  y[4 * q + 2] += v.z * weight[z];
+                  y[4 * q + 3] += v.w * weight[z];
+                }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] *= inv;
+          }
+#pragma unroll
+          for (int q = 0; q < 32 / UE; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (UE == 4) {
+                w[e] = __float_as_uint(y[(4 * q + e) % 32]);
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[(8 * q + 2 * e) % 32], y[(8 * q + 2 * e + 1) % 32]);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            *reinterpret_cast<uint4*>(rows_s + (size_t)lane * HD * sizeof(T) + (((c / UE + q) ^ lane) % UR) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+        T* out = reinterpret_cast<T*>(PLANES == 2 ? static_cast<void*>(a.o) : static_cast<void*>(a.o16));
+#pragma unroll 4
+        for (int k = 0; k < UR; ++k) {                          // 32 units a step: 32 / UR rows
+          const int row = (k * 32 + lane) / UR, q = lane % UR, ri = (i & ~31) + row, rt = ri * inv_g >> 16;
+          const uint4 y = *reinterpret_cast<const uint4*>(rows_s + (size_t)row * HD * sizeof(T) + ((q ^ row) % UR) * 16);
+          if (rt < TT && t0 + tile * TT + rt < rows) {
+            T* p = out + (size_t)(r0 + t0 + tile * TT + rt) * a.o_ld + (size_t)(g * G + ri - rt * G) * HD + q * UE;
+            if (o_vec) {
+              *reinterpret_cast<uint4*>(p) = y;
+            } else {
+              const T* v = reinterpret_cast<const T*>(&y);
+#pragma unroll
+              for (int e = 0; e < UE; ++e) p[e] = v[e];
+            }
+          }
+        }
+      }
     }
   }
   tc_fence_before();
@@ -970,7 +977,8 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   auto k = kv8_prefill_kernel<HD, PLANES, VEC>;
   static bool attr = false;
   if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 2048);   // the rest: static
+    // all but what is static
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem - 2048);
     if (e != cudaSuccess) return e;
     attr = true;
   }
@@ -990,7 +998,8 @@ cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return s2_launch(&cfg, k, a, slots, (int)kv8_ticket_bytes(kv8_sms()), o_vec, 65536u / (a.H / a.Hkv) + 1);   // i / G = i * inv_g >> 16, i < 128
+  const unsigned inv_g = 65536u / (a.H / a.Hkv) + 1;      // i / G = i * inv_g >> 16, i < 128
+  return s2_launch(&cfg, k, a, slots, (int)kv8_ticket_bytes(kv8_sms()), o_vec, inv_g);
 }
 template <int HD, int PLANES>
 cudaError_t launch(const Kv8Args& a, cudaStream_t st) {
