@@ -121,12 +121,13 @@ struct DecState {           // one piece of a (sequence, kv head): all rows, log
 // equal runs: ragged lengths, one long sequence and many short ones load every
 // SM alike.  A run is taken by as many warps as there are kv heads, one head
 // each, side by side, so that a page is read whole at about one time (read
-// head by head, with 2 KB here and there, the memory gives half: 26 us instead
-// of 17 for 65 MB).  Each warp streams its head's part of the pages through
-// its own ring in shared memory (one copy brings 16 keys and 16 values) and
-// shares no barrier with another.  A sequence that a run holds whole is
-// finished by it; one that is cut is joined by the last of its runs to arrive,
-// in order, in two levels where there are many.
+// head by head, with 2 KB here and there, the memory gives two thirds: the
+// loop over 65 MB then took 26 us, and 17 side by side).  Each warp streams
+// its head's part of the pages through its own ring in shared memory (one copy
+// brings 16 keys and 16 values) and shares no barrier with another.  A
+// sequence that a run holds whole is finished by it; one that is cut is joined
+// by the last of its runs to arrive, in order, in two levels where there are
+// many.
 //
 // Products: mma.sync m16n8k16 with the up to 8 query rows (new rows x heads
 // of the kv head) as f16 hi parts in rows 0..7 and lo parts in rows 8..15, so
@@ -136,6 +137,13 @@ struct DecState {           // one piece of a (sequence, kv head): all rows, log
 // n, and dims n * HD/8 .. of the values of keys 2c, 2c + 1, 2c + 8, 2c + 9.
 // The block scale of K multiplies the scores; the one of V goes into the
 // weights, with the running exponent E handled like the running maximum.
+//
+// Bound by memory where the keys are many: 128 sequences of 200 to 1,700 tokens,
+// 8 heads of 128 (250 MB): 55.5 us, 4.5 TB/s over all, 6 TB/s in the loop; 32 of
+// 900 to 1,090 (65 MB): 25.6 us, of which a start of 1.7 us and round trips of
+// half a microsecond each (queries, append, ticket, join) with the tail of the
+// joins are more than half.  mma.sync, not tcgen05: with at most 8 rows its tile of
+// 128 would be empty, and the tensor pipe is 17 % busy as it is.
 template <int HD, bool VEC>
 __global__ void __launch_bounds__(kDecWarps * 32, 1)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Kv8Args a,
