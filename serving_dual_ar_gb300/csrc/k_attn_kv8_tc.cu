@@ -269,7 +269,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   constexpr int ST = L::kStages, kBlock = 128 * 128;   // a 64-dim block: 128 rows x 128 bytes
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
-  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_s;
   __shared__ int nan_s[HD];
   __shared__ int nan_any, last_s;
@@ -297,6 +297,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
       mbar_init(&v_full[i], 128);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 128);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
     }
@@ -484,14 +485,15 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           }
         umma_commit(&s_full[t]);
       };
-      auto pv = [&](int t, int st, uint32_t acc) {
+      // keys 16 k0 .. 16 k1 - 1 of the step
+      auto pv = [&](int t, int st, int k0, int k1, uint32_t acc) {
         const uint32_t vt = v_d + (st * L::kTile >> 4);
 #pragma unroll
         for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
-          for (int ks = 0; ks < kPreKeys / 16; ++ks)
-            umma_ts(tm + 256 + t * 128, tm + t * 128 + p * 64 + ks * 8, vt + (ks * 2048 >> 4), i_pv,
-                    p < PLANES - 1 || ks > 0 ? 1u : acc);
+          for (int ks = k0; ks < k1; ++ks)
+            umma_ts(tm + 256 + t * 128, tm + t * 128 + (PLANES == 1 ? 64 : p * 64) + ks * 8, vt + (ks * 2048 >> 4), i_pv,
+                    p < PLANES - 1 || ks > k0 ? 1u : acc);
       };
       mbar_wait(&q_full, 0, nullptr);
       mbar_wait(&k_full[0], 0, nullptr);
@@ -504,9 +506,15 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr);
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
+          if (PLANES == 1) {
+            mbar_wait(&p_half[t], (uint32_t)j & 1u, nullptr);
+            tc_fence_after();
+            pv(t, st, 4, 8, 1u);
+          }
           mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr);
           tc_fence_after();
-          pv(t, st, PLANES == 1 || small_s[j] ? 1u : 0u);
+          if (PLANES == 1) pv(t, st, 0, 4, 1u);
+          else pv(t, st, 0, 8, small_s[j] ? 1u : 0u);
           if (t == nt - 1) umma_commit(&v_empty[st]);
           if (j + 1 < steps) {
             if (t == 0) {
@@ -701,7 +709,6 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           tmem_ld32_start(ts + 96, s1);
           largest(2, s0);
           tmem_ld32_done(s1);
-          tmem_ld32_start(ts, s0);
           largest(3, s1);
         } else {
 #pragma unroll
@@ -745,7 +752,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             return !decltype(masks)::value || sees ? p : 0.f;
           };
           if constexpr (PLANES == 1) {
-            // 32 keys at a time into tensor memory as f16, over their scores
+            // 32 keys at a time into tensor memory as f16: the last 64, whose scores
+            // are here still, first, and all over those scores' columns.  The
+            // products of that half begin under the other's arithmetic.
             auto weights = [&](int c, const uint32_t (&r)[32]) {
               uint32_t hi[16];
 #pragma unroll
@@ -756,19 +765,21 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
                 const __half2 h = __floats2half2_rn(x, y);
                 hi[e] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              tmem_st16(ts + 16 * c, hi);
+              tmem_st16(ts + 64 + 16 * c, hi);
             };
+            weights(2, s0);
+            tmem_ld32_start(ts, s0);
+            weights(3, s1);
+            if (!small) {            // else the pages are added to O first
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&p_half[tile]);
+            }
             tmem_ld32_done(s0);
             tmem_ld32_start(ts + 32, s1);
             weights(0, s0);
             tmem_ld32_done(s1);
-            tmem_ld32_start(ts + 64, s0);
             weights(1, s1);
-            tmem_ld32_done(s0);
-            tmem_ld32_start(ts + 96, s1);
-            weights(2, s0);
-            tmem_ld32_done(s1);
-            weights(3, s1);
           } else {
             // 16 keys at a time; the low parts of the first half are kept back
             // until the scores in their columns are read
@@ -818,8 +829,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
         tmem_wait_st();
         if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
-        if (small) add_small_pages<HD, PLANES>(to, ts, small, a, table + (j0 + j) * kPrePages, g, ev);
+        if (small) add_small_pages<HD, PLANES>(to, ts + (PLANES == 1 ? 64 : 0), small, a, table + (j0 + j) * kPrePages, g, ev);
         tc_fence_before();
+        if (PLANES == 1 && small) mbar_arrive(&p_half[tile]);
         mbar_arrive(&p_full[tile]);
       }
       // All other waits hang on the products too; where these did not end, the
