@@ -25,15 +25,18 @@ constexpr int kPreStepBytes = 4;              // what is kept of each step
 // Groups of four warps: two of softmax, one for keys and one for values (one
 // for both with an fp32 output, where the products take twice the time), one
 // for the products.  The launch's registers are shared out anew among them:
-// with an fp32 output a softmax thread holds its row's output too.
+// with an fp32 output a softmax thread holds its row's output too.  The keys'
+// and values' warps want theirs for loads ahead (8,000 tokens: 554 us with 72 a
+// thread, 515 with 88).
 template <int PLANES>
 struct PreRoles {
   static constexpr int kWiden = PLANES == 1 ? 2 : 1, kGroups = 3 + kWiden, kThreads = kGroups * 128;
   static constexpr int kMma = 8 + 4 * kWiden;                 // first warp of the products' group
   static constexpr int kRegs = PLANES == 1 ? 96 : 128;        // a thread, at launch
-  static constexpr int kRegsSoftmax = PLANES == 1 ? 136 : 208, kRegsWiden = PLANES == 1 ? 72 : 64,
-                       kRegsMma = PLANES == 1 ? 64 : 32;
-  static_assert(2 * kRegsSoftmax + kWiden * kRegsWiden + kRegsMma == kGroups * kRegs, "the launch's registers");
+  static constexpr int kRegsSoftmax = PLANES == 1 ? 128 : 192, kRegsWiden = 88, kRegsMma = PLANES == 1 ? 48 : 40;
+  // the shares are no more than the launch has, and each moves the way of its instruction
+  static_assert(2 * kRegsSoftmax + kWiden * kRegsWiden + kRegsMma <= kGroups * kRegs, "the launch's registers");
+  static_assert(kRegsSoftmax >= kRegs && kRegsWiden <= kRegs && kRegsMma <= kRegs, "inc and dec");
 };
 
 template <int HD, int PLANES>
