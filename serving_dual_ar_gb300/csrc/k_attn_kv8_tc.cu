@@ -132,6 +132,7 @@ S2_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 S2_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 S2_DEV void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" :: "l"(p)); }
+S2_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
 // A barrier of the n threads that are softmax rows.
 S2_DEV void softmax_sync(int n) { asm volatile("bar.sync 1, %0;" :: "r"(n) : "memory"); }
 template <int N>
@@ -357,6 +358,12 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   {
     constexpr int LPR = HD / 8, TPW = 32 / LPR;                       // lanes of a row, tokens of a warp
     const int l = lane % LPR, d = 8 * l;
+    // all rows on their way from memory at once (16 prompts behind cached tokens: 67 -> 66 us)
+    for (int q = warp * TPW + lane / LPR; q < 2 * TT; q += kThreads / 32 * TPW)
+      if (t0 + q < rows && l % 4 == 0)
+#pragma unroll 1
+        for (int h = 0; h < G; ++h)
+          prefetch_l2(a.qkv + (size_t)(r0 + t0 + q) * a.qkv_ld + (g * G + h) * HD + d);
     float gain[8];
     load8<VEC>(a.q_gain + d, gain);
     float mx = 0.f;
