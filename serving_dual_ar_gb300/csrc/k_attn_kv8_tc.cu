@@ -146,15 +146,12 @@ S2_DEV float ex2p(float x) {
 }
 
 template <bool VEC>
-S2_DEV void load8(const float* p, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; e += 4) {
-    const float4 x = VEC ? *reinterpret_cast<const float4*>(p + e) : make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]);
-    v[e] = x.x;
-    v[e + 1] = x.y;
-    v[e + 2] = x.z;
-    v[e + 3] = x.w;
-  }
+S2_DEV void load4(const float* p, float* v) {
+  const float4 x = VEC ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = x.z;
+  v[3] = x.w;
 }
 
 // Two e4m3 bytes (the low ones of w) as f16x2 times f.
@@ -349,23 +346,24 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
-  // queries (the rows that the append before this kernel reads too), eight dims
-  // a lane: norm, RoPE, log2(e) / sqrt(HD), and one power of two for the whole
+  // queries (the rows that the append before this kernel reads too), four dims
+  // and the four that they are rotated with a lane: norm, RoPE, log2(e) / sqrt(HD), and one power of two for the whole
   // launch: a normed row times the gains has no value above sqrt(HD) times the
   // largest gain, which goes to 2^9 .. 2^10 (its typical values then to 2^6: a
   // pair of f16 is good to 2^-22 of a value, and to 2^-34 of the largest)
   float qf;                                 // the power of two back
   {
     constexpr int LPR = HD / 8, TPW = 32 / LPR;                       // lanes of a row, tokens of a warp
-    const int l = lane % LPR, d = 8 * l;
+    const int l = lane % LPR, d = 4 * l;
     // all rows on their way from memory at once (16 prompts behind cached tokens: 67 -> 66 us)
     for (int q = warp * TPW + lane / LPR; q < 2 * TT; q += kThreads / 32 * TPW)
       if (t0 + q < rows && l % 4 == 0)
 #pragma unroll 1
         for (int h = 0; h < G; ++h)
-          prefetch_l2(a.qkv + (size_t)(r0 + t0 + q) * a.qkv_ld + (g * G + h) * HD + d);
+          prefetch_l2(a.qkv + (size_t)(r0 + t0 + q) * a.qkv_ld + (g * G + h) * HD + 8 * l);
     float gain[8];
-    load8<VEC>(a.q_gain + d, gain);
+    load4<VEC>(a.q_gain + d, gain);
+    load4<VEC>(a.q_gain + HD / 2 + d, gain + 4);
     float mx = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(gain[e]));
@@ -382,18 +380,18 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
       const bool live = q < 2 * TT && t0 + q < rows;
       const int tok = live ? t0 + q : t0;
       const float* x0 = a.qkv + (size_t)(r0 + tok) * a.qkv_ld + g * G * HD + d;
-      uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile + (d / 64) * kBlock;
-      float co[8], si[8];
-      load8<VEC>(a.rope_cos + (size_t)(pos0 + tok) * (HD / 2) + d % (HD / 2), co);
-      load8<VEC>(a.rope_sin + (size_t)(pos0 + tok) * (HD / 2) + d % (HD / 2), si);
-      const float turn = l < LPR / 2 ? -1.f : 1.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) si[e] *= turn;
+      uint8_t* q_hi = sm + L::kQ + tile * PLANES * L::kTile + (l & 1) * 8;
+      float co[4], si[4];
+      load4<VEC>(a.rope_cos + (size_t)(pos0 + tok) * (HD / 2) + d, co);
+      load4<VEC>(a.rope_sin + (size_t)(pos0 + tok) * (HD / 2) + d, si);
 #pragma unroll 1
       for (int h = 0; h < G; h += 2) {
         float x[2][8];
-        load8<VEC>(x0 + h * HD, x[0]);
-        load8<VEC>(x0 + min(h + 1, G - 1) * HD, x[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          load4<VEC>(x0 + min(h + k, G - 1) * HD, x[k]);
+          load4<VEC>(x0 + min(h + k, G - 1) * HD + HD / 2, x[k] + 4);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float ss = 0.f;
@@ -407,10 +405,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           for (int e = 0; e < 8; ++e) x[k][e] = live ? x[k][e] * (f * gain[e]) : 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w0 = __shfl_xor_sync(0xffffffffu, x[k][2 * e], LPR / 2);
-            const float w1 = __shfl_xor_sync(0xffffffffu, x[k][2 * e + 1], LPR / 2);
-            const float u = x[k][2 * e] * co[2 * e] + w0 * si[2 * e];
-            const float v = x[k][2 * e + 1] * co[2 * e + 1] + w1 * si[2 * e + 1];
+            const int i = 2 * e % 4;
+            const float u = e < 2 ? x[k][i] * co[i] - x[k][i + 4] * si[i] : x[k][i + 4] * co[i] + x[k][i] * si[i];
+            const float v = e < 2 ? x[k][i + 1] * co[i + 1] - x[k][i + 5] * si[i + 1]
+                                  : x[k][i + 5] * co[i + 1] + x[k][i + 1] * si[i + 1];
             const __half2 y = __floats2half2_rn(u, v);
             const float2 yf = __half22float2(y);
             const __half2 r = __floats2half2_rn(u - yf.x, v - yf.y);
@@ -418,9 +416,14 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             lo[e] = *reinterpret_cast<const uint32_t*>(&r);
           }
           if (q < 2 * TT && h + k < G) {
-            uint8_t* to = q_hi + sw128_offset(i0 + h + k, l % 8);
-            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (PLANES == 2) *reinterpret_cast<uint4*>(to + L::kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            uint8_t* to = q_hi + sw128_offset(i0 + h + k, l / 2);
+            uint8_t* to2 = HD == 128 ? to + kBlock : q_hi + sw128_offset(i0 + h + k, 4 + l / 2);
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to2) = make_uint2(hi[2], hi[3]);
+            if (PLANES == 2) {
+              *reinterpret_cast<uint2*>(to + L::kTile) = make_uint2(lo[0], lo[1]);
+              *reinterpret_cast<uint2*>(to2 + L::kTile) = make_uint2(lo[2], lo[3]);
+            }
           }
         }
       }
