@@ -255,11 +255,11 @@ __device__ constexpr size_t part_floats() { return (size_t)2 * kPreRows * (HD + 
 // with the sums in tensor memory, 2.9e-7 so).
 //
 // Bound on paper by the products (2,048 clocks a step for both tiles), in fact by
-// the softmax threads' way through tensor memory and by issue slots (62 % taken,
-// the tensor pipe 47 % busy).  With the append before it: 8,000 tokens, 32 query
+// the softmax threads' way through tensor memory and by issue slots: 4,400 clocks
+// a step (issue slots 62 % taken, the tensor pipe 47 % busy).  With the append before it: 8,000 tokens, 32 query
 // and 8 kv heads of 128, bf16: 512 us, 1,020 TFLOP/s, 53 % of what a bf16 matrix
-// product reaches; 1,024, fp32: 59 us; 16 prompts of about 94 tokens behind 600 to
-// 900 cached ones, bf16: 66 us, each CTA's start (14,000 clocks) a third of it.
+// product reaches; 1,024, fp32: 58 us; 16 prompts of about 94 tokens behind 600 to
+// 900 cached ones, bf16: 65 us, each CTA's start (12,500 clocks) over a quarter of it.
 template <int HD, int PLANES, bool VEC>
 __global__ void __launch_bounds__(PreRoles<PLANES>::kThreads, 1)
 kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, int o_vec, unsigned inv_g) {
