@@ -170,6 +170,19 @@ def test_block_scales_far_apart(b, kind):
     s.check(o, False)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_block_scales_far_apart_in_a_bf16_prompt(b, hd):
+    s = Setup([150, 60, 0], [140, 2, 33], 8, 2, hd, seed=25, spread=20)
+    s.qkv[150:, (s.H + s.Hkv) * s.hd:] *= np.float32(2.0 ** -18)
+    s.upload()
+    o, ws = s.run(b, "prefill", True)
+    torch.cuda.synchronize()
+    s.check(o, True, planes=1)
+    o2, _ = s.run(b, "prefill", True, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2)
+
+
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
 def test_scales_a_bit_beside_a_power_of_two(b, kind):
     s = Setup([150, 61], [1, 1], 8, 2, 128, seed=17)
