@@ -226,7 +226,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   auto head_of = [&](int s) { return (s >> 16) * lay.heads + h; };
   // the unit u0 + t, looked up by lane t % 32
   auto look_up = [&](int t) {
-    Unit x{-1, 0, {-1, -1}, {1.f, 1.f}, {1.f, 1.f}};
+    // a page that is not there has the least scale: it must not raise the exponent
+    // that the values of others are held against
+    const float least = pow2f(kKv8EMin);
+    Unit x{-1, 0, {-1, -1}, {least, least}, {least, least}};
     if (t >= n) return x;
     unsigned u = u0 + t;
     int group = 0, b = 0;                       // last b with first unit <= u
