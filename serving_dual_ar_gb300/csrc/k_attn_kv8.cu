@@ -107,14 +107,22 @@ struct UnitBits {
 };
 
 // Weights carry 2^kDecBias, and the running maximum may lag by kDecLag, so that a
-// weight of at most 2^14 fits f16 and the accumulators are rescaled rarely.
+// weight of at most 2^14 fits f16 and the accumulators are rescaled rarely.  Over
+// 2^20 keys the sums stay below 2^60 (l) and 2^43 (o), and l above 2^-32.
 constexpr int kDecBias = 6, kDecLag = 8;
+// A page whose value scale lies more than kDecFar binades below the largest one
+// met is looked at row by row: where its largest weight x scale is that far below
+// the row's, o is lifted for its products by up to 2^kDecLift (to 2^107 at most).
+constexpr int kDecFar = 10, kDecLift = 64;
 
 template <int HD>
 struct DecState {           // one piece of a (sequence, kv head): all rows, log2 domain
   float o[HD / 8][4];       // tile t: dims n * HD/8 + t of column n; [0..1] hi part of row r, [2..3] lo part
-  float m, l;               // row r = lane / 4 (l: this lane's keys)
-  int E;                    // o counts in units of 2^(E - kDecBias)
+  // Row r = lane / 4.  m: the largest score + exponent of its value block's scale
+  // so far, or up to kDecLag below; l (this lane's keys) sums 2^(score - m), and o
+  // 2^(score + exponent - m + kDecBias) times the e4m3 values.
+  float m, l;
+  int e;                    // largest exponent of a value scale so far
 };
 
 // The work is the list of all pages in the order (sequence, page), cut into
@@ -135,8 +143,14 @@ struct DecState {           // one piece of a (sequence, kv head): all rows, log
 // dims in Q K^T and of dims in the output is free, and is chosen such that
 // each lane's bytes are contiguous: lane (n, c) takes dims c * HD/4 .. of key
 // n, and dims n * HD/8 .. of the values of keys 2c, 2c + 1, 2c + 8, 2c + 9.
-// The block scale of K multiplies the scores; the one of V goes into the
-// weights, with the running exponent E handled like the running maximum.
+// The block scale of K multiplies the scores; the one of V, 2^e, goes into the
+// weights, and the running maximum is that of score + e.  So a weight in f16 is
+// held against the largest weight x scale among the keys that its row sees: a
+// block of large values that has next to no weight takes no bits from the
+// others, and keeps its own where weight x scale counts (with a maximum of the
+// scores and another of e, weights of 2^-33 on values of 2^48 were lost).  A
+// scale bounds its block's values, and a row may see none of the large ones:
+// pages far below the largest scale are added with o lifted to them.
 //
 // Bound by memory where the keys are many: 128 sequences of 200 to 1,700 tokens,
 // 8 heads of 128 (250 MB): 55.5 us, 4.5 TB/s over all, 6 TB/s in the loop; 32 of
@@ -226,8 +240,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   auto head_of = [&](int s) { return (s >> 16) * lay.heads + h; };
   // the unit u0 + t, looked up by lane t % 32
   auto look_up = [&](int t) {
-    // a page that is not there has the least scale: it must not raise the exponent
-    // that the values of others are held against
+    // a page that is not there has the least scale, which no other is far below
     const float least = pow2f(kKv8EMin);
     Unit x{-1, 0, {-1, -1}, {least, least}, {least, least}};
     if (t >= n) return x;
@@ -298,8 +311,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     g = head_of(s);
     pos = pos_s[b];
     st.m = -INFINITY;
+    st.e = kKv8EMin;
     st.l = polls > 1 ? 0.f : __int_as_float(0x7fffffff);
-    st.E = kKv8EMin;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -452,7 +465,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     float* slot = whole ? nullptr : parts + (((size_t)run * 2 + k) * lay.heads + h) * lay.slot_floats;
     st.l += __shfl_xor_sync(0xffffffffu, st.l, 1);
     st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
-    float f = pow2f(st.E - kDecBias);
+    float f = pow2f(-kDecBias);
     if (whole) f = st.l == 0.f ? 0.f : f * (1.f / st.l);
     __syncwarp();
     if (r < R) {
@@ -696,6 +709,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
     __syncwarp();
   };
 
+  auto lift_by = [&](int e) {
+    const float y = pow2f(e);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) st.o[q][k] *= y;
+  };
+
   Unit cur = look_up(lane), nxt = cur;
   if (lane < min(D, n)) issue(cur, lane);
   UnitBits bits{0u, 0u};
@@ -784,32 +805,48 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
         for (int e = 0; e < 4 * kDecPages; ++e)
           if (e / 2 * 8 + 2 * c + (e & 1) > lim || !(there >> (e / 4) & 1)) p[e] = -INFINITY;
       }
-      float mx = p[0];
+      float mx = -INFINITY;
 #pragma unroll
-      for (int e = 1; e < 4 * kDecPages; ++e) mx = fmaxf(mx, p[e]);
+      for (int i = 0; i < kDecPages; ++i)
+        mx = fmaxf(mx, fmaxf(fmaxf(p[4 * i], p[4 * i + 1]), fmaxf(p[4 * i + 2], p[4 * i + 3])) + (float)ve[i]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int E0 = max(st.E, ve[0]);
-      if (__any_sync(0xffffffffu, mx > st.m + (float)kDecLag) || E0 > st.E) {
+      if (__any_sync(0xffffffffu, mx > st.m + (float)kDecLag)) {
         const float mn = fmaxf(st.m, mx);
-        const float x = mn == -INFINITY ? 1.f : ex2(st.m - mn), y = x * pow2f(st.E - E0);
+        const float x = mn == -INFINITY ? 1.f : ex2(st.m - mn);
         st.l *= x;
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st.o[q][e] *= y;
+          for (int e = 0; e < 4; ++e) st.o[q][e] *= x;
         st.m = mn;
-        st.E = E0;
       }
-      // weights times 2^kDecBias and the block's scale over 2^E: at most 2^14,
-      // at least 2^6 for the largest; a pair of f16 then is good to 2^-22 of
-      // each and 2^-31 of the largest
+      // weights times 2^kDecBias and the block's scale: at most 2^14, at least
+      // 2^6 for the largest; a pair of f16 then is good to 2^-22 of each and
+      // 2^-31 of the largest
       const float ref = st.m == -INFINITY ? 0.f : st.m;
-      const int E1 = max(E0, ve[1]);
+      int lift[kDecPages] = {};
+      bool lifted = false;
+      st.e = max(st.e, max(ve[0], ve[1]));
+      if (min(ve[0], ve[1]) < st.e - kDecFar) {
+#pragma unroll
+        for (int i = 0; i < kDecPages; ++i)
+          if (ve[i] < st.e - kDecFar && (there >> i & 1)) {
+            float x = fmaxf(fmaxf(p[4 * i], p[4 * i + 1]), fmaxf(p[4 * i + 2], p[4 * i + 3]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            x = ref - (x + (float)ve[i]);            // infinity: no key is seen
+            const bool far = x > (float)kDecFar && x < INFINITY;
+            if (__any_sync(0xffffffffu, far && r < R)) {
+              lifted = true;
+              if (far) lift[i] = (int)fminf(x, (float)kDecLift);
+            }
+          }
+      }
       uint32_t pa[kDecPages][4];
 #pragma unroll
       for (int i = 0; i < kDecPages; ++i) {
-        const int up = kDecBias + ve[i] - (i ? E1 : E0);
+        const int up = kDecBias + ve[i] + lift[i];
         const float sub = ref - (float)up;
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[4 * i + e] = ex2(p[4 * i + e] - sub);
@@ -821,16 +858,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
       // O += P V
 #pragma unroll
       for (int i = 0; i < kDecPages; ++i) {
-        // page by page: rows that do not see the second one's larger values
-        // keep all bits of theirs
-        if (i && E1 > E0) {
-          const float y = pow2f(E0 - E1);
-#pragma unroll
-          for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[q][e] *= y;
-          st.E = E1;
-        }
+        if (lifted) lift_by(lift[i] - (i ? lift[i - 1] : 0));
         const uint8_t* xv = blk + i * PB + kKv8Page * HD;
         uint32_t v[4][HD / 32];
 #pragma unroll
@@ -854,6 +882,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
           mma_f16(st.o[4 * k + 3], pa[i], f16x2_of_e4m3((uint16_t)(a23 >> 16)), f16x2_of_e4m3((uint16_t)(b23 >> 16)));
         }
       }
+      if (lifted) lift_by(-lift[kDecPages - 1]);
     }
     __syncwarp();
     // the slot is free: the unit D further on

@@ -4,10 +4,13 @@ of two and so do their weights, against a 64-bit restatement.
 The bound is in terms of what a row sums up: A = sum p_j |v_j|, weighted, and
 not the largest |v|.  A relative error e in every weight and an error d in every
 score (see kv8_util.tolerance) move o = sum p_j v_j / sum p_j by at most
-(2 d + 2 e) A.  A weight times its block's scale 2^e_j goes into the products as
-f16 values: the largest p_j 2^e_j of the row stands at 2^6 at least, so that
-f16's smallest step, 2^-24, rounds every key's by at most 2^-31 of the largest;
-with codes of at most 448, n keys add n 2^-31 C, C = 448 max p_j 2^e_j.
+(2 d + 2 e) A.  A weight times its block's scale, p_j 2^e_j, goes into the products
+as f16 values: the row's largest stands at 2^6 at least, so that f16's smallest
+step, 2^-24, rounds every other by at most 2^-31 of it.  A block's scale may be far
+above what the row sees of the block, so the largest one counts only among blocks
+whose scale is at most 2^10 times key j's; if it is in another block, key j's
+block stands at 2^-4 at least or by itself: 2^-21 of the block's largest p_j 2^e_j,
+or 2^-95 of the row's largest.  That times the key's largest code is its error.
 """
 
 import numpy as np
@@ -21,8 +24,8 @@ from test_kv8_gpu import EPS, Setup, b  # noqa: E402, F401  (b: the fixture)
 
 
 def weighted(s, cache):
-    """(A, C, n): A [T, H, hd], C [T, H] and the number of keys [T] of each row."""
-    A, C, n_keys = np.zeros((s.T, s.H, s.hd)), np.zeros((s.T, s.H)), np.ones(s.T)
+    """(A, D): A [T, H, hd], and D [T, H], the sum over a row's keys of what f16's smallest step can move."""
+    A, D = np.zeros((s.T, s.H, s.hd)), np.zeros((s.T, s.H))
     for i in range(s.B):
         r0, n, p0 = int(s.row0[i]), int(s.new[i]), int(s.pos[i])
         if n == 0 or p0 < 0:
@@ -30,9 +33,9 @@ def weighted(s, cache):
         x = s.qkv[r0:r0 + n, :(s.H + 2 * s.Hkv) * s.hd].reshape(n, -1, s.hd)
         q = ref.norm_rope(x[:, :s.H], s.qg, s.cos[p0:p0 + n], s.sin[p0:p0 + n], EPS)
         k, v, ok = cache.keys_values(s.table[i], p0 + n)
-        pages = np.where(ok, s.table[i][np.arange(p0 + n) // 16], 0)
+        at = np.arange(p0 + n) // 16
+        pages = np.where(ok, s.table[i][at], 0)
         see = ok[None] & (np.arange(p0 + n)[None] <= (p0 + np.arange(n))[:, None])
-        n_keys[r0:r0 + n] = p0 + n
         for h in range(s.H):
             g = h // (s.H // s.Hkv)
             z = np.where(see, q[:, h] @ k[:, g].T / np.sqrt(s.hd), -np.inf)
@@ -40,17 +43,23 @@ def weighted(s, cache):
             w = np.where(see, np.exp(z - np.where(np.isfinite(top), top, 0)), 0.0)
             w /= np.maximum(w.sum(-1, keepdims=True), 1e-300)
             A[r0:r0 + n, h] = w @ np.abs(v[:, g])
-            C[r0:r0 + n, h] = 448 * (w * 2.0 ** cache.exps[pages, 1, g].astype(float)).max(-1)
-    return A, C, n_keys
+            e = cache.exps[pages, 1, g]
+            c = w * 2.0 ** e.astype(float)                                   # [n, keys]
+            block = np.stack([c[:, at == p].max(-1) for p in range(at[-1] + 1)], -1)
+            far = np.stack([np.where(e <= e[16 * p] + 10, c, 0).max(-1) for p in range(at[-1] + 1)], -1)
+            step = np.maximum(np.maximum(2.0 ** -31 * far, 2.0 ** -21 * block),
+                              2.0 ** -95 * block.max(-1, keepdims=True))
+            D[r0:r0 + n, h] = step[:, at] @ (np.abs(v[:, g]).max(-1) / 2.0 ** e)     # codes of 448 at most
+    return A, D
 
 
 def check(s, o, bf16, planes):
     cache, want, SV = s.want()
     got = o.float().cpu().numpy()[:s.T, :s.H * s.hd].reshape(want.shape).astype(np.float64)
-    A, C, n = weighted(s, cache)
+    A, D = weighted(s, cache)
     u = 2.0 ** -17 + (2.0 ** -11 if planes == 1 else 0)
     e = 2.0 ** -16 + (2.0 ** -11 if planes == 1 else 0)
-    tol = (2 * SV[..., :1] * u + 2 * e) * A + (n[:, None] * 2.0 ** -31 * C)[..., None]
+    tol = (2 * SV[..., :1] * u + 2 * e) * A + D[..., None]
     tol += (2.0 ** -8 if bf16 else 2.0 ** -23) * np.abs(want) + 1e-40
     err = np.abs(got - want)
     assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:5].tolist())
@@ -77,6 +86,8 @@ def turned_away(s, i, page, lam, by):
     p = s.table[i, page]
     s.exps[p, 0] = ref.exponent(x)
     s.codes[p, 0] = ref.encode(x / 2.0 ** s.exps[p, 0][:, None, None])
+    if by == "zeros":
+        s.codes[p, 1], by = 0, 40
     s.exps[p, 1] += by
     assert np.abs(s.exps[p]).max() <= 32
 
@@ -95,3 +106,44 @@ def test_small_values_beside_a_missing_page(b, kind, missing):
     torch.cuda.synchronize()
     want = check(s, o, False, 2)
     assert (want != 0).any()
+
+
+# ---------------------------------------------------------------- large values with little weight
+
+# lam: the page's weights are e^(-lam sqrt(hd)) of the others'; by: its values are 2^by of theirs
+FAR = [
+    (4.5, 24),     # nothing of the page is left: the others' values stand alone
+    (3.0, 12),     # the same with values that f16 holds beside each other
+    (3.0, 45),     # weights of 2^-49, values of 2^45: both count
+    (2.0, 48),     # weights of 2^-33: the page is all that counts
+    (-3.0, -12),   # the page has all the weight, the others values of 2^12: both count
+    (0.0, 40),     # equal weights
+    (0.0, "zeros"),   # equal weights, and zeros in a block whose scale is 2^40 times the others'
+    (-2.0, "zeros"),  # the same with the weight on the zeros
+]
+
+
+@pytest.mark.parametrize("page", [0, 3, 5])
+@pytest.mark.parametrize("lam,by", FAR)
+def test_decode_of_far_values(b, lam, by, page):
+    s = Setup([100, 99], [2, 2], 8, 4, 128, seed=32)
+    shifted(s, -8 if by == -12 else -20)
+    for i in range(2):
+        turned_away(s, i, page, lam, by)
+    s.upload()
+    o, _ = s.run(b, "decode", False)
+    torch.cuda.synchronize()
+    check(s, o, False, 2)
+
+
+@pytest.mark.parametrize("lam,by", FAR)
+def test_decode_of_far_values_in_another_run(b, lam, by):
+    """A long sequence, cut into runs: pages of the kind in different ones."""
+    s = Setup([3000, 40], [1, 1], 8, 2, 64, seed=33)
+    shifted(s, -8 if by == -12 else -20)
+    turned_away(s, 0, 3, lam, by)
+    turned_away(s, 0, 150, lam, by)
+    s.upload()
+    o, ws = s.run(b, "decode", True)
+    torch.cuda.synchronize()
+    check(s, o, True, 2)
