@@ -17,9 +17,11 @@ constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
 // Weights carry 2^kPreBias; the running maximum may lag by kPreLag.
 constexpr int kPreBias = 6, kPreLag = 8;
-// Binades below its step's largest scale from which on a page's values are added
-// apart: until there 2^-9 of the scale, e4m3's least, is an f16 value.
-constexpr int kPreSmall = 14;
+// Binades by which the value scales of a step's pages may differ and count as one:
+// the values then are f16 relative to the largest (exactly), and the step's weights
+// carry that one.  A step whose scales differ by more, or one of whose pages lies
+// more than kPreFar below the largest scale met, goes page by page (spread_step).
+constexpr int kPreNear = 3, kPreFar = 10;
 constexpr int kPreStepBytes = 4;              // what is kept of each step
 
 // Groups of four warps: two of softmax, one for keys and one for values (one
@@ -177,53 +179,113 @@ __device__ __noinline__ uint4 without_nan(uint4 y, int* first, int* any, int key
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The keys of the pages in ``small`` (a bit each) into a row's output by fp32
-// arithmetic: weights from where they were put in tensor memory, times the
-// page's values over 2^ev.  For pages whose values are so small next to others
-// of their step that they would not survive as f16 relative to the step's
-// scale; a row may see those and not the others.
+// What is kept of a step: the largest scale exponent of its pages' keys, which
+// pages are there (a bit each), the largest and the smallest exponent of their
+// values.  Whether it goes page by page; e_top is the largest exponent of values so far.
+S2_DEV bool goes_by_page(const char4& step, int& e_top) {
+  e_top = max(e_top, (int)step.z);
+  return step.z - step.w > kPreNear || step.w < e_top - kPreFar;
+}
+
+// A step of one row page by page: the row's maximum and sum as new (m, l), its
+// weights to where the products read them, each with its page's scale.  A scale
+// bounds its block's values, and a row may see none of the large ones: a page whose
+// largest weight x scale is more than kPreFar binades below the row's is added to
+// O by fp32 arithmetic.  In a code of its own, since steps like it are rare.  last:
+// the row's last key of the step, left: the keys of the step, table: its pages.
+// Called by whole warps.
 template <int HD, int PLANES>
-__device__ __noinline__ void add_small_pages(uint32_t t_o, uint32_t t_p, uint32_t small, const Kv8Args& a,
-                                             const int* table, int g, int ev) {
+__device__ __noinline__ float2 spread_step(uint32_t t_o, uint32_t t_s, float f, float m, float l, int e_top, int last,
+                                           uint32_t there, const Kv8Args& a, const int* table, int left, int g) {
+  const int lane = threadIdx.x & 31;
+  int e_page = kKv8EMin;                                   // of page ``lane``
+  if (lane < kPrePages && lane * kKv8Page < left && (there >> lane & 1))
+    e_page = kv8_scale_exp(a.scale[((size_t)table[lane] * 2 + 1) * a.Hkv + g]);
+  __syncwarp();
+  float s[kPreKeys];
+#pragma unroll
+  for (int c = 0; c < kPreKeys; c += 16) {
+    uint32_t r[16];
+    tmem_ld16(t_s + c, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      s[c + i] = c + i <= last && (there >> (c / kKv8Page) & 1) ? __uint_as_float(r[i]) : -INFINITY;
+  }
+  auto top_of = [&](int q) {                               // its largest score + exponent
+    float x = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kKv8Page; ++i) x = fmaxf(x, s[kKv8Page * q + i]);
+    return fmaf(x, f, (float)__shfl_sync(0xffffffffu, e_page, q));
+  };
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < kPrePages; ++q) mx = fmaxf(mx, top_of(q));
+  if (__any_sync(0xffffffffu, mx > m + (float)kPreLag)) {
+    const float mn = fmaxf(m, mx), y = mn == -INFINITY ? 1.f : ex2p(m - mn);
+    l *= y;
+    m = mn;
+    if (PLANES == 1)
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 8) {
+        float o[8];
+        tmem_ld8(t_o + c, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= y;
+        tmem_st8(t_o + c, o);
+      }
+  }
+  if (PLANES == 2) {                                       // the products add to O in such a step
+    const float zero[8] = {};
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 8) tmem_st8(t_o + c, zero);
+  }
+  const float base = (float)kPreBias - (m == -INFINITY ? 0.f : m);
 #pragma unroll 1
   for (int q = 0; q < kPrePages; ++q) {
-    if (!(small >> q & 1)) continue;
-    const size_t blk = ((size_t)table[q] * 2 + 1) * a.Hkv + g;
-    const uint8_t* v = a.kv + blk * (kKv8Page * HD);
-    const float by = pow2f(kv8_scale_exp(a.scale[blk]) - ev);
-    float p[kKv8Page];
+    const int e = __shfl_sync(0xffffffffu, e_page, q);
+    const float off = (float)e + base, x = top_of(q);
+    float p[kKv8Page], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kKv8Page; ++i) p[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < PLANES; ++k) {
-      float w[8];
-      tmem_ld8(t_p + 64 * k + 8 * q, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(w[i]);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-        p[2 * i] += f.x * by;
-        p[2 * i + 1] += f.y * by;
-      }
+    for (int i = 0; i < kKv8Page; ++i) {
+      p[i] = ex2p(fmaf(s[kKv8Page * q + i], f, off));
+      sum += p[i];
     }
+    l = fmaf(sum, pow2f(-e - kPreBias), l);
+    if (__any_sync(0xffffffffu, e < e_top - kPreFar && x > -INFINITY && m - x > (float)kPreFar)) {
+      const uint8_t* v = a.kv + (((size_t)table[q] * 2 + 1) * a.Hkv + g) * (kKv8Page * HD);
 #pragma unroll 1
-    for (int c = 0; c < HD; c += 8) {
-      float o[8];
-      tmem_ld8(t_o + c, o);
+      for (int c = 0; c < HD; c += 8) {
+        float o[8];
+        tmem_ld8(t_o + c, o);
 #pragma unroll
-      for (int k = 0; k < kKv8Page; ++k) {
-        const uint2 x = *reinterpret_cast<const uint2*>(v + k * HD + c);
+        for (int k = 0; k < kKv8Page; ++k) {
+          const uint2 w = *reinterpret_cast<const uint2*>(v + k * HD + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t h = f16x2_of_e4m3((uint16_t)((e < 2 ? x.x : x.y) >> (e & 1) * 16));
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-          o[2 * e] += f.x == f.x ? p[k] * f.x : 0.f;           // NaN: see nan_s
-          o[2 * e + 1] += f.y == f.y ? p[k] * f.y : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h = f16x2_of_e4m3((uint16_t)((i < 2 ? w.x : w.y) >> (i & 1) * 16));
+            const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h));
+            o[2 * i] += y.x == y.x ? p[k] * y.x : 0.f;           // NaN: see nan_s
+            o[2 * i + 1] += y.y == y.y ? p[k] * y.y : 0.f;
+          }
         }
+        tmem_st8(t_o + c, o);
       }
-      tmem_st8(t_o + c, o);
+#pragma unroll
+      for (int i = 0; i < kKv8Page; ++i) p[i] = 0.f;
     }
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+      const float2 hf = __half22float2(h);
+      const __half2 d = __floats2half2_rn(p[2 * i] - hf.x, p[2 * i + 1] - hf.y);
+      hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    tmem_put8(t_s + (PLANES == 1 ? 64 : 0) + 8 * q, hi);
+    if (PLANES == 2) tmem_put8(t_s + 64 + 8 * q, lo);
   }
+  return make_float2(m, l);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -247,6 +309,10 @@ __device__ constexpr size_t part_floats() { return (size_t)2 * kPreRows * (HD + 
 // S and P share tensor memory (P is written over S as f16, and is the A operand
 // from there), O stays in it; V is read as [key][dim], MN-major, so nothing is
 // transposed.  While one tile's softmax runs, the other tile's products do.
+// The value scale 2^e goes into the weights, and the running maximum is that of
+// score + e: a weight in f16 is held against the largest weight x scale among the
+// keys that its row sees.  With a maximum of the scores and another of e, rows lost
+// bits to pages without weight, and weights of 2^-33 on values of 2^48 were lost.
 // PLANES = 2 (fp32 output): Q and P as f16 pairs hi + lo, twice the products,
 // the low ones first.  The tensor cores cut what they add to an accumulator
 // off, toward zero; over a thousand steps that grows to 2^-16 of the output.
@@ -441,37 +507,27 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   pdl_launch_next();
   pdl_wait();      // the new rows are in their pages
 
-  // per step: the largest scale exponents of its pages, which pages are there, and
-  // which have small values
-  int8_t* ek_s = reinterpret_cast<int8_t*>(sm + L::kMeta);
-  int8_t* ev_s = ek_s + steps;
-  uint8_t* there_s = reinterpret_cast<uint8_t*>(ev_s + steps);
-  uint8_t* small_s = there_s + steps;
+  char4* step_s = reinterpret_cast<char4*>(sm + L::kMeta);              // see goes_by_page
   {
     const int pages = (keys + kKv8Page - 1) / kKv8Page - j0 * kPrePages;   // of this range on
     for (int i0 = warp * 32; i0 < steps * kPrePages; i0 += kThreads) {
       const int i = i0 + lane, page = i < pages ? table[j0 * kPrePages + i] : -1;
       const bool in = page >= 0 && page < a.n_pages;
-      int ek = kKv8EMin, ev = kKv8EMin;
+      int ek = kKv8EMin, hi = kKv8EMin, lo = kKv8EMax;
       if (in) {
         const float* s = a.scale + (size_t)page * 2 * a.Hkv + g;
         ek = kv8_scale_exp(s[0]);
-        ev = kv8_scale_exp(s[a.Hkv]);
+        hi = lo = kv8_scale_exp(s[a.Hkv]);
       }
-      const int own = ev;
 #pragma unroll
       for (int o = 1; o < kPrePages; o <<= 1) {
         ek = max(ek, __shfl_xor_sync(0xffffffffu, ek, o));
-        ev = max(ev, __shfl_xor_sync(0xffffffffu, ev, o));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       }
       const unsigned there = __ballot_sync(0xffffffffu, in || i >= pages) >> (lane & 24) & 0xff;
-      const unsigned small = __ballot_sync(0xffffffffu, in && ev - own > kPreSmall) >> (lane & 24) & 0xff;
-      if ((lane & 7) == 0 && i < steps * kPrePages) {
-        small_s[i / kPrePages] = (uint8_t)small;
-        ek_s[i / kPrePages] = (int8_t)ek;
-        ev_s[i / kPrePages] = (int8_t)ev;
-        there_s[i / kPrePages] = (uint8_t)there;
-      }
+      if ((lane & 7) == 0 && i < steps * kPrePages)
+        step_s[i / kPrePages] = make_char4((signed char)ek, (signed char)there, (signed char)hi, (signed char)lo);
     }
   }
   tc_fence_before();
@@ -513,9 +569,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
       tc_fence_after();
       for (int t = 0; t < nt; ++t) qk(t, 0);
       umma_commit(&k_empty[0]);
+      int e_top = kKv8EMin;
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int st = j % ST, sn = (j + 1) % ST;
+        const bool by_page = PLANES == 2 && goes_by_page(step_s[j], e_top);
         mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr);
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
@@ -527,7 +585,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr);
           tc_fence_after();
           if (PLANES == 1) pv(t, st, 0, 4, 1u);
-          else pv(t, st, 0, 8, small_s[j] ? 1u : 0u);
+          else pv(t, st, 0, 8, by_page ? 1u : 0u);
           if (t == nt - 1) umma_commit(&v_empty[st]);
           if (j + 1 < steps) {
             if (t == 0) {
@@ -589,6 +647,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         }
       }
     };
+    int e_top = kKv8EMin;
     load_ids(0, page);
     load_ids(1, page_next);
     load_scales(page, sc);
@@ -597,18 +656,22 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
     for (int j = 0; j < steps; ++j) {
       const int st = j % ST;
       int page_2[2];
+      const char4 step = step_s[j];
+      const bool by_page = goes_by_page(step, e_top);
       load_ids(j + 2, page_2);
       load_scales(page_next, sc_next);
 #pragma unroll
       for (int k = 0; k < KINDS; ++k) {
         const int kind = first + k;
-        // the two pages' scales over the step's largest one
+        // the two pages' scales over the step's largest one; values whose weights
+        // carry the page's scale as they are
         __half2 by[2];
-        const int top = kind ? ev_s[j] : ek_s[j], small = kind ? small_s[j] >> (w * 2) : 0;
+        const int top = kind ? step.z : step.x;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          by[i] = __float2half2_rn(page[i] < 0 || (small >> i & 1) ? 0.f
-                                                                   : pow2f(max(kv8_scale_exp(sc[k][i]) - top, -60)));
+          by[i] = __float2half2_rn(page[i] < 0 ? 0.f
+                                   : kind && by_page ? 1.f
+                                                     : pow2f(max(kv8_scale_exp(sc[k][i]) - top, -60)));
         mbar_wait(kind ? &v_empty[st] : &k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr);
         uint8_t* to = sm + (kind ? L::kV : L::kK) + st * L::kTile + (u / 4) * kBlock;
         if (kind) {
@@ -654,8 +717,11 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
       const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
       const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
       const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
+      // m: the largest score + exponent of its value scale so far, or up to kPreLag
+      // below; l sums 2^(score - m), the output 2^(score + exponent - m + kPreBias)
+      // times the e4m3 values
       float m = -INFINITY, l = 0.f;
-      int E = kKv8EMin;
+      int e_top = kKv8EMin;
       float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
       auto clear_o = [&] {
         const float zero[8] = {};
@@ -680,12 +746,32 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         for (int c = 0; c < HD; ++c) acc[c] = 0.f;
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
-        const int k0 = (j0 + j) * kPreKeys, ev = ev_s[j];
-        const uint32_t there = there_s[j], small = small_s[j];
+        const int k0 = (j0 + j) * kPreKeys;
+        const char4 step_j = step_s[j];
+        const int ev = step_j.z;
+        const uint32_t there = (uint8_t)step_j.y;
+        const bool by_page = goes_by_page(step_j, e_top);
         const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
-        const float f = qf * pow2f(ek_s[j]);
+        const float f = qf * pow2f(step_j.x);
         mbar_wait(&s_full[tile], (uint32_t)j & 1u, nullptr);
         tc_fence_after();
+        if (PLANES == 2 && j > 0) add_step();
+        if (by_page) {
+          const float2 ml = spread_step<HD, PLANES>(to, ts, f, m, l, e_top, lim - k0, there, a,
+                                                    table + (j0 + j) * kPrePages, keys - k0, g);
+          if constexpr (PLANES == 2) {
+            const float y = ml.x == -INFINITY ? 1.f : ex2p(m - ml.x);
+#pragma unroll
+            for (int c = 0; c < HD; ++c) acc[c] *= y;
+          }
+          m = ml.x;
+          l = ml.y;
+          tmem_wait_st();
+          tc_fence_before();
+          if (PLANES == 1) mbar_arrive(&p_half[tile]);
+          mbar_arrive(&p_full[tile]);
+          continue;
+        }
         // keys of this row: bit e of word c of 32 keys
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (masked) {
@@ -697,7 +783,6 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             if (!(there >> (2 * c + 1) & 1)) see[c] &= 0xffffu;
           }
         }
-        if (PLANES == 2 && j > 0) add_step();
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto largest = [&](int c, const uint32_t (&s)[32]) {
           if (masked) {
@@ -732,30 +817,27 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           }
         }
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        mx *= f;
-        const int En = max(E, ev);
-        if (__any_sync(0xffffffffu, mx > m + (float)kPreLag) || En > E) {
+        mx = fmaf(mx, f, (float)ev);
+        if (__any_sync(0xffffffffu, mx > m + (float)kPreLag)) {
           const float mn = fmaxf(m, mx);
           const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
           l *= y;
-          const float z = y * pow2f(E - En);
           if constexpr (PLANES == 2) {
 #pragma unroll
-            for (int c = 0; c < HD; ++c) acc[c] *= z;
+            for (int c = 0; c < HD; ++c) acc[c] *= y;
           } else if (j > 0) {  // the products before this step's S are complete
 #pragma unroll 1
             for (int c = 0; c < HD; c += 8) {
               float v[8];
               tmem_ld8(to + c, v);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] *= z;
+              for (int e = 0; e < 8; ++e) v[e] *= y;
               tmem_st8(to + c, v);
             }
           }
           m = mn;
-          E = En;
         }
-        const int up = kPreBias + ev - E;
+        const int up = kPreBias + ev;
         const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
         float sum[4] = {};
         auto step = [&](auto masks) {
@@ -783,11 +865,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             weights(2, s0);
             tmem_ld32_start(ts, s0);
             weights(3, s1);
-            if (!small) {            // else the pages are added to O first
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive(&p_half[tile]);
-            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_half[tile]);
             tmem_ld32_done(s0);
             tmem_ld32_start(ts + 32, s1);
             weights(0, s0);
@@ -841,10 +921,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         else step(std::false_type());
         l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-up);
         tmem_wait_st();
-        if (PLANES == 2 && small) clear_o();       // this step's products then add to what the pages gave
-        if (small) add_small_pages<HD, PLANES>(to, ts + (PLANES == 1 ? 64 : 0), small, a, table + (j0 + j) * kPrePages, g, ev);
         tc_fence_before();
-        if (PLANES == 1 && small) mbar_arrive(&p_half[tile]);
         mbar_arrive(&p_full[tile]);
       }
       // All other waits hang on the products too; where these did not end, the
@@ -870,7 +947,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
         }
       };
-      float inv = l == 0.f ? 0.f : pow2f(E - kPreBias) / l;
+      float inv = l == 0.f ? 0.f : pow2f(-kPreBias) / l;
       float weight[kPreMaxSplits];                            // of each range
       const float4* parts = nullptr;
       bool mine = true;
@@ -883,7 +960,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           float y[32];
-          own(c, pow2f(E - kPreBias), y);
+          own(c, pow2f(-kPreBias), y);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             reinterpret_cast<float4*>(part)[(c / 4 + q) * kPreRows + i] =

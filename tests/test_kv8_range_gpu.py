@@ -11,6 +11,8 @@ above what the row sees of the block, so the largest one counts only among block
 whose scale is at most 2^10 times key j's; if it is in another block, key j's
 block stands at 2^-4 at least or by itself: 2^-21 of the block's largest p_j 2^e_j,
 or 2^-95 of the row's largest.  That times the key's largest code is its error.
+In prompts the blocks of 128 keys whose scales lie within 2^3 of each other count
+as of the largest of these scales: 2^3 times the steps.
 """
 
 import numpy as np
@@ -53,13 +55,13 @@ def weighted(s, cache):
     return A, D
 
 
-def check(s, o, bf16, planes):
+def check(s, o, bf16, planes, prompt=False):
     cache, want, SV = s.want()
     got = o.float().cpu().numpy()[:s.T, :s.H * s.hd].reshape(want.shape).astype(np.float64)
     A, D = weighted(s, cache)
     u = 2.0 ** -17 + (2.0 ** -11 if planes == 1 else 0)
     e = 2.0 ** -16 + (2.0 ** -11 if planes == 1 else 0)
-    tol = (2 * SV[..., :1] * u + 2 * e) * A + D[..., None]
+    tol = (2 * SV[..., :1] * u + 2 * e) * A + (8 if prompt else 1) * D[..., None]
     tol += (2.0 ** -8 if bf16 else 2.0 ** -23) * np.abs(want) + 1e-40
     err = np.abs(got - want)
     assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:5].tolist())
@@ -104,7 +106,7 @@ def test_small_values_beside_a_missing_page(b, kind, missing):
     s.upload()
     o, _ = s.run(b, kind, False)
     torch.cuda.synchronize()
-    want = check(s, o, False, 2)
+    want = check(s, o, False, 2, kind == "prefill")
     assert (want != 0).any()
 
 
@@ -147,3 +149,31 @@ def test_decode_of_far_values_in_another_run(b, lam, by):
     o, ws = s.run(b, "decode", True)
     torch.cuda.synchronize()
     check(s, o, True, 2)
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("page", [0, 5])
+@pytest.mark.parametrize("lam,by", FAR)
+def test_prompt_of_far_values(b, lam, by, page, bf16):
+    s = Setup([150, 99, 600], [70, 1, 3], 4, 2, 128, seed=34)
+    shifted(s, -8 if by == -12 else -20)
+    for i in range(3):
+        turned_away(s, i, page, lam, by)
+    s.upload()
+    o, _ = s.run(b, "prefill", bf16)
+    torch.cuda.synchronize()
+    check(s, o, bf16, 1 if bf16 else 2, True)
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("lam,by", FAR)
+def test_prompt_of_far_values_in_another_range(b, lam, by, bf16):
+    """Few rows behind many keys, which are cut into ranges."""
+    s = Setup([2000], [3], 4, 2, 64, seed=35)
+    shifted(s, -8 if by == -12 else -20)
+    turned_away(s, 0, 3, lam, by)
+    turned_away(s, 0, 100, lam, by)
+    s.upload()
+    o, _ = s.run(b, "prefill", bf16)
+    torch.cuda.synchronize()
+    check(s, o, bf16, 1 if bf16 else 2, True)
