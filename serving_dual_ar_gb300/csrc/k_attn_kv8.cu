@@ -293,7 +293,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant
   };
 
   uint32_t qa[KS][4];        // query fragments: {hi, lo} x {dims 4t, 4t+1 | 4t+2, 4t+3}
-  uint32_t polls = 2000000;  // of a wait; 1 after one that gave up
+  uint32_t polls = a.polls;  // of a wait; 1 after one that gave up
   float qf = 0.f;            // 2^-(exponent given to row r's query)
   DecState<HD> st;
   int seg = -1, pos = 0, b = 0, g = 0;

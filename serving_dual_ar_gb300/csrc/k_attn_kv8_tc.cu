@@ -339,7 +339,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   __shared__ __align__(8) uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_s;
   __shared__ int nan_s[HD];
-  __shared__ int nan_any, last_s;
+  __shared__ int nan_any, last_s, gave_up_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.H / a.Hkv, TT = kPreRows / G;                       // tokens of a tile
   const int g = blockIdx.y, slot = slots - 1 - (int)blockIdx.x;       // long rows first
@@ -370,6 +370,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
     }
     fence_mbar_init();
     nan_any = 0;
+    gave_up_s = 0;
   }
   for (int i = tid; i < HD; i += kThreads) nan_s[i] = 0x7fffffff;
   __syncthreads();
@@ -534,6 +535,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
+  // A bounded wait.  A role whose wait has run out leaves its loop and arrives at no
+  // barrier any more, so that nothing is made of what it did not wait for: the waits
+  // for it run out too, up to the rows, which are NaN then.
+  auto came = [&](uint64_t& bar, uint32_t parity) { return mbar_wait(&bar, parity, nullptr, a.polls); };
 
   if (warp >= W::kMma) {
     // ------------------------------------------------ products
@@ -564,40 +569,49 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             umma_ts(tm + 256 + t * 128, tm + t * 128 + (PLANES == 1 ? 64 : p * 64) + ks * 8, vt + (ks * 2048 >> 4), i_pv,
                     p < PLANES - 1 || ks > k0 ? 1u : acc);
       };
-      mbar_wait(&q_full, 0, nullptr);
-      mbar_wait(&k_full[0], 0, nullptr);
-      tc_fence_after();
-      for (int t = 0; t < nt; ++t) qk(t, 0);
-      umma_commit(&k_empty[0]);
-      int e_top = kKv8EMin;
+      int left = nt;                                          // tiles whose last products are to come
+      auto products = [&] {
+        if (!came(q_full, 0) || !came(k_full[0], 0)) return;
+        tc_fence_after();
+        for (int t = 0; t < nt; ++t) qk(t, 0);
+        umma_commit(&k_empty[0]);
+        int e_top = kKv8EMin;
 #pragma unroll 1
-      for (int j = 0; j < steps; ++j) {
-        const int st = j % ST, sn = (j + 1) % ST;
-        const bool by_page = PLANES == 2 && goes_by_page(step_s[j], e_top);
-        mbar_wait(&v_full[st], (uint32_t)(j / ST) & 1u, nullptr);
+        for (int j = 0; j < steps; ++j) {
+          const int st = j % ST, sn = (j + 1) % ST;
+          const bool by_page = PLANES == 2 && goes_by_page(step_s[j], e_top);
+          if (!came(v_full[st], (uint32_t)(j / ST) & 1u)) return;
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          if (PLANES == 1) {
-            mbar_wait(&p_half[t], (uint32_t)j & 1u, nullptr);
-            tc_fence_after();
-            pv(t, st, 4, 8, 1u);
-          }
-          mbar_wait(&p_full[t], (uint32_t)j & 1u, nullptr);
-          tc_fence_after();
-          if (PLANES == 1) pv(t, st, 0, 4, 1u);
-          else pv(t, st, 0, 8, by_page ? 1u : 0u);
-          if (t == nt - 1) umma_commit(&v_empty[st]);
-          if (j + 1 < steps) {
-            if (t == 0) {
-              mbar_wait(&k_full[sn], (uint32_t)((j + 1) / ST) & 1u, nullptr);
+          for (int t = 0; t < nt; ++t) {
+            if (PLANES == 1) {
+              if (!came(p_half[t], (uint32_t)j & 1u)) return;
               tc_fence_after();
+              pv(t, st, 4, 8, 1u);
             }
-            qk(t, sn);
-            if (t == nt - 1) umma_commit(&k_empty[sn]);
-          } else {
-            umma_commit(&o_full[t]);
+            if (!came(p_full[t], (uint32_t)j & 1u)) return;
+            tc_fence_after();
+            if (PLANES == 1) pv(t, st, 0, 4, 1u);
+            else pv(t, st, 0, 8, by_page ? 1u : 0u);
+            if (t == nt - 1) umma_commit(&v_empty[st]);
+            if (j + 1 < steps) {
+              if (t == 0) {
+                if (!came(k_full[sn], (uint32_t)((j + 1) / ST) & 1u)) return;
+                tc_fence_after();
+              }
+              qk(t, sn);
+              if (t == nt - 1) umma_commit(&k_empty[sn]);
+            } else {
+              umma_commit(&o_full[t]);
+              --left;
+            }
           }
         }
+      };
+      products();
+      if (left > 0) {        // a wait ran out: the rows wait for what was issued, and are told
+        *static_cast<volatile int*>(&gave_up_s) = 1;
+        __threadfence_block();
+        for (int t = nt - left; t < nt; ++t) umma_commit(&o_full[t]);
       }
     }
     __syncwarp();
@@ -672,7 +686,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           by[i] = __float2half2_rn(page[i] < 0 ? 0.f
                                    : kind && by_page ? 1.f
                                                      : pow2f(max(kv8_scale_exp(sc[k][i]) - top, -60)));
-        mbar_wait(kind ? &v_empty[st] : &k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u, nullptr);
+        if (!came(kind ? v_empty[st] : k_empty[st], ((uint32_t)(j / ST) & 1u) ^ 1u)) goto left_off;
         uint8_t* to = sm + (kind ? L::kV : L::kK) + st * L::kTile + (u / 4) * kBlock;
         if (kind) {
           uint32_t nan = 0;
@@ -707,6 +721,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         for (int k = 0; k < KINDS; ++k) sc[k][i] = sc_next[k][i];
       }
     }
+  left_off:;
   } else {
     // ------------------------------------------------ softmax, a row per thread
     more_regs<W::kRegsSoftmax>();
@@ -753,7 +768,10 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         const bool by_page = goes_by_page(step_j, e_top);
         const bool masked = k0 + kPreKeys - 1 > lim_min || there != 0xff;
         const float f = qf * pow2f(step_j.x);
-        mbar_wait(&s_full[tile], (uint32_t)j & 1u, nullptr);
+        if (!__all_sync(0xffffffffu, came(s_full[tile], (uint32_t)j & 1u))) {
+          l = __int_as_float(0x7fffffff);
+          break;
+        }
         tc_fence_after();
         if (PLANES == 2 && j > 0) add_step();
         if (by_page) {
@@ -924,12 +942,13 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         tc_fence_before();
         mbar_arrive(&p_full[tile]);
       }
-      // All other waits hang on the products too; where these did not end, the
-      // output is NaN (and tensor memory is not freed under them before one more wait).
+      // The products read shared memory and write tensor memory, which are given
+      // back behind this wait: it has all its polls, and twice.
       if (!mbar_wait(&o_full[tile], 0, nullptr)) {
         mbar_wait(&o_full[tile], 0, nullptr);
         l = __int_as_float(0x7fffffff);
       }
+      if (*static_cast<volatile int*>(&gave_up_s)) l = __int_as_float(0x7fffffff);
       tc_fence_after();
       add_step();
       const bool nans = nan_any != 0;

@@ -245,6 +245,7 @@ struct Kv8Args {
   const int* table = nullptr; int table_ld = 0;
   float* o = nullptr; __nv_bfloat16* o16 = nullptr; int o_ld = 0;     // one of the two
   void* ws = nullptr;
+  unsigned polls = 2000000;  // of a wait inside the kernels, until it gives up
 };
 constexpr int kKv8MaxSeqs = 1024;
 constexpr int kKv8MaxRows = 8;      // decode: m * H / Hkv

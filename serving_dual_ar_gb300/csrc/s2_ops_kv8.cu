@@ -5,6 +5,7 @@
 #include "s2_kernels.h"
 
 #include <algorithm>
+#include <cstdlib>
 #include <new>
 #include <vector>
 
@@ -23,6 +24,16 @@ static bool aligned(const void* p, uintptr_t n) { return !(reinterpret_cast<uint
 static bool shape_ok(int B, int H, int Hkv, int hd) {
   return B >= 1 && B <= kKv8MaxSeqs && Hkv >= 1 && Hkv <= 4096 && H >= Hkv && H % Hkv == 0 && H / Hkv <= 8 &&
          (hd == 64 || hd == 128);
+}
+
+// S2_FAULT_KV8_POLLS=n (read once): waits inside the attention kernels give up
+// after n polls, for the tests of what they leave then.
+static unsigned wait_polls() {
+  static const unsigned n = [] {
+    const char* e = std::getenv("S2_FAULT_KV8_POLLS");
+    return e ? (unsigned)std::atoi(e) : Kv8Args().polls;
+  }();
+  return n;
 }
 
 // The arguments that both attention calls have; false if one of them is refused.
@@ -61,6 +72,7 @@ static bool fill_args(Kv8Args& a, const float* qkv, int qkv_ld, int B, int H, in
   a.o16 = o_bf16 ? static_cast<__nv_bfloat16*>(o) : nullptr;
   a.o_ld = o_ld;
   a.ws = workspace;
+  a.polls = wait_polls();
   return true;
 }
 
