@@ -406,16 +406,22 @@ def s2op_kv8_unpack_pages(kv8, kv_scale, n_src, src, kv, kv_bf16, n_dst, dst, n,
                                      ptr(dst), n, Hkv, hd, _stream(stream)), "s2op_kv8_unpack_pages")
 
 
-def _host_i32(a):
+def _host_i32(a, what):
     """A host int32 array of the page indices a (numpy, list or host tensor)."""
     if getattr(a, "is_cuda", False):
         raise ValueError("page pairs are host arrays")
+    a = np.asarray(a)
+    if a.dtype != np.int32 and a.size:
+        if a.dtype.kind not in "iu":
+            raise ValueError("page indices are integers")
+        if a.min() < -2**31 or a.max() >= 2**31:      # 32 bits of it would name another page
+            raise S2Error(S2_EINVAL, what)
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
 def s2op_kv_copy_pages(kv, page_bytes, scale, scale_bytes, n_pages, layers, src, dst, n, stream=None):
     """Pages src[i] -> dst[i] (host arrays) in each layer of a pool, with their scales if given."""
-    src, dst = _host_i32(src), _host_i32(dst)
+    src, dst = _host_i32(src, "s2op_kv_copy_pages"), _host_i32(dst, "s2op_kv_copy_pages")
     if src.size < n or dst.size < n:
         raise ValueError("fewer page pairs than n")
     _check(LIB.s2op_kv_copy_pages(ptr(kv), page_bytes, ptr(scale), scale_bytes, n_pages, layers, ptr(src),
@@ -424,7 +430,7 @@ def s2op_kv_copy_pages(kv, page_bytes, scale, scale_bytes, n_pages, layers, src,
 
 def s2op_kv_remap_pages(table, rows, cols, table_ld, src, dst, n, stream=None):
     """Entries src[i] of a device page table become dst[i] (host arrays)."""
-    src, dst = _host_i32(src), _host_i32(dst)
+    src, dst = _host_i32(src, "s2op_kv_remap_pages"), _host_i32(dst, "s2op_kv_remap_pages")
     if src.size < n or dst.size < n:
         raise ValueError("fewer page pairs than n")
     _check(LIB.s2op_kv_remap_pages(ptr(table), rows, cols, table_ld, ptr(src), ptr(dst), n, _stream(stream)),

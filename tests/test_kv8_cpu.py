@@ -147,3 +147,30 @@ def test_restated_exponent():
     x = np.zeros((6, 1, 1))
     x[:, 0, 0] = [0, 448, 448.5, 3.5, 3.5000005, np.inf]
     np.testing.assert_array_equal(ref.exponent(x), [-32, 0, 1, -7, -6, 32])
+
+
+@pytest.mark.parametrize("bad", [np.array([2 ** 32 + 1]), np.array([2 ** 31]), np.array([-2 ** 32]), [2 ** 33],
+                                 np.array([2 ** 32 + 1], np.uint64)], ids=str)
+def test_page_indices_beyond_32_bits_are_outside_the_pool(lib, bad):
+    """Not pages of the pool whose number is what 32 bits of them give."""
+    for src, dst in ((bad, [2]), ([2], bad)):
+        with pytest.raises(lib.S2Error) as e:
+            lib.s2op_kv_copy_pages(P, 16, None, 0, 4, 1, src, dst, 1)
+        assert e.value.status == lib.S2_EINVAL
+        with pytest.raises(lib.S2Error) as e:
+            lib.s2op_kv_remap_pages(P, 0, 2, 2, src, dst, 1)
+        assert e.value.status == lib.S2_EINVAL
+
+
+@pytest.mark.parametrize("bad", [[1.5], np.array([1.0]), [True], ["1"]], ids=str)
+def test_page_indices_are_integers(lib, bad):
+    with pytest.raises(ValueError):
+        lib.s2op_kv_copy_pages(P, 16, None, 0, 4, 1, bad, [2], 1)
+    with pytest.raises(ValueError):
+        lib.s2op_kv_remap_pages(P, 0, 2, 2, [2], bad, 1)
+
+
+def test_page_indices_of_any_integer_type(lib):
+    for t in (np.int64, np.uint64, np.int16, np.int32):
+        lib.s2op_kv_remap_pages(P, 0, 2, 2, np.array([1], t), np.array([2], t), 1)     # no rows: nothing to do
+    lib.s2op_kv_remap_pages(P, 0, 2, 2, [], [], 0)
