@@ -66,3 +66,16 @@ def test_nan_key_is_seen_by_its_rows_alone(b, kind, bf16):
     assert nan[:4, 2:].all() and not nan[:4, :2].any()
     assert nan[6:8, :2].all() and not nan[4:6].any() and not nan[6:8, 2:].any()
     assert not nan[8:].any()
+
+
+@pytest.mark.parametrize("kind,bf16", [("decode", False), ("decode", True), ("prefill", False), ("prefill", True)])
+@pytest.mark.parametrize("gain", [5, 20])
+def test_large_gains(b, kind, bf16, gain):
+    """Scores of tens and hundreds: few keys have all the weight, and what a rounding
+    of the queries does is multiplied by the score."""
+    s = Setup([150, 64, 900], [8, 8, 8] if kind == "decode" else [33, 1, 140], 3, 3, 128, seed=52)
+    s.qg *= np.float32(gain)
+    s.upload()
+    o, _ = s.run(b, kind, bf16)
+    torch.cuda.synchronize()
+    s.check(o, bf16, planes=1 if bf16 and kind == "prefill" else 2)
