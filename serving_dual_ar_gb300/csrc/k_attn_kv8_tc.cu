@@ -15,13 +15,21 @@ constexpr int kPreKeys = 128;                 // keys of a step
 constexpr int kPrePages = kPreKeys / kKv8Page;
 constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two tiles
-// Weights carry 2^kPreBias; the running maximum may lag by kPreLag.
-constexpr int kPreBias = 6, kPreLag = 8;
-// Binades by which the value scales of a step's pages may differ and count as one:
-// the values then are f16 relative to the largest (exactly), and the step's weights
-// carry that one.  A step whose scales differ by more, or one of whose pages lies
-// more than kPreFar below the largest scale met, goes page by page (spread_step).
-constexpr int kPreNear = 3, kPreFar = 10;
+// Weights carry 2^bias, and the running maximum may lag by ``lag``: they are 2^15 at
+// most.  f16 pairs (an fp32 output) get the better resolution of a short lag, which
+// costs more rescaling where scores are large (single f16, gains of 5: 607 us for
+// 8,000 tokens with a lag of 4, 580 with 8).
+template <int PLANES>
+struct PreScale {
+  static constexpr int kBias = PLANES == 1 ? 7 : 11, kLag = 15 - kBias;
+};
+// Binades by which the value scales of a step's pages may lie below the largest one
+// met: the values then are f16 relative to the step's largest (exactly), and the
+// step's weights carry that one.  The row's largest weight still stands at 2^-7
+// (pairs: 2^-3) then, so that the others are good to 2^-18 (2^-22) of it.  A step
+// with a page further down goes page by page (spread_step), which takes three
+// times as long, and more where pages are added apart.
+constexpr int kPreFar = 14;
 constexpr int kPreStepBytes = 4;              // what is kept of each step
 
 // Groups of four warps: two of softmax, one for keys and one for values (one
@@ -184,7 +192,7 @@ __device__ __noinline__ uint4 without_nan(uint4 y, int* first, int* any, int key
 // values.  Whether it goes page by page; e_top is the largest exponent of values so far.
 S2_DEV bool goes_by_page(const char4& step, int& e_top) {
   e_top = max(e_top, (int)step.z);
-  return step.z - step.w > kPreNear || step.w < e_top - kPreFar;
+  return step.w < e_top - kPreFar;
 }
 
 // A step of one row page by page: the row's maximum and sum as new (m, l), its
@@ -220,26 +228,20 @@ __device__ __noinline__ float2 spread_step(uint32_t t_o, uint32_t t_s, float f, 
   float mx = -INFINITY;
 #pragma unroll 1
   for (int q = 0; q < kPrePages; ++q) mx = fmaxf(mx, top_of(q));
-  if (__any_sync(0xffffffffu, mx > m + (float)kPreLag)) {
+  if (__any_sync(0xffffffffu, mx > m + (float)PreScale<PLANES>::kLag)) {
     const float mn = fmaxf(m, mx), y = mn == -INFINITY ? 1.f : ex2p(m - mn);
     l *= y;
     m = mn;
-    if (PLANES == 1)
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 8) {
-        float o[8];
-        tmem_ld8(t_o + c, o);
+    for (int c = 0; c < HD; c += 8) {
+      float o[8];
+      tmem_ld8(t_o + c, o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= y;
-        tmem_st8(t_o + c, o);
-      }
+      for (int e = 0; e < 8; ++e) o[e] *= y;
+      tmem_st8(t_o + c, o);
+    }
   }
-  if (PLANES == 2) {                                       // the products add to O in such a step
-    const float zero[8] = {};
-#pragma unroll 1
-    for (int c = 0; c < HD; c += 8) tmem_st8(t_o + c, zero);
-  }
-  const float base = (float)kPreBias - (m == -INFINITY ? 0.f : m);
+  const float base = (float)PreScale<PLANES>::kBias - (m == -INFINITY ? 0.f : m);
 #pragma unroll 1
   for (int q = 0; q < kPrePages; ++q) {
     const int e = __shfl_sync(0xffffffffu, e_page, q);
@@ -250,7 +252,7 @@ __device__ __noinline__ float2 spread_step(uint32_t t_o, uint32_t t_s, float f, 
       p[i] = ex2p(fmaf(s[kKv8Page * q + i], f, off));
       sum += p[i];
     }
-    l = fmaf(sum, pow2f(-e - kPreBias), l);
+    l = fmaf(sum, pow2f(-e - PreScale<PLANES>::kBias), l);
     if (__any_sync(0xffffffffu, e < e_top - kPreFar && x > -INFINITY && m - x > (float)kPreFar)) {
       const uint8_t* v = a.kv + (((size_t)table[q] * 2 + 1) * a.Hkv + g) * (kKv8Page * HD);
 #pragma unroll 1
@@ -575,11 +577,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         tc_fence_after();
         for (int t = 0; t < nt; ++t) qk(t, 0);
         umma_commit(&k_empty[0]);
-        int e_top = kKv8EMin;
 #pragma unroll 1
         for (int j = 0; j < steps; ++j) {
           const int st = j % ST, sn = (j + 1) % ST;
-          const bool by_page = PLANES == 2 && goes_by_page(step_s[j], e_top);
           if (!came(v_full[st], (uint32_t)(j / ST) & 1u)) return;
 #pragma unroll 1
           for (int t = 0; t < nt; ++t) {
@@ -591,7 +591,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
             if (!came(p_full[t], (uint32_t)j & 1u)) return;
             tc_fence_after();
             if (PLANES == 1) pv(t, st, 0, 4, 1u);
-            else pv(t, st, 0, 8, by_page ? 1u : 0u);
+            else pv(t, st, 0, 8, 0u);
             if (t == nt - 1) umma_commit(&v_empty[st]);
             if (j + 1 < steps) {
               if (t == 0) {
@@ -732,9 +732,9 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
       const int lim_min = pos0 + t0 + tile * TT;             // of the tile's first row
       const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
       const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
-      // m: the largest score + exponent of its value scale so far, or up to kPreLag
-      // below; l sums 2^(score - m), the output 2^(score + exponent - m + kPreBias)
-      // times the e4m3 values
+      // m: the largest score + exponent of its value scale so far, or up to the lag
+      // below; l sums 2^(score - m), the output 2^(score + exponent - m + bias) times
+      // the e4m3 values
       float m = -INFINITY, l = 0.f;
       int e_top = kKv8EMin;
       float acc[PLANES == 2 ? HD : 1];                       // PLANES 2: the row's output so far
@@ -775,13 +775,24 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         tc_fence_after();
         if (PLANES == 2 && j > 0) add_step();
         if (by_page) {
+          if constexpr (PLANES == 2)       // the output so far over to O, free until the products of this step
+#pragma unroll
+            for (int c = 0; c < HD; c += 8) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = acc[c + e];
+              tmem_st8(to + c, y);
+            }
           const float2 ml = spread_step<HD, PLANES>(to, ts, f, m, l, e_top, lim - k0, there, a,
                                                     table + (j0 + j) * kPrePages, keys - k0, g);
-          if constexpr (PLANES == 2) {
-            const float y = ml.x == -INFINITY ? 1.f : ex2p(m - ml.x);
+          if constexpr (PLANES == 2)
 #pragma unroll
-            for (int c = 0; c < HD; ++c) acc[c] *= y;
-          }
+            for (int c = 0; c < HD; c += 8) {
+              float y[8];
+              tmem_ld8(to + c, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[c + e] = y[e];
+            }
           m = ml.x;
           l = ml.y;
           tmem_wait_st();
@@ -836,7 +847,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
         }
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         mx = fmaf(mx, f, (float)ev);
-        if (__any_sync(0xffffffffu, mx > m + (float)kPreLag)) {
+        if (__any_sync(0xffffffffu, mx > m + (float)PreScale<PLANES>::kLag)) {
           const float mn = fmaxf(m, mx);
           const float y = mn == -INFINITY ? 1.f : ex2p(m - mn);
           l *= y;
@@ -855,7 +866,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           }
           m = mn;
         }
-        const int up = kPreBias + ev;
+        const int up = PreScale<PLANES>::kBias + ev;
         const float sub = (m == -INFINITY ? 0.f : m) - (float)up;
         float sum[4] = {};
         auto step = [&](auto masks) {
@@ -966,7 +977,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
           if (nans && nan_s[c + e] <= lim) y[e] = __int_as_float(0x7fffffff);
         }
       };
-      float inv = l == 0.f ? 0.f : pow2f(-kPreBias) / l;
+      float inv = l == 0.f ? 0.f : pow2f(-PreScale<PLANES>::kBias) / l;
       float weight[kPreMaxSplits];                            // of each range
       const float4* parts = nullptr;
       bool mine = true;
@@ -979,7 +990,7 @@ kv8_prefill_kernel(const __grid_constant__ Kv8Args a, int slots, int parts_off, 
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           float y[32];
-          own(c, pow2f(-kPreBias), y);
+          own(c, pow2f(-PreScale<PLANES>::kBias), y);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             reinterpret_cast<float4*>(part)[(c / 4 + q) * kPreRows + i] =

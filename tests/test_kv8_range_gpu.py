@@ -11,8 +11,12 @@ above what the row sees of the block, so the largest one counts only among block
 whose scale is at most 2^10 times key j's; if it is in another block, key j's
 block stands at 2^-4 at least or by itself: 2^-21 of the block's largest p_j 2^e_j,
 or 2^-95 of the row's largest.  That times the key's largest code is its error.
-In prompts the blocks of 128 keys whose scales lie within 2^3 of each other count
-as of the largest of these scales: 2^3 times the steps.
+In prompts the largest stands at 2^11 at least (2^7 with a bf16 output), a step is
+2^-36 (2^-32) of it, and the blocks of 128 keys count as of the largest of their
+scales, which is at most 2^14 times the scale of each: 2^-22 (2^-18) of the row's
+largest p_j 2^e_j.  And a block more than 2^14 below the largest scale met stands by
+itself, so that no more than the largest weight among blocks of up to 2^14 times key
+j's scale counts for j, at that scale: 2^-22 (2^-18) of this weight times 2^e_j.
 """
 
 import numpy as np
@@ -25,7 +29,7 @@ import kv8_util as ref  # noqa: E402
 from test_kv8_gpu import EPS, Setup, b  # noqa: E402, F401  (b: the fixture)
 
 
-def weighted(s, cache):
+def weighted(s, cache, prompt, bf16):
     """(A, D): A [T, H, hd], and D [T, H], the sum over a row's keys of what f16's smallest step can move."""
     A, D = np.zeros((s.T, s.H, s.hd)), np.zeros((s.T, s.H))
     for i in range(s.B):
@@ -51,6 +55,10 @@ def weighted(s, cache):
             far = np.stack([np.where(e <= e[16 * p] + 10, c, 0).max(-1) for p in range(at[-1] + 1)], -1)
             step = np.maximum(np.maximum(2.0 ** -31 * far, 2.0 ** -21 * block),
                               2.0 ** -95 * block.max(-1, keepdims=True))
+            if prompt:
+                near = np.stack([np.where(e <= e[16 * p] + 14, w, 0).max(-1) for p in range(at[-1] + 1)], -1)
+                step = (2.0 ** -18 if bf16 else 2.0 ** -22) * np.minimum(near * 2.0 ** e[::16],
+                                                                       block.max(-1, keepdims=True))
             D[r0:r0 + n, h] = step[:, at] @ (np.abs(v[:, g]).max(-1) / 2.0 ** e)     # codes of 448 at most
     return A, D
 
@@ -58,10 +66,10 @@ def weighted(s, cache):
 def check(s, o, bf16, planes, prompt=False):
     cache, want, SV = s.want()
     got = o.float().cpu().numpy()[:s.T, :s.H * s.hd].reshape(want.shape).astype(np.float64)
-    A, D = weighted(s, cache)
+    A, D = weighted(s, cache, prompt, bf16)
     u = 2.0 ** -17 + (2.0 ** -11 if planes == 1 else 0)
     e = 2.0 ** -16 + (2.0 ** -11 if planes == 1 else 0)
-    tol = (2 * SV[..., :1] * u + 2 * e) * A + (8 if prompt else 1) * D[..., None]
+    tol = (2 * SV[..., :1] * u + 2 * e) * A + D[..., None]
     tol += (2.0 ** -8 if bf16 else 2.0 ** -23) * np.abs(want) + 1e-40
     err = np.abs(got - want)
     assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:5].tolist())
@@ -116,6 +124,8 @@ def test_small_values_beside_a_missing_page(b, kind, missing):
 FAR = [
     (4.5, 24),     # nothing of the page is left: the others' values stand alone
     (3.0, 12),     # the same with values that f16 holds beside each other
+    (3.0, 14),     # the last scale that prompts take together with the others'
+    (3.0, 15),     # the first that they do not
     (3.0, 45),     # weights of 2^-49, values of 2^45: both count
     (2.0, 48),     # weights of 2^-33: the page is all that counts
     (-3.0, -12),   # the page has all the weight, the others values of 2^12: both count
