@@ -244,19 +244,30 @@ int s2op_attn_decode_noalloc(const float* qkv, int qkv_ld, int B, int m, int H, 
  * beyond 448 * 2^32, infinities among them, saturate).  Rounding is to nearest
  * even, on keys that are normed and rotated to about 2^-44, so the bytes of a
  * token depend neither on the batch nor on whether a prompt or a single step
- * appended it.  New rows in a block with older ones take the larger of both
- * scales; where it grows, the older rows are rescaled (exact, but for values
- * that become e4m3 subnormals).  Scales are powers of two as these calls write
+ * appended it, with one exception.  New rows in a block with older ones take the
+ * larger of both scales; where it grows, the older rows are rescaled, which is
+ * exact but for values that become e4m3 subnormals: these are rounded a second
+ * time, and may differ by one rounding from what one call with all the rows
+ * would have stored.  Scales are powers of two as these calls write
  * them: in place of another value the power of two next to it is taken.
  *
  * hd is 64 or 128, H / Hkv 1..8, B 1..1024.  qkv rows as in s2op_attn_decode:
  * [q (H*hd) | k (Hkv*hd) | v (Hkv*hd)], fp32, qkv_ld >= (H + 2 Hkv) hd;
  * rope_cos / rope_sin [n_pos][hd/2]; sequence b's page j is table[b *
  * table_ld + j].  o: rows of H*hd values, pitch o_ld, fp32 (o_bf16 = 0) or
- * bf16 (1).  Softmax statistics and sums are fp32; the products run on the
- * tensor cores, e4m3 values being exact in f16, with q and the probabilities
- * as f16 pairs (hi + lo, 22 bits) -- in prompt attention with a bf16 output as
- * single f16 (11 bits), since its own rounding is coarser by 8 times.
+ * bf16 (1).  Softmax statistics and sums are fp32 (a row of q or k has to have a
+ * sum of squares that fp32 holds); the products run on the tensor cores, e4m3
+ * values being exact in f16, with q and the probabilities as f16 pairs (hi + lo,
+ * 22 bits).  A probability times its block's scale 2^e is held against the largest
+ * of these in its row: single tokens round it by 2^-31 of the largest among blocks
+ * of up to 2^10 times its scale, prompts by 2^-22 (2^-18 with a bf16 output) of the
+ * largest probability among blocks of up to 2^14 times its scale, at its scale; a
+ * block of larger values counts only as far as its weight.  Prompt attention with a
+ * bf16 output takes q and the probabilities as single f16 (11 bits): the
+ * probabilities' rounding is an eighth of the output's, q's moves a score by up to
+ * 2^-11 sum |q_i k_i| / sqrt(hd), which grows with the scores (with gains of 0.5 to
+ * 1.5 the error is 1.02 times that of the output's rounding alone, with query gains
+ * of 20 times that 1.29 times); an fp32 output has pairs.
  *
  * A sequence whose new positions do not lie in [0, min(n_pos, 16 table_ld))
  * (pos[b] = -1, for instance: a padded batch) is left out: nothing is stored

@@ -18,11 +18,11 @@ constexpr int kDecSmem = 227 * 1024;
 constexpr int kDecFlight = 128 * 1024;
 constexpr int kDecPages = 2;       // pages of a unit of work
 // Units of a run at least: a cut costs a joining, about as long as a few units
-// (one sequence of 1,090 tokens: 15.2 us with 3, 16.9 us with 6).
+// (one sequence of 1,090 tokens: 15.7 us with 3, 17.7 us with 6).
 constexpr int kDecMinUnits = 3;
 // What starting and ending a sequence costs, in units: the cut counts it (128
-// sequences of up to 1,700 tokens: 57.0 us with 2, 55.3 us with 4; 32 of about
-// 1,000: 27.7 and 25.6 us).
+// sequences of up to 1,700 tokens: 57.8 us with 2, 56.0 us with 4; 32 of about
+// 1,000: 27.6 and 25.9 us).
 constexpr int kDecSeqUnits = 4;
 // Pieces that are joined at once, one per lane; more are joined in two levels
 // of about the square root each.
@@ -153,8 +153,8 @@ struct DecState {           // one piece of a (sequence, kv head): all rows, log
 // pages far below the largest scale are added with o lifted to them.
 //
 // Bound by memory where the keys are many: 128 sequences of 200 to 1,700 tokens,
-// 8 heads of 128 (250 MB): 55.5 us, 4.5 TB/s over all, 6 TB/s in the loop; 32 of
-// 900 to 1,090 (65 MB): 25.6 us, of which a start of 1.7 us and round trips of
+// 8 heads of 128 (250 MB): 56.0 us, 4.5 TB/s over all, 6 TB/s in the loop; 32 of
+// 900 to 1,090 (65 MB): 25.9 us, of which a start of 1.7 us and round trips of
 // half a microsecond each (queries, append, ticket, join) with the tail of the
 // joins are more than half.  mma.sync, not tcgen05: with at most 8 rows its tile of
 // 128 would be empty, and the tensor pipe is 17 % busy as it is.

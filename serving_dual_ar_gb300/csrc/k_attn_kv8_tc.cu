@@ -18,7 +18,7 @@ constexpr int kPreTmem = 512;                 // S / P of two tiles, O of two ti
 // Weights carry 2^bias, and the running maximum may lag by ``lag``: they are 2^15 at
 // most.  f16 pairs (an fp32 output) get the better resolution of a short lag, which
 // costs more rescaling where scores are large (single f16, gains of 5: 607 us for
-// 8,000 tokens with a lag of 4, 580 with 8).
+// 8,000 tokens with a lag of 4, 572 with 8).
 template <int PLANES>
 struct PreScale {
   static constexpr int kBias = PLANES == 1 ? 7 : 11, kLag = 15 - kBias;
@@ -36,8 +36,8 @@ constexpr int kPreStepBytes = 4;              // what is kept of each step
 // for both with an fp32 output, where the products take twice the time), one
 // for the products.  The launch's registers are shared out anew among them:
 // with an fp32 output a softmax thread holds its row's output too.  The keys'
-// and values' warps want theirs for loads ahead (8,000 tokens: 554 us with 72 a
-// thread, 515 with 88).
+// and values' warps want theirs for loads ahead (8,000 tokens: 561 us with 72 a
+// thread, 511 with 88).
 template <int PLANES>
 struct PreRoles {
   static constexpr int kWiden = PLANES == 1 ? 2 : 1, kGroups = 3 + kWiden, kThreads = kGroups * 128;
@@ -320,12 +320,18 @@ __device__ constexpr size_t part_floats() { return (size_t)2 * kPreRows * (HD + 
 // off, toward zero; over a thousand steps that grows to 2^-16 of the output.
 // So each step's P V starts from zero, and the row's thread adds it up, rounded
 // to nearest, in registers (error against 64 bits behind 8,000 tokens: 1.7e-5
-// with the sums in tensor memory, 2.9e-7 so).
+// with the sums in tensor memory, 3.0e-7 so).
+// PLANES = 1 (bf16 output): Q and P as single f16.  P is rounded by at most 2^-11 of
+// each weight, an eighth of the output's own rounding.  Q's rounding moves a score
+// by up to 2^-11 of sum |q k|, so that its part grows with the scores: the error
+// against 64 bits is 1.02 times that of the output's rounding alone with gains of
+// 0.5 to 1.5, 1.06 times with query gains five times as large, 1.29 times with
+// twenty.  Pairs would take 1,054 us for 8,000 tokens (as with an fp32 output).
 //
 // Bound on paper by the products (2,048 clocks a step for both tiles), in fact by
 // the softmax threads' way through tensor memory and by issue slots: 4,400 clocks
-// a step (issue slots 62 % taken, the tensor pipe 47 % busy).  With the append before it: 8,000 tokens, 32 query
-// and 8 kv heads of 128, bf16: 512 us, 1,020 TFLOP/s, 53 % of what a bf16 matrix
+// a step (issue slots 62 % taken, the tensor pipe 48 % busy).  With the append before it: 8,000 tokens, 32 query
+// and 8 kv heads of 128, bf16: 509 us, 1,030 TFLOP/s, 53 % of what a bf16 matrix
 // product reaches; 1,024, fp32: 58 us; 16 prompts of about 94 tokens behind 600 to
 // 900 cached ones, bf16: 65 us, each CTA's start (12,500 clocks) over a quarter of it.
 template <int HD, int PLANES, bool VEC>

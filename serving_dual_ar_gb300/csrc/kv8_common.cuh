@@ -4,9 +4,10 @@
 // scales [2][Hkv], powers of two.  A block is the 16 rows of one (page, K or
 // V, head); its scale is 2^e with the smallest e in [-32, 32] whose 448 * 2^e
 // covers the block's largest magnitude.  With scales that are powers of two a
-// change of scale moves the exponents of the stored values and nothing else
-// (values that become e4m3 subnormals round once more), so a block filled
-// token by token holds the bytes that it would hold if filled at once.
+// change of scale moves the exponents of the stored values and nothing else, so a
+// block filled token by token holds the bytes that it would hold if filled at once
+// -- but for values that become e4m3 subnormals when the scale grows behind them,
+// which were rounded before and are rounded once more.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -113,7 +114,7 @@ S2_DEV float round_odd(Two a) {
 // inverse root (one Newton step on the float one) and the rotation run in
 // two-float arithmetic (about 44 bits), because the result is rounded to 8
 // bits at once: whether a prompt or a single step appends a token, in
-// whatever batch, the cache gets the same bytes.  Everything else of the
+// whatever batch, it is rounded from the same value.  Everything else of the
 // attention is fp32.
 template <int HD>
 S2_DEV void kv8_key_row(const float* __restrict__ x, const float* __restrict__ gain,
