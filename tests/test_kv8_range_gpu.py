@@ -39,6 +39,7 @@ def weighted(s, cache, prompt, bf16):
         x = s.qkv[r0:r0 + n, :(s.H + 2 * s.Hkv) * s.hd].reshape(n, -1, s.hd)
         q = ref.norm_rope(x[:, :s.H], s.qg, s.cos[p0:p0 + n], s.sin[p0:p0 + n], EPS)
         k, v, ok = cache.keys_values(s.table[i], p0 + n)
+        v = np.where(ok[:, None, None], v, 0.0)
         at = np.arange(p0 + n) // 16
         pages = np.where(ok, s.table[i][at], 0)
         see = ok[None] & (np.arange(p0 + n)[None] <= (p0 + np.arange(n))[:, None])
@@ -187,3 +188,27 @@ def test_prompt_of_far_values_in_another_range(b, lam, by, bf16):
     o, _ = s.run(b, "prefill", bf16)
     torch.cuda.synchronize()
     check(s, o, bf16, 1 if bf16 else 2, True)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_calls_at_random(b, seed):
+    """Head layouts, lengths, value scales, missing pages and blocks of zeros at random."""
+    r = np.random.default_rng(1000 + seed)
+    Hkv, G, hd, B = r.choice([1, 2, 3, 5]), r.choice([1, 2, 3, 4, 8]), int(r.choice([64, 128])), r.choice([1, 2, 3, 7])
+    H, Hkv, kind, bf16 = int(Hkv * G), int(Hkv), ["decode", "prefill"][seed % 2], bool(r.integers(2))
+    pos = r.choice([0, 3, 15, 16, 40, 130, 300, 777, 1500], B) + r.integers(0, 20, B)
+    new = np.full(B, r.integers(1, 8 // G + 1)) if kind == "decode" else r.choice([1, 2, 17, 64, 150], B)
+    s = Setup(pos, new, H, Hkv, hd, seed=seed, pad=int(r.choice([0, 4, 3])), spread=float(r.choice([0, 2, 6, 9, 18])))
+    s.exps[:, 0] = np.clip(s.exps[:, 0], -9, -6)              # keys of ordinary sizes
+    s.qg *= np.float32(r.choice([1, 1, 4]))
+    v = s.qkv[:, (H + Hkv) * hd:(H + 2 * Hkv) * hd]
+    v *= (2.0 ** (r.integers(-20, 21, s.T + 2) * r.integers(0, 2)))[:, None].astype(np.float32)
+    if seed % 3 == 0:
+        for i in r.integers(0, B, 3):
+            s.table[i, r.integers(0, (pos[i] + new[i] + 15) // 16)] = r.choice([-1, s.n_pages, 1 << 30])
+    if seed % 4 == 0:
+        s.codes[r.integers(0, s.n_pages, 4), 1] = 0
+    s.upload()
+    o, _ = s.run(b, kind, bf16)
+    torch.cuda.synchronize()
+    check(s, o, bf16, 1 if bf16 and kind == "prefill" else 2, kind == "prefill")
