@@ -338,6 +338,77 @@ int s2op_kv_copy_pages(void* kv, size_t page_bytes, void* scale, size_t scale_by
 int s2op_kv_remap_pages(int32_t* table, int rows, int cols, int table_ld, const int32_t* src,
                         const int32_t* dst, int n, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit weights and 8-bit rows.  A decode step of few sequences is bound by
+ * reading the weights once; these calls keep them in 4 bits, a quarter of the
+ * bf16 matrices' bytes, and the rows that meet them in 8.
+ *
+ * A row of K values is held in groups of 32 with a power of two 2^e each (the
+ * OCP microscaling formats MXFP4 and MXFP8).  e is the smallest of [-126, 120]
+ * with largest magnitude <= top * 2^e; the values divided by 2^e are rounded to
+ * nearest, ties to even: no finite value saturates.
+ *   weights, e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives; top 6): codes
+ *   [N][Kp/2] bytes, value 2i in the low and 2i+1 in the high four bits of
+ *   byte i, Kp = K rounded up to a multiple of 128, padded with zeros; 32-byte
+ *   aligned, s2op_w4_code_bytes(N, K) in all.
+ *   rows, e4m3 (top 448): [T][ld8] bytes, 16-byte aligned, ld8 a multiple of
+ *   16, ld8 >= K.  Bytes from K on are neither read nor written.
+ *   scales: bytes e + 127 (255: NaN) of row r, group g at
+ *     ((r / 128) * ceil(K / 128) + g / 4) * 512 + r % 32 * 16 + r / 32 % 4 * 4 + g % 4,
+ *   tiles of 128 rows x 4 groups; 16-byte aligned, s2op_mx_scale_bytes(rows, K)
+ *   in all.  Groups beyond K hold 2^0 in rows that exist; the bytes of rows that
+ *   do not exist are neither written nor used.
+ * Sizes: any N, T in [0, 2^24] (none: nothing is done) and K in [1, 2^20].
+ * Plain matrices are fp32 or bf16 (*_bf16 = 1) with a row pitch ld* of at least
+ * their columns, aligned to their elements (16-byte aligned rows are read and
+ * written fastest).  S2_EINVAL for a NULL or misaligned pointer, a pitch or a
+ * size out of range. */
+size_t s2op_w4_code_bytes(int N, int K);
+size_t s2op_mx_scale_bytes(int rows, int K);
+
+/* Weights W [N][K] into codes and scales.  A group that holds a NaN or an
+ * infinity becomes NaN as a whole. */
+int s2op_w4_pack(const void* W, int w_bf16, int N, int K, int ldw, void* codes, void* scale,
+                 void* stream);
+/* The reverse: code * 2^e, exact in fp32 and in bf16. */
+int s2op_w4_unpack(const void* codes, const void* scale, int N, int K, void* W, int w_bf16, int ldw,
+                   void* stream);
+
+/* Rows X [T][K] to 8 bits with scales.  NaN and infinities are stored as NaN
+ * and do not count for the scales. */
+int s2op_mx8_pack(const void* X, int x_bf16, int ldx, int T, int K, void* y8, int ld8,
+                  void* y_scale, void* stream);
+
+/* h = x + r (r NULL: x), rounded to x's type and stored to H, then
+ *   y = h / sqrt(mean_k h^2 + eps) * gain,  to 8 bits with scales
+ * as in s2op_mx8_pack.  y is computed to about 2^-44 before it is rounded, so
+ * its codes do not depend on the order of the sum.  gain: fp32 [K]; eps >= 0.
+ * H: of x's type; may be X itself (then ldh = ldx) and, without r, NULL; R may
+ * be H.  Otherwise the operands do not overlap.  A row with a NaN or an
+ * infinity in h, or without a square above zero and eps = 0, is NaN in y8. */
+int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int r_bf16, int ldr,
+                         int T, int K, const float* gain, float eps, void* H, int ldh, void* y8,
+                         int ld8, void* y_scale, void* stream);
+
+/* Products with 4-bit weights:
+ *   Y[t, n] (op)= sum_k X[t, k] W[n, k],   n < N
+ *   mode 0: Y = y;  1: Y += y (residual);  2: rows (2i, 2i+1) of W hold
+ *   (gate_i, up_i): Y[t, i] = silu(gate) * up, N even.
+ * Y: fp32 or bf16 (y_bf16 = 1), apart from the other operands; sums are fp32,
+ * rounded once as they are stored.
+ * s2op_w4_gemv: B = 1..8 plain rows X; workspace: at least
+ * s2op_w4_gemv_workspace_bytes(K, B) bytes, 16-byte aligned, of any content (0
+ * bytes for sizes that are refused).  Calls that may overlap in time need one
+ * each.
+ * s2op_w4_gemm: T rows of 8 bits with scales, from s2op_mx8_pack or
+ * s2op_add_rmsnorm_mx8. */
+size_t s2op_w4_gemv_workspace_bytes(int K, int B);
+int s2op_w4_gemv(const void* codes, const void* scale, int N, int K, const void* X, int x_bf16,
+                 int ldx, int B, void* Y, int y_bf16, int ldy, int mode, void* workspace,
+                 void* stream);
+int s2op_w4_gemm(const void* codes, const void* scale, int N, int K, const void* X8, int ld8,
+                 const void* x_scale, int T, void* Y, int y_bf16, int ldy, int mode, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -96,6 +96,15 @@ def _load():
         "s2op_attn_prefill_kv8_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
         "s2op_attn_prefill_kv8": (i32, [vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, f32, vp, vp, i32, vp,
                                         vp, i32, vp, i32, vp, i32, i32, vp, vp]),
+        "s2op_w4_code_bytes": (sz, [i32, i32]),
+        "s2op_mx_scale_bytes": (sz, [i32, i32]),
+        "s2op_w4_pack": (i32, [vp, i32, i32, i32, i32, vp, vp, vp]),
+        "s2op_w4_unpack": (i32, [vp, vp, i32, i32, vp, i32, i32, vp]),
+        "s2op_mx8_pack": (i32, [vp, i32, i32, i32, i32, vp, i32, vp, vp]),
+        "s2op_add_rmsnorm_mx8": (i32, [vp, i32, i32, vp, i32, i32, i32, i32, vp, f32, vp, i32, vp, i32, vp, vp]),
+        "s2op_w4_gemv_workspace_bytes": (sz, [i32, i32]),
+        "s2op_w4_gemv": (i32, [vp, vp, i32, i32, vp, i32, i32, i32, vp, i32, i32, i32, vp, vp]),
+        "s2op_w4_gemm": (i32, [vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, i32, i32, vp]),
         "s2op_kv8_pack_pages": (i32, [vp, i32, i32, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp]),
         "s2op_kv8_unpack_pages": (i32, [vp, vp, i32, vp, vp, i32, i32, vp, i32, i32, i32, vp]),
         "s2op_kv_copy_pages": (i32, [vp, sz, vp, sz, i32, i32, vp, vp, i32, vp]),
@@ -435,6 +444,51 @@ def s2op_kv_remap_pages(table, rows, cols, table_ld, src, dst, n, stream=None):
         raise ValueError("fewer page pairs than n")
     _check(LIB.s2op_kv_remap_pages(ptr(table), rows, cols, table_ld, ptr(src), ptr(dst), n, _stream(stream)),
            "s2op_kv_remap_pages")
+
+
+def s2op_w4_code_bytes(N, K):
+    return LIB.s2op_w4_code_bytes(N, K)
+
+
+def s2op_mx_scale_bytes(rows, K):
+    return LIB.s2op_mx_scale_bytes(rows, K)
+
+
+def s2op_w4_pack(W, w_bf16, N, K, ldw, codes, scale, stream=None):
+    """Weights to 4 bits: codes uint8 [N, ceil(K / 128) * 64], scale uint8 of s2op_mx_scale_bytes(N, K)."""
+    _check(LIB.s2op_w4_pack(ptr(W), int(w_bf16), N, K, ldw, ptr(codes), ptr(scale), _stream(stream)), "s2op_w4_pack")
+
+
+def s2op_w4_unpack(codes, scale, N, K, W, w_bf16, ldw, stream=None):
+    _check(LIB.s2op_w4_unpack(ptr(codes), ptr(scale), N, K, ptr(W), int(w_bf16), ldw, _stream(stream)),
+           "s2op_w4_unpack")
+
+
+def s2op_mx8_pack(X, x_bf16, ldx, T, K, y8, ld8, y_scale, stream=None):
+    """Rows to e4m3 bytes y8 uint8 (or float8_e4m3fn) [T, ld8] and scales uint8 of s2op_mx_scale_bytes(T, K)."""
+    _check(LIB.s2op_mx8_pack(ptr(X), int(x_bf16), ldx, T, K, ptr(y8), ld8, ptr(y_scale), _stream(stream)),
+           "s2op_mx8_pack")
+
+
+def s2op_add_rmsnorm_mx8(X, x_bf16, ldx, R, r_bf16, ldr, T, K, gain, eps, H, ldh, y8, ld8, y_scale, stream=None):
+    _check(LIB.s2op_add_rmsnorm_mx8(ptr(X), int(x_bf16), ldx, ptr(R), int(r_bf16), ldr, T, K, ptr(gain), eps, ptr(H),
+                                    ldh, ptr(y8), ld8, ptr(y_scale), _stream(stream)), "s2op_add_rmsnorm_mx8")
+
+
+def s2op_w4_gemv_workspace_bytes(K, B):
+    return LIB.s2op_w4_gemv_workspace_bytes(K, B)
+
+
+def s2op_w4_gemv(codes, scale, N, K, X, x_bf16, ldx, B, Y, y_bf16, ldy, mode, workspace, stream=None):
+    """1..8 plain rows times 4-bit weights (mode 0 store, 1 add, 2 SwiGLU of interleaved rows)."""
+    _check(LIB.s2op_w4_gemv(ptr(codes), ptr(scale), N, K, ptr(X), int(x_bf16), ldx, B, ptr(Y), int(y_bf16), ldy, mode,
+                            ptr(workspace), _stream(stream)), "s2op_w4_gemv")
+
+
+def s2op_w4_gemm(codes, scale, N, K, X8, ld8, x_scale, T, Y, y_bf16, ldy, mode, stream=None):
+    """Rows of 8 bits with scales times 4-bit weights, modes as in s2op_w4_gemv."""
+    _check(LIB.s2op_w4_gemm(ptr(codes), ptr(scale), N, K, ptr(X8), ld8, ptr(x_scale), T, ptr(Y), int(y_bf16), ldy,
+                            mode, _stream(stream)), "s2op_w4_gemm")
 
 
 def s2op_stream_read_scratch_bytes(n_ops):

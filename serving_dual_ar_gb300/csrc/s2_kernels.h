@@ -270,6 +270,59 @@ struct Kv8PackArgs {
 cudaError_t launch_kv8_pack(const Kv8PackArgs& p, cudaStream_t st);
 cudaError_t launch_kv8_unpack(const Kv8PackArgs& p, cudaStream_t st);
 
+// ------------------------------------------------------------------ rows of 8 and 4 bits, products with them
+// Rows as e4m3 bytes / e2m1 codes with a power of two per 32 values; scale
+// bytes in tiles (mx_common.cuh).  vec: rows of the plain operands start on
+// 16-byte boundaries.
+struct Mx8PackArgs {
+  const void* x = nullptr; int x_bf16 = 0; long long ldx = 0;
+  int T = 0, K = 0;
+  uint8_t* y8 = nullptr; long long ld8 = 0;
+  uint8_t* scale = nullptr;
+  int vec = 0;
+};
+cudaError_t launch_mx8_pack(const Mx8PackArgs& p, cudaStream_t st);
+
+struct Two { float hi, lo; };      // an unevaluated sum
+
+struct AddNormMx8Args {
+  const void* x = nullptr; int x_bf16 = 0; long long ldx = 0;
+  const void* r = nullptr; int r_bf16 = 0; long long ldr = 0;   // null: no residual
+  void* h = nullptr; long long ldh = 0;                         // x + r; may be x
+  int T = 0, K = 0;
+  const float* gain = nullptr; float eps = 0.f;
+  Two inv_k = {0.f, 0.f};                                       // 1 / K
+  uint8_t* y8 = nullptr; long long ld8 = 0;
+  uint8_t* scale = nullptr;
+  int vec = 0, gain_vec = 0;
+};
+cudaError_t launch_add_rmsnorm_mx8(const AddNormMx8Args& p, cudaStream_t st);
+
+struct W4PackArgs {
+  void* w = nullptr; int w_bf16 = 0; long long ldw = 0;
+  int N = 0, K = 0;
+  uint8_t* codes = nullptr; uint8_t* scale = nullptr;
+  int vec = 0;
+};
+cudaError_t launch_w4_pack(const W4PackArgs& p, cudaStream_t st);
+cudaError_t launch_w4_unpack(const W4PackArgs& p, cudaStream_t st);
+
+enum W4Mode { W4_STORE = 0, W4_ADD = 1, W4_SWIGLU = 2 };
+struct W4GemmArgs {
+  const uint8_t* codes = nullptr; const uint8_t* scale = nullptr;
+  int N = 0, K = 0;
+  const void* x = nullptr; int x_bf16 = 0; long long ldx = 0;   // plain rows, or
+  const uint8_t* x8 = nullptr; long long ld8 = 0;               // e4m3 rows
+  const uint8_t* x_scale = nullptr;
+  int T = 0;
+  void* y = nullptr; int y_bf16 = 0; long long ldy = 0;
+  int mode = W4_STORE;
+  void* ws = nullptr;
+};
+cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st);
+size_t w4_gemv_ws_bytes(int K, int B);
+cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st);
+
 // Page copies within a pool of ``layers`` x n_pages pages, and the rewriting
 // of page tables: pairs are host arrays and travel as kernel arguments.
 constexpr int kPagePairs = 2000;
