@@ -1,92 +1,384 @@
-// Products of rows with 4-bit weights (mx_common.cuh):
+// Products of rows with 4-bit weights (mx_common.cuh) on the tensor cores:
 //   Y[t, n] (op)= sum_k X[t, k] W[n, k].
+//
+// The weights are the M = 128 operand (e2m1), the rows the N = TN operand
+// (e4m3), both K-major; tcgen05.mma kind::mxf8f6f4 multiplies them with their
+// scales as they are held.  So no weight passes through a register: the TMA
+// engine spreads a tile's 8 KB of codes to the 16 KB that the MMA reads, and
+// scale tiles go from shared to tensor memory in the order that they have in
+// memory.  A tile of 128 weights' k costs 8.7 KB of the memory stream and 4 MMAs
+// of 32 k, so few rows are bound by memory and many by the tensor cores.
+//
+// Sums: the tensor core cuts what it adds below the last bit of its fp32 sum,
+// which leans towards zero, so 512 k at most are summed there; these partial
+// sums are added up in registers, rounded to nearest (two accumulators take
+// turns).
+//
+// Few rows do not have tiles for every SM: then K is cut into up to eight parts
+// which form a thread-block cluster and add their sums in the order of the
+// parts through distributed shared memory.
 #include "mx_common.cuh"
+#include "tc_common.cuh"
+#include "tma_map.h"
 
 namespace s2 {
 
 namespace {
 
+constexpr int kW4Threads = 192;    // warp 0: copies, warp 1: MMAs, warps 2-5: sums and output
+constexpr int kW4Chunk = 4;        // k-tiles (of 128) summed in tensor memory
+
+struct W4Params {
+  int N, T, KT, n_tiles, mode, y_bf16;
+  long long ldy;
+  const uint8_t* w_scale;
+  const uint8_t* x_scale;
+  void* y;
+  unsigned polls;
+};
+
 S2_DEV float w4_silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-template <typename TY>
-S2_DEV void w4_store(TY* y, float v, int mode) {
-  *y = from_f<TY>(mode == W4_ADD ? to_f(*y) + v : v);
+// A wait that ends when another one of the CTA gave up.
+S2_DEV bool w4_wait(uint64_t* bar, uint32_t parity, unsigned polls, volatile int* fail) {
+  for (unsigned i = 0; i < polls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*fail) return false;
+  }
+  *fail = 1;
+  return false;
 }
 
-// Four consecutive values of row t from k on.
-template <typename TX> S2_DEV void x_values(const W4GemmArgs& a, int t, int k, int KT, float (&v)[4]) {
-  const TX* row = static_cast<const TX*>(a.x) + (long long)t * a.ldx;
+S2_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = k + i < a.K ? to_f(row[k + i]) : 0.f;
-}
-template <> S2_DEV void x_values<uint8_t>(const W4GemmArgs& a, int t, int k, int KT, float (&v)[4]) {
-  const uint8_t* row = a.x8 + (long long)t * a.ld8;
-  const float s = mx_scale(a.x_scale[mx_scale_at(t, k / 128, KT) + (k / 32) % 4]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = k + i < a.K ? mx_e4m3(row[k + i]) * s : 0.f;
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// One warp per two features and four rows of X; a lane takes four of 128 k.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(128) w4_gemm_kernel(W4GemmArgs a) {
-  const int lane = threadIdx.x & 31, KT = (a.K + 127) / 128;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 2;
-  if (n0 >= a.N) return;
-  for (int t0 = blockIdx.y * 4; t0 < a.T; t0 += gridDim.y * 4) {
-    float acc[2][4] = {};
-    for (int kt = 0; kt < KT; ++kt) {
-      const int k = kt * 128 + lane * 4;
-      float w[2][4], x[4][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = min(n0 + j, a.N - 1);
-        const uint32_t c = *reinterpret_cast<const uint16_t*>(a.codes + (size_t)n * (KT * 64) + k / 2);
-        const float s = mx_scale(a.scale[mx_scale_at(n, kt, KT) + lane / 8]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[j][i] = mx_e2m1((c >> (4 * i)) & 15u) * s;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) x_values<TX>(a, min(t0 + q, a.T - 1), k, KT, x[q]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j][q] = fmaf(w[j][i], x[q][i], acc[j][q]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float y0 = warp_sum(acc[0][q]), y1 = warp_sum(acc[1][q]);
-      if (lane || t0 + q >= a.T) continue;
-      TY* y = static_cast<TY*>(a.y) + (long long)(t0 + q) * a.ldy;
-      if (a.mode == W4_SWIGLU) {
-        y[n0 / 2] = from_f<TY>(w4_silu_mul(y0, y1));
-      } else {
-        w4_store(y + n0, y0, a.mode);
-        if (n0 + 1 < a.N) w4_store(y + n0 + 1, y1, a.mode);
-      }
-    }
+constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + 1024; }
+constexpr int w4_tmem_cols(int need) { return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512; }
+
+// One output of row t, feature n (every lane of a warp: 32 features).
+S2_DEV void w4_out(const W4Params& p, int t, int n, int lane, float v) {
+  if (p.mode == W4_SWIGLU) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+    if ((lane & 1) || n >= p.N) return;
+    v = w4_silu_mul(v, u);
+    n >>= 1;
+  } else if (n >= p.N) {
+    return;
+  }
+  const long long at = t * p.ldy + n;
+  if (p.y_bf16) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+    *y = __float2bfloat16_rn(p.mode == W4_ADD ? __bfloat162float(*y) + v : v);
+  } else {
+    float* y = static_cast<float*>(p.y) + at;
+    *y = p.mode == W4_ADD ? *y + v : v;
   }
 }
 
-template <typename TX>
-cudaError_t launch_simple(const W4GemmArgs& a, cudaStream_t st) {
-  void* args[] = {const_cast<W4GemmArgs*>(&a)};
-  const void* k = a.y_bf16 ? (const void*)w4_gemm_kernel<TX, __nv_bfloat16> : (const void*)w4_gemm_kernel<TX, float>;
-  const dim3 grid((a.N + 7) / 8, min((a.T + 3) / 4, 65535));
-  const cudaError_t e = cudaLaunchKernel(k, grid, dim3(128), args, 0, st);
-  if (e == cudaSuccess) ++g_launch_count;
-  return e;
+// P: rows of the operand per row of X (parts of its values, added up).
+template <int TN, int STAGES, int P, bool CL>
+__global__ void __launch_bounds__(kW4Threads)
+w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W4Params p) {
+  constexpr int STAGE = w4_stage_bytes(TN), B_AT = 128 * 128, SF_AT = B_AT + TN * 128;
+  constexpr int SF_COLS = 2 * TN, TM_COLS = w4_tmem_cols(2 * TN + STAGES * 8);
+  constexpr int TB = TN / P;             // rows of X in a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_fail;
+  volatile int* fail = &s_fail;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_tile = blockIdx.x % p.n_tiles, n0 = n_tile * 128, t0 = blockIdx.x / p.n_tiles * TN;
+  const int S = CL ? (int)gridDim.z : 1, split = CL ? (int)blockIdx.z : 0;
+  const int kt0 = (int)((long long)split * p.KT / S);
+  const int nk = (int)((long long)(split + 1) * p.KT / S) - kt0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 128);
+    }
+    mbar_init(&drained, 1);
+    s_fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&tmem_base)), "r"(TM_COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  // behind the allocation: CTAs of the next kernel may now take what is left
+  pdl_launch_next();
+  pdl_wait();
+
+  float acc[TN];
+  int issued = 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint8_t* ws = p.w_scale + ((size_t)n_tile * p.KT + kt0) * kMxTile;
+      const uint8_t* xs = p.x_scale + ((size_t)(t0 >> 7) * p.KT + kt0) * kMxTile;
+      for (int s = 0; s < nk; ++s) {
+        const int slot = s % STAGES;
+        if (s >= STAGES && !w4_wait(&empty[slot], ((s / STAGES) + 1) & 1, p.polls, fail)) break;
+        uint8_t* st = smem + slot * STAGE;
+        mbar_arrive_expect_tx(&full[slot], 128 * 64 + TN * 128 + 1024);   // codes count as they lie in memory
+        tma_load_2d(st, &map_w, (kt0 + s) * 128, n0, &full[slot]);
+        bulk_g2s(st + SF_AT, ws + (size_t)s * kMxTile, kMxTile, &full[slot]);
+        tma_load_2d(st + B_AT, &map_x, (kt0 + s) * 128, t0, &full[slot]);
+        bulk_g2s(st + SF_AT + kMxTile, xs + (size_t)s * kMxTile, kMxTile, &full[slot]);
+        issued = s + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int s = 0; s < nk; ++s) {
+        const int slot = s % STAGES, c = s / kW4Chunk, buf = c & 1;
+        if (s % kW4Chunk == 0 && c >= 2 && !w4_wait(&acc_empty[buf], ((c >> 1) + 1) & 1, p.polls, fail)) break;
+        if (!w4_wait(&full[slot], (s / STAGES) & 1, p.polls, fail)) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + slot * STAGE), sf = tmem + SF_COLS + slot * 8;
+        tmem_cp_scales(sf, a + SF_AT);
+        tmem_cp_scales(sf + 4, a + SF_AT + kMxTile);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          umma_mxf8f6f4(tmem + buf * TN, smem_desc_sw128(a + 32 * j), smem_desc_sw128(a + B_AT + 32 * j),
+                        idesc_e2m1_e4m3(128, TN, j), sf, sf + 4, s % kW4Chunk > 0 || j > 0);
+        umma_commit(&empty[slot]);
+        if (s % kW4Chunk == kW4Chunk - 1 || s == nk - 1) umma_commit(&acc_full[buf]);
+      }
+      umma_commit(&drained);
+    }
+  } else {
+    const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
+    const int chunks = (nk + kW4Chunk - 1) / kW4Chunk;
+    for (int c = 0; c < chunks; ++c) {
+      const int buf = c & 1;
+      if (!w4_wait(&acc_full[buf], (c >> 1) & 1, p.polls, fail)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < TN; i += 16) {
+        float v[16];
+        tmem_ld16(tmem + lane_at + buf * TN + i, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i + j] = c ? acc[i + j] + v[j] : v[j];
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[buf]);
+    }
+  }
+  __syncwarp();
+  // behind a wait that gave up, products and copies may still be under way:
+  // shared and tensor memory are used again and given back when they are done
+  mbar_wait(&drained, 0, nullptr);
+  if (threadIdx.x == 0)
+    for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+      mbar_wait(&full[j % STAGES], (j / STAGES) & 1, nullptr);
+  __syncthreads();
+
+  const int rows = min(TB, p.T - t0), f = (warp & 3) * 32 + lane, n = n0 + f;
+  const bool give_up = *fail != 0;
+  if (warp >= 2) {
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {       // into the first TB, behind those still to be read
+      float v = acc[b * P + P - 1];
+#pragma unroll
+      for (int i = P - 2; i >= 0; --i) v += acc[b * P + i];
+      acc[b] = give_up ? __uint_as_float(0x7fffffffu) : v;
+    }
+  }
+  if (CL) {
+    float* red = reinterpret_cast<float*>(smem);
+    if (warp >= 2) {
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+        if (b < rows) red[b * 128 + f] = acc[b];
+    }
+    cluster_sync_all();
+    if (warp >= 2) {
+      for (int b = split; b < rows; b += S) {
+        float part[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) part[s] = s < S ? ld_dsmem_f32(red + b * 128 + f, (uint32_t)s) : 0.f;
+        float v = part[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+          if (s < S) v += part[s];
+        w4_out(p, t0 + b, n, lane, v);
+      }
+    }
+    cluster_sync_all();
+  } else if (warp >= 2) {
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+      if (b < rows) w4_out(p, t0 + b, n, lane, acc[b]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TM_COLS) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- plain rows as 8-bit parts
+
+// A row of fp32 (bf16) values as P = 6 (3) rows of e4m3 values whose scales
+// fall by 2^4 from one to the next: each takes four bits or more of what the
+// ones before it left, exactly.  What remains lies below 2^-10 of the last
+// row's scale, 2^-38 (2^-26) of the group's largest magnitude.
+constexpr int kParts32 = 6, kParts16 = 3;
+
+template <typename T, int P>
+__global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* rows8, long long ld8, uint8_t* scale) {
+  pdl_launch_next();
+  const int lane = threadIdx.x & 31, KT = (a.K + 127) / 128;
+  const int u = blockIdx.x * 8 + (threadIdx.x >> 5);       // a warp: 128 values of a row, four a lane
+  if (u >= a.T * KT) return;
+  const int b = u / KT, kt = u % KT, k0 = kt * 128 + lane * 4;
+  const T* x = static_cast<const T*>(a.x) + b * a.ldx;
+  float v[4], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = k0 + i < a.K ? to_f(x[k0 + i]) : 0.f;
+    if (!(fabsf(v[i]) <= 3.402823466e38f)) v[i] = __uint_as_float(0x7fffffffu);
+    m = fmaxf(m, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = mx8_exponent(m);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int ep = max(e - 4 * p, kMxEMin);
+    const float f = mx_pow2(-ep), g = mx_pow2(ep);
+    const uint32_t c = mx_e4m3x2(v[0] * f, v[1] * f) | (mx_e4m3x2(v[2] * f, v[3] * f) << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? fmaf(-mx_e4m3(c >> (8 * i)), g, v[i]) : 0.f;
+    const long long row = (long long)b * P + p;
+    *reinterpret_cast<uint32_t*>(rows8 + row * ld8 + k0) = c;
+    uint32_t w = (uint32_t)(ep + 127) << (lane / 8 * 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 16);
+    if (lane == 0) *reinterpret_cast<uint32_t*>(scale + mx_scale_at(row, kt, KT)) = w;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+int w4_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
+template <int TN, int STAGES, int P, bool CL>
+cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Params& p, dim3 grid, cudaStream_t st) {
+  constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
+  static_assert(TN / P * 512 <= STAGES * w4_stage_bytes(TN), "a tile's sums fit the stages");
+  auto k = w4_tc_kernel<TN, STAGES, P, CL>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kW4Threads);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = grid.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL ? 2 : 1;
+  return s2_launch(&cfg, k, mw, mx, p);
+}
+
+// Rows8: T * P rows of the operand.
+template <int TN, int STAGES, int P>
+cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale,
+                      cudaStream_t st) {
+  const int KT = (a.K + 127) / 128;
+  CUtensorMap mw, mx;
+  if (!tma_map_w4(&mw, a.codes, a.N, KT * 128)) return cudaErrorInvalidValue;
+  if (!tma_map_u8_2d(&mx, rows8, (long long)a.T * P, a.K, ld8, TN)) return cudaErrorInvalidValue;
+  W4Params p;
+  p.N = a.N;
+  p.T = a.T;
+  p.KT = KT;
+  p.mode = a.mode;
+  p.y_bf16 = a.y_bf16;
+  p.ldy = a.ldy;
+  p.w_scale = a.scale;
+  p.x_scale = x_scale;
+  p.y = a.y;
+  p.polls = a.polls;
+  p.n_tiles = (a.N + 127) / 128;
+  const long long tiles = (long long)p.n_tiles * (P > 1 ? 1 : (a.T + TN - 1) / TN);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  // as many parts of K as give the SMs their CTAs, two k-tiles each at least
+  constexpr int OCC = TN <= 64 ? 2 : 1;
+  const long long room = (long long)w4_sms() * OCC / tiles;
+  int S = (int)(room < 8 ? room : 8);
+  if (S > KT / 2) S = KT / 2;
+  if (S > 1) return launch_tc<TN, STAGES, P, true>(mw, mx, p, dim3((unsigned)tiles, 1, S), st);
+  return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3((unsigned)tiles), st);
 }
 
 }  // namespace
 
-size_t w4_gemv_ws_bytes(int K, int B) { return 16; }
-
-cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st) {
-  return a.x_bf16 ? launch_simple<__nv_bfloat16>(a, st) : launch_simple<float>(a, st);
+size_t w4_gemv_ws_bytes(int K, int B) {
+  const size_t KT = (K + 127) / 128;
+  return KT * kMxTile + (size_t)B * kParts32 * KT * 128;
 }
 
-cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) { return launch_simple<uint8_t>(a, st); }
+cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st) {
+  const int KT = (a.K + 127) / 128, P = a.x_bf16 ? kParts16 : kParts32;
+  uint8_t* scale = static_cast<uint8_t*>(a.ws);
+  uint8_t* rows8 = scale + (size_t)KT * kMxTile;
+  const long long ld8 = KT * 128LL;
+  const dim3 grid((a.T * KT + 7) / 8);
+  if (a.x_bf16) w4_parts_kernel<__nv_bfloat16, kParts16><<<grid, 256, 0, st>>>(a, rows8, ld8, scale);
+  else w4_parts_kernel<float, kParts32><<<grid, 256, 0, st>>>(a, rows8, ld8, scale);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  ++g_launch_count;
+  W4GemmArgs q = a;
+  q.K = (int)ld8;        // the parts' rows are padded with zeros
+  if (a.x_bf16)
+    return a.T * P <= 16 ? launch_tn<16, 5, kParts16>(q, rows8, ld8, scale, st)
+                         : launch_tn<32, 5, kParts16>(q, rows8, ld8, scale, st);
+  return a.T * P <= 16 ? launch_tn<16, 5, kParts32>(q, rows8, ld8, scale, st)
+         : a.T * P <= 32 ? launch_tn<32, 5, kParts32>(q, rows8, ld8, scale, st)
+                         : launch_tn<48, 4, kParts32>(q, rows8, ld8, scale, st);
+}
+
+cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
+  if (a.T <= 16) return launch_tn<16, 5, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 32) return launch_tn<32, 5, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 64) return launch_tn<64, 4, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  return launch_tn<128, 6, 1>(a, a.x8, a.ld8, a.x_scale, st);
+}
 
 }  // namespace s2

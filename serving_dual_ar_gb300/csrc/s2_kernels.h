@@ -318,6 +318,7 @@ struct W4GemmArgs {
   void* y = nullptr; int y_bf16 = 0; long long ldy = 0;
   int mode = W4_STORE;
   void* ws = nullptr;
+  unsigned polls = 2000000;  // of a wait inside the kernel, until it gives up
 };
 cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st);
 size_t w4_gemv_ws_bytes(int K, int B);

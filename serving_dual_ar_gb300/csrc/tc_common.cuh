@@ -77,6 +77,31 @@ S2_DEV void tmem_st8(uint32_t taddr, const float (&v)[8]) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Block-scaled MMA (kind::mxf8f6f4): e2m1 A and e4m3 B, both K-major in
+// shared memory (e2m1: 16 values in 8 of each 16 bytes), one power-of-two scale
+// (ue8m0) per row and 32 k, fp32 D.  One instruction covers 32 k; the byte of
+// the scale columns' words that it takes is ``sf`` for both operands.
+__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(int m, int n, int sf) {
+  return ((uint32_t)sf << 4) | (5u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
+}
+S2_DEV void umma_mxf8f6f4(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t tmem_sfa,
+                          uint32_t tmem_sfb, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      :: "r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(tmem_sfa), "r"(tmem_sfb), "r"(accum) : "memory");
+}
+// A scale tile (32 rows of 16 bytes, contiguous) from shared memory into four
+// tensor-memory columns, repeated in each quarter of the lanes.
+S2_DEV void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)(128 >> 4) << 32;    // 8 rows x 16 B to the next eight rows
+  d |= (uint64_t)1 << 46;             // descriptor version; no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(d) : "memory");
+}
+
 // 2-D tiled TMA load of the box at (x = column, y = row) of `map` into shared
 // memory, completing on `bar` (the _hint form carries an L2 cache policy).
 S2_DEV void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
