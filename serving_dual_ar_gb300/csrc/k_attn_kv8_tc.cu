@@ -89,14 +89,6 @@ S2_DEV void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
       :: "r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accum), "r"(kDescHi) : "memory");
 }
-// One lane of a converged warp, chosen such that the compiler knows that it is
-// one: the products' operands then go to uniform registers as they are, where
-// a branch by lane number has each of them moved there in a loop over lanes.
-S2_DEV bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
-}
 S2_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "

@@ -10,9 +10,9 @@
 // of 32 k, so few rows are bound by memory and many by the tensor cores.
 //
 // Sums: the tensor core cuts what it adds below the last bit of its fp32 sum,
-// which leans towards zero, so 512 k at most are summed there; these partial
-// sums are added up in registers, rounded to nearest (two accumulators take
-// turns).
+// which leans towards zero, so the tiles of one round through the shared-memory
+// stages (768 k at most) are summed there; these partial sums are added up in
+// registers, rounded to nearest (two accumulators take turns).
 //
 // Few rows do not have tiles for every SM: then K is cut into up to eight parts
 // which form a thread-block cluster and add their sums in the order of the
@@ -21,12 +21,16 @@
 #include "tc_common.cuh"
 #include "tma_map.h"
 
+#include <atomic>
+
 namespace s2 {
 
 namespace {
 
-constexpr int kW4Threads = 192;    // warp 0: copies, warp 1: MMAs, warps 2-5: sums and output
-constexpr int kW4Chunk = 4;        // k-tiles (of 128) summed in tensor memory
+// Warp 0: copies, warp 1: MMAs, then groups of four for sums and output, up to
+// 64 columns each.
+constexpr int w4_groups(int tn) { return (tn + 63) / 64; }
+constexpr int w4_threads(int tn) { return (2 + 4 * w4_groups(tn)) * 32; }
 
 struct W4Params {
   int N, T, KT, n_tiles, mode, y_bf16;
@@ -49,49 +53,78 @@ S2_DEV bool w4_wait(uint64_t* bar, uint32_t parity, unsigned polls, volatile int
   return false;
 }
 
-S2_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 16 columns of this thread's tensor-memory lane; not there before tmem_wait_ld.
+S2_DEV void tmem_issue16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+template <int N>
+S2_DEV void tmem_ld_row(uint32_t taddr, float (&v)[N]) {   // N columns, one wait
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tmem_issue16(taddr + i, r + i);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; ++i) {
+    asm volatile("" : "+r"(r[i]));      // read behind the wait
+    v[i] = __uint_as_float(r[i]);
+  }
+}
+
+// A box of a tensor map, and a scale tile, to shared memory.
+S2_DEV void w4_load_2d(uint32_t dst, uint64_t map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+S2_DEV void w4_load(uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(kMxTile), "r"(bar) : "memory");
 }
 
 constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + 1024; }
 constexpr int w4_tmem_cols(int need) { return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512; }
 
-// One output of row t, feature n (every lane of a warp: 32 features).
-S2_DEV void w4_out(const W4Params& p, int t, int n, int lane, float v) {
-  if (p.mode == W4_SWIGLU) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, 1);
-    if ((lane & 1) || n >= p.N) return;
-    v = w4_silu_mul(v, u);
-    n >>= 1;
-  } else if (n >= p.N) {
-    return;
+// Where a warp's outputs go: feature n of consecutive rows.
+template <int MODE, typename TY>
+struct W4Out {
+  TY* at;
+  long long ldy;
+  bool live;
+  S2_DEV W4Out(const W4Params& p, int t, int n)
+      : at(static_cast<TY*>(p.y) + t * p.ldy + (MODE == W4_SWIGLU ? n >> 1 : n)), ldy(p.ldy),
+        live(n < p.N && !(MODE == W4_SWIGLU && (n & 1))) {}
+  S2_DEV void put(int row, float v) const {      // every lane of a warp: 32 features
+    TY* y = at + row * ldy;
+    if (MODE == W4_SWIGLU) v = w4_silu_mul(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    if (live) *y = from_f<TY>(MODE == W4_ADD ? to_f(*y) + v : v);
   }
-  const long long at = t * p.ldy + n;
-  if (p.y_bf16) {
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
-    *y = __float2bfloat16_rn(p.mode == W4_ADD ? __bfloat162float(*y) + v : v);
-  } else {
-    float* y = static_cast<float*>(p.y) + at;
-    *y = p.mode == W4_ADD ? *y + v : v;
+};
+template <typename F>
+S2_DEV void w4_with_out(const W4Params& p, int t, int n, F f) {
+  switch (p.mode * 2 + p.y_bf16) {
+    case 0: f(W4Out<W4_STORE, float>(p, t, n)); break;
+    case 1: f(W4Out<W4_STORE, __nv_bfloat16>(p, t, n)); break;
+    case 2: f(W4Out<W4_ADD, float>(p, t, n)); break;
+    case 3: f(W4Out<W4_ADD, __nv_bfloat16>(p, t, n)); break;
+    case 4: f(W4Out<W4_SWIGLU, float>(p, t, n)); break;
+    default: f(W4Out<W4_SWIGLU, __nv_bfloat16>(p, t, n)); break;
   }
 }
 
 // P: rows of the operand per row of X (parts of its values, added up).
 template <int TN, int STAGES, int P, bool CL>
-__global__ void __launch_bounds__(kW4Threads)
+__global__ void __launch_bounds__(w4_threads(TN))
 w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W4Params p) {
   constexpr int STAGE = w4_stage_bytes(TN), B_AT = 128 * 128, SF_AT = B_AT + TN * 128;
   constexpr int SF_COLS = 2 * TN, TM_COLS = w4_tmem_cols(2 * TN + STAGES * 8);
-  constexpr int TB = TN / P;             // rows of X in a tile
+  constexpr int GN = TN / w4_groups(TN); // columns of a group of warps
+  constexpr int GB = GN / P;             // rows of X in them
+  static_assert(P == 1 || GN == TN, "parts of a row lie in one group");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
@@ -112,7 +145,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], 4 * w4_groups(TN));
     }
     mbar_init(&drained, 1);
     s_fail = 0;
@@ -131,106 +164,129 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   pdl_launch_next();
   pdl_wait();
 
-  float acc[TN];
-  int issued = 0;
+  float acc[GN];
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint8_t* ws = p.w_scale + ((size_t)n_tile * p.KT + kt0) * kMxTile;
       const uint8_t* xs = p.x_scale + ((size_t)(t0 >> 7) * p.KT + kt0) * kMxTile;
-      for (int s = 0; s < nk; ++s) {
-        const int slot = s % STAGES;
-        if (s >= STAGES && !w4_wait(&empty[slot], ((s / STAGES) + 1) & 1, p.polls, fail)) break;
-        uint8_t* st = smem + slot * STAGE;
-        mbar_arrive_expect_tx(&full[slot], 128 * 64 + TN * 128 + 1024);   // codes count as they lie in memory
-        tma_load_2d(st, &map_w, (kt0 + s) * 128, n0, &full[slot]);
-        bulk_g2s(st + SF_AT, ws + (size_t)s * kMxTile, kMxTile, &full[slot]);
-        tma_load_2d(st + B_AT, &map_x, (kt0 + s) * 128, t0, &full[slot]);
-        bulk_g2s(st + SF_AT + kMxTile, xs + (size_t)s * kMxTile, kMxTile, &full[slot]);
-        issued = s + 1;
+      const uint64_t mw = reinterpret_cast<uint64_t>(&map_w), mx = reinterpret_cast<uint64_t>(&map_x);
+      const uint32_t sm = smem_u32(smem);
+      int k = kt0 * 128, left = nk;
+      bool ok = true;
+      for (int r = 0; left > 0 && ok; ++r) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) {
+          if (left <= 0 || (r > 0 && !(ok = w4_wait(&empty[i], (r + 1) & 1, p.polls, fail)))) break;
+          const uint32_t st = sm + i * STAGE, bar = smem_u32(&full[i]);
+          mbar_arrive_expect_tx(&full[i], 128 * 64 + TN * 128 + 1024);   // codes count as they lie in memory
+          w4_load_2d(st, mw, k, n0, bar);
+          w4_load(st + SF_AT, ws, bar);
+          w4_load_2d(st + B_AT, mx, k, t0, bar);
+          w4_load(st + SF_AT + kMxTile, xs, bar);
+          ws += kMxTile;
+          xs += kMxTile;
+          k += 128;
+          --left;
+        }
       }
+      // behind a wait that gave up, copies may still be under way
+      for (int s = max(nk - left - STAGES, 0); s < nk - left; ++s) mbar_wait(&full[s % STAGES], (s / STAGES) & 1, nullptr);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      for (int s = 0; s < nk; ++s) {
-        const int slot = s % STAGES, c = s / kW4Chunk, buf = c & 1;
-        if (s % kW4Chunk == 0 && c >= 2 && !w4_wait(&acc_empty[buf], ((c >> 1) + 1) & 1, p.polls, fail)) break;
-        if (!w4_wait(&full[slot], (s / STAGES) & 1, p.polls, fail)) break;
-        tc_fence_after();
-        const uint32_t a = smem_u32(smem + slot * STAGE), sf = tmem + SF_COLS + slot * 8;
-        tmem_cp_scales(sf, a + SF_AT);
-        tmem_cp_scales(sf + 4, a + SF_AT + kMxTile);
+    if (elect_one()) {
+      const uint32_t st0 = desc_lo(smem_u32(smem)), sf0 = tmem + SF_COLS;
+      int left = nk;
+      bool ok = true;
+      for (int r = 0; left > 0 && ok; ++r) {
+        if (r >= 2 && !w4_wait(&acc_empty[r & 1], ((r >> 1) + 1) & 1, p.polls, fail)) break;
+        const uint32_t d = tmem + (r & 1) * TN;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          umma_mxf8f6f4(tmem + buf * TN, smem_desc_sw128(a + 32 * j), smem_desc_sw128(a + B_AT + 32 * j),
-                        idesc_e2m1_e4m3(128, TN, j), sf, sf + 4, s % kW4Chunk > 0 || j > 0);
-        umma_commit(&empty[slot]);
-        if (s % kW4Chunk == kW4Chunk - 1 || s == nk - 1) umma_commit(&acc_full[buf]);
+        for (int i = 0; i < STAGES; ++i) {
+          if (left <= 0 || !(ok = w4_wait(&full[i], r & 1, p.polls, fail))) break;
+          tc_fence_after();
+          const uint32_t st = st0 + (i * STAGE >> 4), sf = sf0 + i * 8;
+          tmem_cp_scales(sf, st + (SF_AT >> 4));
+          tmem_cp_scales(sf + 4, st + ((SF_AT + kMxTile) >> 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            umma_mxf8f6f4(d, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf, sf + 4, i + j > 0);
+          umma_commit(&empty[i]);
+          --left;
+        }
+        if (ok) umma_commit(&acc_full[r & 1]);
       }
       umma_commit(&drained);
     }
   } else {
-    const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
-    const int chunks = (nk + kW4Chunk - 1) / kW4Chunk;
-    for (int c = 0; c < chunks; ++c) {
-      const int buf = c & 1;
-      if (!w4_wait(&acc_full[buf], (c >> 1) & 1, p.polls, fail)) break;
+    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp - 2) / 4 * GN;
+    const int rounds = (nk + STAGES - 1) / STAGES;
+    for (int r = 0; r < rounds; ++r) {
+      const int buf = r & 1;
+      if (!w4_wait(&acc_full[buf], (r >> 1) & 1, p.polls, fail)) break;
       tc_fence_after();
+      if (r == 0) {
+        tmem_ld_row<GN>(from, acc);
+      } else {
+        float v[GN];
+        tmem_ld_row<GN>(from + buf * TN, v);
 #pragma unroll
-      for (int i = 0; i < TN; i += 16) {
-        float v[16];
-        tmem_ld16(tmem + lane_at + buf * TN + i, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) acc[i + j] = c ? acc[i + j] + v[j] : v[j];
+        for (int i = 0; i < GN; ++i) acc[i] += v[i];
       }
       tc_fence_before();
-      mbar_arrive(&acc_empty[buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
     }
   }
   __syncwarp();
-  // behind a wait that gave up, products and copies may still be under way:
-  // shared and tensor memory are used again and given back when they are done
+  // shared and tensor memory are used again and given back when products and
+  // copies are done, behind a wait that gave up, too
   mbar_wait(&drained, 0, nullptr);
-  if (threadIdx.x == 0)
-    for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
-      mbar_wait(&full[j % STAGES], (j / STAGES) & 1, nullptr);
   __syncthreads();
 
-  const int rows = min(TB, p.T - t0), f = (warp & 3) * 32 + lane, n = n0 + f;
-  const bool give_up = *fail != 0;
+  // this group's rows of X: b0 .. b0 + GB - 1 of the tile
+  const int b0 = warp < 2 ? 0 : (warp - 2) / 4 * GB;
+  const int rows = min(GB, p.T - t0 - b0), f = (warp & 3) * 32 + lane, n = n0 + f;
   if (warp >= 2) {
 #pragma unroll
-    for (int b = 0; b < TB; ++b) {       // into the first TB, behind those still to be read
+    for (int b = 0; b < GB; ++b) {       // into the first GB, behind those still to be read
       float v = acc[b * P + P - 1];
 #pragma unroll
       for (int i = P - 2; i >= 0; --i) v += acc[b * P + i];
-      acc[b] = give_up ? __uint_as_float(0x7fffffffu) : v;
+      acc[b] = v;
+    }
+    if (*fail) {
+#pragma unroll
+      for (int b = 0; b < GB; ++b) acc[b] = __uint_as_float(0x7fffffffu);
     }
   }
   if (CL) {
-    float* red = reinterpret_cast<float*>(smem);
+    float* red = reinterpret_cast<float*>(smem) + b0 * 128 + f;
     if (warp >= 2) {
 #pragma unroll
-      for (int b = 0; b < TB; ++b)
-        if (b < rows) red[b * 128 + f] = acc[b];
+      for (int b = 0; b < GB; ++b)
+        if (b < rows) red[b * 128] = acc[b];
     }
     cluster_sync_all();
-    if (warp >= 2) {
-      for (int b = split; b < rows; b += S) {
-        float part[8];
+    if (warp >= 2)
+      w4_with_out(p, t0 + b0, n, [&](auto out) {
+        for (int b = split; b < rows; b += S) {
+          float part[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) part[s] = s < S ? ld_dsmem_f32(red + b * 128 + f, (uint32_t)s) : 0.f;
-        float v = part[0];
+          for (int s = 0; s < 8; ++s) part[s] = s < S ? ld_dsmem_f32(red + b * 128, (uint32_t)s) : 0.f;
+          float v = part[0];
 #pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < S) v += part[s];
-        w4_out(p, t0 + b, n, lane, v);
-      }
-    }
+          for (int s = 1; s < 8; ++s)
+            if (s < S) v += part[s];
+          out.put(b, v);
+        }
+      });
     cluster_sync_all();
   } else if (warp >= 2) {
+    w4_with_out(p, t0 + b0, n, [&](auto out) {
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
-      if (b < rows) w4_out(p, t0 + b, n, lane, acc[b]);
+      for (int b = 0; b < GB; ++b)
+        if (b < rows) out.put(b, acc[b]);
+    });
   }
   tc_fence_before();
   __syncthreads();
@@ -284,23 +340,16 @@ __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* ro
 
 // ---------------------------------------------------------------- host side
 
-int w4_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 template <int TN, int STAGES, int P, bool CL>
 cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Params& p, dim3 grid, cudaStream_t st) {
   constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
-  static_assert(TN / P * 512 <= STAGES * w4_stage_bytes(TN), "a tile's sums fit the stages");
+  static_assert(TN * 512 <= STAGES * w4_stage_bytes(TN), "a tile's sums fit the stages");
   auto k = w4_tc_kernel<TN, STAGES, P, CL>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kW4Threads);
+  cfg.blockDim = dim3(w4_threads(TN));
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -313,6 +362,35 @@ cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Para
   cfg.attrs = attr;
   cfg.numAttrs = CL ? 2 : 1;
   return s2_launch(&cfg, k, mw, mx, p);
+}
+
+// Clusters of S CTAs that are on the current device at once (kept per device).
+template <int TN, int STAGES, int P>
+int cluster_room(int S) {
+  static std::atomic<int> kept[16][9];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 16 && kept[dev][S].load()) return kept[dev][S].load() - 1;
+  constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
+  auto k = w4_tc_kernel<TN, STAGES, P, true>;
+  int n = 0;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, S);
+    cfg.blockDim = dim3(w4_threads(TN));
+    cfg.dynamicSmemBytes = SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = S;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  if (dev < 16) kept[dev][S].store(n + 1);
+  return n;
 }
 
 // Rows8: T * P rows of the operand.
@@ -337,11 +415,9 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   p.n_tiles = (a.N + 127) / 128;
   const long long tiles = (long long)p.n_tiles * (P > 1 ? 1 : (a.T + TN - 1) / TN);
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  // as many parts of K as give the SMs their CTAs, two k-tiles each at least
-  constexpr int OCC = TN <= 64 ? 2 : 1;
-  const long long room = (long long)w4_sms() * OCC / tiles;
-  int S = (int)(room < 8 ? room : 8);
-  if (S > KT / 2) S = KT / 2;
+  // as many parts of K as have room on the SMs at once, two k-tiles each at least
+  int S = KT / 2 < 8 ? KT / 2 : 8;
+  while (S > 1 && tiles > cluster_room<TN, STAGES, P>(S)) --S;
   if (S > 1) return launch_tc<TN, STAGES, P, true>(mw, mx, p, dim3((unsigned)tiles, 1, S), st);
   return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3((unsigned)tiles), st);
 }

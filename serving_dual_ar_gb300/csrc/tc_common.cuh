@@ -85,21 +85,38 @@ __host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(int m, int n, int sf) {
   return ((uint32_t)sf << 4) | (5u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
          ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
 }
-S2_DEV void umma_mxf8f6f4(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t tmem_sfa,
+// Descriptors by their low words, address / 16 (the high words are constants):
+// operands in 128-byte swizzled rows, scales without a swizzle, eight rows of
+// 16 bytes after eight.
+S2_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) & 0x3FFF; }
+constexpr uint32_t kDescHiSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHiScales = (128 >> 4) | (1u << 14);
+S2_DEV void umma_mxf8f6f4(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t tmem_sfa,
                           uint32_t tmem_sfb, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-      :: "r"(tmem_d), "l"(a), "l"(b), "r"(idesc), "r"(tmem_sfa), "r"(tmem_sfb), "r"(accum) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 x, {%1, %7};\n\tmov.b64 y, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], x, y, %3, [%4], [%5], p;\n\t}"
+      :: "r"(tmem_d), "r"(a), "r"(b), "r"(idesc), "r"(tmem_sfa), "r"(tmem_sfb), "r"(accum), "r"(kDescHiSw128)
+      : "memory");
 }
 // A scale tile (32 rows of 16 bytes, contiguous) from shared memory into four
 // tensor-memory columns, repeated in each quarter of the lanes.
-S2_DEV void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(128 >> 4) << 32;    // 8 rows x 16 B to the next eight rows
-  d |= (uint64_t)1 << 46;             // descriptor version; no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(d) : "memory");
+S2_DEV void tmem_cp_scales(uint32_t taddr, uint32_t scales) {
+  asm volatile(
+      "{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], x;\n\t}"
+      :: "r"(taddr), "r"(scales), "r"(kDescHiScales) : "memory");
+}
+
+// One lane of a converged warp, chosen such that the compiler knows that it is
+// one: the operands of products and copies then go to uniform registers as they
+// are, where a branch by lane number has each of them moved there in a loop over
+// lanes.
+S2_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // 2-D tiled TMA load of the box at (x = column, y = row) of `map` into shared
