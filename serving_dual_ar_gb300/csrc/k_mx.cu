@@ -93,8 +93,8 @@ constexpr int kUnits = 4;   // (row, 128 values) of a half-warp, all loaded befo
 
 template <typename T>
 __global__ void __launch_bounds__(256) mx8_pack_kernel(Mx8PackArgs p) {
-  pdl_wait();
   pdl_launch_next();
+  pdl_wait();
   const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
   const long long units = (long long)p.T * KT;
   const long long u0 = (long long)blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(256) mx8_pack_kernel(Mx8PackArgs p) {
 template <typename TX, typename TR, int C>
 __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p) {
   __shared__ float part[2][32];
-  pdl_wait();
   pdl_launch_next();
+  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   const int KT = (p.K + 127) / 128;
   const long long row = blockIdx.x;
@@ -347,8 +347,19 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(W4PackArgs p) {
   }
 }
 
-cudaError_t launch(const void* k, dim3 grid, int threads, void** args, cudaStream_t st) {
-  const cudaError_t e = cudaLaunchKernel(k, grid, dim3(threads), args, 0, st);
+// early: the CTAs may come to their SMs before the kernel ahead in the stream
+// has ended, and wait there.
+cudaError_t launch(const void* k, dim3 grid, int threads, void** args, cudaStream_t st, bool early) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, k, args);
   if (e == cudaSuccess) ++g_launch_count;
   return e;
 }
@@ -362,7 +373,7 @@ unsigned unit_blocks(long long rows, int K) {
 cudaError_t launch_mx8_pack(const Mx8PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<Mx8PackArgs*>(&p)};
   const void* k = p.x_bf16 ? (const void*)mx8_pack_kernel<__nv_bfloat16> : (const void*)mx8_pack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.T, p.K)), 256, args, st);
+  return launch(k, dim3(unit_blocks(p.T, p.K)), 256, args, st, true);
 }
 
 template <int C>
@@ -381,19 +392,19 @@ cudaError_t launch_add_rmsnorm_mx8(const AddNormMx8Args& p, cudaStream_t st) {
   const int c = runs <= 512 ? 1 : runs <= 2048 ? 2 : 0;
   const int nt = c ? ((runs + c - 1) / c + 31) / 32 * 32 : 1024;
   const void* k = c == 1 ? norm_kernel<1>(p) : c == 2 ? norm_kernel<2>(p) : norm_kernel<0>(p);
-  return launch(k, dim3(p.T), nt, args, st);
+  return launch(k, dim3(p.T), nt, args, st, true);
 }
 
 cudaError_t launch_w4_pack(const W4PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<W4PackArgs*>(&p)};
   const void* k = p.w_bf16 ? (const void*)w4_pack_kernel<__nv_bfloat16> : (const void*)w4_pack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st);
+  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st, false);
 }
 
 cudaError_t launch_w4_unpack(const W4PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<W4PackArgs*>(&p)};
   const void* k = p.w_bf16 ? (const void*)w4_unpack_kernel<__nv_bfloat16> : (const void*)w4_unpack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st);
+  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st, false);
 }
 
 }  // namespace s2

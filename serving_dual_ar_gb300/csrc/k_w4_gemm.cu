@@ -10,8 +10,7 @@
 // of 32 k, so few rows are bound by memory and many by the tensor cores.
 //
 // Sums: the tensor core cuts what it adds below the last bit of its fp32 sum,
-// which leans towards zero, so the tiles of one round through the shared-memory
-// stages (768 k at most) are summed there; these partial sums are added up in
+// which leans towards zero, so seven tiles (896 k) at most are summed there; these partial sums are added up in
 // registers, rounded to nearest (two accumulators take turns).
 //
 // Few rows do not have tiles for every SM: then K is cut into up to eight parts
@@ -98,10 +97,14 @@ struct W4Out {
   S2_DEV W4Out(const W4Params& p, int t, int n)
       : at(static_cast<TY*>(p.y) + t * p.ldy + (MODE == W4_SWIGLU ? n >> 1 : n)), ldy(p.ldy),
         live(n < p.N && !(MODE == W4_SWIGLU && (n & 1))) {}
-  S2_DEV void put(int row, float v) const {      // every lane of a warp: 32 features
-    TY* y = at + row * ldy;
+  // What row's output is added to; asked for ahead of put, since a load behind
+  // a store waits for it.
+  S2_DEV float get(int row, bool there) const {
+    return MODE == W4_ADD && live && there ? to_f(at[row * ldy]) : 0.f;
+  }
+  S2_DEV void put(int row, float v, float before) const {      // every lane of a warp: 32 features
     if (MODE == W4_SWIGLU) v = w4_silu_mul(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    if (live) *y = from_f<TY>(MODE == W4_ADD ? to_f(*y) + v : v);
+    if (live) at[row * ldy] = from_f<TY>(MODE == W4_ADD ? before + v : v);
   }
 };
 template <typename F>
@@ -116,18 +119,28 @@ S2_DEV void w4_with_out(const W4Params& p, int t, int n, F f) {
   }
 }
 
+// Four values into another CTA of the cluster, counted by its barrier; both
+// addresses are this CTA's own of the same places.
+S2_DEV void st_async4(uint32_t at, float x, float y, float z, float w, uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a, m;\n\tmapa.shared::cluster.u32 a, %0, %6;\n\tmapa.shared::cluster.u32 m, %5, %6;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%1, %2, %3, %4}, [m];\n\t}"
+      :: "r"(at), "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar), "r"(rank) : "memory");
+}
+
 // P: rows of the operand per row of X (parts of its values, added up).
 template <int TN, int STAGES, int P, bool CL>
 __global__ void __launch_bounds__(w4_threads(TN))
 w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W4Params p) {
   constexpr int STAGE = w4_stage_bytes(TN), B_AT = 128 * 128, SF_AT = B_AT + TN * 128;
+  constexpr int CH = STAGES >= 8 ? STAGES / 2 : STAGES;   // k-tiles summed in tensor memory
   constexpr int SF_COLS = 2 * TN, TM_COLS = w4_tmem_cols(2 * TN + STAGES * 8);
   constexpr int GN = TN / w4_groups(TN); // columns of a group of warps
   constexpr int GB = GN / P;             // rows of X in them
   static_assert(P == 1 || GN == TN, "parts of a row lie in one group");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained, joined;
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail;
   volatile int* fail = &s_fail;
@@ -148,8 +161,11 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
       mbar_init(&acc_empty[i], 4 * w4_groups(TN));
     }
     mbar_init(&drained, 1);
+    mbar_init(&joined, 1);
     s_fail = 0;
     fence_mbar_init();
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -162,35 +178,52 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   const uint32_t tmem = tmem_base;
   // behind the allocation: CTAs of the next kernel may now take what is left
   pdl_launch_next();
-  pdl_wait();
+  if (CL) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   float acc[GN];
   if (warp == 0) {
     if (elect_one()) {
+      const uint64_t mw = reinterpret_cast<uint64_t>(&map_w), mx = reinterpret_cast<uint64_t>(&map_x);
       const uint8_t* ws = p.w_scale + ((size_t)n_tile * p.KT + kt0) * kMxTile;
       const uint8_t* xs = p.x_scale + ((size_t)(t0 >> 7) * p.KT + kt0) * kMxTile;
-      const uint64_t mw = reinterpret_cast<uint64_t>(&map_w), mx = reinterpret_cast<uint64_t>(&map_x);
       const uint32_t sm = smem_u32(smem);
       int k = kt0 * 128, left = nk;
+      auto weights = [&](int i, int ahead) {      // codes count as they lie in memory
+        mbar_arrive_expect_tx(&full[i], 128 * 64 + TN * 128 + 1024);
+        w4_load_2d(sm + i * STAGE, mw, k + ahead * 128, n0, smem_u32(&full[i]));
+        w4_load(sm + i * STAGE + SF_AT, ws + ahead * kMxTile, smem_u32(&full[i]));
+      };
+      auto rows = [&](int i) {
+        w4_load_2d(sm + i * STAGE + B_AT, mx, k, t0, smem_u32(&full[i]));
+        w4_load(sm + i * STAGE + SF_AT + kMxTile, xs, smem_u32(&full[i]));
+        ws += kMxTile;
+        xs += kMxTile;
+        k += 128;
+        --left;
+      };
+      // The first weights are under way before the kernel ahead has ended; the
+      // rows are what it may have written.
+      const int first = min(nk, STAGES);
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i)
+        if (i < first) weights(i, i);
+      pdl_wait();
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i)
+        if (i < first) rows(i);
       bool ok = true;
-      for (int r = 0; left > 0 && ok; ++r) {
+      for (int r = 1; left > 0 && ok; ++r) {
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) {
-          if (left <= 0 || (r > 0 && !(ok = w4_wait(&empty[i], (r + 1) & 1, p.polls, fail)))) break;
-          const uint32_t st = sm + i * STAGE, bar = smem_u32(&full[i]);
-          mbar_arrive_expect_tx(&full[i], 128 * 64 + TN * 128 + 1024);   // codes count as they lie in memory
-          w4_load_2d(st, mw, k, n0, bar);
-          w4_load(st + SF_AT, ws, bar);
-          w4_load_2d(st + B_AT, mx, k, t0, bar);
-          w4_load(st + SF_AT + kMxTile, xs, bar);
-          ws += kMxTile;
-          xs += kMxTile;
-          k += 128;
-          --left;
+          if (left <= 0 || !(ok = w4_wait(&empty[i], (r + 1) & 1, p.polls, fail))) break;
+          weights(i, 0);
+          rows(i);
         }
       }
       // behind a wait that gave up, copies may still be under way
-      for (int s = max(nk - left - STAGES, 0); s < nk - left; ++s) mbar_wait(&full[s % STAGES], (s / STAGES) & 1, nullptr);
+      mbar_wait(&drained, 0, nullptr);
+      for (int s = *fail ? max(nk - left - STAGES, 0) : nk; s < nk - left; ++s)
+        mbar_wait(&full[s % STAGES], (s / STAGES) & 1, nullptr);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -198,33 +231,35 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
       int left = nk;
       bool ok = true;
       for (int r = 0; left > 0 && ok; ++r) {
-        if (r >= 2 && !w4_wait(&acc_empty[r & 1], ((r >> 1) + 1) & 1, p.polls, fail)) break;
-        const uint32_t d = tmem + (r & 1) * TN;
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) {
-          if (left <= 0 || !(ok = w4_wait(&full[i], r & 1, p.polls, fail))) break;
+          if (left <= 0) break;
+          const int c = r * (STAGES / CH) + i / CH, buf = c & 1;
+          if (i % CH == 0 && c >= 2 && !(ok = w4_wait(&acc_empty[buf], ((c >> 1) + 1) & 1, p.polls, fail))) break;
+          if (!(ok = w4_wait(&full[i], r & 1, p.polls, fail))) break;
           tc_fence_after();
           const uint32_t st = st0 + (i * STAGE >> 4), sf = sf0 + i * 8;
           tmem_cp_scales(sf, st + (SF_AT >> 4));
           tmem_cp_scales(sf + 4, st + ((SF_AT + kMxTile) >> 4));
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_mxf8f6f4(d, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf, sf + 4, i + j > 0);
+            umma_mxf8f6f4(tmem + buf * TN, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf,
+                          sf + 4, i % CH + j > 0);
           umma_commit(&empty[i]);
-          --left;
+          if (--left == 0 || i % CH == CH - 1) umma_commit(&acc_full[buf]);
         }
-        if (ok) umma_commit(&acc_full[r & 1]);
       }
       umma_commit(&drained);
     }
   } else {
+    pdl_wait();     // outputs and what they are added to
     const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp - 2) / 4 * GN;
-    const int rounds = (nk + STAGES - 1) / STAGES;
-    for (int r = 0; r < rounds; ++r) {
-      const int buf = r & 1;
-      if (!w4_wait(&acc_full[buf], (r >> 1) & 1, p.polls, fail)) break;
+    const int chunks = (nk + CH - 1) / CH;
+    for (int c = 0; c < chunks; ++c) {
+      const int buf = c & 1;
+      if (!w4_wait(&acc_full[buf], (c >> 1) & 1, p.polls, fail)) break;
       tc_fence_after();
-      if (r == 0) {
+      if (c == 0) {
         tmem_ld_row<GN>(from, acc);
       } else {
         float v[GN];
@@ -260,32 +295,72 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     }
   }
   if (CL) {
-    float* red = reinterpret_cast<float*>(smem) + b0 * 128 + f;
+    // Four rows of the tile (quad q) are joined by part q % S: every part stores
+    // its sums straight into that one's shared memory, whose barrier counts the
+    // bytes.
+    constexpr int JOIN_AT = STAGES * STAGE;
+    const int quads = (min(TN / P, p.T - t0) + 3) / 4, mine = split < quads ? (quads - split + S - 1) / S : 0;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&joined, mine * S * 2048);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp >= 2) {
+      const uint32_t slot = smem_u32(smem + JOIN_AT) + f * 16, bar = smem_u32(&joined);
+      int to = b0 / 4 % S, at = b0 / 4 / S * S + split;
 #pragma unroll
-      for (int b = 0; b < GB; ++b)
-        if (b < rows) red[b * 128] = acc[b];
-    }
-    cluster_sync_all();
-    if (warp >= 2)
-      w4_with_out(p, t0 + b0, n, [&](auto out) {
-        for (int b = split; b < rows; b += S) {
-          float part[8];
+      for (int b = 0; b < GB; b += 4) {
+        if (b < rows)
+          st_async4(slot + at * 2048, acc[b], b + 1 < GB ? acc[b + 1] : 0.f, b + 2 < GB ? acc[b + 2] : 0.f,
+                    b + 3 < GB ? acc[b + 3] : 0.f, bar, to);
+        if (++to == S) {
+          to = 0;
+          at += S;
+        }
+      }
+      w4_with_out(p, t0, n, [&](auto out) {
+        constexpr int Q = 3;      // quads whose rows are asked for at once
+        const int live = min(TN / P, p.T - t0);
+        bool came = false;
+        for (int i0 = (warp - 2) / 4; i0 < mine; i0 += Q * w4_groups(TN)) {
+          float before[Q][4];
 #pragma unroll
-          for (int s = 0; s < 8; ++s) part[s] = s < S ? ld_dsmem_f32(red + b * 128, (uint32_t)s) : 0.f;
-          float v = part[0];
+          for (int q = 0; q < Q; ++q)
 #pragma unroll
-          for (int s = 1; s < 8; ++s)
-            if (s < S) v += part[s];
-          out.put(b, v);
+            for (int j = 0; j < 4; ++j) {
+              const int b = (split + (i0 + q * w4_groups(TN)) * S) * 4 + j;
+              before[q][j] = out.get(b, b < live);
+            }
+          // far longer than a part may take to give up: none stores to a CTA that is gone
+          came = came || mbar_wait(&joined, 0, nullptr, 32000000u);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const int i = i0 + q * w4_groups(TN), b = (split + i * S) * 4;
+            if (i >= mine) break;
+            const float4* from = reinterpret_cast<const float4*>(smem + JOIN_AT) + i * S * 128 + f;
+            float4 v = from[0];
+            for (int s = 1; s < S; ++s) {
+              const float4 u = from[s * 128];
+              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            if (!came) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
+            out.put(b, v.x, before[q][0]);
+            if (b + 1 < live) out.put(b + 1, v.y, before[q][1]);
+            if (b + 2 < live) out.put(b + 2, v.z, before[q][2]);
+            if (b + 3 < live) out.put(b + 3, v.w, before[q][3]);
+          }
         }
       });
-    cluster_sync_all();
+    }
   } else if (warp >= 2) {
     w4_with_out(p, t0 + b0, n, [&](auto out) {
+      constexpr int Q = GB < 16 ? GB : 16;
 #pragma unroll
-      for (int b = 0; b < GB; ++b)
-        if (b < rows) out.put(b, acc[b]);
+      for (int b = 0; b < GB; b += Q) {
+        float before[Q];
+#pragma unroll
+        for (int j = 0; j < Q; ++j) before[j] = out.get(b + j, b + j < GB && b + j < rows);
+#pragma unroll
+        for (int j = 0; j < Q; ++j)
+          if (b + j < GB && b + j < rows) out.put(b + j, acc[b + j < GB ? b + j : 0], before[j]);
+      }
     });
   }
   tc_fence_before();
@@ -307,6 +382,7 @@ constexpr int kParts32 = 6, kParts16 = 3;
 template <typename T, int P>
 __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* rows8, long long ld8, uint8_t* scale) {
   pdl_launch_next();
+  pdl_wait();
   const int lane = threadIdx.x & 31, KT = (a.K + 127) / 128;
   const int u = blockIdx.x * 8 + (threadIdx.x >> 5);       // a warp: 128 values of a row, four a lane
   if (u >= a.T * KT) return;
@@ -340,10 +416,16 @@ __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* ro
 
 // ---------------------------------------------------------------- host side
 
+// Stages, in clusters a tile's quads of rows from up to eight parts, and room to start on
+// 1,024 bytes.
+template <int TN, int STAGES, int P, bool CL>
+constexpr int w4_smem() {
+  return STAGES * w4_stage_bytes(TN) + (CL ? ((TN / P + 3) / 4 + 7) * 2048 : 0) + 1024;
+}
+
 template <int TN, int STAGES, int P, bool CL>
 cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Params& p, dim3 grid, cudaStream_t st) {
-  constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
-  static_assert(TN * 512 <= STAGES * w4_stage_bytes(TN), "a tile's sums fit the stages");
+  constexpr int SMEM = w4_smem<TN, STAGES, P, CL>();
   auto k = w4_tc_kernel<TN, STAGES, P, CL>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
@@ -371,7 +453,7 @@ int cluster_room(int S) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 16 && kept[dev][S].load()) return kept[dev][S].load() - 1;
-  constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
+  constexpr int SMEM = w4_smem<TN, STAGES, P, true>();
   auto k = w4_tc_kernel<TN, STAGES, P, true>;
   int n = 0;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess) {
@@ -393,8 +475,8 @@ int cluster_room(int S) {
   return n;
 }
 
-// Rows8: T * P rows of the operand.
-template <int TN, int STAGES, int P>
+// rows8: T * P rows of the operand.  SC: stages where parts of K are joined.
+template <int TN, int STAGES, int P, int SC = STAGES>
 cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale,
                       cudaStream_t st) {
   const int KT = (a.K + 127) / 128;
@@ -417,8 +499,8 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   // as many parts of K as have room on the SMs at once, two k-tiles each at least
   int S = KT / 2 < 8 ? KT / 2 : 8;
-  while (S > 1 && tiles > cluster_room<TN, STAGES, P>(S)) --S;
-  if (S > 1) return launch_tc<TN, STAGES, P, true>(mw, mx, p, dim3((unsigned)tiles, 1, S), st);
+  while (S > 1 && tiles > cluster_room<TN, SC, P>(S)) --S;
+  if (S > 1) return launch_tc<TN, SC, P, true>(mw, mx, p, dim3((unsigned)tiles, 1, S), st);
   return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3((unsigned)tiles), st);
 }
 
@@ -434,27 +516,33 @@ cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st) {
   uint8_t* scale = static_cast<uint8_t*>(a.ws);
   uint8_t* rows8 = scale + (size_t)KT * kMxTile;
   const long long ld8 = KT * 128LL;
-  const dim3 grid((a.T * KT + 7) / 8);
-  if (a.x_bf16) w4_parts_kernel<__nv_bfloat16, kParts16><<<grid, 256, 0, st>>>(a, rows8, ld8, scale);
-  else w4_parts_kernel<float, kParts32><<<grid, 256, 0, st>>>(a, rows8, ld8, scale);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.T * KT + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a.x_bf16 ? s2_launch(&cfg, w4_parts_kernel<__nv_bfloat16, kParts16>, a, rows8, ld8, scale)
+                                 : s2_launch(&cfg, w4_parts_kernel<float, kParts32>, a, rows8, ld8, scale);
   if (e != cudaSuccess) return e;
-  ++g_launch_count;
   W4GemmArgs q = a;
   q.K = (int)ld8;        // the parts' rows are padded with zeros
   if (a.x_bf16)
-    return a.T * P <= 16 ? launch_tn<16, 5, kParts16>(q, rows8, ld8, scale, st)
-                         : launch_tn<32, 5, kParts16>(q, rows8, ld8, scale, st);
-  return a.T * P <= 16 ? launch_tn<16, 5, kParts32>(q, rows8, ld8, scale, st)
-         : a.T * P <= 32 ? launch_tn<32, 5, kParts32>(q, rows8, ld8, scale, st)
-                         : launch_tn<48, 4, kParts32>(q, rows8, ld8, scale, st);
+    return a.T * P <= 16 ? launch_tn<16, 10, kParts16>(q, rows8, ld8, scale, st)
+                         : launch_tn<32, 8, kParts16>(q, rows8, ld8, scale, st);
+  return a.T * P <= 16 ? launch_tn<16, 10, kParts32>(q, rows8, ld8, scale, st)
+         : a.T * P <= 32 ? launch_tn<32, 8, kParts32>(q, rows8, ld8, scale, st)
+                         : launch_tn<48, 8, kParts32>(q, rows8, ld8, scale, st);
 }
 
 cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
-  if (a.T <= 16) return launch_tn<16, 5, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  if (a.T <= 32) return launch_tn<32, 5, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  if (a.T <= 64) return launch_tn<64, 4, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  return launch_tn<128, 6, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 16) return launch_tn<16, 10, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 32) return launch_tn<32, 8, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
 }
 
 }  // namespace s2
