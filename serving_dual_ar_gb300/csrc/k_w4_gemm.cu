@@ -32,15 +32,13 @@ constexpr int w4_groups(int tn) { return (tn + 63) / 64; }
 constexpr int w4_threads(int tn) { return (2 + 4 * w4_groups(tn)) * 32; }
 
 struct W4Params {
-  int N, T, KT, n_tiles, mode, y_bf16;
+  int N, T, KT, n_tiles, tiles, chunk, mode, y_bf16;
   long long ldy;
   const uint8_t* w_scale;
   const uint8_t* x_scale;
   void* y;
   unsigned polls;
 };
-
-S2_DEV float w4_silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // A wait that ends when another one of the CTA gave up.
 S2_DEV bool w4_wait(uint64_t* bar, uint32_t parity, unsigned polls, volatile int* fail) {
@@ -85,26 +83,38 @@ S2_DEV void w4_load(uint32_t dst, const void* src, uint32_t bar) {
                :: "r"(dst), "l"(src), "r"(kMxTile), "r"(bar) : "memory");
 }
 
-constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + 1024; }
+constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + (tn > 128 ? 2048 : 1024); }
 constexpr int w4_tmem_cols(int need) { return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512; }
 
-// Where a warp's outputs go: feature n of consecutive rows.
+// Where a warp's outputs go: feature n (32 of them) of consecutive rows.
 template <int MODE, typename TY>
 struct W4Out {
   TY* at;
   long long ldy;
   bool live;
   S2_DEV W4Out(const W4Params& p, int t, int n)
-      : at(static_cast<TY*>(p.y) + t * p.ldy + (MODE == W4_SWIGLU ? n >> 1 : n)), ldy(p.ldy),
-        live(n < p.N && !(MODE == W4_SWIGLU && (n & 1))) {}
+      : at(static_cast<TY*>(p.y) + t * p.ldy + (MODE == W4_SWIGLU ? n >> 1 : n)), ldy(p.ldy), live(n < p.N) {
+    // gate and up lie in an even lane and the odd one beside it: the odd one
+    // takes the second of two rows
+    if (MODE == W4_SWIGLU && (n & 1)) at += p.ldy;
+  }
   // What row's output is added to; asked for ahead of put, since a load behind
   // a store waits for it.
   S2_DEV float get(int row, bool there) const {
     return MODE == W4_ADD && live && there ? to_f(at[row * ldy]) : 0.f;
   }
-  S2_DEV void put(int row, float v, float before) const {      // every lane of a warp: 32 features
-    if (MODE == W4_SWIGLU) v = w4_silu_mul(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    if (live) at[row * ldy] = from_f<TY>(MODE == W4_ADD ? before + v : v);
+  // Rows row and row + 1, n of them (0, 1 or 2).
+  S2_DEV void put(int row, int n, float v0, float v1, float before0, float before1) const {
+    if (MODE == W4_SWIGLU) {
+      const bool odd = threadIdx.x & 1;
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+      const float g = odd ? got : v0, u = odd ? v1 : got;
+      // exp to 2 units, the quotient to 2 more
+      if (live && n > (odd ? 1 : 0)) at[row * ldy] = from_f<TY>(__fdividef(g, 1.f + expf(-g)) * u);
+    } else {
+      if (live && n > 0) at[row * ldy] = from_f<TY>(MODE == W4_ADD ? before0 + v0 : v0);
+      if (live && n > 1) at[(row + 1) * ldy] = from_f<TY>(MODE == W4_ADD ? before1 + v1 : v1);
+    }
   }
 };
 template <typename F>
@@ -116,6 +126,21 @@ S2_DEV void w4_with_out(const W4Params& p, int t, int n, F f) {
     case 3: f(W4Out<W4_ADD, __nv_bfloat16>(p, t, n)); break;
     case 4: f(W4Out<W4_SWIGLU, float>(p, t, n)); break;
     default: f(W4Out<W4_SWIGLU, __nv_bfloat16>(p, t, n)); break;
+  }
+}
+
+// ``rows`` of a group's rows.
+template <int GB, int N, typename OUT>
+S2_DEV void w4_put_rows(const OUT& out, const float (&v)[N], int rows) {
+  constexpr int Q = 16;      // rows asked for at once
+#pragma unroll
+  for (int b = 0; b < GB; b += Q) {
+    float before[Q];
+#pragma unroll
+    for (int j = 0; j < Q; ++j) before[j] = b + j < GB ? out.get(b + j, b + j < rows) : 0.f;
+#pragma unroll
+    for (int j = 0; j < Q; j += 2)
+      if (b + j < GB) out.put(b + j, rows - b - j, v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j], before[j], before[j + 1]);
   }
 }
 
@@ -341,28 +366,197 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
               v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
             }
             if (!came) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
-            out.put(b, v.x, before[q][0]);
-            if (b + 1 < live) out.put(b + 1, v.y, before[q][1]);
-            if (b + 2 < live) out.put(b + 2, v.z, before[q][2]);
-            if (b + 3 < live) out.put(b + 3, v.w, before[q][3]);
+            out.put(b, live - b, v.x, v.y, before[q][0], before[q][1]);
+            out.put(b + 2, live - b - 2, v.z, v.w, before[q][2], before[q][3]);
           }
         }
       });
     }
   } else if (warp >= 2) {
-    w4_with_out(p, t0 + b0, n, [&](auto out) {
-      constexpr int Q = GB < 16 ? GB : 16;
-#pragma unroll
-      for (int b = 0; b < GB; b += Q) {
-        float before[Q];
-#pragma unroll
-        for (int j = 0; j < Q; ++j) before[j] = out.get(b + j, b + j < GB && b + j < rows);
-#pragma unroll
-        for (int j = 0; j < Q; ++j)
-          if (b + j < GB && b + j < rows) out.put(b + j, acc[b + j < GB ? b + j : 0], before[j]);
-      }
-    });
+    w4_with_out(p, t0 + b0, n, [&](auto out) { w4_put_rows<GB>(out, acc, rows); });
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TM_COLS) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+
+// As w4_tc_kernel for more tiles than SMs: a CTA stays and takes tile after
+// tile; copies and MMAs of the next one run on while this one's sums are written
+// out.  TN = 256: one accumulator, which the next tile may use as soon as it has
+// been read to registers; TN = 128: two that take turns.
+template <int TN, int STAGES>
+__global__ void __launch_bounds__(w4_threads(TN))
+w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                  const W4Params p) {
+  constexpr int STAGE = w4_stage_bytes(TN), B_AT = 128 * 128, SF_AT = B_AT + TN * 128;
+  constexpr int ST = (TN + 127) / 128, SFC = 4 + 4 * ST;       // tiles of row scales, scale columns of a stage
+  constexpr int NB = TN > 192 ? 1 : 2, SF_COLS = NB * TN, TM_COLS = w4_tmem_cols(SF_COLS + STAGES * SFC);
+  constexpr int GN = TN / w4_groups(TN);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_fail;
+  volatile int* fail = &s_fail;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KT = p.KT, chunks = (KT + p.chunk - 1) / p.chunk;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * w4_groups(TN));
+    }
+    mbar_init(&drained, 1);
+    s_fail = 0;
+    fence_mbar_init();
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&tmem_base)), "r"(TM_COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_next();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint64_t mw = reinterpret_cast<uint64_t>(&map_w), mx = reinterpret_cast<uint64_t>(&map_x);
+      const uint32_t sm = smem_u32(smem), full0 = smem_u32(full);
+      const int row_tiles = (p.T + 127) >> 7;
+      int slot = 0, done = 0;
+      uint32_t st = sm, parity = 1;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < p.tiles && ok; tile += gridDim.x) {
+        const int n_tile = tile % p.n_tiles, t0 = tile / p.n_tiles * TN;
+        const uint8_t* ws = p.w_scale + (size_t)n_tile * KT * kMxTile;
+        const uint8_t* xs = p.x_scale + (size_t)(t0 >> 7) * KT * kMxTile;
+        // behind the last rows there is no scale tile; another one's serves
+        const size_t next = (t0 >> 7) + 1 < row_tiles ? (size_t)KT * kMxTile : 0;
+        for (int k = 0; k < KT * 128; k += 128) {
+          if (!(ok = w4_wait(&empty[slot], parity, p.polls, fail))) break;
+          const uint32_t bar = full0 + slot * 8;
+          mbar_arrive_expect_tx(&full[slot], 128 * 64 + TN * 128 + (1 + ST) * kMxTile);
+          w4_load_2d(st, mw, k, n_tile * 128, bar);
+          w4_load_2d(st + B_AT, mx, k, t0, bar);
+          w4_load(st + SF_AT, ws, bar);
+          w4_load(st + SF_AT + kMxTile, xs, bar);
+          if (ST > 1) w4_load(st + SF_AT + 2 * kMxTile, xs + next, bar);
+          ws += kMxTile;
+          xs += kMxTile;
+          st += STAGE;
+          ++done;
+          if (++slot == STAGES) {
+            slot = 0;
+            st = sm;
+            parity ^= 1;
+          }
+        }
+      }
+      // behind a wait that gave up, copies may still be under way
+      mbar_wait(&drained, 0, nullptr);
+      for (int s = *fail ? max(done - STAGES, 0) : done; s < done; ++s)
+        mbar_wait(&full[s % STAGES], (s / STAGES) & 1, nullptr);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t st0 = desc_lo(smem_u32(smem));
+      int slot = 0, buf = 0;
+      uint32_t st = st0, sf = tmem + SF_COLS, parity = 0, acc_parity = 1;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < p.tiles && ok; tile += gridDim.x) {
+        // a tile of 192 rows may begin in the middle of a scale tile, 32 rows a column
+        const uint32_t sfb = 4 + (TN % 128 ? (tile / p.n_tiles * TN & 127) >> 5 : 0);
+        for (int left = KT; left > 0 && ok;) {
+          if (!(ok = w4_wait(&acc_empty[buf], acc_parity, p.polls, fail))) break;
+          const int most = min(left, p.chunk);
+          tc_fence_after();
+          for (int i = 0; i < most; ++i) {
+            if (!(ok = w4_wait(&full[slot], parity, p.polls, fail))) break;
+            tc_fence_after();
+            tmem_cp_scales(sf, st + (SF_AT >> 4));
+#pragma unroll
+            for (int j = 0; j < ST; ++j) tmem_cp_scales(sf + 4 + 4 * j, st + ((SF_AT + (1 + j) * kMxTile) >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              umma_mxf8f6f4(tmem + buf * TN, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf,
+                            sf + sfb, i + j > 0);
+            umma_commit(&empty[slot]);
+            st += STAGE >> 4;
+            sf += SFC;
+            if (++slot == STAGES) {
+              slot = 0;
+              st = st0;
+              sf = tmem + SF_COLS;
+              parity ^= 1;
+            }
+          }
+          if (!ok) break;
+          umma_commit(&acc_full[buf]);
+          left -= most;
+          if (++buf == NB) {
+            buf = 0;
+            acc_parity ^= 1;
+          }
+        }
+      }
+      umma_commit(&drained);
+    }
+  } else {
+    const int group = (warp - 2) / 4, f = (warp & 3) * 32 + lane;
+    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * GN;
+    int buf = 0;
+    uint32_t parity = 0;
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+      float acc[GN];
+      bool ok = true;
+      for (int c = 0; c < chunks; ++c) {
+        if (!(ok = w4_wait(&acc_full[buf], parity, p.polls, fail))) break;
+        tc_fence_after();
+        if (c == 0) {
+          tmem_ld_row<GN>(from + buf * TN, acc);
+        } else if (TN <= 192) {      // one chunk otherwise
+#pragma unroll
+          for (int i = 0; i < GN; i += 32) {
+            float v[32];
+            tmem_ld_row<32>(from + buf * TN + i, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[i + j] += v[j];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (++buf == NB) {
+          buf = 0;
+          parity ^= 1;
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < GN; ++i) acc[i] = __uint_as_float(0x7fffffffu);
+      }
+      const int t0 = tile / p.n_tiles * TN + group * GN;
+      w4_with_out(p, t0, tile % p.n_tiles * 128 + f, [&](auto out) { w4_put_rows<GN>(out, acc, p.T - t0); });
+    }
+  }
+  __syncwarp();
+  mbar_wait(&drained, 0, nullptr);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -475,33 +669,73 @@ int cluster_room(int S) {
   return n;
 }
 
+// Tensor maps and parameters; T * P rows in tiles of TN.
+template <int TN, int P>
+bool w4_fill(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale, CUtensorMap* mw,
+             CUtensorMap* mx, W4Params* p) {
+  p->N = a.N;
+  p->T = a.T;
+  p->KT = (a.K + 127) / 128;
+  p->n_tiles = (a.N + 127) / 128;
+  const long long tiles = (long long)p->n_tiles * (P > 1 ? 1 : (a.T + TN - 1) / TN);
+  p->tiles = (int)tiles;
+  p->chunk = 7;
+  p->mode = a.mode;
+  p->y_bf16 = a.y_bf16;
+  p->ldy = a.ldy;
+  p->w_scale = a.scale;
+  p->x_scale = x_scale;
+  p->y = a.y;
+  p->polls = a.polls;
+  return tiles <= 0x3fffffff && tma_map_w4(mw, a.codes, a.N, p->KT * 128) &&
+         tma_map_u8_2d(mx, rows8, (long long)a.T * P, a.K, ld8, TN);
+}
+
 // rows8: T * P rows of the operand.  SC: stages where parts of K are joined.
 template <int TN, int STAGES, int P, int SC = STAGES>
 cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale,
                       cudaStream_t st) {
-  const int KT = (a.K + 127) / 128;
   CUtensorMap mw, mx;
-  if (!tma_map_w4(&mw, a.codes, a.N, KT * 128)) return cudaErrorInvalidValue;
-  if (!tma_map_u8_2d(&mx, rows8, (long long)a.T * P, a.K, ld8, TN)) return cudaErrorInvalidValue;
   W4Params p;
-  p.N = a.N;
-  p.T = a.T;
-  p.KT = KT;
-  p.mode = a.mode;
-  p.y_bf16 = a.y_bf16;
-  p.ldy = a.ldy;
-  p.w_scale = a.scale;
-  p.x_scale = x_scale;
-  p.y = a.y;
-  p.polls = a.polls;
-  p.n_tiles = (a.N + 127) / 128;
-  const long long tiles = (long long)p.n_tiles * (P > 1 ? 1 : (a.T + TN - 1) / TN);
-  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  if (!w4_fill<TN, P>(a, rows8, ld8, x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
   // as many parts of K as have room on the SMs at once, two k-tiles each at least
-  int S = KT / 2 < 8 ? KT / 2 : 8;
-  while (S > 1 && tiles > cluster_room<TN, SC, P>(S)) --S;
-  if (S > 1) return launch_tc<TN, SC, P, true>(mw, mx, p, dim3((unsigned)tiles, 1, S), st);
-  return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3((unsigned)tiles), st);
+  int S = p.KT / 2 < 8 ? p.KT / 2 : 8;
+  while (S > 1 && p.tiles > cluster_room<TN, SC, P>(S)) --S;
+  if (S > 1) return launch_tc<TN, SC, P, true>(mw, mx, p, dim3(p.tiles, 1, S), st);
+  return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3(p.tiles), st);
+}
+
+int w4_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
+template <int TN, int STAGES>
+cudaError_t launch_rows(const W4GemmArgs& a, cudaStream_t st) {
+  CUtensorMap mw, mx;
+  W4Params p;
+  if (!w4_fill<TN, 1>(a, a.x8, a.ld8, a.x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
+  // an output of bf16 does not see what the tensor core's sums lose, 2^-24 of
+  // them with each of the steps of 32 k
+  if (a.y_bf16) p.chunk = p.KT;
+  else if (TN > 192) return cudaErrorInvalidValue;
+  constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
+  auto k = w4_tc_rows_kernel<TN, STAGES>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(min(p.tiles, w4_sms()));
+  cfg.blockDim = dim3(w4_threads(TN));
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return s2_launch(&cfg, k, mw, mx, p);
 }
 
 }  // namespace
@@ -542,7 +776,23 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   if (a.T <= 16) return launch_tn<16, 10, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 32) return launch_tn<32, 8, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 128) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
+  // Tiles of 128, 192 or 256 rows by what a pass over the SMs would take, in
+  // units of 10 ns: a k-tile 25, 32 or 45 (1,024 rows times 19,456 x 2,560: 44.6,
+  // 42.2 and 38.9 us), a tile's end 60; or tiles of 128 with K in S parts.
+  const int KT = (a.K + 127) / 128, n_tiles = (a.N + 127) / 128, sms = w4_sms();
+  auto cost = [&](int tn, int k_tile) {
+    const long long tiles = (long long)n_tiles * ((a.T + tn - 1) / tn);
+    return (tiles + sms - 1) / sms * (KT * k_tile + 60);
+  };
+  const long long c128 = cost(128, 25), c192 = cost(192, 32), c256 = a.y_bf16 ? cost(256, 45) : 1LL << 60;
+  const long long best = c128 < c192 ? (c128 < c256 ? c128 : c256) : (c192 < c256 ? c192 : c256);
+  const long long tiles = (long long)n_tiles * ((a.T + 127) / 128);
+  int S = KT / 2 < 8 ? KT / 2 : 8;
+  while (S > 1 && tiles > cluster_room<128, 4, 1>(S)) --S;
+  if (S > 1 && (KT + S - 1) / S * 27LL + 250 < best) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
+  if (c256 == best) return launch_rows<256, 4>(a, st);
+  return c192 == best ? launch_rows<192, 5>(a, st) : launch_rows<128, 6>(a, st);
 }
 
 }  // namespace s2
