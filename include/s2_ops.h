@@ -346,7 +346,7 @@ int s2op_kv_remap_pages(int32_t* table, int rows, int cols, int table_ld, const 
  * A row of K values is held in groups of 32 with a power of two 2^e each (the
  * OCP microscaling formats MXFP4 and MXFP8).  e is the smallest of [-126, 120]
  * with largest magnitude <= top * 2^e; the values divided by 2^e are rounded to
- * nearest, ties to even: no finite value saturates.
+ * nearest, ties to even: no finite value but weights beyond 6 * 2^120 saturates.
  *   weights, e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives; top 6): codes
  *   [N][Kp/2] bytes, value 2i in the low and 2i+1 in the high four bits of
  *   byte i, Kp = K rounded up to a multiple of 128, padded with zeros; 32-byte

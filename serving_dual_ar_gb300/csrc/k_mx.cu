@@ -87,58 +87,202 @@ S2_DEV void store_codes8(uint8_t* row, int k0, int K, uint2 c) {
   }
 }
 
+// ---------------------------------------------------------------- two floats an instruction
+
+using F2 = unsigned long long;
+S2_DEV F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+S2_DEV void f2_split(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+S2_DEV F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+S2_DEV F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+S2_DEV F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+S2_DEV F2 f2_neg(F2 a) { return a ^ 0x8000000080000000ull; }
+S2_DEV F2 f2_sub(F2 a, F2 b) { return f2_add(a, f2_neg(b)); }
+
+// Eight values as they lie in memory, 16-byte aligned.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  uint4 a, b;
+  S2_DEV void load(const float* p) {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *reinterpret_cast<const uint4*>(p + 4);
+  }
+  S2_DEV void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  S2_DEV void get(F2 (&v)[4]) const {
+    v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
+    v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
+    v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
+    v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
+  }
+};
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  S2_DEV void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  S2_DEV void zero() { a = make_uint4(0, 0, 0, 0); }
+  S2_DEV void get(F2 (&v)[4]) const {
+    v[0] = f2(bf16lo(a.x), bf16hi(a.x));
+    v[1] = f2(bf16lo(a.y), bf16hi(a.y));
+    v[2] = f2(bf16lo(a.z), bf16hi(a.z));
+    v[3] = f2(bf16lo(a.w), bf16hi(a.w));
+  }
+};
+
+S2_DEV float f2_max8(const F2 (&v)[4]) {   // of the magnitudes; NaN does not count
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_split(v[i], a, b);
+    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  }
+  return m;
+}
+// mx8_exponent of finite magnitudes by its bits: 1.75 is 0x600000 of a mantissa.
+S2_DEV int exponent_of_bits(uint32_t u) { return max((int)((u + 0x1fffffu) >> 23) - 135, kMxEMin); }
+S2_DEV uint2 f2_e4m3(const F2 (&v)[4], float q) {   // v * q to e4m3
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_split(f2_mul(v[i], f2(q, q)), a, b);
+    c[i] = mx_e4m3x2(a, b);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 // ---------------------------------------------------------------- rows to 8 bits
 
-constexpr int kUnits = 4;   // (row, 128 values) of a half-warp, all loaded before the first is rounded
+// Units (row, 128 values) of a half-warp, 16 apart, all loaded before the first
+// is rounded.  One division a thread finds the first: with one in 64 bits for
+// each unit 8,000 x 4,096 bf16 values took 33 us to round, not PACK_US.
+constexpr int kUnits = 4;
+struct Units {
+  long long row;
+  int kt;
+  S2_DEV Units(int KT, int units = kUnits) {
+    const long long u = (long long)blockIdx.x * (16 * units) + (threadIdx.x >> 4);
+    row = u <= 0x7fffffff ? (int)u / KT : u / KT;
+    kt = (int)(u - row * KT);
+  }
+  S2_DEV void next(int KT, int rows, int kts) {      // 16 units: rows x KT + kts
+    row += rows;
+    kt += kts;
+    if (kt >= KT) {
+      kt -= KT;
+      ++row;
+    }
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(256) mx8_pack_kernel(Mx8PackArgs p) {
   pdl_launch_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
-  const long long units = (long long)p.T * KT;
-  const long long u0 = (long long)blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
+  const Units first(KT);
+  Units u = first;
   float v[kUnits][8];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int k0 = (int)(u - row * KT) * 128 + (lane & 15) * 8;
-    if (u < units) {
-      load_row8(static_cast<const T*>(p.x) + row * p.ldx, k0, p.K, p.vec, v[i]);
-    } else {
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts))
+    load_row8(static_cast<const T*>(p.x) + u.row * p.ldx, u.kt * 128 + (lane & 15) * 8, u.row < p.T ? p.K : 0, p.vec,
+              v[i]);
+  u = first;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int kt = (int)(u - row * KT), k0 = kt * 128 + (lane & 15) * 8;
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
     uint32_t byte;
     const uint2 c = round8(v[i], (k0 & ~31) < p.K, byte);
     const uint32_t w = scale_word(byte, lane);
-    if (u >= units) continue;
-    store_codes8(p.y8 + row * p.ld8, k0, p.K, c);
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(row, kt, KT)) = w;
+    if (u.row >= p.T) continue;
+    store_codes8(p.y8 + u.row * p.ld8, k0, p.K, c);
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
+  }
+}
+
+// The same where rows start on 16 bytes and K is a multiple of 8, in registers few
+// enough that an SM has loads under way all the time (8,000 x 4,096 bf16 values
+// 31 -> PACK_US).
+template <typename T> constexpr int kVecUnits = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+__global__ void __launch_bounds__(256, 5) mx8_pack_vec_kernel(Mx8PackArgs p) {
+  constexpr int U = kVecUnits<T>;
+  pdl_launch_next();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
+  const Units first(KT, U);
+  Units u = first;
+  Raw8<T> raw[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
+    if (u.row < p.T && k0 < p.K) raw[i].load(static_cast<const T*>(p.x) + u.row * p.ldx + k0);
+    else raw[i].zero();
+  }
+  u = first;
+#pragma unroll
+  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
+    F2 v[4];
+    raw[i].get(v);
+    const uint32_t m = __float_as_uint(max_of_group(f2_max8(v)));
+    const int e = exponent_of_bits(m);
+    uint2 c = f2_e4m3(v, mx_pow2(-min(e, kMxEMax)));
+    uint32_t byte = (k0 & ~31) < p.K ? (uint32_t)(e + 127) : 127u;
+    if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f2_split(v[j], w[2 * j], w[2 * j + 1]);
+      c = round8(w, (k0 & ~31) < p.K, byte);
+    }
+    const uint32_t w = scale_word(byte, lane);
+    if (u.row >= p.T) continue;
+    if (k0 < p.K) *reinterpret_cast<uint2*>(p.y8 + u.row * p.ld8 + k0) = c;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
   }
 }
 
 // ---------------------------------------------------------------- residual + RMSNorm to 8 bits
 
 // One CTA per row: h = x + r (rounded to x's type and stored), then y = h /
-// sqrt(mean h^2 + eps) * gain to e4m3 with scales.  The result is rounded to
-// 8 bits at once, so it is computed to about 2^-44 (sum of squares, inverse
-// root and products as unevaluated sums of two floats): the codes are those
-// of the exact values whatever the order of the sum.  A thread holds its
-// values in registers between the sum and the rounding (C runs of 8; C = 0:
-// any length, h read back).  A row whose sum of squares leaves fp32's range
-// is taken once more scaled by 2^-80 or 2^64 (2^120).  A row with a NaN or an
-// infinity is NaN throughout.
-template <typename TX, typename TR, int C>
+// sqrt(mean h^2 + eps) * gain to e4m3 with scales.  The codes are those of the
+// exact values, whatever the order of the sum: the sum of squares, its inverse
+// root and the products are unevaluated sums of two floats (about 2^-44).  Rows of
+// any length and alignment; h is read back for the rounding.  A row whose sum of
+// squares leaves fp32's range is taken once more scaled by 2^-80 or 2^64 (2^120).  A row with a
+// NaN or an infinity is NaN throughout.
+// 1 / sqrt(s / K + eps): a Newton step on the float one.  NaN for a row with a
+// NaN or an infinity, or with nothing at all and no eps.
+S2_DEV Two inverse_root(Two s, Two inv_k, float eps) {
+  Two m = two_prod(s.hi, inv_k.hi);
+  m.lo = __fmaf_rn(s.hi, inv_k.lo, __fmaf_rn(s.lo, inv_k.hi, m.lo));
+  m = add(quick_two(m.hi, m.lo), Two{eps, 0.f});
+  if (!(m.hi < __uint_as_float(0x7f800000u) && m.hi > 0.f)) return {__uint_as_float(0x7fffffffu), 0.f};
+  const float r0 = rsqrtf(m.hi);
+  const Two q = two_prod(r0, r0);
+  Two t = mul(m, q.hi);
+  t.lo = __fmaf_rn(m.hi, q.lo, t.lo);
+  const float d = __fsub_rn(__fsub_rn(1.f, t.hi), t.lo);
+  return quick_two(r0, __fmul_rn(__fmul_rn(0.5f, r0), d));
+}
+
+template <typename TX, typename TR>
 __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p) {
-  __shared__ float part[2][32];
+  __shared__ float2 part[32];
   pdl_launch_next();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
@@ -148,13 +292,13 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
   const TR* r = p.r ? static_cast<const TR*>(p.r) + row * p.ldr : nullptr;
   TX* h = static_cast<TX*>(p.h) + row * p.ldh;
   const int runs = KT * 16;               // runs of 8 values, the row's padding included
-  constexpr int CR = C ? C : 1;
-  float v[CR][8];
+  float v[8];
 
   auto sum_up = [](const float (&a)[8], float f, Two& s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const Two q = two_prod(a[i] * f, a[i] * f);
+      const float v = f == 1.f ? a[i] : a[i] * f;
+      const Two q = two_prod(v, v);
       const Two t = two_sum(s.hi, q.hi);
       s = {t.hi, __fadd_rn(s.lo, __fadd_rn(t.lo, q.lo))};
     }
@@ -169,47 +313,43 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
     }
     if (h != x || r) store_row8(h, k0, p.K, p.vec, a);
   };
+  auto join = [](Two a, Two b) {                 // their sum, lo not brought below hi's last bit
+    const Two t = two_sum(a.hi, b.hi);
+    return Two{t.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), t.lo)};
+  };
   auto total = [&](Two s) {                      // over the CTA, the same in every thread
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      s = add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+      s = join(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+    if (nt == 32) return quick_two(s.hi, s.lo);
+    __syncthreads();                             // of the pass before
+    if (lane == 0) part[warp] = make_float2(s.hi, s.lo);
     __syncthreads();
-    if (lane == 0) {
-      part[0][warp] = s.hi;
-      part[1][warp] = s.lo;
-    }
-    __syncthreads();
-    Two t = lane < nt / 32 ? Two{part[0][lane], part[1][lane]} : Two{0.f, 0.f};
+    float2 q = part[0];
+    Two t = {q.x, q.y};
+    if (nt <= 256) {
+      for (int w = 1; w < nt / 32; ++w) {
+        q = part[w];
+        t = join(t, Two{q.x, q.y});
+      }
+    } else {
+      q = lane < nt / 32 ? part[lane] : make_float2(0.f, 0.f);
+      t = {q.x, q.y};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      t = add(t, Two{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
-    return t;
+      for (int o = 16; o > 0; o >>= 1)
+        t = join(t, Two{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+    }
+    return quick_two(t.hi, t.lo);
   };
 
   Two s;
   float f = 1.f, ef;
   for (int pass = 0;; ++pass) {
     s = {0.f, 0.f};
-    if (C) {
-#pragma unroll
-      for (int c = 0; c < CR; ++c) {
-        const int run = tid + c * nt;
-        if (pass == 0) {
-          if (run < runs) {
-            joined(run * 8, v[c]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
-          }
-        }
-        sum_up(v[c], f, s);
-      }
-    } else {
-      for (int run = tid; run < runs; run += nt) {
-        if (pass == 0) joined(run * 8, v[0]);
-        else load_row8(h, run * 8, p.K, p.vec, v[0]);
-        sum_up(v[0], f, s);
-      }
+    for (int run = tid; run < runs; run += nt) {
+      if (pass == 0) joined(run * 8, v);
+      else load_row8(h, run * 8, p.K, p.vec, v);
+      sum_up(v, f, s);
     }
     s = total(s);
     // fp32 holds the squares' sum to the last bits of two floats between about
@@ -220,54 +360,187 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
                                                                                    : 1.8446744073709552e19f;  // 2^64
     else break;
   }
-  // 1 / sqrt(s / K + eps): a Newton step on the float one
-  Two m = two_prod(s.hi, p.inv_k.hi);
-  m.lo = __fmaf_rn(s.hi, p.inv_k.lo, __fmaf_rn(s.lo, p.inv_k.hi, m.lo));
-  m = add(quick_two(m.hi, m.lo), Two{ef, 0.f});
-  Two rs;
-  if (m.hi < __uint_as_float(0x7f800000u) && m.hi > 0.f) {
-    const float r0 = rsqrtf(m.hi);
-    const Two q = two_prod(r0, r0);
-    Two t = mul(m, q.hi);
-    t.lo = __fmaf_rn(m.hi, q.lo, t.lo);
-    const float d = __fsub_rn(__fsub_rn(1.f, t.hi), t.lo);
-    rs = quick_two(r0, __fmul_rn(__fmul_rn(0.5f, r0), d));
-  } else {
-    rs = {__uint_as_float(0x7fffffffu), 0.f};   // a NaN or an infinity in the row, or nothing at all without eps
-  }
-  auto finish = [&](int run, float (&a)[8]) {
-    const int k0 = run * 8, kt = run >> 4;
+  const Two rs = inverse_root(s, p.inv_k, ef);
+  for (int run0 = 0; run0 < runs; run0 += nt) {
+    const int run = run0 + tid, k0 = run * 8;
     float y[8], g[8];
-    load_row8(p.gain, k0, p.K, p.gain_vec, g);
+    load_row8(h, k0, run < runs ? p.K : 0, p.vec, v);
+    load_row8(p.gain, k0, run < runs ? p.K : 0, p.gain_vec, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float af = a[i] * f;
-      Two q = two_prod(af, rs.hi);
-      q.lo = __fmaf_rn(af, rs.lo, q.lo);
-      const Two t = two_prod(q.hi, g[i]);
-      y[i] = round_odd(quick_two(t.hi, __fmaf_rn(q.lo, g[i], t.lo)));
+      const float a = v[i] * f;
+      Two q = two_prod(a, rs.hi);
+      q.lo = __fmaf_rn(a, rs.lo, q.lo);
+      const Two z = two_prod(q.hi, g[i]);
+      y[i] = k0 + i < p.K ? round_odd(quick_two(z.hi, __fmaf_rn(q.lo, g[i], z.lo))) : 0.f;
     }
-    if (k0 + 8 > p.K)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k0 + i >= p.K) y[i] = 0.f;
     uint32_t byte;
     const uint2 c = round8(y, (k0 & ~31) < p.K, byte);
     const uint32_t w = scale_word(byte, lane);
-    if (run < runs) {
-      store_codes8(p.y8 + row * p.ld8, k0, p.K, c);
-      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(row, kt, KT)) = w;
-    }
-  };
-  if (C) {
+    if (run >= runs) continue;
+    store_codes8(p.y8 + row * p.ld8, k0, p.K, c);
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(row, run >> 4, KT)) = w;
+  }
+}
+
+// The same for aligned rows with K a multiple of 8 and up to 2,048 runs, C of them
+// a thread, held in registers, with two floats an instruction.  y is taken in fp32
+// first, and where that is too near the middle of two codes, or a group's largest
+// value too near the end of a scale's reach, with the 44 bits.  Bound by the instructions of the sum
+// of squares and the rounding before (62 a value, 8,000 x 2,560 fp32 rows 51 us),
+// NORM_US now.
+template <typename TX, typename TR, int C>
+__global__ void __launch_bounds__(C == 1 ? 32 : C == 2 ? 256 : 512) add_rmsnorm_mx8_vec_kernel(AddNormMx8Args p) {
+  __shared__ float2 part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int KT = (p.K + 127) / 128;
+  const long long row = blockIdx.x;
+  const TX* x = static_cast<const TX*>(p.x) + row * p.ldx;
+  const TR* r = p.r ? static_cast<const TR*>(p.r) + row * p.ldr : nullptr;
+  TX* h = static_cast<TX*>(p.h) + row * p.ldh;
+  pdl_launch_next();
+  pdl_wait();
+
+  Raw8<TX> xs[C];
+  Raw8<TR> rs8[C];
 #pragma unroll
-    for (int c = 0; c < CR; ++c) finish(tid + c * nt, v[c]);
-  } else {
-    for (int run0 = 0; run0 < runs; run0 += nt) {
-      const int run = run0 + tid;
-      load_row8(h, run * 8, run < runs ? p.K : 0, p.vec, v[0]);
-      finish(run, v[0]);
+  for (int c = 0; c < C; ++c) {
+    const int k0 = (tid + c * nt) * 8;
+    xs[c].zero();
+    rs8[c].zero();
+    if (k0 < p.K) {
+      xs[c].load(x + k0);
+      if (r) rs8[c].load(r + k0);
     }
+  }
+  F2 v[C][4];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k0 = (tid + c * nt) * 8;
+    xs[c].get(v[c]);
+    if (r) {
+      F2 b[4];
+      rs8[c].get(b);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[c][i] = f2_add(v[c][i], b[i]);
+        if (sizeof(TX) == 2) {
+          float lo, hi;
+          f2_split(v[c][i], lo, hi);
+          const __nv_bfloat162 q = __floats2bfloat162_rn(lo, hi);
+          w[i] = *reinterpret_cast<const uint32_t*>(&q);
+          v[c][i] = f2(bf16lo(w[i]), bf16hi(w[i]));
+        }
+      }
+      if (k0 < p.K) {
+        if (sizeof(TX) == 2) {
+          *reinterpret_cast<uint4*>(h + k0) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          reinterpret_cast<ulonglong2*>(h + k0)[0] = make_ulonglong2(v[c][0], v[c][1]);
+          reinterpret_cast<ulonglong2*>(h + k0)[1] = make_ulonglong2(v[c][2], v[c][3]);
+        }
+      }
+    } else if (h != x && k0 < p.K) {
+      *reinterpret_cast<uint4*>(h + k0) = xs[c].a;
+      if (sizeof(TX) == 4) reinterpret_cast<ulonglong2*>(h + k0)[sizeof(TX) == 4] = make_ulonglong2(v[c][2], v[c][3]);
+    }
+  }
+
+  auto join = [](Two a, Two b) {                 // their sum, lo not brought below hi's last bit
+    const Two t = two_sum(a.hi, b.hi);
+    return Two{t.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), t.lo)};
+  };
+  // The sum of (f v)^2 over the CTA, the same in every thread.
+  auto sum_up = [&](float f) {
+    F2 s = 0, lo = 0;
+    const F2 ff = f2(f, f), minus = f2(-1.f, -1.f);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 a = f == 1.f ? v[c][i] : f2_mul(v[c][i], ff);
+        const F2 q = f2_mul(a, a), miss = f2_fma(f2_mul(a, minus), a, q);     // q - a^2, exactly
+        const F2 t = f2_add(s, q), b = f2_sub(t, s);
+        const F2 err = f2_add(f2_sub(s, f2_sub(t, b)), f2_sub(q, b));
+        lo = f2_add(lo, f2_sub(err, miss));
+        s = t;
+      }
+    float s0, s1, l0, l1;
+    f2_split(s, s0, s1);
+    f2_split(lo, l0, l1);
+    Two t = join(Two{s0, l0}, Two{s1, l1});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      t = join(t, Two{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+    if (C > 1) {
+      __syncthreads();                           // of the pass before
+      if (lane == 0) part[warp] = make_float2(t.hi, t.lo);
+      __syncthreads();
+      float2 q = part[0];
+      t = {q.x, q.y};
+      for (int w = 1; w < nt / 32; ++w) {
+        q = part[w];
+        t = join(t, Two{q.x, q.y});
+      }
+    }
+    return quick_two(t.hi, t.lo);
+  };
+  float f = 1.f;
+  Two s = sum_up(1.f);
+  float ef = p.eps;
+  // fp32 holds the squares' sum to the last bits of two floats between about
+  // 2^-79 a value and 2^120 in all
+  if (!(s.hi < 1.329e36f && s.hi * p.inv_k.hi + ef >= 1.654e-24f))
+    for (int pass = 0; pass < 3; ++pass) {
+      if (pass == 0 && !(s.hi < 1.329e36f)) f = 8.2718061255302767e-25f;                         // 2^-80
+      else if (pass < 2 && f >= 1.f && s.hi * p.inv_k.hi + ef < 1.654e-24f) f = pass ? 1.3292279957849159e36f   // 2^120
+                                                                                     : 1.8446744073709552e19f;  // 2^64
+      else break;
+      s = sum_up(f);
+      ef = p.eps * f * f;
+    }
+  const Two rs = inverse_root(s, p.inv_k, ef);
+
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int run = tid + c * nt, k0 = run * 8, kt = run >> 4;
+    Raw8<float> graw;
+    graw.zero();
+    if (k0 < p.K) graw.load(p.gain + k0);
+    F2 g[4], y[4];
+    graw.get(g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = f2_mul(f2_mul(v[c][i], f2(rs.hi, rs.hi)), g[i]);   // off by less than 2^-22
+    const uint32_t m = __float_as_uint(max_of_group(f2_max8(y)));
+    const int e = exponent_of_bits(m);
+    const float q = mx_pow2(-min(e, kMxEMax));
+    uint2 code = f2_e4m3(y, q * (1.f - 4.76837158203125e-7f));                            // 1 -+ 2^-21
+    const uint2 above = f2_e4m3(y, q * (1.f + 4.76837158203125e-7f));
+    // sure where both are the same, the group's largest is 16 steps from the end of a
+    // scale's reach or more, and it is far from fp32's ends: 2^-100 to 2^127
+    const bool sure = f == 1.f && code.x == above.x && code.y == above.y &&
+                      (m == 0u || (((m + 0x20000fu) & 0x7fffffu) >= 0x20u && m - 0x0d800000u < 0x71800000u));
+    uint32_t byte = (k0 & ~31) < p.K ? (uint32_t)(e + 127) : 127u;
+    if (__any_sync(0xffffffffu, !sure)) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a[2], b[2];
+        f2_split(v[c][i / 2], a[0], a[1]);
+        f2_split(g[i / 2], b[0], b[1]);
+        const float af = a[i % 2] * f;
+        Two z = two_prod(af, rs.hi);
+        z.lo = __fmaf_rn(af, rs.lo, z.lo);
+        const Two t = two_prod(z.hi, b[i % 2]);
+        w[i] = k0 < p.K ? round_odd(quick_two(t.hi, __fmaf_rn(z.lo, b[i % 2], t.lo))) : 0.f;
+      }
+      code = round8(w, (k0 & ~31) < p.K, byte);
+    }
+    const uint32_t w = scale_word(byte, lane);
+    if (kt >= KT) continue;
+    if (k0 < p.K) *reinterpret_cast<uint2*>(p.y8 + row * p.ld8 + k0) = code;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(row, kt, KT)) = w;
   }
 }
 
@@ -277,27 +550,18 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
 // NaN or an infinity gets the scale NaN.
 template <typename T>
 __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs p) {
-  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
-  const long long units = (long long)p.N * KT;
-  const long long u0 = (long long)blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
+  const Units first(KT);
+  Units u = first;
   float v[kUnits][8];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int k0 = (int)(u - row * KT) * 128 + (lane & 15) * 8;
-    if (u < units) {
-      load_row8(static_cast<const T*>(p.w) + row * p.ldw, k0, p.K, p.vec, v[i]);
-    } else {
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts))
+    load_row8(static_cast<const T*>(p.w) + u.row * p.ldw, u.kt * 128 + (lane & 15) * 8, u.row < p.N ? p.K : 0, p.vec,
+              v[i]);
+  u = first;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int kt = (int)(u - row * KT), k0 = kt * 128 + (lane & 15) * 8;
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) odd |= !(fabsf(v[i][j]) < __uint_as_float(0x7f800000u));
@@ -310,40 +574,89 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs p) {
     for (int j = 0; j < 4; ++j) c |= mx_e2m1x2(v[i][2 * j] * f, v[i][2 * j + 1] * f) << (8 * j);
     if (nan) c = 0;
     const uint32_t w = scale_word((k0 & ~31) >= p.K ? 127u : nan ? 255u : (uint32_t)(e + 127), lane);
-    if (u >= units) continue;
-    *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (KT * 64) + k0 / 2) = c;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(row, kt, KT)) = w;
+    if (u.row >= p.N) continue;
+    *reinterpret_cast<uint32_t*>(p.codes + (size_t)u.row * (KT * 64) + k0 / 2) = c;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
   }
+}
+
+// Aligned rows with K a multiple of 8, as mx8_pack_vec_kernel.
+template <typename T>
+__global__ void __launch_bounds__(256, 5) w4_pack_vec_kernel(W4PackArgs p) {
+  constexpr int U = kVecUnits<T>;
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
+  const Units first(KT, U);
+  Units u = first;
+  Raw8<T> raw[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
+    if (u.row < p.N && k0 < p.K) raw[i].load(static_cast<const T*>(p.w) + u.row * p.ldw + k0);
+    else raw[i].zero();
+  }
+  u = first;
+#pragma unroll
+  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
+    const int k0 = u.kt * 128 + (lane & 15) * 8;
+    F2 v[4];
+    raw[i].get(v);
+    // by their bits NaN and infinities are above all else
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max((uint32_t)v[j] & 0x7fffffffu, (uint32_t)(v[j] >> 32) & 0x7fffffffu));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool nan = m >= 0x7f800000u;
+    // 1.5 is 0x400000 of a mantissa
+    const int e = min(max((int)((m + 0x3fffffu) >> 23) - 129, kMxEMin), kMxEMax);
+    const float q = mx_pow2(-e);
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      f2_split(f2_mul(v[j], f2(q, q)), a, b);
+      c |= mx_e2m1x2(a, b) << (8 * j);
+    }
+    const uint32_t w = scale_word((k0 & ~31) >= p.K ? 127u : nan ? 255u : (uint32_t)(e + 127), lane);
+    if (u.row >= p.N) continue;
+    *reinterpret_cast<uint32_t*>(p.codes + (size_t)u.row * (KT * 64) + k0 / 2) = nan ? 0u : c;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
+  }
+}
+
+// Two e2m1 codes (a byte's) as floats.
+S2_DEV F2 f2_of_e2m1x2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(byte));
+  float a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(a), "=f"(b) : "r"(h));
+  return f2(a, b);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) w4_unpack_kernel(W4PackArgs p) {
-  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
-  const long long units = (long long)p.N * KT;
-  const long long u0 = (long long)blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
+  const Units first(KT);
+  Units u = first;
   uint32_t c[kUnits], w[kUnits];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int kt = (int)(u - row * KT), k0 = kt * 128 + (lane & 15) * 8;
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts)) {
     c[i] = w[i] = 0;
-    if (u < units) {
-      c[i] = *reinterpret_cast<const uint32_t*>(p.codes + (size_t)row * (KT * 64) + k0 / 2);
-      w[i] = *reinterpret_cast<const uint32_t*>(p.scale + mx_scale_at(row, kt, KT));
+    if (u.row < p.N) {
+      c[i] = *reinterpret_cast<const uint32_t*>(p.codes + (size_t)u.row * (KT * 64) + u.kt * 64 + (lane & 15) * 4);
+      w[i] = *reinterpret_cast<const uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT));
     }
   }
+  u = first;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const long long u = u0 + 16 * i;
-    const long long row = u / KT;
-    const int k0 = (int)(u - row * KT) * 128 + (lane & 15) * 8;
-    if (u >= units) continue;
+  for (int i = 0; i < kUnits; ++i, u.next(KT, rows, kts)) {
+    if (u.row >= p.N) continue;
     const float s = mx_scale((w[i] >> (((lane >> 2) & 3) * 8)) & 255u);
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = mx_e2m1((c[i] >> (4 * j)) & 15u) * s;
-    store_row8(static_cast<T*>(p.w) + row * p.ldw, k0, p.K, p.vec, v);
+    for (int j = 0; j < 4; ++j) f2_split(f2_mul(f2_of_e2m1x2(c[i] >> (8 * j)), f2(s, s)), v[2 * j], v[2 * j + 1]);
+    store_row8(static_cast<T*>(p.w) + u.row * p.ldw, u.kt * 128 + (lane & 15) * 8, p.K, p.vec, v);
   }
 }
 
@@ -364,41 +677,52 @@ cudaError_t launch(const void* k, dim3 grid, int threads, void** args, cudaStrea
   return e;
 }
 
-unsigned unit_blocks(long long rows, int K) {
-  return (unsigned)((rows * ((K + 127) / 128) + 16 * kUnits - 1) / (16 * kUnits));
+unsigned unit_blocks(long long rows, int K, int units = kUnits) {
+  const long long n = (rows * ((K + 127) / 128) + 16 * units - 1) / (16 * units);
+  return n <= 0x7fffffff ? (unsigned)n : 0;      // a grid of 0 is refused
 }
 
 }  // namespace
 
 cudaError_t launch_mx8_pack(const Mx8PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<Mx8PackArgs*>(&p)};
-  const void* k = p.x_bf16 ? (const void*)mx8_pack_kernel<__nv_bfloat16> : (const void*)mx8_pack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.T, p.K)), 256, args, st, true);
+  const bool vec = p.vec && p.K % 8 == 0;
+  const void* k = vec ? (p.x_bf16 ? (const void*)mx8_pack_vec_kernel<__nv_bfloat16> : (const void*)mx8_pack_vec_kernel<float>)
+                      : (p.x_bf16 ? (const void*)mx8_pack_kernel<__nv_bfloat16> : (const void*)mx8_pack_kernel<float>);
+  const int units = !vec ? kUnits : p.x_bf16 ? kVecUnits<__nv_bfloat16> : kVecUnits<float>;
+  return launch(k, dim3(unit_blocks(p.T, p.K, units)), 256, args, st, true);
 }
 
-template <int C>
-static const void* norm_kernel(const AddNormMx8Args& p) {
-  if (p.x_bf16)
-    return p.r_bf16 ? (const void*)add_rmsnorm_mx8_kernel<__nv_bfloat16, __nv_bfloat16, C>
-                    : (const void*)add_rmsnorm_mx8_kernel<__nv_bfloat16, float, C>;
-  return p.r_bf16 ? (const void*)add_rmsnorm_mx8_kernel<float, __nv_bfloat16, C>
-                  : (const void*)add_rmsnorm_mx8_kernel<float, float, C>;
+// Variants by type and, for aligned rows of up to 2,048 runs, runs a thread: one in
+// a single warp; two, which halve what the sum over the CTA costs a value; four,
+// where with two an SM would hold two CTAs only and wait for one's loads under the
+// other's barriers (2,000 x 9,728 fp32 rows 63 -> NORM4_US).
+template <typename TX, typename TR>
+static const void* norm_kernel(int c) {
+  return c == 1   ? (const void*)add_rmsnorm_mx8_vec_kernel<TX, TR, 1>
+         : c == 2 ? (const void*)add_rmsnorm_mx8_vec_kernel<TX, TR, 2>
+         : c == 4 ? (const void*)add_rmsnorm_mx8_vec_kernel<TX, TR, 4>
+                  : (const void*)add_rmsnorm_mx8_kernel<TX, TR>;
 }
 
 cudaError_t launch_add_rmsnorm_mx8(const AddNormMx8Args& p, cudaStream_t st) {
   void* args[] = {const_cast<AddNormMx8Args*>(&p)};
   const int runs = (p.K + 127) / 128 * 16;
-  // threads: a run of 8 each up to 512 of them, then two, then any number
-  const int c = runs <= 512 ? 1 : runs <= 2048 ? 2 : 0;
-  const int nt = c ? ((runs + c - 1) / c + 31) / 32 * 32 : 1024;
-  const void* k = c == 1 ? norm_kernel<1>(p) : c == 2 ? norm_kernel<2>(p) : norm_kernel<0>(p);
+  const int c = !p.vec || !p.gain_vec || p.K % 8 ? 0 : runs <= 32 ? 1 : runs <= 512 ? 2 : runs <= 2048 ? 4 : 0;
+  const int nt = c ? ((runs + c - 1) / c + 31) / 32 * 32 : runs < 1024 ? (runs + 31) / 32 * 32 : 1024;
+  const void* k = p.x_bf16 ? p.r_bf16 ? norm_kernel<__nv_bfloat16, __nv_bfloat16>(c) : norm_kernel<__nv_bfloat16, float>(c)
+                  : p.r_bf16 ? norm_kernel<float, __nv_bfloat16>(c)
+                             : norm_kernel<float, float>(c);
   return launch(k, dim3(p.T), nt, args, st, true);
 }
 
 cudaError_t launch_w4_pack(const W4PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<W4PackArgs*>(&p)};
-  const void* k = p.w_bf16 ? (const void*)w4_pack_kernel<__nv_bfloat16> : (const void*)w4_pack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st, false);
+  const bool vec = p.vec && p.K % 8 == 0;
+  const void* k = vec ? (p.w_bf16 ? (const void*)w4_pack_vec_kernel<__nv_bfloat16> : (const void*)w4_pack_vec_kernel<float>)
+                      : (p.w_bf16 ? (const void*)w4_pack_kernel<__nv_bfloat16> : (const void*)w4_pack_kernel<float>);
+  const int units = !vec ? kUnits : p.w_bf16 ? kVecUnits<__nv_bfloat16> : kVecUnits<float>;
+  return launch(k, dim3(unit_blocks(p.N, p.K, units)), 256, args, st, false);
 }
 
 cudaError_t launch_w4_unpack(const W4PackArgs& p, cudaStream_t st) {

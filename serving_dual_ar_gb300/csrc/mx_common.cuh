@@ -5,8 +5,9 @@
 // goes from memory to the scale columns of tensor memory as it lies.
 //
 // A group's scale is 2^e with the smallest e in [-126, 120] whose top * 2^e
-// covers the group's largest magnitude (top: 448 for e4m3, 6 for e2m1), so no
-// finite value saturates and the division by the scale is exact.
+// covers the group's largest magnitude (top: 448 for e4m3, 6 for e2m1), so the
+// division by the scale is exact and no finite value saturates but weights beyond
+// 6 * 2^120.
 #pragma once
 
 #include "s2_common.cuh"
