@@ -32,7 +32,10 @@ constexpr int w4_groups(int tn) { return (tn + 63) / 64; }
 constexpr int w4_threads(int tn) { return (2 + 4 * w4_groups(tn)) * 32; }
 
 struct W4Params {
-  int N, T, KT, n_tiles, tiles, chunk, mode, y_bf16;
+  int N, T, K, KT, n_tiles, tiles, chunk, mode, y_bf16;
+  const void* x;         // plain rows
+  long long ldx;
+  int x_vec;
   long long ldy;
   const uint8_t* w_scale;
   const uint8_t* x_scale;
@@ -153,19 +156,95 @@ S2_DEV void st_async4(uint32_t at, float x, float y, float z, float w, uint32_t 
       :: "r"(at), "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar), "r"(rank) : "memory");
 }
 
-// P: rows of the operand per row of X (parts of its values, added up).
-template <int TN, int STAGES, int P, bool CL>
-__global__ void __launch_bounds__(w4_threads(TN))
+// ---------------------------------------------------------------- plain rows as 8-bit parts
+
+// A row of fp32 (bf16) values as P = 6 (3) rows of e4m3 values whose scales
+// fall by 2^4 from one to the next: each takes four bits or more of what the
+// ones before it left, exactly.  What remains lies below 2^-10 of the last
+// row's scale, 2^-38 (2^-26) of the group's largest magnitude.
+constexpr int kParts32 = 6, kParts16 = 3;
+// Up to this many rows' parts are made by the CTAs that multiply them.  With 6,144
+// x 2,560 weights 1, 2 and 4 fp32 rows take 5.3, 5.9 and 10.3 us that way, and 5.9,
+// 6.0 and 6.4 us with a kernel ahead that leaves them in memory; bf16 rows 5.4, 5.7
+// and 6.7 against 5.6, 5.7 and 5.8.
+constexpr int kPlainRows = 2;
+
+// Four values of a lane, 128 of a warp, as they lie in memory (vec: on 16 bytes;
+// zeros from K on), and as floats.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+  float4 q;
+  S2_DEV void load(const float* row, int k0, int K, bool vec) {
+    if (vec && k0 + 4 <= K)
+      q = *reinterpret_cast<const float4*>(row + k0);
+    else
+      q = make_float4(k0 < K ? row[k0] : 0.f, k0 + 1 < K ? row[k0 + 1] : 0.f, k0 + 2 < K ? row[k0 + 2] : 0.f,
+                      k0 + 3 < K ? row[k0 + 3] : 0.f);
+  }
+  S2_DEV void get(float (&v)[4]) const { v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w; }
+};
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 q;
+  S2_DEV void load(const __nv_bfloat16* row, int k0, int K, bool vec) {
+    const uint16_t* r = reinterpret_cast<const uint16_t*>(row) + k0;
+    if (vec && k0 + 4 <= K)
+      q = *reinterpret_cast<const uint2*>(r);
+    else
+      q = make_uint2((k0 < K ? r[0] : 0u) | (k0 + 1 < K ? (uint32_t)r[1] << 16 : 0u),
+                     (k0 + 2 < K ? r[2] : 0u) | (k0 + 3 < K ? (uint32_t)r[3] << 16 : 0u));
+  }
+  S2_DEV void get(float (&v)[4]) const {
+    v[0] = bf16lo(q.x), v[1] = bf16hi(q.x), v[2] = bf16lo(q.y), v[3] = bf16hi(q.y);
+  }
+};
+// put(p, codes, scales): part p's four bytes of each lane, and the bytes of its
+// four groups' scales as one word.
+template <int P, typename F>
+S2_DEV void parts_of(float (&v)[4], int lane, F put) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!(fabsf(v[i]) <= 3.402823466e38f)) v[i] = __uint_as_float(0x7fffffffu);
+    m = fmaxf(m, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = mx8_exponent(m);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int ep = max(e - 4 * p, kMxEMin);
+    const float f = mx_pow2(-ep), g = mx_pow2(ep);
+    const uint32_t c = mx_e4m3x2(v[0] * f, v[1] * f) | (mx_e4m3x2(v[2] * f, v[3] * f) << 16);
+    if (p < P - 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? fmaf(-mx_e4m3(c >> (8 * i)), g, v[i]) : 0.f;
+    }
+    uint32_t w = (uint32_t)(ep + 127) << (lane / 8 * 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 16);
+    put(p, c, w);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// P: rows of the operand per row of X (parts of its values, added up).  TX: the
+// type of plain rows whose parts four warps of the CTA make, each every fourth
+// k-tile's; uint8_t: rows of 8 bits in memory.
+template <int TN, int STAGES, int P, bool CL, typename TX>
+__global__ void __launch_bounds__(w4_threads(TN) + (sizeof(TX) > 1 ? 128 : 0))
 w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const W4Params p) {
   constexpr int STAGE = w4_stage_bytes(TN), B_AT = 128 * 128, SF_AT = B_AT + TN * 128;
   constexpr int CH = STAGES >= 8 ? STAGES / 2 : STAGES;   // k-tiles summed in tensor memory
   constexpr int SF_COLS = 2 * TN, TM_COLS = w4_tmem_cols(2 * TN + STAGES * 8);
+  constexpr bool PLAIN = sizeof(TX) > 1;
+  constexpr int OUT_WARPS = 2 + 4 * w4_groups(TN);      // behind them those that make parts
   constexpr int GN = TN / w4_groups(TN); // columns of a group of warps
   constexpr int GB = GN / P;             // rows of X in them
   static_assert(P == 1 || GN == TN, "parts of a row lie in one group");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained, joined;
+  __shared__ __align__(8) uint64_t full[STAGES], made[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drained, joined;
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail;
   volatile int* fail = &s_fail;
@@ -179,6 +258,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
+      if (PLAIN) mbar_init(&made[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -190,7 +270,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     s_fail = 0;
     fence_mbar_init();
     asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+    if (!PLAIN) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -214,13 +294,15 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
       const uint32_t sm = smem_u32(smem);
       int k = kt0 * 128, left = nk;
       auto weights = [&](int i, int ahead) {      // codes count as they lie in memory
-        mbar_arrive_expect_tx(&full[i], 128 * 64 + TN * 128 + 1024);
+        mbar_arrive_expect_tx(&full[i], 128 * 64 + kMxTile + (PLAIN ? 0 : TN * 128 + kMxTile));
         w4_load_2d(sm + i * STAGE, mw, k + ahead * 128, n0, smem_u32(&full[i]));
         w4_load(sm + i * STAGE + SF_AT, ws + ahead * kMxTile, smem_u32(&full[i]));
       };
       auto rows = [&](int i) {
-        w4_load_2d(sm + i * STAGE + B_AT, mx, k, t0, smem_u32(&full[i]));
-        w4_load(sm + i * STAGE + SF_AT + kMxTile, xs, smem_u32(&full[i]));
+        if (!PLAIN) {
+          w4_load_2d(sm + i * STAGE + B_AT, mx, k, t0, smem_u32(&full[i]));
+          w4_load(sm + i * STAGE + SF_AT + kMxTile, xs, smem_u32(&full[i]));
+        }
         ws += kMxTile;
         xs += kMxTile;
         k += 128;
@@ -262,6 +344,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
           const int c = r * (STAGES / CH) + i / CH, buf = c & 1;
           if (i % CH == 0 && c >= 2 && !(ok = w4_wait(&acc_empty[buf], ((c >> 1) + 1) & 1, p.polls, fail))) break;
           if (!(ok = w4_wait(&full[i], r & 1, p.polls, fail))) break;
+          if (PLAIN && !(ok = w4_wait(&made[i], r & 1, p.polls, fail))) break;
           tc_fence_after();
           const uint32_t st = st0 + (i * STAGE >> 4), sf = sf0 + i * 8;
           tmem_cp_scales(sf, st + (SF_AT >> 4));
@@ -275,6 +358,39 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         }
       }
       umma_commit(&drained);
+    }
+  } else if (PLAIN && warp >= OUT_WARPS) {
+    if constexpr (PLAIN) {
+      pdl_wait();
+      constexpr int B = kPlainRows;
+      // every row's values are asked for at once, and a tile ahead
+      Raw4<TX> raw[B];
+      auto load = [&](int s) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          raw[b].load(static_cast<const TX*>(p.x) + min(b, p.T - 1) * p.ldx, (kt0 + s) * 128 + lane * 4, p.K, p.x_vec);
+      };
+      if (warp - OUT_WARPS < nk) load(warp - OUT_WARPS);
+      for (int s = warp - OUT_WARPS; s < nk; s += 4) {
+        const int slot = s % STAGES;
+        float v[B][4];
+#pragma unroll
+        for (int b = 0; b < B; ++b) raw[b].get(v[b]);
+        if (s + 4 < nk) load(s + 4);
+        if (s >= STAGES && !w4_wait(&empty[slot], (s / STAGES + 1) & 1, p.polls, fail)) break;
+        uint8_t* rows8 = smem + slot * STAGE + B_AT;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (b < p.T)
+            parts_of<P>(v[b], lane, [&](int i, uint32_t c, uint32_t w) {
+              const int row = b * P + i;
+              *reinterpret_cast<uint32_t*>(rows8 + sw128_offset(row, lane >> 2) + (lane & 3) * 4) = c;
+              if (lane == 0) *reinterpret_cast<uint32_t*>(rows8 + TN * 128 + kMxTile + mx_scale_at(row, 0, 1)) = w;
+            });
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&made[slot]);
+      }
     }
   } else {
     pdl_wait();     // outputs and what they are added to
@@ -304,9 +420,10 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   __syncthreads();
 
   // this group's rows of X: b0 .. b0 + GB - 1 of the tile
-  const int b0 = warp < 2 ? 0 : (warp - 2) / 4 * GB;
+  const bool writes = warp >= 2 && warp < OUT_WARPS;
+  const int b0 = writes ? (warp - 2) / 4 * GB : 0;
   const int rows = min(GB, p.T - t0 - b0), f = (warp & 3) * 32 + lane, n = n0 + f;
-  if (warp >= 2) {
+  if (writes) {
 #pragma unroll
     for (int b = 0; b < GB; ++b) {       // into the first GB, behind those still to be read
       float v = acc[b * P + P - 1];
@@ -327,7 +444,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     const int quads = (min(TN / P, p.T - t0) + 3) / 4, mine = split < quads ? (quads - split + S - 1) / S : 0;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&joined, mine * S * 2048);
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (warp >= 2) {
+    if (writes) {
       const uint32_t slot = smem_u32(smem + JOIN_AT) + f * 16, bar = smem_u32(&joined);
       int to = b0 / 4 % S, at = b0 / 4 / S * S + split;
 #pragma unroll
@@ -372,7 +489,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         }
       });
     }
-  } else if (warp >= 2) {
+  } else if (writes) {
     w4_with_out(p, t0 + b0, n, [&](auto out) { w4_put_rows<GB>(out, acc, rows); });
   }
   tc_fence_before();
@@ -565,14 +682,7 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   }
 }
 
-// ---------------------------------------------------------------- plain rows as 8-bit parts
-
-// A row of fp32 (bf16) values as P = 6 (3) rows of e4m3 values whose scales
-// fall by 2^4 from one to the next: each takes four bits or more of what the
-// ones before it left, exactly.  What remains lies below 2^-10 of the last
-// row's scale, 2^-38 (2^-26) of the group's largest magnitude.
-constexpr int kParts32 = 6, kParts16 = 3;
-
+// The parts in memory, for rows that the product's own warps would not keep up with.
 template <typename T, int P>
 __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* rows8, long long ld8, uint8_t* scale) {
   pdl_launch_next();
@@ -581,31 +691,15 @@ __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* ro
   const int u = blockIdx.x * 8 + (threadIdx.x >> 5);       // a warp: 128 values of a row, four a lane
   if (u >= a.T * KT) return;
   const int b = u / KT, kt = u % KT, k0 = kt * 128 + lane * 4;
-  const T* x = static_cast<const T*>(a.x) + b * a.ldx;
-  float v[4], m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = k0 + i < a.K ? to_f(x[k0 + i]) : 0.f;
-    if (!(fabsf(v[i]) <= 3.402823466e38f)) v[i] = __uint_as_float(0x7fffffffu);
-    m = fmaxf(m, fabsf(v[i]));
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int e = mx8_exponent(m);
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int ep = max(e - 4 * p, kMxEMin);
-    const float f = mx_pow2(-ep), g = mx_pow2(ep);
-    const uint32_t c = mx_e4m3x2(v[0] * f, v[1] * f) | (mx_e4m3x2(v[2] * f, v[3] * f) << 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? fmaf(-mx_e4m3(c >> (8 * i)), g, v[i]) : 0.f;
+  Raw4<T> raw;
+  raw.load(static_cast<const T*>(a.x) + b * a.ldx, k0, a.K, a.vec);
+  float v[4];
+  raw.get(v);
+  parts_of<P>(v, lane, [&](int p, uint32_t c, uint32_t w) {
     const long long row = (long long)b * P + p;
     *reinterpret_cast<uint32_t*>(rows8 + row * ld8 + k0) = c;
-    uint32_t w = (uint32_t)(ep + 127) << (lane / 8 * 8);
-    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-    w |= __shfl_xor_sync(0xffffffffu, w, 16);
     if (lane == 0) *reinterpret_cast<uint32_t*>(scale + mx_scale_at(row, kt, KT)) = w;
-  }
+  });
 }
 
 // ---------------------------------------------------------------- host side
@@ -617,15 +711,15 @@ constexpr int w4_smem() {
   return STAGES * w4_stage_bytes(TN) + (CL ? ((TN / P + 3) / 4 + 7) * 2048 : 0) + 1024;
 }
 
-template <int TN, int STAGES, int P, bool CL>
+template <int TN, int STAGES, int P, bool CL, typename TX>
 cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Params& p, dim3 grid, cudaStream_t st) {
   constexpr int SMEM = w4_smem<TN, STAGES, P, CL>();
-  auto k = w4_tc_kernel<TN, STAGES, P, CL>;
+  auto k = w4_tc_kernel<TN, STAGES, P, CL, TX>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(w4_threads(TN));
+  cfg.blockDim = dim3(w4_threads(TN) + (sizeof(TX) > 1 ? 128 : 0));
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -641,19 +735,19 @@ cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Para
 }
 
 // Clusters of S CTAs that are on the current device at once (kept per device).
-template <int TN, int STAGES, int P>
+template <int TN, int STAGES, int P, typename TX = uint8_t>
 int cluster_room(int S) {
   static std::atomic<int> kept[16][9];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 16 && kept[dev][S].load()) return kept[dev][S].load() - 1;
   constexpr int SMEM = w4_smem<TN, STAGES, P, true>();
-  auto k = w4_tc_kernel<TN, STAGES, P, true>;
+  auto k = w4_tc_kernel<TN, STAGES, P, true, TX>;
   int n = 0;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, S);
-    cfg.blockDim = dim3(w4_threads(TN));
+    cfg.blockDim = dim3(w4_threads(TN) + (sizeof(TX) > 1 ? 128 : 0));
     cfg.dynamicSmemBytes = SMEM;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -687,22 +781,27 @@ bool w4_fill(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uin
   p->x_scale = x_scale;
   p->y = a.y;
   p->polls = a.polls;
+  p->K = a.K;
+  p->x = a.x;
+  p->ldx = a.ldx;
+  p->x_vec = a.vec;
   return tiles <= 0x3fffffff && tma_map_w4(mw, a.codes, a.N, p->KT * 128) &&
-         tma_map_u8_2d(mx, rows8, (long long)a.T * P, a.K, ld8, TN);
+         (!rows8 || tma_map_u8_2d(mx, rows8, (long long)a.T * P, a.K, ld8, TN));
 }
 
-// rows8: T * P rows of the operand.  SC: stages where parts of K are joined.
-template <int TN, int STAGES, int P, int SC = STAGES>
+// rows8: T * P rows of the operand (null: plain rows of TX).  SC: stages where
+// parts of K are joined.
+template <int TN, int STAGES, int P, int SC = STAGES, typename TX = uint8_t>
 cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale,
                       cudaStream_t st) {
-  CUtensorMap mw, mx;
+  CUtensorMap mw, mx = {};
   W4Params p;
   if (!w4_fill<TN, P>(a, rows8, ld8, x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
   // as many parts of K as have room on the SMs at once, two k-tiles each at least
   int S = p.KT / 2 < 8 ? p.KT / 2 : 8;
-  while (S > 1 && p.tiles > cluster_room<TN, SC, P>(S)) --S;
-  if (S > 1) return launch_tc<TN, SC, P, true>(mw, mx, p, dim3(p.tiles, 1, S), st);
-  return launch_tc<TN, STAGES, P, false>(mw, mx, p, dim3(p.tiles), st);
+  while (S > 1 && p.tiles > cluster_room<TN, SC, P, TX>(S)) --S;
+  if (S > 1) return launch_tc<TN, SC, P, true, TX>(mw, mx, p, dim3(p.tiles, 1, S), st);
+  return launch_tc<TN, STAGES, P, false, TX>(mw, mx, p, dim3(p.tiles), st);
 }
 
 int w4_sms() {
@@ -747,6 +846,9 @@ size_t w4_gemv_ws_bytes(int K, int B) {
 
 cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st) {
   const int KT = (a.K + 127) / 128, P = a.x_bf16 ? kParts16 : kParts32;
+  if (a.T <= kPlainRows)
+    return a.x_bf16 ? launch_tn<16, 10, kParts16, 10, __nv_bfloat16>(a, nullptr, 0, nullptr, st)
+                    : launch_tn<16, 10, kParts32, 10, float>(a, nullptr, 0, nullptr, st);
   uint8_t* scale = static_cast<uint8_t*>(a.ws);
   uint8_t* rows8 = scale + (size_t)KT * kMxTile;
   const long long ld8 = KT * 128LL;

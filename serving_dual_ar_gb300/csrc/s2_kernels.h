@@ -311,7 +311,8 @@ enum W4Mode { W4_STORE = 0, W4_ADD = 1, W4_SWIGLU = 2 };
 struct W4GemmArgs {
   const uint8_t* codes = nullptr; const uint8_t* scale = nullptr;
   int N = 0, K = 0;
-  const void* x = nullptr; int x_bf16 = 0; long long ldx = 0;   // plain rows, or
+  const void* x = nullptr; int x_bf16 = 0; long long ldx = 0;   // plain rows (vec: on 16 bytes), or
+  int vec = 0;
   const uint8_t* x8 = nullptr; long long ld8 = 0;               // e4m3 rows
   const uint8_t* x_scale = nullptr;
   int T = 0;

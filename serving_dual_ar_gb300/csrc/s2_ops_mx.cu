@@ -153,6 +153,7 @@ extern "C" int s2op_w4_gemv(const void* codes, const void* scale, int N, int K, 
   a.x = X;
   a.x_bf16 = x_bf16 ? 1 : 0;
   a.ldx = ldx;
+  a.vec = vec_ok(X, x_bf16, ldx);
   a.ws = workspace;
   return status(launch_w4_gemv(a, static_cast<cudaStream_t>(stream)));
 }
