@@ -763,6 +763,13 @@ int cluster_room(int S) {
   return n;
 }
 
+int w4_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
 // Tensor maps and parameters; T * P rows in tiles of TN.
 template <int TN, int P>
 bool w4_fill(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale, CUtensorMap* mw,
@@ -801,14 +808,13 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   int S = p.KT / 2 < 8 ? p.KT / 2 : 8;
   while (S > 1 && p.tiles > cluster_room<TN, SC, P, TX>(S)) --S;
   if (S > 1) return launch_tc<TN, SC, P, true, TX>(mw, mx, p, dim3(p.tiles, 1, S), st);
+  // More tiles than SMs: half the stages, so that two CTAs share an SM and one's
+  // start and end lie under the other's products (1 row times 20,000 x 2,560 11.2 ->
+  // 7.8 us, times 156,032 x 2,560 50.5 -> 41.2).
+  if constexpr (TN <= 64) {
+    if (p.tiles > w4_sms()) return launch_tc<TN, (STAGES + 1) / 2, P, false, TX>(mw, mx, p, dim3(p.tiles), st);
+  }
   return launch_tc<TN, STAGES, P, false, TX>(mw, mx, p, dim3(p.tiles), st);
-}
-
-int w4_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
 }
 
 template <int TN, int STAGES>
@@ -878,7 +884,7 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   if (a.T <= 16) return launch_tn<16, 10, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 32) return launch_tn<32, 8, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  if (a.T <= 128) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 128 && (a.N + 127) / 128 <= w4_sms()) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
   // Tiles of 128, 192 or 256 rows by what a pass over the SMs would take, in
   // units of 10 ns: a k-tile 25, 32 or 45 (1,024 rows times 19,456 x 2,560: 44.6,
   // 42.2 and 38.9 us), a tile's end 60; or tiles of 128 with K in S parts.
