@@ -555,33 +555,41 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
       const uint64_t mw = reinterpret_cast<uint64_t>(&map_w), mx = reinterpret_cast<uint64_t>(&map_x);
       const uint32_t sm = smem_u32(smem), full0 = smem_u32(full);
       const int row_tiles = (p.T + 127) >> 7;
-      int slot = 0, done = 0;
-      uint32_t st = sm, parity = 1;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < p.tiles && ok; tile += gridDim.x) {
-        const int n_tile = tile % p.n_tiles, t0 = tile / p.n_tiles * TN;
-        const uint8_t* ws = p.w_scale + (size_t)n_tile * KT * kMxTile;
-        const uint8_t* xs = p.x_scale + (size_t)(t0 >> 7) * KT * kMxTile;
-        // behind the last rows there is no scale tile; another one's serves
-        const size_t next = (t0 >> 7) + 1 < row_tiles ? (size_t)KT * kMxTile : 0;
-        for (int k = 0; k < KT * 128; k += 128) {
-          if (!(ok = w4_wait(&empty[slot], parity, p.polls, fail))) break;
-          const uint32_t bar = full0 + slot * 8;
-          mbar_arrive_expect_tx(&full[slot], 128 * 64 + TN * 128 + (1 + ST) * kMxTile);
-          w4_load_2d(st, mw, k, n_tile * 128, bar);
+      int tile = blockIdx.x, left = 0, done = 0, n0 = 0, t0 = 0, k = 0;
+      const uint8_t *ws = nullptr, *xs = nullptr;
+      size_t next = 0;
+      // stages by number, so that their addresses are constants: what one thread
+      // issues for a k-tile has to take less time than the tile's products
+      for (uint32_t parity = 1; tile < p.tiles; parity ^= 1) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) {
+          if (left == 0) {
+            if (tile >= p.tiles) break;
+            n0 = tile % p.n_tiles * 128;
+            t0 = tile / p.n_tiles * TN;
+            ws = p.w_scale + (size_t)(n0 >> 7) * KT * kMxTile;
+            xs = p.x_scale + (size_t)(t0 >> 7) * KT * kMxTile;
+            // behind the last rows there is no scale tile; another one's serves
+            next = (t0 >> 7) + 1 < row_tiles ? (size_t)KT * kMxTile : 0;
+            k = 0;
+            left = KT;
+          }
+          if (!w4_wait(&empty[i], parity, p.polls, fail)) {
+            tile = p.tiles;
+            break;
+          }
+          const uint32_t st = sm + i * STAGE, bar = full0 + i * 8;
+          mbar_arrive_expect_tx(&full[i], 128 * 64 + TN * 128 + (1 + ST) * kMxTile);
+          w4_load_2d(st, mw, k, n0, bar);
           w4_load_2d(st + B_AT, mx, k, t0, bar);
           w4_load(st + SF_AT, ws, bar);
           w4_load(st + SF_AT + kMxTile, xs, bar);
           if (ST > 1) w4_load(st + SF_AT + 2 * kMxTile, xs + next, bar);
           ws += kMxTile;
           xs += kMxTile;
-          st += STAGE;
+          k += 128;
           ++done;
-          if (++slot == STAGES) {
-            slot = 0;
-            st = sm;
-            parity ^= 1;
-          }
+          if (--left == 0) tile += gridDim.x;
         }
       }
       // behind a wait that gave up, copies may still be under way
@@ -591,43 +599,50 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t st0 = desc_lo(smem_u32(smem));
-      int slot = 0, buf = 0;
-      uint32_t st = st0, sf = tmem + SF_COLS, parity = 0, acc_parity = 1;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < p.tiles && ok; tile += gridDim.x) {
-        // a tile of 192 rows may begin in the middle of a scale tile, 32 rows a column
-        const uint32_t sfb = 4 + (TN % 128 ? (tile / p.n_tiles * TN & 127) >> 5 : 0);
-        for (int left = KT; left > 0 && ok;) {
-          if (!(ok = w4_wait(&acc_empty[buf], acc_parity, p.polls, fail))) break;
-          const int most = min(left, p.chunk);
-          tc_fence_after();
-          for (int i = 0; i < most; ++i) {
-            if (!(ok = w4_wait(&full[slot], parity, p.polls, fail))) break;
-            tc_fence_after();
-            tmem_cp_scales(sf, st + (SF_AT >> 4));
+      const uint32_t st0 = desc_lo(smem_u32(smem)), sf0 = tmem + SF_COLS;
+      int tile = blockIdx.x, left = 0, chunk = 0, buf = 0;      // k-tiles of the tile, and of the sum under way
+      uint32_t d = tmem, sfb = 4, acc_parity = 1, accum = 0;
+      for (uint32_t parity = 0; tile < p.tiles; parity ^= 1) {
 #pragma unroll
-            for (int j = 0; j < ST; ++j) tmem_cp_scales(sf + 4 + 4 * j, st + ((SF_AT + (1 + j) * kMxTile) >> 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              umma_mxf8f6f4(tmem + buf * TN, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf,
-                            sf + sfb, i + j > 0);
-            umma_commit(&empty[slot]);
-            st += STAGE >> 4;
-            sf += SFC;
-            if (++slot == STAGES) {
-              slot = 0;
-              st = st0;
-              sf = tmem + SF_COLS;
-              parity ^= 1;
+        for (int i = 0; i < STAGES; ++i) {
+          if (chunk == 0) {
+            if (tile >= p.tiles) break;
+            if (left == 0) {
+              left = KT;
+              // a tile of 192 rows may begin in the middle of a scale tile, 32 rows a column
+              sfb = 4 + (TN % 128 ? (tile / p.n_tiles * TN & 127) >> 5 : 0);
             }
+            if (!w4_wait(&acc_empty[buf], acc_parity, p.polls, fail)) {
+              tile = p.tiles;
+              break;
+            }
+            chunk = min(left, p.chunk);
+            d = tmem + buf * TN;
+            accum = 0;
           }
-          if (!ok) break;
-          umma_commit(&acc_full[buf]);
-          left -= most;
-          if (++buf == NB) {
-            buf = 0;
-            acc_parity ^= 1;
+          if (!w4_wait(&full[i], parity, p.polls, fail)) {
+            tile = p.tiles;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = st0 + (i * STAGE >> 4), sf = sf0 + i * SFC;
+          tmem_cp_scales(sf, st + (SF_AT >> 4));
+#pragma unroll
+          for (int j = 0; j < ST; ++j) tmem_cp_scales(sf + 4 + 4 * j, st + ((SF_AT + (1 + j) * kMxTile) >> 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            umma_mxf8f6f4(d, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf, sf + sfb, accum);
+            accum = 1;
+          }
+          umma_commit(&empty[i]);
+          --left;
+          if (--chunk == 0) {
+            umma_commit(&acc_full[buf]);
+            if (left == 0) tile += gridDim.x;
+            if (++buf == NB) {
+              buf = 0;
+              acc_parity ^= 1;
+            }
           }
         }
       }
