@@ -10,12 +10,20 @@
 // of 32 k, so few rows are bound by memory and many by the tensor cores.
 //
 // Sums: the tensor core cuts what it adds below the last bit of its fp32 sum,
-// which leans towards zero, so seven tiles (896 k) at most are summed there; these partial sums are added up in
-// registers, rounded to nearest (two accumulators take turns).
+// which leans towards zero, so seven tiles (896 k) at most are summed there; these
+// partial sums are added up in registers, rounded to nearest (two accumulators
+// take turns).
+//
+// One thread issues all copies and one all MMAs of a CTA: elected lanes (a branch
+// by lane number moves each operand to a uniform register in a loop over lanes:
+// 1,024 rows times 19,456 x 2,560 took 141 us, 91 with them) and stages by number
+// (77), then CTAs that stay (39).
 //
 // Few rows do not have tiles for every SM: then K is cut into up to eight parts
 // which form a thread-block cluster and add their sums in the order of the
-// parts through distributed shared memory.
+// parts through distributed shared memory.  Clusters that wait for one another
+// must not also wait for tensor memory that the other holds: each CTA of a cluster
+// takes more than half of an SM's shared memory, so no two of them meet on one.
 #include "mx_common.cuh"
 #include "tc_common.cuh"
 #include "tma_map.h"
@@ -53,7 +61,7 @@ S2_DEV bool w4_wait(uint64_t* bar, uint32_t parity, unsigned polls, volatile int
   return false;
 }
 
-// 16 columns of this thread's tensor-memory lane; not there before tmem_wait_ld.
+// 16 columns of this thread's tensor-memory lane, there after the next wait.
 S2_DEV void tmem_issue16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -75,7 +83,7 @@ S2_DEV void tmem_ld_row(uint32_t taddr, float (&v)[N]) {   // N columns, one wai
   }
 }
 
-// A box of a tensor map, and a scale tile, to shared memory.
+// A box of a tensor map, or a scale tile, to shared memory.
 S2_DEV void w4_load_2d(uint32_t dst, uint64_t map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -87,7 +95,15 @@ S2_DEV void w4_load(uint32_t dst, const void* src, uint32_t bar) {
 }
 
 constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + (tn > 128 ? 2048 : 1024); }
-constexpr int w4_tmem_cols(int need) { return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512; }
+constexpr int w4_tmem_cols(int need) {
+  return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
+
+S2_DEV float w4_inverse(float x) {      // to one unit, subnormal results included
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // Where a warp's outputs go: feature n (32 of them) of consecutive rows.
 template <int MODE, typename TY>
@@ -112,8 +128,7 @@ struct W4Out {
       const bool odd = threadIdx.x & 1;
       const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
       const float g = odd ? got : v0, u = odd ? v1 : got;
-      // exp to 2 units, the quotient to 2 more
-      if (live && n > (odd ? 1 : 0)) at[row * ldy] = from_f<TY>(__fdividef(g, 1.f + expf(-g)) * u);
+      if (live && n > (odd ? 1 : 0)) at[row * ldy] = from_f<TY>(g * w4_inverse(1.f + expf(-g)) * u);
     } else {
       if (live && n > 0) at[row * ldy] = from_f<TY>(MODE == W4_ADD ? before0 + v0 : v0);
       if (live && n > 1) at[(row + 1) * ldy] = from_f<TY>(MODE == W4_ADD ? before1 + v1 : v1);
@@ -143,7 +158,8 @@ S2_DEV void w4_put_rows(const OUT& out, const float (&v)[N], int rows) {
     for (int j = 0; j < Q; ++j) before[j] = b + j < GB ? out.get(b + j, b + j < rows) : 0.f;
 #pragma unroll
     for (int j = 0; j < Q; j += 2)
-      if (b + j < GB) out.put(b + j, rows - b - j, v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j], before[j], before[j + 1]);
+      if (b + j < GB)
+        out.put(b + j, rows - b - j, v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j], before[j], before[j + 1]);
   }
 }
 
@@ -160,8 +176,9 @@ S2_DEV void st_async4(uint32_t at, float x, float y, float z, float w, uint32_t 
 
 // A row of fp32 (bf16) values as P = 6 (3) rows of e4m3 values whose scales
 // fall by 2^4 from one to the next: each takes four bits or more of what the
-// ones before it left, exactly.  What remains lies below 2^-10 of the last
-// row's scale, 2^-38 (2^-26) of the group's largest magnitude.
+// ones before it left, exactly.  What remains is 2^-10 of the last row's scale at
+// most, 2^-37 (2^-25) of the group's largest magnitude, and nothing of values
+// within 2^13 (2^17) of that.
 constexpr int kParts32 = 6, kParts16 = 3;
 // Up to this many rows' parts are made by the CTAs that multiply them.  With 6,144
 // x 2,560 weights 1, 2 and 4 fp32 rows take 5.3, 5.9 and 10.3 us that way, and 5.9,
@@ -228,6 +245,10 @@ S2_DEV void parts_of(float (&v)[4], int lane, F put) {
 
 // ---------------------------------------------------------------- few rows
 
+// One tile of 128 weights and TN rows a CTA, or one part of K of it.  A k-tile of
+// the stream is 8.7 KB of weights; ten stages of 16 rows keep 87 KB an SM under way,
+// which 6 TB/s need (1 row times 19,456 x 20,480: 34.9 us, 6.1 TB/s; five stages 41.9).
+// The weights of the first stages are asked for ahead of the kernel before.
 // P: rows of the operand per row of X (parts of its values, added up).  TX: the
 // type of plain rows whose parts four warps of the CTA make, each every fourth
 // k-tile's; uint8_t: rows of 8 bits in memory.
@@ -335,6 +356,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t st0 = desc_lo(smem_u32(smem)), sf0 = tmem + SF_COLS;
+      const uint32_t sfb = 4 + ((t0 & 127) >> 5);      // a tile of 64 rows: the scale tile's first or second half
       int left = nk;
       bool ok = true;
       for (int r = 0; left > 0 && ok; ++r) {
@@ -352,7 +374,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             umma_mxf8f6f4(tmem + buf * TN, st + 2 * j, st + (B_AT >> 4) + 2 * j, idesc_e2m1_e4m3(128, TN, j), sf,
-                          sf + 4, i % CH + j > 0);
+                          sf + sfb, i % CH + j > 0);
           umma_commit(&empty[i]);
           if (--left == 0 || i % CH == CH - 1) umma_commit(&acc_full[buf]);
         }
@@ -505,7 +527,12 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
 // As w4_tc_kernel for more tiles than SMs: a CTA stays and takes tile after
 // tile; copies and MMAs of the next one run on while this one's sums are written
 // out.  TN = 256: one accumulator, which the next tile may use as soon as it has
-// been read to registers; TN = 128: two that take turns.
+// been read to registers; below that two that take turns.  At 1,024 rows times 19,456
+// x 2,560 (38.8 us, 2.6 PFLOP/s) a k-tile of 256 rows takes about 650 clocks, 512 of
+// them MMAs; the first tile of a CTA, whose weights come from memory, 2 us more than
+// the others, the start 3 us and the last tile's output 2 us.  Half of the rows'
+// copies shared by two CTAs changed nothing; two tiles of weights against 128 rows
+// took 40.7 us.
 template <int TN, int STAGES>
 __global__ void __launch_bounds__(w4_threads(TN))
 w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -653,11 +680,11 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * GN;
     int buf = 0;
     uint32_t parity = 0;
+    bool ok = true;      // behind a wait that gave up all further tiles are NaN
     for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
       float acc[GN];
-      bool ok = true;
       for (int c = 0; c < chunks; ++c) {
-        if (!(ok = w4_wait(&acc_full[buf], parity, p.polls, fail))) break;
+        if (!ok || !(ok = w4_wait(&acc_full[buf], parity, p.polls, fail))) break;
         tc_fence_after();
         if (c == 0) {
           tmem_ld_row<GN>(from + buf * TN, acc);
@@ -719,8 +746,8 @@ __global__ void __launch_bounds__(256) w4_parts_kernel(W4GemmArgs a, uint8_t* ro
 
 // ---------------------------------------------------------------- host side
 
-// Stages, in clusters a tile's quads of rows from up to eight parts, and room to start on
-// 1,024 bytes.
+// Stages, in clusters a tile's quads of rows from up to eight parts, and room to
+// start on 1,024 bytes.
 template <int TN, int STAGES, int P, bool CL>
 constexpr int w4_smem() {
   return STAGES * w4_stage_bytes(TN) + (CL ? ((TN / P + 3) / 4 + 7) * 2048 : 0) + 1024;
@@ -812,7 +839,8 @@ bool w4_fill(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uin
 }
 
 // rows8: T * P rows of the operand (null: plain rows of TX).  SC: stages where
-// parts of K are joined.
+// parts of K are joined (32 rows times 2,560 x 9,728 in six parts 6.6 us; through
+// loads from the parts' shared memory, between two cluster barriers, 9.3).
 template <int TN, int STAGES, int P, int SC = STAGES, typename TX = uint8_t>
 cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uint8_t* x_scale,
                       cudaStream_t st) {
@@ -832,15 +860,16 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   return launch_tc<TN, STAGES, P, false, TX>(mw, mx, p, dim3(p.tiles), st);
 }
 
+constexpr int kWholeSum = 128;      // k-tiles
+
 template <int TN, int STAGES>
 cudaError_t launch_rows(const W4GemmArgs& a, cudaStream_t st) {
   CUtensorMap mw, mx;
   W4Params p;
   if (!w4_fill<TN, 1>(a, a.x8, a.ld8, a.x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
   // an output of bf16 does not see what the tensor core's sums lose, 2^-24 of
-  // them with each of the steps of 32 k
-  if (a.y_bf16) p.chunk = p.KT;
-  else if (TN > 192) return cudaErrorInvalidValue;
+  // them on the average with each step of 32 k
+  if (a.y_bf16) p.chunk = min(p.KT, kWholeSum);
   constexpr int SMEM = STAGES * w4_stage_bytes(TN) + 1024;
   auto k = w4_tc_rows_kernel<TN, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -890,25 +919,27 @@ cudaError_t launch_w4_gemv(const W4GemmArgs& a, cudaStream_t st) {
   if (a.x_bf16)
     return a.T * P <= 16 ? launch_tn<16, 10, kParts16>(q, rows8, ld8, scale, st)
                          : launch_tn<32, 8, kParts16>(q, rows8, ld8, scale, st);
-  return a.T * P <= 16 ? launch_tn<16, 10, kParts32>(q, rows8, ld8, scale, st)
-         : a.T * P <= 32 ? launch_tn<32, 8, kParts32>(q, rows8, ld8, scale, st)
-                         : launch_tn<48, 8, kParts32>(q, rows8, ld8, scale, st);
+  return a.T * P <= 32 ? launch_tn<32, 8, kParts32>(q, rows8, ld8, scale, st)
+                       : launch_tn<48, 8, kParts32>(q, rows8, ld8, scale, st);
 }
 
 cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   if (a.T <= 16) return launch_tn<16, 10, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 32) return launch_tn<32, 8, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
-  if (a.T <= 128 && (a.N + 127) / 128 <= w4_sms()) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
+  const int KT = (a.K + 127) / 128, n_tiles = (a.N + 127) / 128, sms = w4_sms();
+  // up to 128 rows in two tiles of 64 where the SMs have room: what K's parts send
+  // one another halves (128 rows times 6,144 x 2,560 10.0 -> 6.6 us, 2,560 x 4,096 7.6 ->
+  // 7.2 us)
+  if (a.T <= 64 || (a.T <= 128 && 2 * n_tiles <= sms)) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 128 && n_tiles <= sms) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
   // Tiles of 128, 192 or 256 rows by what a pass over the SMs would take, in
   // units of 10 ns: a k-tile 25, 32 or 45 (1,024 rows times 19,456 x 2,560: 44.6,
   // 42.2 and 38.9 us), a tile's end 60; or tiles of 128 with K in S parts.
-  const int KT = (a.K + 127) / 128, n_tiles = (a.N + 127) / 128, sms = w4_sms();
   auto cost = [&](int tn, int k_tile) {
     const long long tiles = (long long)n_tiles * ((a.T + tn - 1) / tn);
     return (tiles + sms - 1) / sms * (KT * k_tile + 60);
   };
-  const long long c128 = cost(128, 25), c192 = cost(192, 32), c256 = a.y_bf16 ? cost(256, 45) : 1LL << 60;
+  const long long c128 = cost(128, 25), c192 = cost(192, 32), c256 = a.y_bf16 && KT <= kWholeSum ? cost(256, 45) : 1LL << 60;
   const long long best = c128 < c192 ? (c128 < c256 ? c128 : c256) : (c192 < c256 ? c192 : c256);
   const long long tiles = (long long)n_tiles * ((a.T + 127) / 128);
   int S = KT / 2 < 8 ? KT / 2 : 8;

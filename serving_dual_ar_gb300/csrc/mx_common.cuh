@@ -51,11 +51,6 @@ S2_DEV uint32_t mx_e2m1x2(float x, float y) {
       : "=r"(r) : "f"(y), "f"(x));
   return r;
 }
-// The value of an e2m1 code: sign, two exponent bits, one mantissa bit.  Its
-// bits at those of a float's are the value times 2^-126.
-S2_DEV float mx_e2m1(uint32_t c) {
-  return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 8.5070591730234616e37f;   // 2^126
-}
 S2_DEV float mx_e4m3(uint32_t b) {
   uint32_t r;
   asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(b & 0xffu));

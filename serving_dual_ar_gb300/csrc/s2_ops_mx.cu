@@ -4,6 +4,8 @@
 #include "s2_ops.h"
 #include "s2_kernels.h"
 
+#include <cstdlib>
+
 using namespace s2;
 
 static int status(cudaError_t e) {
@@ -119,6 +121,16 @@ extern "C" int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const vo
   return status(launch_add_rmsnorm_mx8(p, static_cast<cudaStream_t>(stream)));
 }
 
+// S2_FAULT_W4_POLLS=n (read once): waits inside the products give up after n
+// polls, for the tests of what they leave then.
+static unsigned wait_polls() {
+  static const unsigned n = [] {
+    const char* e = std::getenv("S2_FAULT_W4_POLLS");
+    return e ? (unsigned)std::atoi(e) : W4GemmArgs().polls;
+  }();
+  return n;
+}
+
 // What both products have; false if an argument is refused.
 static bool fill_product(W4GemmArgs& a, const void* codes, const void* scale, int N, int K, int T, void* Y, int y_bf16,
                          int ldy, int mode) {
@@ -132,6 +144,7 @@ static bool fill_product(W4GemmArgs& a, const void* codes, const void* scale, in
   a.y_bf16 = y_bf16 ? 1 : 0;
   a.ldy = ldy;
   a.mode = mode;
+  a.polls = wait_polls();
   return true;
 }
 static bool product_shape_ok(int N, int K, int mode) {

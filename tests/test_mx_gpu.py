@@ -453,3 +453,162 @@ def test_graphs_share_a_gemv_workspace_one_after_the_other(s2):
         x = host(X)
         A = np.abs(x) @ np.abs(wv).T
         assert (np.abs(host(Y) - x @ wv.T) <= (sum_bound(K) + 2.0 ** -24) * A).all()
+
+
+# ---------------------------------------------------------------- sizes
+
+def on_gpu(codes, sc, N, K, x, rows):
+    """The products of x (float64) with some rows of the weights, on the GPU in 64 bits; A of each."""
+    rows = torch.as_tensor(rows, device="cuda")
+    nib = torch.stack([codes[rows] & 15, codes[rows] >> 4], -1).view(len(rows), -1)[:, :K].long()
+    g = torch.arange((K + 31) // 32, device="cuda")
+    r = rows[:, None]
+    at = ((r // 128) * ((K + 127) // 128) + g // 4) * 512 + r % 32 * 16 + r // 32 % 4 * 4 + g % 4
+    s = torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), sc.view(-1)[at].int() - 127)
+    w = torch.from_numpy(U.VALUE4).cuda()[nib] * s.repeat_interleave(32, 1)[:, :K]
+    return x @ w.T, x.abs() @ w.abs().T
+
+
+def random_weights(N, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randint(0, 256, (N, U.up(K, 128) // 2), dtype=torch.uint8, device="cuda", generator=g)
+    sc = torch.randint(118, 126, (U.up(N, 128) * U.up(K, 128) // 32,), dtype=torch.uint8, device="cuda", generator=g)
+    return codes, sc
+
+
+def many(s2, T, N, K, ty, mode, seed, rows=None):
+    codes, sc = random_weights(N, K, seed)
+    x = U.rows(np.random.RandomState(seed), T, K)
+    x8, xs = U.pack8(x)
+    xv = torch.from_numpy(U.unpack8(x8, xs, T, K)).cuda()
+    cols = N // 2 if mode == 2 else N
+    Y = torch.full((T, cols), 0.5, dtype=TYPES[ty], device="cuda")
+    s2.s2op_w4_gemm(codes, sc, N, K, dev(x8), x8.shape[1], dev(xs), T, Y, ty == "bf16", cols, mode)
+    rows = np.arange(N) if rows is None else np.asarray(rows)
+    v, A = on_gpu(codes, sc, N, K, xv, rows)
+    if mode == 2:
+        want = torch.nn.functional.silu(v[:, 0::2]) * v[:, 1::2]
+        got = Y.double()[:, torch.as_tensor(rows[0::2] // 2, device="cuda")]
+    else:
+        want = v + 0.5 if mode == 1 else v
+        got = Y.double()[:, torch.as_tensor(rows, device="cuda")]
+    tol = torch.from_numpy(bounds(A.cpu().numpy(), v.cpu().numpy(), 0.5, want.cpu().numpy(), ty, mode, K)).cuda()
+    # bf16 outputs of many rows are summed in the tensor core over up to 16,384 k
+    if ty == "bf16":
+        tol = tol + 34 * 2.0 ** -23 / 32 * (K / 32) * (A if mode != 2 else A[:, 0::2] * A[:, 1::2])
+    off = ((got - want).abs() / tol).max().item()
+    assert off <= 1, off
+
+
+# tiles of 128, 192 and 256 rows by CTAs that stay, ends of tiles and of K inside them, and tiles of 128 in parts of K
+@pytest.mark.parametrize("ty,mode", [("f32", 0), ("bf16", 0), ("f32", 1), ("bf16", 2)])
+@pytest.mark.parametrize("T,N,K", [(1000, 19456, 256), (1024, 19456, 384), (700, 6144, 640), (160, 19500, 300), (250, 20000, 130),
+                                   (385, 10000, 64), (150, 2560, 2560), (130, 25000, 256), (120, 20000, 100), (3000, 700, 1000)])
+def test_gemm_many(s2, T, N, K, ty, mode):
+    many(s2, T, N, K, ty, mode, T + N)
+
+
+@pytest.mark.parametrize("T", [1, 3, 17, 40, 70])
+def test_gemm_more_tiles_than_sms(s2, T):
+    rs = np.random.RandomState(T)
+    for N in (19457, 40000):
+        rows = np.unique(np.concatenate([[0, 1, 127, 128, N - 2, N - 1], rs.randint(0, N, 500)]))
+        many(s2, T, N, 700, "f32", 0, N + T, rows)
+
+
+def test_weights_beyond_32_bits(s2):
+    """Codes of more than 4 GB, and scale tiles and outputs that lie as far: a few rows of them."""
+    N, K = (1 << 21) + 3, 4160
+    rs = np.random.RandomState(0)
+    rows = np.unique(np.concatenate([[0, N - 1, N - 2], rs.randint(0, N, 300)]))
+    many(s2, 2, N, K, "f32", 0, 3, rows)
+    codes, sc = random_weights(N, K, 3)
+    X = dev(U.rows(rs, 1, K), "f32")
+    Y = torch.zeros(1, N, device="cuda")
+    s2.s2op_w4_gemv(codes, sc, N, K, X, False, K, 1, Y, False, N, 0, guarded(s2.s2op_w4_gemv_workspace_bytes(K, 1)))
+    v, A = on_gpu(codes, sc, N, K, X.double(), rows)
+    assert bool(((Y[:, torch.as_tensor(rows, device="cuda")].double() - v).abs() <= sum_bound(K) * A).all())
+
+
+def test_rows_beyond_32_bits(s2):
+    """Rows whose pitch takes the last ones beyond 2^31 elements."""
+    T, K, N, ld = 70000, 96, 40, 32768
+    codes, sc = random_weights(N, K, 5)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    X[:, :K] = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+    y8 = torch.zeros(T, ld, dtype=torch.uint8, device="cuda")
+    ys = guarded(s2.s2op_mx_scale_bytes(T, K))
+    s2.s2op_mx8_pack(X, True, ld, T, K, y8, ld, ys)
+    H = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    z8, zs = torch.zeros(T, 96, dtype=torch.uint8, device="cuda"), guarded(s2.s2op_mx_scale_bytes(T, K))
+    gain = torch.ones(K, device="cuda")
+    s2.s2op_add_rmsnorm_mx8(X, True, ld, X, True, ld, T, K, gain, 1e-6, H, ld, z8, 96, zs)
+    Y = torch.empty(T, ld, device="cuda")
+    s2.s2op_w4_gemm(codes, sc, N, K, y8, ld, ys, T, Y, False, ld, 0)
+    at = torch.tensor([0, 1, 65535, 65536, 69998, 69999], device="cuda")
+    x = host(X[at, :K])
+    v, e = U.round8(x)
+    assert np.array_equal(U.VALUE8[host(y8[at, :K])], v)
+    p, A = on_gpu(codes, sc, N, K, torch.from_numpy(v * 2.0 ** np.repeat(e, 32, 1)).cuda(), np.arange(N))
+    assert bool(((Y[at, :N].double() - p).abs() <= sum_bound(K) * A).all())
+    h = host(dev(2 * x, "bf16"))
+    assert np.array_equal(host(H[at, :K]), h)
+    v, e = U.round8(norm64(h, np.ones(K), float(np.float32(1e-6))))
+    assert np.array_equal(U.VALUE8[host(z8[at])], v)
+
+
+def test_nothing_to_do(s2):
+    none = torch.zeros(0, 64, device="cuda")
+    s2.s2op_mx8_pack(none, False, 64, 0, 64, none, 64, none)
+    s2.s2op_w4_pack(none, False, 0, 64, 64, none, none)
+    s2.s2op_w4_gemm(none, none, 0, 64, none, 64, none, 0, none, False, 0, 0)
+    torch.cuda.synchronize()
+
+
+def test_first_call_may_be_captured():
+    """A process whose first calls are under capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    child = """
+import sys
+sys.path[:0] = ["tests", "."]
+import numpy as np, torch
+import test_mx_gpu as m
+from serving_dual_ar_gb300 import binding as s2
+rs = np.random.RandomState(3)
+layer = m.Layer(s2, rs, 5, 256, 768)
+x, r = m.dev(m.U.rows(rs, 5, 256), "f32"), m.dev(m.U.rows(rs, 5, 256), "bf16")
+torch.cuda.synchronize()
+st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=st):
+    layer.run(x, r, st)
+g.replay()
+torch.cuda.synchronize()
+layer.check(x, r)
+print("CAPTURED_OK")
+"""
+    r = subprocess.run([sys.executable, "-c", child], cwd=root, capture_output=True, text=True, timeout=300)
+    assert "CAPTURED_OK" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+def test_two_streams_at_once(s2):
+    """Products that overlap on the GPU, of kernels that take all of an SM's tensor memory and of ones that do not."""
+    rs = np.random.RandomState(8)
+    jobs = []
+    for T, N, K in ((600, 4096, 1024), (1, 2560, 2560), (100, 2560, 1024), (20, 20000, 512)):
+        codes, sc = random_weights(N, K, T)
+        x8, xs = U.pack8(U.rows(rs, T, K))
+        args = (codes, sc, N, K, dev(x8), K, dev(xs), T)
+        Y, want = torch.zeros(T, N, device="cuda"), torch.zeros(T, N, device="cuda")
+        s2.s2op_w4_gemm(*args, want, False, N, 0)
+        jobs.append((args, Y, want, N, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for args, Y, want, N, st in jobs:
+            s2.s2op_w4_gemm(*args, Y, False, N, 0, st)
+    torch.cuda.synchronize()
+    for args, Y, want, N, st in jobs:
+        assert torch.equal(Y, want)
