@@ -123,6 +123,14 @@ template <> struct Raw8<float> {
     b = *reinterpret_cast<const uint4*>(p + 4);
   }
   S2_DEV void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  // Bits of the largest magnitude of the four lanes' 32 values; infinity's or above
+  // if there is an infinity or a NaN.
+  S2_DEV uint32_t group_max() const {
+    const uint32_t k = 0x7fffffffu;
+    uint32_t m = max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)), max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
   S2_DEV void get(F2 (&v)[4]) const {
     v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
     v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
@@ -134,6 +142,13 @@ template <> struct Raw8<__nv_bfloat16> {
   uint4 a;
   S2_DEV void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
   S2_DEV void zero() { a = make_uint4(0, 0, 0, 0); }
+  S2_DEV uint32_t group_max() const {      // two at a time
+    const uint32_t k = 0x7fff7fffu;
+    uint32_t m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return max(m & 0xffff0000u, m << 16);
+  }
   S2_DEV void get(F2 (&v)[4]) const {
     v[0] = f2(bf16lo(a.x), bf16hi(a.x));
     v[1] = f2(bf16lo(a.y), bf16hi(a.y));
@@ -173,8 +188,8 @@ constexpr int kUnits = 4;
 struct Units {
   long long row;
   int kt;
-  S2_DEV Units(int KT, int units = kUnits) {
-    const long long u = (long long)blockIdx.x * (16 * units) + (threadIdx.x >> 4);
+  S2_DEV Units(int KT) {
+    const long long u = (long long)blockIdx.x * (16 * kUnits) + (threadIdx.x >> 4);
     row = u <= 0x7fffffff ? (int)u / KT : u / KT;
     kt = (int)(u - row * KT);
   }
@@ -213,46 +228,57 @@ __global__ void __launch_bounds__(256) mx8_pack_kernel(Mx8PackArgs p) {
   }
 }
 
-// The same where rows start on 16 bytes and K is a multiple of 8, two floats an
-// instruction and in registers few enough that an SM has loads under way all the
-// time: 8,000 x 4,096 bf16 values in 20.0 us (5.0 TB/s; 31.9 as above), 8,000 x 2,560
-// fp32 values in 17.7 us (5.8 TB/s).
-template <typename T> constexpr int kVecUnits = sizeof(T) == 2 ? 4 : 2;
+// The same where rows start on 16 bytes and K is a multiple of 8: a warp takes 256
+// columns of consecutive rows, whose addresses lie a pitch apart, with two floats
+// an instruction and in registers few enough that an SM has loads under way all the
+// time.  8,000 x 4,096 bf16 values in 17.1 us (5.8 TB/s), 8,000 x 2,560 fp32 values in
+// 16.7 us (6.2 TB/s); the first was 31.9 us as above, bound by its instructions, most of them for
+// addresses.
+template <typename T> constexpr int kVecRows = sizeof(T) == 2 ? 4 : 2;   // a power of two up to 32
+struct Strip {
+  int row0, kt, k0;      // first row, and this lane's column block and first column
+  S2_DEV Strip(int KT, int rows) {
+    const int segs = (KT + 1) / 2, w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    row0 = w / segs * rows;
+    kt = w % segs * 2 + (lane >> 4);
+    k0 = kt * 128 + (lane & 15) * 8;
+  }
+};
 template <typename T>
 __global__ void __launch_bounds__(256, 5) mx8_pack_vec_kernel(Mx8PackArgs p) {
-  constexpr int U = kVecUnits<T>;
+  constexpr int U = kVecRows<T>;
   pdl_launch_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
-  const Units first(KT, U);
-  Units u = first;
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
+  const Strip s(KT, U);
+  const bool in = s.k0 < p.K;
+  const T* x = static_cast<const T*>(p.x) + s.row0 * p.ldx + s.k0;
   Raw8<T> raw[U];
 #pragma unroll
-  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
-    const int k0 = u.kt * 128 + (lane & 15) * 8;
-    if (u.row < p.T && k0 < p.K) raw[i].load(static_cast<const T*>(p.x) + u.row * p.ldx + k0);
+  for (int i = 0; i < U; ++i, x += p.ldx) {
+    if (in && s.row0 + i < p.T) raw[i].load(x);
     else raw[i].zero();
   }
-  u = first;
+  uint8_t* y = p.y8 + s.row0 * p.ld8 + s.k0;
+  uint8_t* scale = p.scale + mx_scale_at(s.row0, s.kt, KT);      // rows that share 32: 16 bytes apart
 #pragma unroll
-  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
-    const int k0 = u.kt * 128 + (lane & 15) * 8;
+  for (int i = 0; i < U; ++i, y += p.ld8, scale += 16) {
     F2 v[4];
     raw[i].get(v);
-    const uint32_t m = __float_as_uint(max_of_group(f2_max8(v)));
+    const uint32_t m = raw[i].group_max();
     const int e = exponent_of_bits(m);
     uint2 c = f2_e4m3(v, mx_pow2(-min(e, kMxEMax)));
-    uint32_t byte = (k0 & ~31) < p.K ? (uint32_t)(e + 127) : 127u;
+    uint32_t byte = (s.k0 & ~31) < p.K ? (uint32_t)(e + 127) : 127u;
     if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {
       float w[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) f2_split(v[j], w[2 * j], w[2 * j + 1]);
-      c = round8(w, (k0 & ~31) < p.K, byte);
+      c = round8(w, (s.k0 & ~31) < p.K, byte);
     }
     const uint32_t w = scale_word(byte, lane);
-    if (u.row >= p.T) continue;
-    if (k0 < p.K) *reinterpret_cast<uint2*>(p.y8 + u.row * p.ld8 + k0) = c;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
+    if (s.row0 + i >= p.T) break;      // the whole warp
+    if (in) *reinterpret_cast<uint2*>(y) = c;
+    if ((lane & 15) == 0 && s.kt < KT) *reinterpret_cast<uint32_t*>(scale) = w;
   }
 }
 
@@ -390,11 +416,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
 // rows with a bf16 residual take 37.6 us (6.0 TB/s); with an instruction for each
 // float it was bound by those, 62 a value, and took 50.9.
 template <typename TX, typename TR, int C>
-__global__ void __launch_bounds__(C == 1 ? 32 : C == 2 ? 256 : 512) add_rmsnorm_mx8_vec_kernel(AddNormMx8Args p) {
+__global__ void __launch_bounds__(C == 1 ? 128 : C == 2 ? 256 : 512) add_rmsnorm_mx8_vec_kernel(AddNormMx8Args p) {
   __shared__ float2 part[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  // C = 1: a row each for four warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = C == 1 ? lane : threadIdx.x, nt = C == 1 ? 32 : blockDim.x;
   const int KT = (p.K + 127) / 128;
-  const long long row = blockIdx.x;
+  const long long row = C == 1 ? blockIdx.x * 4LL + warp : blockIdx.x;
+  if (row >= p.T) return;
   const TX* x = static_cast<const TX*>(p.x) + row * p.ldx;
   const TR* r = p.r ? static_cast<const TR*>(p.r) + row * p.ldr : nullptr;
   TX* h = static_cast<TX*>(p.h) + row * p.ldh;
@@ -460,10 +489,11 @@ __global__ void __launch_bounds__(C == 1 ? 32 : C == 2 ? 256 : 512) add_rmsnorm_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const F2 a = f == 1.f ? v[c][i] : f2_mul(v[c][i], ff);
-        const F2 q = f2_mul(a, a), miss = f2_fma(f2_mul(a, minus), a, q);     // q - a^2, exactly
+        // q - a^2, exactly: nothing where the values have 8 bits
+        const F2 q = f2_mul(a, a), miss = sizeof(TX) == 2 ? 0 : f2_fma(f2_mul(a, minus), a, q);
         const F2 t = f2_add(s, q), b = f2_sub(t, s);
         const F2 err = f2_add(f2_sub(s, f2_sub(t, b)), f2_sub(q, b));
-        lo = f2_add(lo, f2_sub(err, miss));
+        lo = f2_add(lo, sizeof(TX) == 2 ? err : f2_sub(err, miss));
         s = t;
       }
     float s0, s1, l0, l1;
@@ -583,29 +613,24 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs p) {
 // Aligned rows with K a multiple of 8, as mx8_pack_vec_kernel.
 template <typename T>
 __global__ void __launch_bounds__(256, 5) w4_pack_vec_kernel(W4PackArgs p) {
-  constexpr int U = kVecUnits<T>;
-  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128, rows = 16 / KT, kts = 16 % KT;
-  const Units first(KT, U);
-  Units u = first;
+  constexpr int U = kVecRows<T>;
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
+  const Strip s(KT, U);
+  const bool in = s.k0 < p.K;
+  const T* x = static_cast<const T*>(p.w) + s.row0 * p.ldw + s.k0;
   Raw8<T> raw[U];
 #pragma unroll
-  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
-    const int k0 = u.kt * 128 + (lane & 15) * 8;
-    if (u.row < p.N && k0 < p.K) raw[i].load(static_cast<const T*>(p.w) + u.row * p.ldw + k0);
+  for (int i = 0; i < U; ++i, x += p.ldw) {
+    if (in && s.row0 + i < p.N) raw[i].load(x);
     else raw[i].zero();
   }
-  u = first;
+  uint8_t* codes = p.codes + (size_t)s.row0 * (KT * 64) + s.k0 / 2;
+  uint8_t* scale = p.scale + mx_scale_at(s.row0, s.kt, KT);
 #pragma unroll
-  for (int i = 0; i < U; ++i, u.next(KT, rows, kts)) {
-    const int k0 = u.kt * 128 + (lane & 15) * 8;
+  for (int i = 0; i < U; ++i, codes += KT * 64, scale += 16) {
     F2 v[4];
     raw[i].get(v);
-    // by their bits NaN and infinities are above all else
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max((uint32_t)v[j] & 0x7fffffffu, (uint32_t)(v[j] >> 32) & 0x7fffffffu));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t m = raw[i].group_max();
     const bool nan = m >= 0x7f800000u;
     // 1.5 is 0x400000 of a mantissa
     const int e = min(max((int)((m + 0x3fffffu) >> 23) - 129, kMxEMin), kMxEMax);
@@ -617,10 +642,12 @@ __global__ void __launch_bounds__(256, 5) w4_pack_vec_kernel(W4PackArgs p) {
       f2_split(f2_mul(v[j], f2(q, q)), a, b);
       c |= mx_e2m1x2(a, b) << (8 * j);
     }
-    const uint32_t w = scale_word((k0 & ~31) >= p.K ? 127u : nan ? 255u : (uint32_t)(e + 127), lane);
-    if (u.row >= p.N) continue;
-    *reinterpret_cast<uint32_t*>(p.codes + (size_t)u.row * (KT * 64) + k0 / 2) = nan ? 0u : c;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_at(u.row, u.kt, KT)) = w;
+    const uint32_t w = scale_word((s.k0 & ~31) >= p.K ? 127u : nan ? 255u : (uint32_t)(e + 127), lane);
+    if (s.row0 + i >= p.N) break;      // the whole warp
+    if (s.kt < KT) {
+      *reinterpret_cast<uint32_t*>(codes) = nan ? 0u : c;
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scale) = w;
+    }
   }
 }
 
@@ -660,6 +687,36 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(W4PackArgs p) {
   }
 }
 
+// Aligned rows with K a multiple of 8.
+template <typename T>
+__global__ void __launch_bounds__(256) w4_unpack_vec_kernel(W4PackArgs p) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31, KT = (p.K + 127) / 128;
+  const Strip s(KT, U);
+  if (s.k0 >= p.K) return;
+  const uint8_t* codes = p.codes + (size_t)s.row0 * (KT * 64) + s.k0 / 2;
+  const uint8_t* scale = p.scale + mx_scale_at(s.row0, s.kt, KT) + ((lane >> 2) & 3);
+  uint32_t c[U], e[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    c[i] = e[i] = 0;
+    if (s.row0 + i < p.N) {
+      c[i] = *reinterpret_cast<const uint32_t*>(codes + (size_t)i * (KT * 64));
+      e[i] = scale[16 * i];
+    }
+  }
+  T* w = static_cast<T*>(p.w) + s.row0 * p.ldw + s.k0;
+#pragma unroll
+  for (int i = 0; i < U; ++i, w += p.ldw) {
+    if (s.row0 + i >= p.N) break;
+    const float f = mx_scale(e[i]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f2_split(f2_mul(f2_of_e2m1x2(c[i] >> (8 * j)), f2(f, f)), v[2 * j], v[2 * j + 1]);
+    store_row8(w, 0, 8, true, v);
+  }
+}
+
 // early: the CTAs may come to their SMs before the kernel ahead in the stream
 // has ended, and wait there.
 cudaError_t launch(const void* k, dim3 grid, int threads, void** args, cudaStream_t st, bool early) {
@@ -677,20 +734,25 @@ cudaError_t launch(const void* k, dim3 grid, int threads, void** args, cudaStrea
   return e;
 }
 
-unsigned unit_blocks(long long rows, int K, int units = kUnits) {
-  const long long n = (rows * ((K + 127) / 128) + 16 * units - 1) / (16 * units);
+unsigned unit_blocks(long long rows, int K) {
+  const long long n = (rows * ((K + 127) / 128) + 16 * kUnits - 1) / (16 * kUnits);
   return n <= 0x7fffffff ? (unsigned)n : 0;      // a grid of 0 is refused
+}
+// Strips of 256 columns and ``step`` rows, eight a CTA, counted in 31 bits.
+bool strips_fit(long long rows, int K) { return rows * ((K + 255) / 256) < 0x7fff0000LL; }
+unsigned strip_blocks(long long rows, int K, int step) {
+  return (unsigned)(((rows + step - 1) / step * ((K + 255) / 256) + 7) / 8);
 }
 
 }  // namespace
 
 cudaError_t launch_mx8_pack(const Mx8PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<Mx8PackArgs*>(&p)};
-  const bool vec = p.vec && p.K % 8 == 0;
+  const bool vec = p.vec && p.K % 8 == 0 && strips_fit(p.T, p.K);
   const void* k = vec ? (p.x_bf16 ? (const void*)mx8_pack_vec_kernel<__nv_bfloat16> : (const void*)mx8_pack_vec_kernel<float>)
                       : (p.x_bf16 ? (const void*)mx8_pack_kernel<__nv_bfloat16> : (const void*)mx8_pack_kernel<float>);
-  const int units = !vec ? kUnits : p.x_bf16 ? kVecUnits<__nv_bfloat16> : kVecUnits<float>;
-  return launch(k, dim3(unit_blocks(p.T, p.K, units)), 256, args, st, true);
+  const int rows = p.x_bf16 ? kVecRows<__nv_bfloat16> : kVecRows<float>;
+  return launch(k, dim3(vec ? strip_blocks(p.T, p.K, rows) : unit_blocks(p.T, p.K)), 256, args, st, true);
 }
 
 // Variants by type and, for aligned rows of up to 2,048 runs, runs a thread: one in
@@ -709,26 +771,29 @@ cudaError_t launch_add_rmsnorm_mx8(const AddNormMx8Args& p, cudaStream_t st) {
   void* args[] = {const_cast<AddNormMx8Args*>(&p)};
   const int runs = (p.K + 127) / 128 * 16;
   const int c = !p.vec || !p.gain_vec || p.K % 8 ? 0 : runs <= 32 ? 1 : runs <= 512 ? 2 : runs <= 2048 ? 4 : 0;
-  const int nt = c ? ((runs + c - 1) / c + 31) / 32 * 32 : runs < 1024 ? (runs + 31) / 32 * 32 : 1024;
+  const int nt = c == 1 ? 128 : c ? ((runs + c - 1) / c + 31) / 32 * 32 : runs < 1024 ? (runs + 31) / 32 * 32 : 1024;
   const void* k = p.x_bf16 ? p.r_bf16 ? norm_kernel<__nv_bfloat16, __nv_bfloat16>(c) : norm_kernel<__nv_bfloat16, float>(c)
                   : p.r_bf16 ? norm_kernel<float, __nv_bfloat16>(c)
                              : norm_kernel<float, float>(c);
-  return launch(k, dim3(p.T), nt, args, st, true);
+  return launch(k, dim3(c == 1 ? (p.T + 3) / 4 : p.T), nt, args, st, true);
 }
 
 cudaError_t launch_w4_pack(const W4PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<W4PackArgs*>(&p)};
-  const bool vec = p.vec && p.K % 8 == 0;
+  const bool vec = p.vec && p.K % 8 == 0 && strips_fit(p.N, p.K);
   const void* k = vec ? (p.w_bf16 ? (const void*)w4_pack_vec_kernel<__nv_bfloat16> : (const void*)w4_pack_vec_kernel<float>)
                       : (p.w_bf16 ? (const void*)w4_pack_kernel<__nv_bfloat16> : (const void*)w4_pack_kernel<float>);
-  const int units = !vec ? kUnits : p.w_bf16 ? kVecUnits<__nv_bfloat16> : kVecUnits<float>;
-  return launch(k, dim3(unit_blocks(p.N, p.K, units)), 256, args, st, false);
+  const int rows = p.w_bf16 ? kVecRows<__nv_bfloat16> : kVecRows<float>;
+  return launch(k, dim3(vec ? strip_blocks(p.N, p.K, rows) : unit_blocks(p.N, p.K)), 256, args, st, false);
 }
 
 cudaError_t launch_w4_unpack(const W4PackArgs& p, cudaStream_t st) {
   void* args[] = {const_cast<W4PackArgs*>(&p)};
-  const void* k = p.w_bf16 ? (const void*)w4_unpack_kernel<__nv_bfloat16> : (const void*)w4_unpack_kernel<float>;
-  return launch(k, dim3(unit_blocks(p.N, p.K)), 256, args, st, false);
+  const bool vec = p.vec && p.K % 8 == 0 && strips_fit(p.N, p.K);
+  const void* k =
+      vec ? (p.w_bf16 ? (const void*)w4_unpack_vec_kernel<__nv_bfloat16> : (const void*)w4_unpack_vec_kernel<float>)
+          : (p.w_bf16 ? (const void*)w4_unpack_kernel<__nv_bfloat16> : (const void*)w4_unpack_kernel<float>);
+  return launch(k, dim3(vec ? strip_blocks(p.N, p.K, 4) : unit_blocks(p.N, p.K)), 256, args, st, false);
 }
 
 }  // namespace s2
