@@ -122,18 +122,26 @@ struct W4Out {
   S2_DEV float get(int row, bool there) const {
     return MODE == W4_ADD && live && there ? to_f(at[row * ldy]) : 0.f;
   }
-  // Rows row and row + 1, n of them (0, 1 or 2).
+  // SwiGLU of two rows: this lane's one of them.
+  S2_DEV static float silu_mul(float v0, float v1) {
+    const bool odd = threadIdx.x & 1;
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+    const float g = odd ? got : v0, u = odd ? v1 : got;
+    return g * w4_inverse(1.f + expf(-g)) * u;
+  }
+  S2_DEV void put_silu(int row, int n, float v) const {
+    if (live && n > (int)(threadIdx.x & 1)) at[row * ldy] = from_f<TY>(v);
+  }
+  // Rows row and row + 1, n of them (none where n <= 0).
   S2_DEV void put(int row, int n, float v0, float v1, float before0, float before1) const {
     if (MODE == W4_SWIGLU) {
-      const bool odd = threadIdx.x & 1;
-      const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-      const float g = odd ? got : v0, u = odd ? v1 : got;
-      if (live && n > (odd ? 1 : 0)) at[row * ldy] = from_f<TY>(g * w4_inverse(1.f + expf(-g)) * u);
+      put_silu(row, n, silu_mul(v0, v1));
     } else {
       if (live && n > 0) at[row * ldy] = from_f<TY>(MODE == W4_ADD ? before0 + v0 : v0);
       if (live && n > 1) at[(row + 1) * ldy] = from_f<TY>(MODE == W4_ADD ? before1 + v1 : v1);
     }
   }
+  static constexpr bool kSilu = MODE == W4_SWIGLU;
 };
 template <typename F>
 S2_DEV void w4_with_out(const W4Params& p, int t, int n, F f) {
@@ -147,19 +155,31 @@ S2_DEV void w4_with_out(const W4Params& p, int t, int n, F f) {
   }
 }
 
-// ``rows`` of a group's rows.
+// ``rows`` of a group's GB rows, 16 at a time: what they are added to is asked for
+// together, and SwiGLU of all of them comes before the first store, or each would
+// wait for its own (32 rows times 19,456 x 2,560 8.8 -> 8.2 us).
 template <int GB, int N, typename OUT>
 S2_DEV void w4_put_rows(const OUT& out, const float (&v)[N], int rows) {
-  constexpr int Q = 16;      // rows asked for at once
+  constexpr int Q = 16;
 #pragma unroll
   for (int b = 0; b < GB; b += Q) {
-    float before[Q];
+    if constexpr (OUT::kSilu) {
+      float r[Q / 2];
 #pragma unroll
-    for (int j = 0; j < Q; ++j) before[j] = b + j < GB ? out.get(b + j, b + j < rows) : 0.f;
+      for (int j = 0; j < Q; j += 2)
+        if (b + j < GB) r[j / 2] = OUT::silu_mul(v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j]);
 #pragma unroll
-    for (int j = 0; j < Q; j += 2)
-      if (b + j < GB)
-        out.put(b + j, rows - b - j, v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j], before[j], before[j + 1]);
+      for (int j = 0; j < Q; j += 2)
+        if (b + j < GB) out.put_silu(b + j, rows - b - j, r[j / 2]);
+    } else {
+      float before[Q];
+#pragma unroll
+      for (int j = 0; j < Q; ++j) before[j] = b + j < GB ? out.get(b + j, b + j < rows) : 0.f;
+#pragma unroll
+      for (int j = 0; j < Q; j += 2)
+        if (b + j < GB)
+          out.put(b + j, rows - b - j, v[b + j], v[b + j + 1 < GB ? b + j + 1 : b + j], before[j], before[j + 1]);
+    }
   }
 }
 
@@ -805,6 +825,14 @@ int cluster_room(int S) {
   return n;
 }
 
+// As many parts of K as have room on the SMs at once, two k-tiles each at least.
+template <int TN, int STAGES, int P, typename TX = uint8_t>
+int w4_parts(int KT, long long tiles) {
+  int S = KT / 2 < 8 ? KT / 2 : 8;
+  while (S > 1 && tiles > cluster_room<TN, STAGES, P, TX>(S)) --S;
+  return S > 1 ? S : 1;
+}
+
 int w4_sms() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -847,9 +875,7 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   CUtensorMap mw, mx = {};
   W4Params p;
   if (!w4_fill<TN, P>(a, rows8, ld8, x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
-  // as many parts of K as have room on the SMs at once, two k-tiles each at least
-  int S = p.KT / 2 < 8 ? p.KT / 2 : 8;
-  while (S > 1 && p.tiles > cluster_room<TN, SC, P, TX>(S)) --S;
+  const int S = w4_parts<TN, SC, P, TX>(p.KT, p.tiles);
   if (S > 1) return launch_tc<TN, SC, P, true, TX>(mw, mx, p, dim3(p.tiles, 1, S), st);
   // More tiles than SMs: half the stages, so that two CTAs share an SM and one's
   // start and end lie under the other's products (1 row times 20,000 x 2,560 11.2 ->
@@ -927,10 +953,14 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   if (a.T <= 16) return launch_tn<16, 10, 1>(a, a.x8, a.ld8, a.x_scale, st);
   if (a.T <= 32) return launch_tn<32, 8, 1>(a, a.x8, a.ld8, a.x_scale, st);
   const int KT = (a.K + 127) / 128, n_tiles = (a.N + 127) / 128, sms = w4_sms();
-  // up to 128 rows in two tiles of 64 where the SMs have room: what K's parts send
-  // one another halves (128 rows times 6,144 x 2,560 10.0 -> 6.6 us, 2,560 x 4,096 7.6 ->
-  // 7.2 us)
-  if (a.T <= 64 || (a.T <= 128 && 2 * n_tiles <= sms)) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  // up to 128 rows in two tiles of 64 where the SMs have room and K's parts do not
+  // get long: what they send one another halves (128 rows times 6,144 x 2,560 10.0 ->
+  // 6.6 us, 2,560 x 4,096 7.6 -> 7.2 us; 2,560 x 9,728, of 26 k-tiles a part, 8.4 -> 9.1)
+  if (a.T <= 128 && 2 * n_tiles <= sms) {
+    const int S = w4_parts<64, 7, 1>(KT, 2 * n_tiles);
+    if ((KT + S - 1) / S <= 20) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
+  }
   if (a.T <= 128 && n_tiles <= sms) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
   // Tiles of 128, 192 or 256 rows by what a pass over the SMs would take, in
   // units of 10 ns: a k-tile 25, 32 or 45 (1,024 rows times 19,456 x 2,560: 44.6,
@@ -942,8 +972,7 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   const long long c128 = cost(128, 25), c192 = cost(192, 32), c256 = a.y_bf16 && KT <= kWholeSum ? cost(256, 45) : 1LL << 60;
   const long long best = c128 < c192 ? (c128 < c256 ? c128 : c256) : (c192 < c256 ? c192 : c256);
   const long long tiles = (long long)n_tiles * ((a.T + 127) / 128);
-  int S = KT / 2 < 8 ? KT / 2 : 8;
-  while (S > 1 && tiles > cluster_room<128, 4, 1>(S)) --S;
+  const int S = w4_parts<128, 4, 1>(KT, tiles);
   if (S > 1 && (KT + S - 1) / S * 27LL + 250 < best) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
   if (c256 == best) return launch_rows<256, 4>(a, st);
   return c192 == best ? launch_rows<192, 5>(a, st) : launch_rows<128, 6>(a, st);
