@@ -361,8 +361,8 @@ int s2op_kv_remap_pages(int32_t* table, int rows, int cols, int table_ld, const 
  * Sizes: any N, T in [0, 2^24] (none: nothing is done) and K in [1, 2^20].
  * Plain matrices are fp32 or bf16 (*_bf16 = 1) with a row pitch ld* of at least
  * their columns, aligned to their elements (16-byte aligned rows are read and
- * written fastest).  S2_EINVAL for a NULL or misaligned pointer, a pitch or a
- * size out of range. */
+ * written fastest).  Operands of a call do not overlap unless it says so.  S2_EINVAL
+ * for a NULL or misaligned pointer, a pitch or a size out of range. */
 size_t s2op_w4_code_bytes(int N, int K);
 size_t s2op_mx_scale_bytes(int rows, int K);
 
@@ -384,7 +384,7 @@ int s2op_mx8_pack(const void* X, int x_bf16, int ldx, int T, int K, void* y8, in
  * as in s2op_mx8_pack.  y is computed to about 2^-44 before it is rounded, so
  * its codes do not depend on the order of the sum.  gain: fp32 [K]; eps >= 0.
  * H: of x's type; may be X itself (then ldh = ldx) and, without r, NULL; R may
- * be H.  Otherwise the operands do not overlap.  A row with a NaN or an
+ * be H (of the same type and pitch).  A row with a NaN or an
  * infinity in h, or without a square above zero and eps = 0, is NaN in y8. */
 int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int r_bf16, int ldr,
                          int T, int K, const float* gain, float eps, void* H, int ldh, void* y8,

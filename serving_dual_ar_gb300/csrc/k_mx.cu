@@ -9,9 +9,9 @@ namespace s2 {
 namespace {
 
 // Values k0 .. k0 + 7 of a row as floats, zeros from K on.  vec: rows start on
-// 16-byte boundaries.
+// 16-byte boundaries.  (No __restrict__: a row may be one that the kernel wrote.)
 template <typename T>
-S2_DEV void load_row8(const T* __restrict__ row, int k0, int K, bool vec, float (&v)[8]) {
+S2_DEV void load_row8(const T* row, int k0, int K, bool vec, float (&v)[8]) {
   if (vec && k0 + 8 <= K) {
     load8(row + k0, v);
   } else {
@@ -20,7 +20,7 @@ S2_DEV void load_row8(const T* __restrict__ row, int k0, int K, bool vec, float 
   }
 }
 template <typename T>
-S2_DEV void store_row8(T* __restrict__ row, int k0, int K, bool vec, const float (&v)[8]) {
+S2_DEV void store_row8(T* row, int k0, int K, bool vec, const float (&v)[8]) {
   if (vec && k0 + 8 <= K) {
     if (sizeof(T) == 4) {
       float4* p = reinterpret_cast<float4*>(row + k0);

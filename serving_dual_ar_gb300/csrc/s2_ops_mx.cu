@@ -4,6 +4,7 @@
 #include "s2_ops.h"
 #include "s2_kernels.h"
 
+#include <cfloat>
 #include <cstdlib>
 
 using namespace s2;
@@ -92,12 +93,14 @@ extern "C" int s2op_mx8_pack(const void* X, int x_bf16, int ldx, int T, int K, v
 extern "C" int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int r_bf16, int ldr, int T,
                                     int K, const float* gain, float eps, void* H, int ldh, void* y8, int ld8,
                                     void* y_scale, void* stream) {
-  if (!rows_ok(T) || !cols_ok(K) || !(eps >= 0.f)) return S2_EINVAL;
+  if (!rows_ok(T) || !cols_ok(K) || !(eps >= 0.f && eps <= FLT_MAX)) return S2_EINVAL;
   if (T == 0) return S2_OK;
   if (!plain_ok(X, x_bf16, ldx, K) || !gain || !aligned(gain, 4) || !rows8_ok(y8, ld8, K, y_scale)) return S2_EINVAL;
   if (R ? !plain_ok(R, r_bf16, ldr, K) || !H : false) return S2_EINVAL;
   if (H && !plain_ok(H, x_bf16, ldh, K)) return S2_EINVAL;
-  if (H == X && ldh != ldx) return S2_EINVAL;   // in place: each row onto itself
+  // in place: each row onto itself
+  if (H == X && ldh != ldx) return S2_EINVAL;
+  if (H && H == R && (ldh != ldr || (x_bf16 != 0) != (r_bf16 != 0))) return S2_EINVAL;
   AddNormMx8Args p;
   p.x = X;
   p.x_bf16 = x_bf16 ? 1 : 0;

@@ -111,3 +111,8 @@ def test_refusals_products(lib):
         assert lib.LIB.s2op_w4_gemm(None, None, n, 64, None, 64, None, t, None, 0, 8, 0, None) == lib.S2_OK
     with pytest.raises(lib.S2Error):
         lib.s2op_w4_gemm(None, None, 8, 64, None, 64, None, 2, None, False, 8, 0)
+
+
+def test_refusals_in_place(lib):
+    good = [A, 0, 64, 2 * A, 0, 64, 4, 64, A, 1e-6, 2 * A, 64, A, 64, A, None]      # the residual's rows overwritten
+    refused(lib, "s2op_add_rmsnorm_mx8", good, [(4, 1), (5, 68), (11, 68), (9, float("inf"))])

@@ -612,3 +612,62 @@ def test_two_streams_at_once(s2):
     torch.cuda.synchronize()
     for args, Y, want, N, st in jobs:
         assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [96, 99, 256])
+def test_w4_pack_nan_in_any_place(s2, K, kind):
+    """A NaN or an infinity makes its group NaN and no other, aligned rows or not."""
+    rs = np.random.RandomState(K)
+    w = rs.standard_normal((40, K))
+    at = rs.randint(0, K, 40)
+    w[np.arange(40), at] = rs.choice([np.nan, np.inf, -np.inf], 40)
+    t = dev(w, kind)
+    codes, sc = guarded(s2.s2op_w4_code_bytes(40, K)), guarded(s2.s2op_mx_scale_bytes(40, K))
+    out = torch.zeros(40, K, device="cuda")
+    s2.s2op_w4_pack(t, kind == "bf16", 40, K, K, codes, sc)
+    s2.s2op_w4_unpack(codes, sc, 40, K, out, False, K)
+    v, e, bad = U.round4(host(t))
+    assert bad.sum() == 40
+    assert same(host(out), np.where(np.repeat(bad, 32, 1)[:, :K], np.nan, v * 2.0 ** np.repeat(e, 32, 1)[:, :K]))
+
+
+@pytest.mark.parametrize("tx,tr", [("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("T,K", [(4000, 2560), (3000, 256), (1000, 9728)])
+def test_add_rmsnorm_of_many_rows(s2, T, K, tx, tr):
+    """Codes and scales of millions of values, next to ties among them, are those of 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, K, device="cuda", generator=g).to(TYPES[tx])
+    r = (0.3 * torch.randn(T, K, device="cuda", generator=g)).to(TYPES[tr])
+    gain = torch.rand(K, device="cuda", generator=g) + 0.5
+    h, y8 = torch.empty_like(x), torch.zeros(T, K, dtype=torch.uint8, device="cuda")
+    ys = guarded(s2.s2op_mx_scale_bytes(T, K))
+    s2.s2op_add_rmsnorm_mx8(x, tx == "bf16", K, r, tr == "bf16", K, T, K, gain, 2.0 ** -20, h, K, y8, K, ys)
+    want = (x.float() + r.float()).to(TYPES[tx])
+    assert torch.equal(h, want)
+    v = want.double()
+    v = v / torch.sqrt(v.square().mean(-1, keepdim=True) + 2.0 ** -20) * gain.double()
+    power = torch.tensor([448 * 2.0 ** e for e in range(U.EMIN, U.EMAX + 1)], dtype=torch.float64, device="cuda")
+    e = torch.searchsorted(power, v.abs().view(T, -1, 32).amax(-1)) + U.EMIN
+    grid = torch.from_numpy(U.E4M3).cuda()
+    z = v / (power / 448)[(e - U.EMIN).repeat_interleave(32, 1)]
+    hi = torch.searchsorted(grid, z.abs()).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    down, up = z.abs() - grid[lo], grid[hi] - z.abs()
+    code = torch.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    assert torch.equal((y8 & 127).long(), code)
+    assert bool(((y8 >= 128) == torch.signbit(z)).all())
+    assert np.array_equal(host(ys), U.tiles((e + 127).byte().cpu().numpy(), K, 0xAB))
+
+
+def test_add_rmsnorm_onto_the_residual(s2):
+    rs = np.random.RandomState(12)
+    for K in (768, 99, 20000):
+        x, r = dev(U.rows(rs, 5, K), "f32"), dev(U.rows(rs, 5, K), "f32")
+        gain = torch.ones(K, device="cuda")
+        y8, ys = torch.zeros(2, 5, U.up(K, 16), dtype=torch.uint8, device="cuda"), guarded(2 * s2.s2op_mx_scale_bytes(5, K))
+        h = torch.empty_like(x)
+        s2.s2op_add_rmsnorm_mx8(x, False, K, r, False, K, 5, K, gain, 1e-6, h, K, y8[0], U.up(K, 16), ys)
+        s2.s2op_add_rmsnorm_mx8(x, False, K, r, False, K, 5, K, gain, 1e-6, r, K, y8[1], U.up(K, 16),
+                                ys[s2.s2op_mx_scale_bytes(5, K):])
+        assert torch.equal(h, r) and torch.equal(y8[0], y8[1])
