@@ -381,8 +381,9 @@ int s2op_mx8_pack(const void* X, int x_bf16, int ldx, int T, int K, void* y8, in
 
 /* h = x + r (r NULL: x), rounded to x's type and stored to H, then
  *   y = h / sqrt(mean_k h^2 + eps) * gain,  to 8 bits with scales
- * as in s2op_mx8_pack.  y is computed to about 2^-44 before it is rounded, so
- * its codes do not depend on the order of the sum.  gain: fp32 [K]; eps >= 0.
+ * as in s2op_mx8_pack.  y is computed to about 2^-44 of itself and 2^-120 of the
+ * gain before it is rounded, so its codes do not depend on the order of the sum.
+ * gain: fp32 [K]; eps >= 0 and finite.
  * H: of x's type; may be X itself (then ldh = ldx) and, without r, NULL; R may
  * be H (of the same type and pitch).  A row with a NaN or an
  * infinity in h, or without a square above zero and eps = 0, is NaN in y8. */

@@ -322,7 +322,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  // behind the allocation: CTAs of the next kernel may now take what is left
+  // Behind the allocation: CTAs of the next kernel may now take what is left.  Of the
+  // kernel ahead, CTAs may still have to allocate; where one fits an SM's shared memory
+  // together with this kernel's, the two ask for 288 of the 512 columns at most.
   pdl_launch_next();
   if (CL) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 

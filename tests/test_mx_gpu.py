@@ -671,3 +671,41 @@ def test_add_rmsnorm_onto_the_residual(s2):
         s2.s2op_add_rmsnorm_mx8(x, False, K, r, False, K, 5, K, gain, 1e-6, r, K, y8[1], U.up(K, 16),
                                 ys[s2.s2op_mx_scale_bytes(5, K):])
         assert torch.equal(h, r) and torch.equal(y8[0], y8[1])
+
+
+@pytest.mark.parametrize("T", [20, 40])
+def test_between_bf16_products(s2, T):
+    """Calls that follow one another without a pause, 4-bit products that start under bf16 ones and hold tensor memory on
+    the same SMs among them, give what each gives alone."""
+    K, N, M = 512, 20000, 512
+    rs = np.random.RandomState(T)
+    a = dev(rs.standard_normal((M, K)) * K ** -0.5, "bf16")
+    b = dev(rs.standard_normal((T, K)), "bf16")
+    wv, codes, sc = weights(rs, N, M)
+    gain = torch.ones(M, device="cuda")
+    h = torch.zeros(T, M, device="cuda")
+    y8, ys = guarded(T * M).view(T, M), guarded(s2.s2op_mx_scale_bytes(T, M))
+    Y, Z = torch.zeros(T, N, device="cuda"), torch.zeros(2, N, device="cuda")
+    ws = guarded(s2.s2op_w4_gemv_workspace_bytes(M, 2))
+
+    def run(after=lambda: None):
+        for _ in range(3):
+            s2.s2op_tc_gemm(a, M, K, b, T, K, h, M, split_k=1)
+            after()
+        s2.s2op_w4_gemv(codes, sc, N, M, h, False, M, 2, Z, False, N, 0, ws)
+        after()
+        s2.s2op_tc_gemm(a, M, K, b, T, K, h, M, epi=1, split_k=1)
+        after()
+        s2.s2op_add_rmsnorm_mx8(h, False, M, None, False, 0, T, M, gain, 1e-6, None, 0, y8, M, ys)
+        after()
+        s2.s2op_w4_gemm(codes, sc, N, M, y8, M, ys, T, Y, False, N, 0)
+        after()
+        return h.clone(), y8.clone(), Y.clone(), Z.clone()
+
+    alone = run(torch.cuda.synchronize)
+    v = host(alone[0])[:2] / 2
+    want = v @ wv.T
+    assert (np.abs(host(alone[3]) - want) <= bounds(np.abs(v) @ np.abs(wv).T, want, 0, want, "f32", 0, M)).all()
+    for _ in range(20):
+        for got, want in zip(run(), alone):
+            assert torch.equal(got, want)
