@@ -376,6 +376,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
         mbar_wait(&full[s % STAGES], (s / STAGES) & 1, nullptr);
     }
   } else if (warp == 1) {
+    pdl_wait();     // polls count from here on, however long the kernel ahead takes
     if (elect_one()) {
       const uint32_t st0 = desc_lo(smem_u32(smem)), sf0 = tmem + SF_COLS;
       const uint32_t sfb = 4 + ((t0 & 127) >> 5);      // a tile of 64 rows: the scale tile's first or second half

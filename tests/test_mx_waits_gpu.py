@@ -67,3 +67,53 @@ def test_outputs_behind_a_wait_that_ran_out_are_nan(polls):
     r = subprocess.run([sys.executable, "-c", CHILD, str(polls)], cwd=root, capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, S2_FAULT_W4_POLLS=str(polls)))
     assert "POLLS_OK" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+LONG = """
+import sys
+import numpy as np, torch
+sys.path[:0] = ["tests", "."]
+import mx_util as U
+from test_mx_gpu import weights, dev, guarded
+from serving_dual_ar_gb300 import binding as b
+
+# a bf16 product of 100 tiles and about 0.3 ms, beside which the calls after it start on the SMs that are left
+M, D = 12800, 65536
+a, x = torch.zeros(M, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(20, D, dtype=torch.bfloat16, device="cuda")
+h = torch.zeros(20, M, device="cuda")
+for kind, T, N, K in ((None, 16, 640, 2560), (None, 100, 256, 300), (None, 700, 256, 300), ("f32", 1, 640, 2560),
+                      ("bf16", 6, 640, 2560)):
+    rs = np.random.RandomState(T)
+    _, codes, sc = weights(rs, N, K)
+    rows = U.rows(rs, T, K)
+    x8, xs = (dev(v) for v in U.pack8(rows))
+    X = dev(rows, kind or "f32")
+    ws = guarded(b.s2op_w4_gemv_workspace_bytes(K, min(T, 8)))
+    Y, Z = torch.zeros(T, N, device="cuda"), torch.zeros(T, N, device="cuda")
+
+    def call(out):
+        if kind is None:
+            b.s2op_w4_gemm(codes, sc, N, K, x8, x8.shape[1], xs, T, out, False, N, 0)
+        else:
+            b.s2op_w4_gemv(codes, sc, N, K, X, kind == "bf16", K, T, out, False, N, 0, ws)
+
+    call(Y)
+    torch.cuda.synchronize()
+    assert not torch.isnan(Y).any(), (kind, T, "too few polls for the product itself")
+    b.s2op_tc_gemm(a, M, D, x, 20, D, h, M, split_k=1)
+    call(Z)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Z), (kind, T)
+print("LONG_OK")
+"""
+
+
+def test_waits_do_not_count_the_kernel_ahead():
+    """A wait gives up after so much of its own kernel's time: with polls for a tenth of a millisecond or so, products
+    behind a kernel that takes longer and lets them start under it come out whole."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", LONG], cwd=root, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, S2_FAULT_W4_POLLS="1000"))
+    assert "LONG_OK" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
