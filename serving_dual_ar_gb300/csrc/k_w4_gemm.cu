@@ -60,6 +60,11 @@ S2_DEV bool w4_wait(uint64_t* bar, uint32_t parity, unsigned polls, volatile int
   *fail = 1;
   return false;
 }
+// The same for a whole warp, with one outcome: what follows it (loads of tensor
+// memory, shuffles) needs every lane, and lanes count their polls each for itself.
+S2_DEV bool w4_wait_warp(uint64_t* bar, uint32_t parity, unsigned polls, volatile int* fail) {
+  return __all_sync(0xffffffffu, w4_wait(bar, parity, polls, fail));
+}
 
 // 16 columns of this thread's tensor-memory lane, there after the next wait.
 S2_DEV void tmem_issue16(uint32_t taddr, uint32_t* r) {
@@ -422,7 +427,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
 #pragma unroll
         for (int b = 0; b < B; ++b) raw[b].get(v[b]);
         if (s + 4 < nk) load(s + 4);
-        if (s >= STAGES && !w4_wait(&empty[slot], (s / STAGES + 1) & 1, p.polls, fail)) break;
+        if (s >= STAGES && !w4_wait_warp(&empty[slot], (s / STAGES + 1) & 1, p.polls, fail)) break;
         uint8_t* rows8 = smem + slot * STAGE + B_AT;
 #pragma unroll
         for (int b = 0; b < B; ++b)
@@ -443,7 +448,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
     const int chunks = (nk + CH - 1) / CH;
     for (int c = 0; c < chunks; ++c) {
       const int buf = c & 1;
-      if (!w4_wait(&acc_full[buf], (c >> 1) & 1, p.polls, fail)) break;
+      if (!w4_wait_warp(&acc_full[buf], (c >> 1) & 1, p.polls, fail)) break;
       tc_fence_after();
       if (c == 0) {
         tmem_ld_row<GN>(from, acc);
@@ -707,7 +712,7 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
       float acc[GN];
       for (int c = 0; c < chunks; ++c) {
-        if (!ok || !(ok = w4_wait(&acc_full[buf], parity, p.polls, fail))) break;
+        if (!ok || !(ok = w4_wait_warp(&acc_full[buf], parity, p.polls, fail))) break;
         tc_fence_after();
         if (c == 0) {
           tmem_ld_row<GN>(from + buf * TN, acc);
@@ -728,7 +733,6 @@ w4_tc_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
           parity ^= 1;
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
 #pragma unroll
         for (int i = 0; i < GN; ++i) acc[i] = __uint_as_float(0x7fffffffu);

@@ -117,3 +117,21 @@ def test_waits_do_not_count_the_kernel_ahead():
     r = subprocess.run([sys.executable, "-c", LONG], cwd=root, capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, S2_FAULT_W4_POLLS="1000"))
     assert "LONG_OK" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+# plain rows whose parts wait for a stage to come free, and tiles of several sums
+LONGER = """CASES = [("f32", 1, 19600, 900), ("bf16", 2, 19600, 900), ("f32", 2, 130, 20480), ("bf16", 1, 140, 16500),
+         (None, 3, 130, 9000), (None, 200, 20000, 1000), (None, 300, 2000, 2560)]
+"""
+
+
+@pytest.mark.parametrize("polls", [5, 50, 200, 800])
+def test_every_lane_of_a_warp_takes_the_same_way_out(polls):
+    """A wait that runs out somewhere in the middle of a product: its warps go on whole, so the product ends."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    child = CHILD[:CHILD.index("CASES")] + LONGER + CHILD[CHILD.index("for i, (kind"):]
+    r = subprocess.run([sys.executable, "-c", child, str(polls)], cwd=root, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, S2_FAULT_W4_POLLS=str(polls)))
+    assert "POLLS_OK" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
