@@ -397,11 +397,8 @@ int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int 
  *   (gate_i, up_i): Y[t, i] = silu(gate) * up, N even.
  * Y: fp32 or bf16 (y_bf16 = 1), apart from the other operands; sums are fp32,
  * rounded once as they are stored.  Rows and weights that are NaN make NaN of their
- * own row or column of Y alone.  codes and scale are read from the moment that the
- * launch may begin, which is ahead of the end of the stream's kernel before if that
- * one allows it (programmatic dependent launch, as the other calls of this section
- * do): a kernel of your own that writes weights and allows that has to be followed
- * by one that does not.  s2op_w4_pack does not.
+ * own row or column of Y alone.  Every operand, the weights among them, is read in
+ * the stream's order: a product may follow the call that writes it directly.
  * s2op_w4_gemv: B = 1..8 plain rows X.  A value is taken whole where it lies within
  * 2^13 (fp32; bf16: 2^17) of the largest of its group of 32, and to 2^-37 (2^-25) of
  * that one where it is smaller.  workspace: at least

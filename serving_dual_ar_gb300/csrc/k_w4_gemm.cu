@@ -45,6 +45,7 @@ struct W4Params {
   long long ldx;
   int x_vec;
   long long ldy;
+  const uint8_t* codes;
   const uint8_t* w_scale;
   const uint8_t* x_scale;
   void* y;
@@ -97,6 +98,11 @@ S2_DEV void w4_load_2d(uint32_t dst, uint64_t map, int x, int y, uint32_t bar) {
 S2_DEV void w4_load(uint32_t dst, const void* src, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(src), "r"(kMxTile), "r"(bar) : "memory");
+}
+
+// Towards L2 alone; both a multiple of 16.
+S2_DEV void w4_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(bytes) : "memory");
 }
 
 constexpr int w4_stage_bytes(int tn) { return 128 * 128 + tn * 128 + (tn > 128 ? 2048 : 1024); }
@@ -273,7 +279,10 @@ S2_DEV void parts_of(float (&v)[4], int lane, F put) {
 // One tile of 128 weights and TN rows a CTA, or one part of K of it.  A k-tile of
 // the stream is 8.7 KB of weights; ten stages of 16 rows keep 87 KB an SM under way,
 // which 6 TB/s need (1 row times 19,456 x 20,480: 34.9 us, 6.1 TB/s; five stages 41.9).
-// The weights of the first stages are asked for ahead of the kernel before.
+// Under the kernel ahead the first stages' weights are brought to L2 (4 bf16 rows
+// times 2,560 x 9,728 7.4 us; without that 8.0); to shared memory they come behind
+// it, as the rows do: it, or one before it, may have written them, and only its end
+// makes that visible.
 // P: rows of the operand per row of X (parts of its values, added up).  TX: the
 // type of plain rows whose parts four warps of the CTA make, each every fourth
 // k-tile's; uint8_t: rows of 8 bits in memory.
@@ -341,38 +350,24 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
       const uint8_t* xs = p.x_scale + ((size_t)(t0 >> 7) * p.KT + kt0) * kMxTile;
       const uint32_t sm = smem_u32(smem);
       int k = kt0 * 128, left = nk;
-      auto weights = [&](int i, int ahead) {      // codes count as they lie in memory
-        mbar_arrive_expect_tx(&full[i], 128 * 64 + kMxTile + (PLAIN ? 0 : TN * 128 + kMxTile));
-        w4_load_2d(sm + i * STAGE, mw, k + ahead * 128, n0, smem_u32(&full[i]));
-        w4_load(sm + i * STAGE + SF_AT, ws + ahead * kMxTile, smem_u32(&full[i]));
-      };
-      auto rows = [&](int i) {
-        if (!PLAIN) {
-          w4_load_2d(sm + i * STAGE + B_AT, mx, k, t0, smem_u32(&full[i]));
-          w4_load(sm + i * STAGE + SF_AT + kMxTile, xs, smem_u32(&full[i]));
-        }
-        ws += kMxTile;
-        xs += kMxTile;
-        k += 128;
-        --left;
-      };
-      // The first weights are under way before the kernel ahead has ended; the
-      // rows are what it may have written.
-      const int first = min(nk, STAGES);
-#pragma unroll
-      for (int i = 0; i < STAGES; ++i)
-        if (i < first) weights(i, i);
-      pdl_wait();
-#pragma unroll
-      for (int i = 0; i < STAGES; ++i)
-        if (i < first) rows(i);
+      pdl_wait();     // nothing is read ahead of it
       bool ok = true;
-      for (int r = 1; left > 0 && ok; ++r) {
+      for (int r = 0; left > 0 && ok; ++r) {
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) {
-          if (left <= 0 || !(ok = w4_wait(&empty[i], (r + 1) & 1, p.polls, fail))) break;
-          weights(i, 0);
-          rows(i);
+          if (left <= 0 || (r > 0 && !(ok = w4_wait(&empty[i], (r + 1) & 1, p.polls, fail)))) break;
+          // codes count as they lie in memory
+          mbar_arrive_expect_tx(&full[i], 128 * 64 + kMxTile + (PLAIN ? 0 : TN * 128 + kMxTile));
+          w4_load_2d(sm + i * STAGE, mw, k, n0, smem_u32(&full[i]));
+          w4_load(sm + i * STAGE + SF_AT, ws, smem_u32(&full[i]));
+          if (!PLAIN) {
+            w4_load_2d(sm + i * STAGE + B_AT, mx, k, t0, smem_u32(&full[i]));
+            w4_load(sm + i * STAGE + SF_AT + kMxTile, xs, smem_u32(&full[i]));
+          }
+          ws += kMxTile;
+          xs += kMxTile;
+          k += 128;
+          --left;
         }
       }
       // behind a wait that gave up, copies may still be under way
@@ -443,6 +438,10 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ 
       }
     }
   } else {
+    // the first stages' weights towards L2, a row a thread of the first group
+    const int first = min(nk, STAGES), row = (int)threadIdx.x - 64;
+    if (row < 128 && n0 + row < p.N) w4_prefetch(p.codes + ((size_t)(n0 + row) * p.KT + kt0) * 64, first * 64);
+    if (row == 0) w4_prefetch(p.w_scale + ((size_t)n_tile * p.KT + kt0) * kMxTile, first * kMxTile);
     pdl_wait();     // outputs and what they are added to
     const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp - 2) / 4 * GN;
     const int chunks = (nk + CH - 1) / CH;
@@ -861,6 +860,7 @@ bool w4_fill(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, const uin
   p->mode = a.mode;
   p->y_bf16 = a.y_bf16;
   p->ldy = a.ldy;
+  p->codes = a.codes;
   p->w_scale = a.scale;
   p->x_scale = x_scale;
   p->y = a.y;

@@ -709,3 +709,58 @@ def test_between_bf16_products(s2, T):
     for _ in range(20):
         for got, want in zip(run(), alone):
             assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- weights written just ahead
+
+@pytest.mark.parametrize("kind,T,N,K", [("f32", 1, 640, 2560), ("bf16", 2, 300, 20000), ("f32", 5, 640, 2560), ("bf16", 8, 640, 2560),
+                                        ("f32", 1, 20000, 512), (None, 1, 640, 2560), (None, 40, 20000, 512),
+                                        (None, 100, 640, 2560), (None, 100, 12000, 512), (None, 300, 6000, 512)])
+def test_weights_packed_just_ahead(s2, kind, T, N, K):
+    """A product directly behind the packing of its weights, or with a call between that starts early, takes the new ones;
+    a packing directly behind a product does not disturb it."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    W = [torch.randn(N, K, device="cuda", generator=g).bfloat16() for _ in range(2)]
+    X = dev(U.rows(np.random.RandomState(T), T, K), kind or "f32")
+    x8, xs = torch.zeros(T, U.up(K, 16), dtype=torch.uint8, device="cuda"), guarded(s2.s2op_mx_scale_bytes(T, K), 0)
+    s2.s2op_mx8_pack(X, kind == "bf16", K, T, K, x8, U.up(K, 16), xs)
+    z8, zs = torch.zeros_like(x8), guarded(s2.s2op_mx_scale_bytes(T, K), 0)
+    codes, sc = guarded(s2.s2op_w4_code_bytes(N, K)), guarded(s2.s2op_mx_scale_bytes(N, K))
+    ws = guarded(s2.s2op_w4_gemv_workspace_bytes(K, min(T, 8)))
+    st = torch.cuda.Stream()
+
+    def pack(i):
+        s2.s2op_w4_pack(W[i], True, N, K, K, codes, sc, st)
+
+    def product(Y):
+        if kind is None:
+            s2.s2op_w4_gemm(codes, sc, N, K, x8, U.up(K, 16), xs, T, Y, False, N, 0, st)
+        else:
+            s2.s2op_w4_gemv(codes, sc, N, K, X, kind == "bf16", K, T, Y, False, N, 0, ws, st)
+
+    def steps(Y):
+        for i in range(len(Y)):
+            pack(i % 2)
+            if i % 4 > 1:
+                s2.s2op_mx8_pack(X, kind == "bf16", K, T, K, z8, U.up(K, 16), zs, st)
+            product(Y[i])
+
+    want = torch.zeros(2, T, N, device="cuda")
+    Y = torch.zeros(16, T, N, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(2):
+        pack(i)
+        torch.cuda.synchronize()
+        product(want[i])
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        steps(Y)
+    for run in (lambda: steps(Y), graph.replay):
+        for _ in range(3):
+            Y.zero_()
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            assert torch.equal(Y, want.repeat(8, 1, 1))
