@@ -24,11 +24,10 @@
 // parts through distributed shared memory.  Clusters that wait for one another
 // must not also wait for tensor memory that the other holds: each CTA of a cluster
 // takes more than half of an SM's shared memory, so no two of them meet on one.
+#include "kept_count.h"
 #include "mx_common.cuh"
 #include "tc_common.cuh"
 #include "tma_map.h"
-
-#include <atomic>
 
 namespace s2 {
 
@@ -804,15 +803,16 @@ cudaError_t launch_tc(const CUtensorMap& mw, const CUtensorMap& mx, const W4Para
 
 // Clusters of S CTAs that are on the current device at once (kept per device).
 template <int TN, int STAGES, int P, typename TX = uint8_t>
-int cluster_room(int S) {
-  static std::atomic<int> kept[16][9];
+cudaError_t cluster_room(int S, int* n) {
+  static KeptCounts<9> kept;
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 16 && kept[dev][S].load()) return kept[dev][S].load() - 1;
-  constexpr int SMEM = w4_smem<TN, STAGES, P, true>();
-  auto k = w4_tc_kernel<TN, STAGES, P, true, TX>;
-  int n = 0;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess) {
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return kept.get(dev, S, n, [&](int* m) {
+    constexpr int SMEM = w4_smem<TN, STAGES, P, true>();
+    auto k = w4_tc_kernel<TN, STAGES, P, true, TX>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, S);
     cfg.blockDim = dim3(w4_threads(TN) + (sizeof(TX) > 1 ? 128 : 0));
@@ -824,19 +824,23 @@ int cluster_room(int S) {
     attr.val.clusterDim.z = S;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) n = 0;
-  }
-  cudaGetLastError();
-  if (dev < 16) kept[dev][S].store(n + 1);
-  return n;
+    return cudaOccupancyMaxActiveClusters(m, k, &cfg);
+  });
 }
 
 // As many parts of K as have room on the SMs at once, two k-tiles each at least.
+// An error of the device is passed on: another number of parts gives other bits.
 template <int TN, int STAGES, int P, typename TX = uint8_t>
-int w4_parts(int KT, long long tiles) {
+cudaError_t w4_parts(int KT, long long tiles, int* parts) {
   int S = KT / 2 < 8 ? KT / 2 : 8;
-  while (S > 1 && tiles > cluster_room<TN, STAGES, P, TX>(S)) --S;
-  return S > 1 ? S : 1;
+  for (; S > 1; --S) {
+    int room = 0;
+    const cudaError_t e = cluster_room<TN, STAGES, P, TX>(S, &room);
+    if (e != cudaSuccess) return e;
+    if (tiles <= room) break;
+  }
+  *parts = S > 1 ? S : 1;
+  return cudaSuccess;
 }
 
 int w4_sms() {
@@ -882,7 +886,9 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   CUtensorMap mw, mx = {};
   W4Params p;
   if (!w4_fill<TN, P>(a, rows8, ld8, x_scale, &mw, &mx, &p)) return cudaErrorInvalidValue;
-  const int S = w4_parts<TN, SC, P, TX>(p.KT, p.tiles);
+  int S = 1;
+  const cudaError_t e = w4_parts<TN, SC, P, TX>(p.KT, p.tiles, &S);
+  if (e != cudaSuccess) return e;
   if (S > 1) return launch_tc<TN, SC, P, true, TX>(mw, mx, p, dim3(p.tiles, 1, S), st);
   // More tiles than SMs: half the stages, so that two CTAs share an SM and one's
   // start and end lie under the other's products (1 row times 20,000 x 2,560 11.2 ->
@@ -965,7 +971,9 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   // get long: what they send one another halves (128 rows times 6,144 x 2,560 10.0 ->
   // 6.6 us, 2,560 x 4,096 7.6 -> 7.2 us; 2,560 x 9,728, of 26 k-tiles a part, 8.4 -> 9.1)
   if (a.T <= 128 && 2 * n_tiles <= sms) {
-    const int S = w4_parts<64, 7, 1>(KT, 2 * n_tiles);
+    int S = 1;
+    const cudaError_t e = w4_parts<64, 7, 1>(KT, 2 * n_tiles, &S);
+    if (e != cudaSuccess) return e;
     if ((KT + S - 1) / S <= 20) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
   }
   if (a.T <= 128 && n_tiles <= sms) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
@@ -979,7 +987,9 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   const long long c128 = cost(128, 25), c192 = cost(192, 32), c256 = a.y_bf16 && KT <= kWholeSum ? cost(256, 45) : 1LL << 60;
   const long long best = c128 < c192 ? (c128 < c256 ? c128 : c256) : (c192 < c256 ? c192 : c256);
   const long long tiles = (long long)n_tiles * ((a.T + 127) / 128);
-  const int S = w4_parts<128, 4, 1>(KT, tiles);
+  int S = 1;
+  const cudaError_t e = w4_parts<128, 4, 1>(KT, tiles, &S);
+  if (e != cudaSuccess) return e;
   if (S > 1 && (KT + S - 1) / S * 27LL + 250 < best) return launch_tn<128, 6, 1, 4>(a, a.x8, a.ld8, a.x_scale, st);
   if (c256 == best) return launch_rows<256, 4>(a, st);
   return c192 == best ? launch_rows<192, 5>(a, st) : launch_rows<128, 6>(a, st);

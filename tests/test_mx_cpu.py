@@ -116,3 +116,19 @@ def test_refusals_products(lib):
 def test_refusals_in_place(lib):
     good = [A, 0, 64, 2 * A, 0, 64, 4, 64, A, 1e-6, 2 * A, 64, A, 64, A, None]      # the residual's rows overwritten
     refused(lib, "s2op_add_rmsnorm_mx8", good, [(4, 1), (5, 68), (11, 68), (9, float("inf"))])
+
+
+def test_a_failed_query_is_not_kept(tmp_path):
+    """What a device is asked for once is kept only where it answered."""
+    import os
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    here = os.path.dirname(os.path.abspath(__file__))
+    csrc = os.path.join(os.path.dirname(here), "serving_dual_ar_gb300", "csrc")
+    exe = str(tmp_path / "kept_count_driver")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", csrc, os.path.join(here, "kept_count_driver.cpp"),
+                    "-o", exe], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True, timeout=60).stdout == "ok\n"
