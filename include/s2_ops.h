@@ -396,7 +396,11 @@ int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int 
  *   mode 0: Y = y;  1: Y += y (residual);  2: rows (2i, 2i+1) of W hold
  *   (gate_i, up_i): Y[t, i] = silu(gate) * up, N even.
  * Y: fp32 or bf16 (y_bf16 = 1), apart from the other operands; sums are fp32,
- * rounded once as they are stored.  Rows and weights that are NaN make NaN of their
+ * rounded to Y's type once, as they are stored.  They are added up on the tensor
+ * cores, which cut towards zero, by about 2^-24 of the sum so far for each 32 k, and
+ * go to sums rounded to nearest every 896 k or sooner; where Y is bf16 and T above
+ * 64, every 16,384 k or sooner (about 2^-15 of sum |x w| at most, which an output
+ * of much smaller size shows).  Rows and weights that are NaN make NaN of their
  * own row or column of Y alone.  Every operand, the weights among them, is read in
  * the stream's order: a product may follow the call that writes it directly.
  * s2op_w4_gemv: B = 1..8 plain rows X.  A value is taken whole where it lies within

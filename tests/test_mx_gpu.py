@@ -764,3 +764,31 @@ def test_weights_packed_just_ahead(s2, kind, T, N, K):
             run()
             torch.cuda.synchronize()
             assert torch.equal(Y, want.repeat(8, 1, 1))
+
+
+# ---------------------------------------------------------------- sums that cancel
+
+@pytest.mark.parametrize("T,N,K,ty", [(1, 256, 16384, "bf16"), (64, 256, 16384, "bf16"), (300, 12000, 2560, "bf16"),
+                                      (1000, 2560, 16384, "bf16"), (600, 19456, 4096, "bf16"), (520, 6144, 17000, "bf16"),
+                                      (1000, 2560, 16384, "f32")])
+def test_sums_that_cancel(s2, T, N, K, ty):
+    """Positive products added to what takes all but their last bits away: what is left shows how the sum was made.
+    Each step of 32 k on the tensor core may cut 2^-23 of the sum so far, four times what it does on the average over a
+    sum that grows evenly (2^-24 of half of it), up to 16,384 k where the output is bf16 and T above 64, 896 otherwise."""
+    codes, sc = random_weights(N, K, K)
+    codes &= 0x77                                               # no signs
+    x8, xs = U.pack8(np.abs(U.rows(np.random.RandomState(T), T, K)))
+    xv = torch.from_numpy(U.unpack8(x8, xs, T, K)).cuda()
+    rows = np.unique(np.concatenate([[0, 127, N - 1], np.random.RandomState(N).randint(0, N, 200)]))
+    v, A = on_gpu(codes, sc, N, K, xv, rows)
+    at = torch.as_tensor(rows, device="cuda")
+    Y = torch.zeros(T, N, dtype=TYPES[ty], device="cuda")
+    Y[:, at] = (-v).to(TYPES[ty])
+    y0 = Y[:, at].double()
+    s2.s2op_w4_gemm(codes, sc, N, K, dev(x8), x8.shape[1], dev(xs), T, Y, ty == "bf16", N, 1)
+    want = y0 + v
+    steps = min(K, 16384 if ty == "bf16" and T > 64 else 896) / 32
+    d = (steps * 2.0 ** -23 + (K / 512 + 17) * 2.0 ** -24) * A
+    d = d + 2.0 ** -24 * (want.abs() + d)                       # the addition
+    d = d + (2.0 ** -8 if ty == "bf16" else 2.0 ** -24) * (want.abs() + d)
+    assert ((Y[:, at].double() - want).abs() / d).max().item() <= 1
