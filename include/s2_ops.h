@@ -403,7 +403,7 @@ int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int 
  * of much smaller size shows).  Rows and weights that are NaN make NaN of their
  * own row or column of Y alone.  Every operand, the weights among them, is read in
  * the stream's order: a product may follow the call that writes it directly.
- * s2op_w4_gemv: B = 1..8 plain rows X.  A value is taken whole where it lies within
+ * s2op_w4_gemv: B = 1..8 plain rows X; infinities in them count as NaN.  A value is taken whole where it lies within
  * 2^13 (fp32; bf16: 2^17) of the largest of its group of 32, and to 2^-37 (2^-25) of
  * that one where it is smaller.  workspace: at least
  * s2op_w4_gemv_workspace_bytes(K, B) bytes, 16-byte aligned, of any content (0

@@ -792,3 +792,20 @@ def test_sums_that_cancel(s2, T, N, K, ty):
     d = d + 2.0 ** -24 * (want.abs() + d)                       # the addition
     d = d + (2.0 ** -8 if ty == "bf16" else 2.0 ** -24) * (want.abs() + d)
     assert ((Y[:, at].double() - want).abs() / d).max().item() <= 1
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 4, 8])
+def test_infinities_of_plain_rows_count_as_nan(s2, T, kind):
+    rs = np.random.RandomState(T)
+    N, K = 140, 500
+    wv, codes, sc = weights(rs, N, K)
+    x = U.rows(rs, T, K)
+    x[T // 2, 300] = np.inf if T % 4 else -np.inf
+    X = dev(x, kind)
+    Y = torch.zeros(T, N, device="cuda")
+    s2.s2op_w4_gemv(codes, sc, N, K, X, kind == "bf16", K, T, Y, False, N, 0, guarded(s2.s2op_w4_gemv_workspace_bytes(K, T)))
+    got = host(Y)
+    assert np.isnan(got[T // 2]).all()
+    x = np.delete(host(X), T // 2, 0)
+    assert (np.abs(np.delete(got, T // 2, 0) - x @ wv.T) <= (sum_bound(K) + 2.0 ** -24) * (np.abs(x) @ np.abs(wv).T)).all()
