@@ -403,11 +403,13 @@ int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int 
  * of much smaller size shows).  Rows and weights that are NaN make NaN of their
  * own row or column of Y alone.  Every operand, the weights among them, is read in
  * the stream's order: a product may follow the call that writes it directly.
- * s2op_w4_gemv: B = 1..8 plain rows X; infinities in them count as NaN.  A value is taken whole where it lies within
- * 2^13 (fp32; bf16: 2^17) of the largest of its group of 32, and to 2^-37 (2^-25) of
- * that one where it is smaller.  workspace: at least
- * s2op_w4_gemv_workspace_bytes(K, B) bytes, 16-byte aligned, of any content (0
- * bytes for sizes that are refused).  Calls that may overlap in time need one
+ * s2op_w4_gemv: B = 1..8 plain rows X; infinities in them count as NaN.  A value is
+ * taken whole where it lies within 2^13 (fp32; bf16: 2^17) of the largest of its
+ * group of 32, and to 2^-37 (2^-25) of that one where it is smaller; of all values
+ * 2^-136 may be missing, which groups below 2^-98 (2^-110) notice.  Their 8-bit parts
+ * are summed apart, so that outputs are finite where sum |x w| < 2^127.  workspace:
+ * at least s2op_w4_gemv_workspace_bytes(K, B) bytes, 16-byte aligned, of any content
+ * (0 bytes for sizes that are refused).  Calls that may overlap in time need one
  * each.
  * s2op_w4_gemm: T rows of 8 bits with scales, from s2op_mx8_pack or
  * s2op_add_rmsnorm_mx8. */

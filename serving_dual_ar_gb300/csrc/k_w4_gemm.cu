@@ -209,7 +209,8 @@ S2_DEV void st_async4(uint32_t at, float x, float y, float z, float w, uint32_t 
 // fall by 2^4 from one to the next: each takes four bits or more of what the
 // ones before it left, exactly.  What remains is 2^-10 of the last row's scale at
 // most, 2^-37 (2^-25) of the group's largest magnitude, and nothing of values
-// within 2^13 (2^17) of that.  NaN stays NaN, and e4m3 has nothing else for an infinity.
+// within 2^13 (2^17) of that; no scale is below 2^-126, so 2^-136 may remain of any
+// value.  NaN stays NaN, and e4m3 has nothing else for an infinity.
 constexpr int kParts32 = 6, kParts16 = 3;
 // Up to this many rows' parts are made by the CTAs that multiply them.  With 6,144
 // x 2,560 weights 1, 2 and 4 fp32 rows take 5.3, 5.9 and 10.3 us that way, and 5.9,
@@ -262,7 +263,12 @@ S2_DEV void parts_of(float (&v)[4], int lane, F put) {
   for (int p = 0; p < P; ++p) {
     const int ep = max(e - 4 * p, kMxEMin);
     const float f = mx_pow2(-ep), g = mx_pow2(ep);
-    const uint32_t c = mx_e4m3x2(v[0] * f, v[1] * f) | (mx_e4m3x2(v[2] * f, v[3] * f) << 16);
+    float q[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f};
+    if (p == 0 && e == kMxEMax) {      // the next code, 256 * 2^120, would be infinite as a sum of fp32
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = fabsf(q[i]) > 240.f ? copysignf(240.f, q[i]) : q[i];
+    }
+    const uint32_t c = mx_e4m3x2(q[0], q[1]) | (mx_e4m3x2(q[2], q[3]) << 16);
     if (p < P - 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? fmaf(-mx_e4m3(c >> (8 * i)), g, v[i]) : 0.f;

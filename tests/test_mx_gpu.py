@@ -809,3 +809,57 @@ def test_infinities_of_plain_rows_count_as_nan(s2, T, kind):
     assert np.isnan(got[T // 2]).all()
     x = np.delete(host(X), T // 2, 0)
     assert (np.abs(np.delete(got, T // 2, 0) - x @ wv.T) <= (sum_bound(K) + 2.0 ** -24) * (np.abs(x) @ np.abs(wv).T)).all()
+
+
+# ---------------------------------------------------------------- plain rows value by value
+
+def unit_weights(s2, K):
+    """The unit matrix: output n of a product with it is value n of the row."""
+    codes, sc = guarded(s2.s2op_w4_code_bytes(K, K), 0), guarded(s2.s2op_mx_scale_bytes(K, K), 127)
+    n = torch.arange(K, device="cuda")
+    codes.view(K, -1)[n, n // 2] = torch.where(n % 2 == 0, 0x02, 0x20).to(torch.uint8)      # 1.0
+    return codes, sc
+
+
+def check_values(s2, x, kind, least):
+    T, K = x.shape
+    X = dev(x.astype(np.float32), kind)
+    codes, sc = unit_weights(s2, K)
+    Y = torch.zeros(T, K, device="cuda")
+    s2.s2op_w4_gemv(codes, sc, K, K, X, kind == "bf16", K, T, Y, False, K, 0, guarded(s2.s2op_w4_gemv_workspace_bytes(K, T), 0xFF))
+    x, got = host(X), host(Y)
+    top = np.zeros((T, U.up(K, 32)))
+    top[:, :K] = np.abs(x)
+    top = np.repeat(top.reshape(T, -1, 32).max(-1), 32, 1)[:, :K]
+    near, left = (2.0 ** -13, 2.0 ** -37) if kind == "f32" else (2.0 ** -17, 2.0 ** -25)
+    whole = (np.abs(x) >= near * top) & (top >= least)
+    assert whole.any() or least > top.max()
+    assert np.array_equal(got[whole], x[whole])
+    assert (np.abs(got - x) <= np.maximum(left * top, 2.0 ** -136)).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 6, 8])
+@pytest.mark.parametrize("K", [100, 1000])
+def test_values_of_plain_rows(s2, K, T, kind):
+    """Values within 2^13 (bf16: 2^17) of their group's largest are taken whole, smaller ones to 2^-37 (2^-25) of it."""
+    rs = np.random.RandomState(K + T)
+    group = np.repeat(2.0 ** rs.uniform(-90, 100, (T, U.up(K, 32) // 32)), 32, 1)[:, :K]
+    x = group * 2.0 ** rs.uniform(-30, 0, (T, K)) * rs.choice([-1, 1], (T, K))
+    x[:, ::7] = group[:, ::7] * 2.0 ** -rs.randint(8, 20, x[:, ::7].shape) * rs.uniform(1, 2, x[:, ::7].shape)
+    x[:, 5::32] = group[:, 5::32]
+    check_values(s2, x, kind, 2.0 ** -95)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 7])
+def test_values_of_tiny_and_huge_rows(s2, T, kind):
+    """Groups next to fp32's ends, subnormals among them: no part has a scale below 2^-126, so 2^-136 may be missing."""
+    rs = np.random.RandomState(T)
+    K = 640
+    group = np.repeat(2.0 ** np.linspace(-148, -94, T * 20).reshape(T, 20), 32, 1)
+    x = group * 2.0 ** rs.uniform(-10, 0, (T, K)) * rs.choice([-1, 1], (T, K))
+    check_values(s2, x, kind, np.inf)
+    x = 2.0 ** rs.uniform(100, 127.99, (T, K)) * rs.choice([-1, 1], (T, K))
+    x[0, :32] = 3.3e38
+    check_values(s2, x, kind, 0.0)
