@@ -863,3 +863,41 @@ def test_values_of_tiny_and_huge_rows(s2, T, kind):
     x = 2.0 ** rs.uniform(100, 127.99, (T, K)) * rs.choice([-1, 1], (T, K))
     x[0, :32] = 3.3e38
     check_values(s2, x, kind, 0.0)
+
+
+# ---------------------------------------------------------------- sizes of a model's larger matrices
+
+@pytest.mark.parametrize("ty,mode", MODES)
+@pytest.mark.parametrize("T,N,K", [(65, 9730, 700), (100, 12000, 1300), (128, 19456, 300)])
+def test_gemm_of_up_to_128_rows_and_many_weights(s2, T, N, K, ty, mode):
+    """Tiles of 128 weights by 128 rows, a CTA each, K whole."""
+    many(s2, T, N, K, ty, mode, T + K)
+
+
+@pytest.mark.parametrize("x_kind", ["f32", "bf16"])
+@pytest.mark.parametrize("ty,mode", [("f32", 0), ("bf16", 1), ("f32", 2)])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 6, 8])
+def test_gemv_of_more_tiles_than_sms(s2, T, ty, mode, x_kind):
+    """Two CTAs share an SM; plain rows' parts made by them, or by a kernel ahead."""
+    rs = np.random.RandomState(T)
+    for N, K in ((19458, 700), (40000, 1500)):
+        codes, sc = random_weights(N, K, N + T)
+        X = dev(U.rows(rs, T, K), x_kind)
+        cols = N // 2 if mode == 2 else N
+        Y = torch.full((T, cols), 0.5, dtype=TYPES[ty], device="cuda")
+        ws = guarded(s2.s2op_w4_gemv_workspace_bytes(K, T), 0xFF)
+        s2.s2op_w4_gemv(codes, sc, N, K, X, x_kind == "bf16", K, T, Y, ty == "bf16", cols, mode, ws)
+        v, A = on_gpu(codes, sc, N, K, X.double(), np.arange(N))
+        want = torch.nn.functional.silu(v[:, 0::2]) * v[:, 1::2] if mode == 2 else v + 0.5 * mode
+        tol = torch.from_numpy(bounds(A.cpu().numpy(), v.cpu().numpy(), 0.5, want.cpu().numpy(), ty, mode, K)).cuda()
+        off = ((Y.double() - want).abs() / tol).max().item()
+        assert off <= 1, (N, off)
+
+
+@pytest.mark.parametrize("x_kind", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (2, 0), (3, 1), (8, 8)])
+def test_pitches_of_one_and_two_plain_rows(s2, pad, shift, x_kind):
+    for T in (1, 2):
+        for K in (424, 413):
+            check_product(s2, np.random.RandomState(pad), T, 386, K, "f32", 0, x_kind, pad, shift)
+            check_product(s2, np.random.RandomState(pad), T, 386, K, "bf16", 2, x_kind, pad, shift)
