@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(256, 5) mx8_pack_vec_kernel(Mx8PackArgs p) {
 // exact values, whatever the order of the sum: the sum of squares, its inverse
 // root and the products are unevaluated sums of two floats (about 2^-44).  Rows of
 // any length and alignment; h is read back for the rounding.  A row whose sum of
-// squares leaves fp32's range is taken once more scaled by 2^-80 or 2^64 (2^120).  A row with a
-// NaN or an infinity is NaN throughout.
+// squares, or eps, leaves fp32's range is taken once more scaled by 2^-80 or 2^64
+// (2^120).  A row with a NaN or an infinity is NaN throughout.
 // 1 / sqrt(s / K + eps): a Newton step on the float one.  NaN for a row with a
 // NaN or an infinity, or with nothing at all and no eps.
 S2_DEV Two inverse_root(Two s, Two inv_k, float eps) {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mx8_kernel(AddNormMx8Args p)
     // fp32 holds the squares' sum to the last bits of two floats between about
     // 2^-79 a value and 2^120 in all
     ef = p.eps * f * f;
-    if (pass == 0 && !(s.hi < 1.329e36f)) f = 8.2718061255302767e-25f;                       // 2^-80
+    if (pass == 0 && !(s.hi + ef < 1.329e36f)) f = 8.2718061255302767e-25f;                       // 2^-80
     else if (pass < 2 && f >= 1.f && s.hi * p.inv_k.hi + ef < 1.654e-24f) f = pass ? 1.3292279957849159e36f   // 2^120
                                                                                    : 1.8446744073709552e19f;  // 2^64
     else break;
@@ -521,9 +521,9 @@ __global__ void __launch_bounds__(C == 1 ? 128 : C == 2 ? 256 : 512) add_rmsnorm
   float ef = p.eps;
   // fp32 holds the squares' sum to the last bits of two floats between about
   // 2^-79 a value and 2^120 in all
-  if (!(s.hi < 1.329e36f && s.hi * p.inv_k.hi + ef >= 1.654e-24f))
+  if (!(s.hi + ef < 1.329e36f && s.hi * p.inv_k.hi + ef >= 1.654e-24f))
     for (int pass = 0; pass < 3; ++pass) {
-      if (pass == 0 && !(s.hi < 1.329e36f)) f = 8.2718061255302767e-25f;                         // 2^-80
+      if (pass == 0 && !(s.hi + ef < 1.329e36f)) f = 8.2718061255302767e-25f;                         // 2^-80
       else if (pass < 2 && f >= 1.f && s.hi * p.inv_k.hi + ef < 1.654e-24f) f = pass ? 1.3292279957849159e36f   // 2^120
                                                                                      : 1.8446744073709552e19f;  // 2^64
       else break;

@@ -901,3 +901,16 @@ def test_pitches_of_one_and_two_plain_rows(s2, pad, shift, x_kind):
         for K in (424, 413):
             check_product(s2, np.random.RandomState(pad), T, 386, K, "f32", 0, x_kind, pad, shift)
             check_product(s2, np.random.RandomState(pad), T, 386, K, "bf16", 2, x_kind, pad, shift)
+
+
+@pytest.mark.parametrize("K", [64, 2560, 99, 20000])
+def test_add_rmsnorm_of_a_large_eps(s2, K):
+    """eps up to fp32's largest number: its sum with the mean square may lie beyond."""
+    rs = np.random.RandomState(K)
+    x = U.rows(rs, 4, K) * np.array([1.0, 1e9, 1e17, 1e19])[:, None]
+    gain = rs.uniform(0.5, 1.5, K).astype(np.float32)
+    for eps in (1e20, 1e36, 3.4028234e38):
+        h, y8, sc = run_norm(s2, x, None, gain, eps, "f32", "f32")
+        v, e = U.round8(norm64(h, gain.astype(np.float64), float(np.float32(eps))))
+        assert same(U.VALUE8[y8], v), eps
+        assert np.array_equal(sc, U.tiles((e + 127).astype(np.uint8), K, 0xAB))
