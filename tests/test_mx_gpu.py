@@ -914,3 +914,19 @@ def test_add_rmsnorm_of_a_large_eps(s2, K):
         v, e = U.round8(norm64(h, gain.astype(np.float64), float(np.float32(eps))))
         assert same(U.VALUE8[y8], v), eps
         assert np.array_equal(sc, U.tiles((e + 127).astype(np.uint8), K, 0xAB))
+
+
+@pytest.mark.parametrize("x_kind", [None, "f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_product_of_opposite_sizes(s2, T, x_kind):
+    """Weights and rows whose scales lie at opposite ends: products of ordinary size."""
+    if x_kind and T > 8:
+        pytest.skip("plain rows: up to 8")
+    rs = np.random.RandomState(T)
+    N, K = 200, 640
+    e = np.repeat(rs.choice([-118, -100, -40, 0, 40, 100], K // 32), 32)
+    w = rs.standard_normal((N, K)) * 2.0 ** np.where(e > 0, e, e + 10.0)
+    x = rs.standard_normal((T, K)) * 2.0 ** -e
+    codes, sc = U.pack4(w)
+    check_product(s2, rs, T, N, K, "f32", 0, x_kind, x=x.astype(np.float32).astype(np.float64),
+                  w=(U.unpack4(codes, sc, N, K), dev(codes), dev(sc)))
