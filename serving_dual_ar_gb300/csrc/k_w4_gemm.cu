@@ -213,9 +213,11 @@ S2_DEV void st_async4(uint32_t at, float x, float y, float z, float w, uint32_t 
 // value.  NaN stays NaN, and e4m3 has nothing else for an infinity.
 constexpr int kParts32 = 6, kParts16 = 3;
 // Up to this many rows' parts are made by the CTAs that multiply them.  With 6,144
-// x 2,560 weights 1, 2 and 4 fp32 rows take 5.3, 5.9 and 10.3 us that way, and 5.9,
-// 6.0 and 6.4 us with a kernel ahead that leaves them in memory; bf16 rows 5.4, 5.7
-// and 6.7 against 5.6, 5.7 and 5.8.
+// x 2,560 weights 1, 2, 3 and 4 fp32 rows take 5.7, 6.4, 8.1 and 9.2 us that way, and
+// 6.7 us with a kernel ahead that leaves them in memory; bf16 rows 5.5, 5.7, 6.7 and
+// 7.3 against 6.2 to 6.3.  The border is the same at 2,560 x 4,096, 2,560 x 9,728,
+// 19,456 x 2,560 and 40,000 x 1,024 (two rows 3 to 14 % faster in the CTAs, three 3 to
+// 29 % slower, but for bf16 rows with the smallest of them, 5.2 for 5.5).
 constexpr int kPlainRows = 2;
 
 // Four values of a lane, 128 of a warp, as they lie in memory (vec: on 16 bytes;
@@ -284,7 +286,7 @@ S2_DEV void parts_of(float (&v)[4], int lane, F put) {
 
 // One tile of 128 weights and TN rows a CTA, or one part of K of it.  A k-tile of
 // the stream is 8.7 KB of weights; ten stages of 16 rows keep 87 KB an SM under way,
-// which 6 TB/s need (1 row times 19,456 x 20,480: 34.9 us, 6.1 TB/s; five stages 41.9).
+// which 6 TB/s need (1 row times 19,456 x 20,480: 36.2 us, 5.9 TB/s; five stages 41.9).
 // Under the kernel ahead the first stages' weights are brought to L2 (4 bf16 rows
 // times 2,560 x 9,728 7.4 us; without that 8.0); to shared memory they come behind
 // it, as the rows do: it, or one before it, may have written them, and only its end
@@ -899,7 +901,7 @@ cudaError_t launch_tn(const W4GemmArgs& a, const uint8_t* rows8, long long ld8, 
   if (S > 1) return launch_tc<TN, SC, P, true, TX>(mw, mx, p, dim3(p.tiles, 1, S), st);
   // More tiles than SMs: half the stages, so that two CTAs share an SM and one's
   // start and end lie under the other's products (1 row times 20,000 x 2,560 11.2 ->
-  // 7.8 us, times 156,032 x 2,560 50.5 -> 41.2).
+  // 8.0 us, times 156,032 x 2,560 50.5 -> 41.5).
   if constexpr (TN <= 64) {
     if (p.tiles > w4_sms()) return launch_tc<TN, (STAGES + 1) / 2, P, false, TX>(mw, mx, p, dim3(p.tiles), st);
   }
@@ -977,8 +979,10 @@ cudaError_t launch_w4_gemm(const W4GemmArgs& a, cudaStream_t st) {
   const int KT = (a.K + 127) / 128, n_tiles = (a.N + 127) / 128, sms = w4_sms();
   if (a.T <= 64) return launch_tn<64, 7, 1>(a, a.x8, a.ld8, a.x_scale, st);
   // up to 128 rows in two tiles of 64 where the SMs have room and K's parts do not
-  // get long: what they send one another halves (128 rows times 6,144 x 2,560 10.0 ->
-  // 6.6 us, 2,560 x 4,096 7.6 -> 7.2 us; 2,560 x 9,728, of 26 k-tiles a part, 8.4 -> 9.1)
+  // get long: what they send one another halves, but each takes in the weights for
+  // itself.  128 rows times 6,144 x 2,560 10.1 -> 6.7 us, 2,560 x 4,096 7.9 -> 7.4, 4,096 x
+  // 4,096 9.0 -> 9.1; 80 rows 8.7 -> 6.6, 6.8 -> 7.0, 7.8 -> 8.8.  Longer parts: 128 rows times
+  // 4,096 x 8,192 11.5 -> 11.8 us, 2,560 x 9,728 10.2 -> 9.9; 80 rows 10.3 -> 11.5, 9.1 -> 9.6.
   if (a.T <= 128 && 2 * n_tiles <= sms) {
     int S = 1;
     const cudaError_t e = w4_parts<64, 7, 1>(KT, 2 * n_tiles, &S);
