@@ -407,7 +407,7 @@ int s2op_add_rmsnorm_mx8(const void* X, int x_bf16, int ldx, const void* R, int 
  * taken whole where it lies within 2^13 (fp32; bf16: 2^17) of the largest of its
  * group of 32, and to 2^-37 (2^-25) of that one where it is smaller; of all values
  * 2^-136 may be missing, which groups below 2^-98 (2^-110) notice.  Their 8-bit parts
- * are summed apart, so that outputs are finite where sum |x w| < 2^127.  workspace:
+ * are summed apart, so that sums are finite where sum |x w| < 2^127.  workspace:
  * at least s2op_w4_gemv_workspace_bytes(K, B) bytes, 16-byte aligned, of any content
  * (0 bytes for sizes that are refused).  Calls that may overlap in time need one
  * each.
